@@ -276,6 +276,153 @@ size_t m4q_attention_workspace_bytes(int64_t H, int64_t Hkv, int64_t M, int64_t 
  * 0 when it uses none, or for an invalid shape. */
 size_t m4q_attention_workspace(int kv_codec, int64_t H, int64_t Hkv, int64_t M, int64_t T, int64_t D);
 
+/* ---------------------------------------------------------------------------
+ * Between the projections and attention: rotary positions, the KV cache
+ * written and read back, attention of drafted trees of tokens over a batch of
+ * caches, and the norms around a block.  A decoder layer's step is
+ *   m4q_norm_residual -> m4q_gemm_heads (Q, K, V) -> m4q_kv_write (with Q)
+ *   -> m4q_attention_tree or m4q_attention -> m4q_gemm -> m4q_norm_residual
+ *   -> m4q_mlp.
+ *
+ * A batch of caches: Kc, Vc hold [B][Hkv][C] rows of D values (D 64 or 128),
+ * C the capacity in rows of every sequence; a row is fp16 (kv_codec
+ * M4Q_KV_F16) or Q8_0 blocks along D (M4Q_Q8_0), as for m4q_attention, whose
+ * caches are those of one sequence with T = C.  B * Hkv * C <= INT32_MAX, and
+ * a Q8_0 cache is a multiple of 16 bytes (always so where C % 4 == 0), else
+ * M4Q_ERR_BAD_SHAPE.  Row b * C + j of every KV head is cache row j of
+ * sequence b: its "slot" is b * C + j.
+ */
+
+/* How rotary positions pair the first `rot` values of a row: value i with
+ * value i + rot / 2, or value 2 i with value 2 i + 1. */
+#define M4Q_ROPE_HALF 0
+#define M4Q_ROPE_INTERLEAVED 1
+
+/* Frequencies of m4q_rope_freqs, f_i = base^(-2 i / rot) radians a position:
+ *  PLAIN   as they are;
+ *  LINEAR  f_i / factor (positions interpolated);
+ *  NTK     base * factor^(rot / (rot - 2)) for base (rot > 2);
+ *  BANDS   by r_i = original f_i / (2 pi), the turns of pair i over the
+ *          original length: f_i / factor where r_i <= low, f_i where r_i >=
+ *          high, the linear mix in between;
+ *  YARN    the same, with the magnitude factor 0.1 ln(factor) + 1. */
+#define M4Q_ROPE_PLAIN 0
+#define M4Q_ROPE_LINEAR 1
+#define M4Q_ROPE_NTK 2
+#define M4Q_ROPE_BANDS 3
+#define M4Q_ROPE_YARN 4
+
+/* Fills the frequency table of m4q_rope and m4q_kv_write: freqs (HOST memory,
+ * rot / 2 entries) receives f_i as turns per position in units of 2^-64, i.e.
+ * round(f_i / (2 pi) 2^64) mod 2^64 (any table of that form may be used), and
+ * *mscale (HOST, may be NULL) the magnitude factor (1, or YARN's).  The
+ * caller copies the table to the device once.  rot even and >= 2, base > 1,
+ * factor >= 1 finite; BANDS and YARN: original > 0, 0 <= low < high, else
+ * M4Q_ERR_INVALID_ARG.  Host work only. */
+int m4q_rope_freqs(int64_t rot, double base, int scaling, double factor, double original, double low,
+                   double high, int64_t* freqs, float* mscale);
+
+/* Rotary positions: Y[h][m] = X[h][m] with each pair (a, b) of its first rot
+ * values turned by pos[m] f_i: (a, b) -> mscale (a cos - b sin, b cos + a sin);
+ * values from rot on are copied.
+ *  - X, Y: fp16 rows of D values for H heads and M tokens; row (h, m) starts
+ *    h * head_stride + m * row_stride elements in (strides multiples of 8,
+ *    else M4Q_ERR_MISALIGNED): head-major as m4q_gemm_heads writes it, or the
+ *    rows of m4q_gemm.  Y may be X (with X's strides), otherwise they do not
+ *    overlap (not checked).
+ *  - pos: int32 [M], any value (a negative position turns backwards).
+ *  - freqs: the table of m4q_rope_freqs on the device; rot a multiple of 16,
+ *    16 <= rot <= D; layout M4Q_ROPE_HALF or _INTERLEAVED.
+ *  - The angle is exact to 2^-32 of a turn at every position, sines, cosines
+ *    and products are fp32, and each value is rounded once. */
+int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t H, int64_t M, int64_t D,
+             const int32_t* pos, const int64_t* freqs, int64_t rot, int layout, float mscale, void* Y,
+             int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream);
+
+/* Writes the K and V rows of M tokens to the caches, K turned as by m4q_rope
+ * on the way (freqs NULL: as it is; pos, rot, layout and mscale are then not
+ * read), and in the same launch turns the tokens' queries (Q NULL: none).
+ *  - K, V: fp16 rows for Hkv heads and M tokens, strides as for m4q_rope.
+ *  - slots: int32 [M], the cache row b * C + j of each token.  A slot outside
+ *    [0, B * C) writes nothing (padding).  Two tokens of one call do not share
+ *    a slot (not checked: the row would mix both).  Rows that no slot names
+ *    are left as they are.
+ *  - A Q8_0 block of 32 values x: d = max|x| / 127 rounded up to fp16, codes
+ *    x / d to the nearest integer, ties to even (none exceeds 127); a block
+ *    with an infinity or a NaN decodes to NaN.  K is quantised from the fp32
+ *    results of its rotation.
+ *  - Q: fp16 rows for H heads and the same M tokens; Qout fp16 [H][M][D], may
+ *    be Q if Q has those strides.  Q needs freqs (else M4Q_ERR_INVALID_ARG).
+ *    H + 2 Hkv <= 65535. */
+int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, const void* V,
+                 int64_t v_head_stride, int64_t v_row_stride, int64_t Hkv, int64_t M, int64_t D,
+                 const int32_t* pos, const int64_t* freqs, int64_t rot, int layout, float mscale,
+                 const int32_t* slots, void* Kc, void* Vc, int kv_codec, int64_t B, int64_t C, const void* Q,
+                 int64_t q_head_stride, int64_t q_row_stride, int64_t H, void* Qout, m4q_stream_t stream);
+
+/* Reads cache rows back: Kout, Vout fp16 [Hkv][n][D], row j the cache row
+ * slots[j] (Q8_0: each value RNE(q d)); a slot outside [0, B * C) gives zeros,
+ * and slots may repeat.  Kc with Kout, or Vc with Vout, may be NULL, not both. */
+int m4q_kv_read(const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t Hkv, int64_t C, int64_t D,
+                const int32_t* slots, int64_t n, void* Kout, void* Vout, m4q_stream_t stream);
+
+/* Attention of N drafted nodes of each of B sequences over its cache (N = 1:
+ * one new token a sequence).  Node i of sequence b sees the cache rows
+ * j < past[b] and, at rows past[b] + a, its ancestors a and itself:
+ *   O[b N + i, h D + d] = sum_j softmax_j(scale Q[h, b N + i] . K[b, h / G, j]) V[b, h / G, j, d]
+ * with G = H / Hkv.  The nodes' own keys and values are in the cache already
+ * (m4q_kv_write with slots b C + past[b] + i).
+ *  - Q: fp16 [H][B N][D]; O: fp16 [B N][H D].
+ *  - past: int32 [B] on the device (read by the kernel: a captured call
+ *    follows its changes), clamped to [0, C]; a node whose row past[b] + i is
+ *    not below C has no key of its own.
+ *  - parents: int32 [B][N] on the device: -1 for a node that continues the
+ *    cached context, else an earlier node (a < i).  Any other value, or a
+ *    parent that is itself unused, marks the node as unused: its output row
+ *    is zero and no node sees it.
+ *  - Rows that a node does not see do not enter its result, whatever they
+ *    hold (infinities and NaN included).
+ *  - D is 64 or 128, H % Hkv == 0 (else M4Q_ERR_BAD_SHAPE); 1 <= N <= 256,
+ *    B, C >= 1, B * N * H <= INT32_MAX, scale finite (else
+ *    M4Q_ERR_INVALID_ARG).
+ *  - Arithmetic as m4q_attention.
+ *  - workspace: m4q_attention_tree_workspace() bytes (not cleared before or
+ *    after, 16-byte aligned) for the partial results of keys split across
+ *    CTAs; NULL or a smaller size runs without a split, slower.  Calls whose
+ *    work overlaps need a workspace each. */
+int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t H,
+                       int64_t Hkv, int64_t N, int64_t C, int64_t D, const int32_t* past,
+                       const int32_t* parents, float scale, void* O, void* workspace, size_t workspace_bytes,
+                       m4q_stream_t stream);
+
+/* Workspace bytes m4q_attention_tree uses for this shape on the current
+ * device (0 when it uses none, or for an invalid shape). */
+size_t m4q_attention_tree_workspace(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C,
+                                    int64_t D);
+
+/* Types of the residual stream of m4q_norm_residual. */
+#define M4Q_RES_F16 0
+#define M4Q_RES_F32 1
+
+/* The residual update and the norms after and before a block, one pass:
+ *   u  = h / rms(h) * w_post                   (w_post NULL: u = h)
+ *   r' = res_scale r + branch_scale gate u     (h NULL: r' = r)
+ *   y  = r' / rms(r') * w_pre                  (w_pre and Y NULL: none)
+ * for each of M rows of D values, rms(x) = sqrt(mean x^2 + eps).
+ *  - h: fp16 [M][D], the block's output; R: the residual stream [M][D] in
+ *    res_type; R_out: r' in res_type (NULL: not written; may be R); Y: fp16
+ *    [M][D] (may be h).
+ *  - w_post, w_pre: fp16 [D].  gate: fp16 [D] (gate_rows 0) or [M][D]
+ *    (gate_rows 1), or NULL.
+ *  - Sums, r' and products are fp32; r' is rounded where it is stored and y is
+ *    formed from the unrounded r'.
+ *  - D % 8 == 0 (else M4Q_ERR_BAD_SHAPE), 8 <= D <= 32768, eps >= 0, scales
+ *    finite; w_post or gate without h, w_pre without Y or Y without w_pre, and
+ *    a call that writes nothing are M4Q_ERR_INVALID_ARG.  16-byte aligned. */
+int m4q_norm_residual(const void* h, const void* R, int res_type, const void* w_post, const void* gate,
+                      int gate_rows, const void* w_pre, int64_t M, int64_t D, float res_scale,
+                      float branch_scale, float eps, void* R_out, void* Y, m4q_stream_t stream);
+
 /* Decode W [N, K] to fp16 Wf16 [N, K] (row-major): each weight (q - z) * d
  * (MLX4: q * s + b) rounded once to nearest even.  The test hook for
  * bit-exact decoding. */

@@ -17,6 +17,11 @@ Functions mirror the C ABI (same names without the ``m4q_`` prefix):
     dequant(w, codec, n, k, out=None)
     mlx4_pack(words, scales, biases, n, k, out=None)
     attention(q, k, v, kv_codec, hkv, t, q_offset=None, causal=True, scale=None, out=None)
+    rope_freqs(rot, base=10000.0, ...), rope(x, pos, freqs, ...)
+    kv_write(k, v, kc, vc, kv_codec, slots, pos=None, freqs=None, ..., q=None)
+    kv_read(kc, vc, kv_codec, slots, ...)
+    attention_tree(q, kc, vc, kv_codec, past, parents, ...)
+    norm_residual(h, r, w_pre, w_post=None, gate=None, ...)
     weight_bytes(codec, n, k), check_finite(t), check_device_status(),
     selftest_wait_timeout(limit_ns), status_string(code), version()
 Activations are read as M whole rows (their element count must be a multiple
@@ -44,6 +49,9 @@ BLOCK_BYTES = {Q4_0: 18, Q8_0: 34, Q2_0: 34, MLX4: 20}
 KV_F16 = 16   # fp16 KV cache values (the quantized KV cache uses Q8_0)
 PATH_AUTO, PATH_GEMV, PATH_TC = 0, 1, 2
 ACT_SILU, ACT_GELU = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = 0, 1, 2, 3, 4
+RES_F16, RES_F32 = 0, 1
 
 OK = 0
 ERR_INVALID_ARG = -1
@@ -83,6 +91,18 @@ SIGNATURES = {
                              ctypes.c_float, _vp, _vp, _sz, _vp]),
     "m4q_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "m4q_attention_workspace": (_sz, [_i32, _i64, _i64, _i64, _i64, _i64]),
+    "m4q_rope_freqs": (_i32, [_i64, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                              ctypes.c_double, _vp, _vp]),
+    "m4q_rope": (_i32, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i32, ctypes.c_float, _vp, _i64, _i64,
+                        _vp]),
+    "m4q_kv_write": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i32,
+                            ctypes.c_float, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "m4q_kv_read": (_i32, [_vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "m4q_attention_tree": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp,
+                                  ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "m4q_attention_tree_workspace": (_sz, [_i32, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "m4q_norm_residual": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _i64, _i64, ctypes.c_float, ctypes.c_float,
+                                 ctypes.c_float, _vp, _vp, _vp]),
     "m4q_weight_bytes": (_sz, [_i32, _i64, _i64]),
     "m4q_check_finite": (_i32, [_vp, _i64, _vp]),
     "m4q_check_device_status": (_i32, [_vp]),
@@ -410,6 +430,278 @@ def attention(q, k, v, kv_codec: int, hkv: int, t: int, q_offset: int | None = N
                              q_offset, int(bool(causal)), float(scale), out.data_ptr(), ws_ptr, ws_bytes,
                              _stream_ptr(stream)), "m4q_attention")
     return out
+
+
+def _one_device(first, *others):
+    """All tensors live on the current device (the library launches there)."""
+    import torch
+    dev = first.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError("tensors are on %s, but cuda:%d is the current device" % (dev, torch.cuda.current_device()))
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors are on %s and %s" % (dev, t.device))
+
+
+def _allocate(shape, dtype, device, stream):
+    """A new tensor that belongs to `stream` (the current one if None)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ints(t, dtype, n, what):
+    _require(t, dtype, what)
+    if t.numel() != n:
+        raise ValueError("%s holds %d values, expected %d" % (what, t.numel(), n))
+
+
+def _head_rows(x, what):
+    """fp16 rows [heads, M, D] with unit-stride values, any head and row
+    strides; returns (heads, M, D, head stride, row stride)."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.float16:
+        raise TypeError("%s must be a torch.float16 tensor" % what)
+    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
+        raise ValueError("%s must be [heads, M, D] with unit-stride rows" % what)
+    if not x.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % what)
+    h, n, d = x.shape
+    return h, n, d, x.stride(0) if h > 1 else 0, x.stride(1) if n > 1 else 0
+
+
+def _cache_shape(kc, vc, kv_codec):
+    """(B, Hkv, C, D) of a pair of caches [B, Hkv, C, row] (or [Hkv, C, row]:
+    one sequence)."""
+    import torch
+    if kv_codec not in (KV_F16, Q8_0):
+        raise M4QError(ERR_UNSUPPORTED_CODEC, "KV cache")
+    for t, what in ((kc, "kc"), (vc, "vc")):
+        if t is not None:
+            _require(t, torch.float16 if kv_codec == KV_F16 else torch.uint8, what)
+            if t.dim() not in (3, 4):
+                raise ValueError("%s must be [B, Hkv, C, row] or [Hkv, C, row]" % what)
+    some = kc if kc is not None else vc
+    if kc is not None and vc is not None and kc.shape != vc.shape:
+        raise ValueError("kc and vc must have one shape")
+    shape = tuple(some.shape) if some.dim() == 4 else (1,) + tuple(some.shape)
+    row = shape[3]
+    d = row if kv_codec == KV_F16 else row // 34 * 32
+    if d not in (64, 128) or (kv_codec != KV_F16 and row % 34):
+        raise ValueError("cache rows of %d are not fp16 or Q8_0 rows of 64 or 128 values" % row)
+    return shape[0], shape[1], shape[2], d
+
+
+def rope_freqs(rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+               original: float = 0.0, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """(freqs, mscale): the table of rotary frequencies for rope and kv_write,
+    int64 [rot / 2] on `device` (turns per position in units of 2^-64), and the
+    magnitude factor of the scaling (m4q_rope_freqs)."""
+    import torch
+    host = (ctypes.c_int64 * max(1, rot // 2))()
+    mscale = ctypes.c_float()
+    _check(load().m4q_rope_freqs(rot, base, scaling, factor, original, low, high, host, ctypes.byref(mscale)),
+           "m4q_rope_freqs")
+    return torch.tensor(list(host), dtype=torch.int64).to(device), float(mscale.value)
+
+
+def _turn_args(pos, freqs, m_):
+    import torch
+    _ints(pos, torch.int32, m_, "pos")
+    _require(freqs, torch.int64, "freqs")
+    return 2 * freqs.numel()
+
+
+def rope(x, pos, freqs, layout: int = ROPE_HALF, mscale: float = 1.0, out=None, stream=None):
+    """Rotary positions: the first 2 * len(freqs) values of each row of x fp16
+    [H, M, D] turned by pos int32 [M].  x may have any head and row strides
+    that are multiples of 8.  out (fp16 [H, M, D], rows that do not overlap)
+    may be x itself."""
+    import torch
+    h, m_, d, hs, rs = _head_rows(x, "x")
+    rot = _turn_args(pos, freqs, m_)
+    if out is None:
+        out = _allocate((h, m_, d), torch.float16, x.device, stream)
+    oh, om, od, ohs, ors = _head_rows(out, "out")
+    if (oh, om, od) != (h, m_, d):
+        raise ValueError("out must be [%d, %d, %d]" % (h, m_, d))
+    steps = sorted(((ohs, oh), (ors, om))) if oh > 1 and om > 1 else [(max(ohs, ors), max(oh, om))]
+    reach = d
+    for step, count in steps:
+        if count > 1 and step < reach:
+            raise ValueError("out's rows overlap")
+        reach = step * count
+    if out.data_ptr() == x.data_ptr() and (hs, rs) != (ohs, ors):
+        raise ValueError("out starts where x does, with other strides")
+    _one_device(x, pos, freqs, out)
+    if h == 0 or m_ == 0:
+        return out
+    _check(load().m4q_rope(x.data_ptr(), hs, rs, h, m_, d, pos.data_ptr(), freqs.data_ptr(), rot, layout, mscale,
+                           out.data_ptr(), ohs, ors, _stream_ptr(stream)), "m4q_rope")
+    return out
+
+
+def kv_write(k, v, kc, vc, kv_codec: int, slots, pos=None, freqs=None, layout: int = ROPE_HALF,
+             mscale: float = 1.0, q=None, q_out=None, stream=None):
+    """Write the rows k, v fp16 [Hkv, M, D] of M tokens to the caches kc, vc
+    [B, Hkv, C, row] at slots int32 [M] (b * C + j; outside the cache: not
+    written), k turned by pos and freqs when given.  With q fp16 [H, M, D] the
+    queries are turned in the same launch and returned as q_out [H, M, D]."""
+    import torch
+    hkv, m_, d, khs, krs = _head_rows(k, "k")
+    vh, vm, vd, vhs, vrs = _head_rows(v, "v")
+    b, ch, c, cd = _cache_shape(kc, vc, kv_codec)
+    if (vh, vm, vd) != (hkv, m_, d) or (ch, cd) != (hkv, d):
+        raise ValueError("k, v and the caches must agree on heads, rows and D")
+    _ints(slots, torch.int32, m_, "slots")
+    rot = 0
+    if freqs is not None:
+        if pos is None:
+            raise ValueError("freqs needs pos")
+        rot = _turn_args(pos, freqs, m_)
+    h, qhs, qrs = 0, 0, 0
+    if q is not None:
+        if freqs is None:
+            raise ValueError("q needs freqs")
+        h, qm, qd, qhs, qrs = _head_rows(q, "q")
+        if (qm, qd) != (m_, d):
+            raise ValueError("q must be [H, %d, %d]" % (m_, d))
+        if q_out is None:
+            q_out = _allocate((h, m_, d), torch.float16, q.device, stream)
+        _result(q_out, (h, m_, d), q.device, "q_out")
+        if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+            raise ValueError("q_out starts where q does, with other strides")
+    _one_device(k, v, kc, vc, slots, pos, freqs, q, q_out if q is not None else None)
+    if m_ == 0:
+        return q_out
+    if q is not None and h == 0:
+        raise ValueError("q has no heads")
+    _check(load().m4q_kv_write(k.data_ptr(), khs, krs, v.data_ptr(), vhs, vrs, hkv, m_, d,
+                               pos.data_ptr() if freqs is not None else None,
+                               freqs.data_ptr() if freqs is not None else None, rot, layout, mscale,
+                               slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, c,
+                               q.data_ptr() if q is not None else None, qhs, qrs, h,
+                               q_out.data_ptr() if q is not None else None, _stream_ptr(stream)), "m4q_kv_write")
+    return q_out if q is not None else None
+
+
+def kv_read(kc, vc, kv_codec: int, slots, k_out=None, v_out=None, stream=None):
+    """(k, v): the cache rows slots int32 [n] of every KV head as fp16 [Hkv, n,
+    D] (a slot outside the cache: zeros).  kc or vc may be None (and so its
+    result)."""
+    import torch
+    if kc is None and vc is None:
+        raise ValueError("kc or vc is needed")
+    b, hkv, c, d = _cache_shape(kc, vc, kv_codec)
+    n = slots.numel()
+    _ints(slots, torch.int32, n, "slots")
+    outs = []
+    for cache, out, what in ((kc, k_out, "k_out"), (vc, v_out, "v_out")):
+        if cache is None:
+            outs.append(None)
+            continue
+        if out is None:
+            out = _allocate((hkv, n, d), torch.float16, cache.device, stream)
+        outs.append(_result(out, (hkv, n, d), cache.device, what))
+    _one_device(slots, kc, vc, *outs)
+    if n:
+        p = [t.data_ptr() if t is not None else None for t in (kc, vc, outs[0], outs[1])]
+        _check(load().m4q_kv_read(p[0], p[1], kv_codec, b, hkv, c, d, slots.data_ptr(), n, p[2], p[3],
+                                  _stream_ptr(stream)), "m4q_kv_read")
+    return outs[0], outs[1]
+
+
+def attention_tree(q, kc, vc, kv_codec: int, past, parents, scale: float | None = None, out=None, workspace=None,
+                   stream=None):
+    """O fp16 [B * N, H * D]: attention of the drafted nodes q fp16 [H, B * N,
+    D] (node i of sequence b is row b * N + i) over the caches kc, vc [B, Hkv,
+    C, row].  A node sees the rows below past int32 [B], its ancestors by
+    parents int32 [B, N] (-1: the context; anything else that is not an earlier
+    used node: unused, a zero row) and itself, at rows past + node.  N = 1 is
+    one new token a sequence.  The workspace is allocated here when not given;
+    workspace=False runs without one (no key split)."""
+    import torch
+    _require(q, torch.float16, "q")
+    b, hkv, c, d = _cache_shape(kc, vc, kv_codec)
+    if kc is None or vc is None or q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [H, B * N, %d], with both caches" % d)
+    h, rows = q.shape[0], q.shape[1]
+    if rows % b:
+        raise ValueError("q holds %d rows, not a whole number for %d sequences" % (rows, b))
+    n = rows // b
+    _ints(past, torch.int32, b, "past")
+    _ints(parents, torch.int32, rows, "parents")
+    if scale is None:
+        scale = float(d) ** -0.5
+    if out is None:
+        out = _allocate((rows, h * d), torch.float16, q.device, stream)
+    _result(out, (rows, h * d), q.device)
+    _one_device(q, kc, vc, past, parents, out, workspace if workspace is not False else None)
+    if rows == 0 or h == 0:
+        return out
+    lib = load()
+    if workspace is None:
+        need = int(lib.m4q_attention_tree_workspace(kv_codec, b, h, hkv, n, c, d))
+        workspace = _allocate((need,), torch.uint8, q.device, stream) if need else None
+    elif workspace is False:
+        workspace = None
+    ws_ptr = workspace.data_ptr() if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib.m4q_attention_tree(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, h, hkv, n, c, d,
+                                  past.data_ptr(), parents.data_ptr(), float(scale), out.data_ptr(), ws_ptr, ws_bytes,
+                                  _stream_ptr(stream)), "m4q_attention_tree")
+    return out
+
+
+def norm_residual(h, r, w_pre, w_post=None, gate=None, res_scale: float = 1.0, branch_scale: float = 1.0,
+                  eps: float = 1e-6, out=None, r_out=None, stream=None):
+    """(y, r_new): r_new = res_scale * r + branch_scale * gate * rmsnorm(h) *
+    w_post, y = rmsnorm(r_new) * w_pre, over the last dimension.  r is fp16 or
+    fp32; h, y and the weights fp16; gate [D] or one value for each of h.
+    Without w_post the branch is not normalised; with h None r is only
+    normalised (r_new is r); with w_pre None there is no y.  r_out may be r,
+    out may be h."""
+    import torch
+    if not isinstance(r, torch.Tensor) or r.dtype not in (torch.float16, torch.float32):
+        raise TypeError("r must be an fp16 or fp32 CUDA tensor")
+    _require(r, r.dtype, "r")
+    if r.dim() < 1:
+        raise ValueError("r needs a last dimension")
+    d = r.shape[-1]
+    m_ = r.numel() // d if d else 0
+    if h is None and (w_post is not None or gate is not None or r_out is not None):
+        raise ValueError("w_post, gate and r_out need h")
+    if h is None and w_pre is None:
+        raise ValueError("nothing to compute")
+    for t, n, what in ((h, m_ * d, "h"), (w_post, d, "w_post"), (w_pre, d, "w_pre")):
+        if t is not None:
+            _require(t, torch.float16, what)
+            if t.numel() != n:
+                raise ValueError("%s holds %d values, expected %d" % (what, t.numel(), n))
+    gate_rows = 0
+    if gate is not None:
+        _require(gate, torch.float16, "gate")
+        if gate.numel() not in (d, m_ * d):
+            raise ValueError("gate must hold D or M * D values")
+        gate_rows = int(gate.numel() != d)
+    y = None
+    if w_pre is not None:
+        y = _allocate(r.shape, torch.float16, r.device, stream) if out is None else _result(out, r.shape, r.device)
+    if h is not None:
+        if r_out is None:
+            r_out = _allocate(r.shape, r.dtype, r.device, stream)
+        _require(r_out, r.dtype, "r_out")
+        if r_out.numel() != m_ * d:
+            raise ValueError("r_out must hold %d values" % (m_ * d))
+    _one_device(r, h, w_pre, w_post, gate, y, r_out)
+    if m_:
+        p = [t.data_ptr() if t is not None else None for t in (h, r, w_post, gate, w_pre, r_out, y)]
+        _check(load().m4q_norm_residual(p[0], p[1], RES_F32 if r.dtype == torch.float32 else RES_F16, p[2], p[3],
+                                        gate_rows, p[4], m_, d, res_scale, branch_scale, eps, p[5], p[6],
+                                        _stream_ptr(stream)), "m4q_norm_residual")
+    return y, r_out if h is not None else r
 
 
 def check_finite(t, stream=None) -> bool:

@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "../../include/m4q.h"
@@ -703,6 +704,259 @@ int m4q_attention(const void* Q, const void* K, const void* V, int kv_codec, int
     return m4q::launch_attention_tc(p, tm_q, tm_k, tm_v, s) == cudaSuccess ? M4Q_OK : M4Q_ERR_CUDA;
   }
   return m4q::launch_attention(p, kv_codec == M4Q_Q8_0, s) == cudaSuccess ? M4Q_OK : M4Q_ERR_CUDA;
+}
+
+// ------------------------------------------------------------ rotary positions, KV cache, norms
+
+}  // extern "C"
+
+namespace {
+
+bool stride_ok(int64_t s) { return s % 8 == 0; }
+
+// A batch of caches [B][Hkv][C] rows of D values.
+int check_cache(int kv_codec, int64_t B, int64_t Hkv, int64_t C, int64_t D) {
+  if (kv_codec != M4Q_KV_F16 && kv_codec != M4Q_Q8_0) return M4Q_ERR_UNSUPPORTED_CODEC;
+  if (B < 1 || Hkv < 1 || C < 1) return M4Q_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return M4Q_ERR_BAD_SHAPE;
+  if (B > INT32_MAX || Hkv > 65535 || C > INT32_MAX || B > INT32_MAX / (Hkv * C)) return M4Q_ERR_BAD_SHAPE;
+  if (kv_codec == M4Q_Q8_0 && (B * Hkv * C * (D / 32 * 34)) % 16 != 0) return M4Q_ERR_BAD_SHAPE;
+  return M4Q_OK;
+}
+
+int check_turn(const int32_t* pos, int64_t D, int64_t rot, int layout, float mscale) {
+  if (!pos || (layout != M4Q_ROPE_HALF && layout != M4Q_ROPE_INTERLEAVED) || !(mscale - mscale == 0.f))
+    return M4Q_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return M4Q_ERR_BAD_SHAPE;
+  if (rot < 16 || rot > D || rot % 16 != 0) return M4Q_ERR_BAD_SHAPE;
+  return M4Q_OK;
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The device's facts and status word, for the launches below.
+int ready(DevInfo* dev, uint32_t** status) {
+  const int rc = current_device_info(dev);
+  if (rc != M4Q_OK) return rc;
+  if (!dev->sm103) return M4Q_ERR_UNSUPPORTED_DEVICE;
+  *status = m4q::status_words();
+  return *status ? M4Q_OK : M4Q_ERR_CUDA;
+}
+
+int done(cudaError_t e) { return e == cudaSuccess ? M4Q_OK : M4Q_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+int m4q_rope_freqs(int64_t rot, double base, int scaling, double factor, double original, double low, double high,
+                   int64_t* freqs, float* mscale) {
+  if (!freqs || rot < 2 || rot % 2 != 0 || rot > 1 << 20) return M4Q_ERR_INVALID_ARG;
+  if (scaling < M4Q_ROPE_PLAIN || scaling > M4Q_ROPE_YARN) return M4Q_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor)) return M4Q_ERR_INVALID_ARG;
+  const bool bands = scaling == M4Q_ROPE_BANDS || scaling == M4Q_ROPE_YARN;
+  if (bands && !(original > 0.0 && std::isfinite(original) && low >= 0.0 && high > low && std::isfinite(high)))
+    return M4Q_ERR_INVALID_ARG;
+  if (scaling == M4Q_ROPE_NTK) {
+    if (rot == 2) return M4Q_ERR_INVALID_ARG;
+    base *= std::pow(factor, (double)rot / (double)(rot - 2));
+    if (!std::isfinite(base)) return M4Q_ERR_INVALID_ARG;
+  }
+  constexpr double kTurn = 6.283185307179586;
+  for (int64_t i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * (double)i / (double)rot);
+    if (scaling == M4Q_ROPE_LINEAR) f /= factor;
+    if (bands) {
+      const double r = original * f / kTurn;
+      const double keep = r <= low ? 0.0 : r >= high ? 1.0 : (r - low) / (high - low);
+      f = (1.0 - keep) * f / factor + keep * f;
+    }
+    freqs[i] = (int64_t)std::llround(std::ldexp(f / kTurn, 64));   // f <= 1: below 2^62
+  }
+  if (mscale) *mscale = scaling == M4Q_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  return M4Q_OK;
+}
+
+int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t H, int64_t M, int64_t D,
+             const int32_t* pos, const int64_t* freqs, int64_t rot, int layout, float mscale, void* Y,
+             int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream) {
+  if (!X || !Y || !freqs) return M4Q_ERR_INVALID_ARG;
+  if (H < 1 || M < 1 || H > 65535 || M > INT32_MAX) return M4Q_ERR_INVALID_ARG;
+  int rc = check_turn(pos, D, rot, layout, mscale);
+  if (rc != M4Q_OK) return rc;
+  if (!aligned16(X) || !aligned16(Y) || !aligned_to(pos, 4) || !aligned_to(freqs, 8) || !stride_ok(x_head_stride) ||
+      !stride_ok(x_row_stride) || !stride_ok(y_head_stride) || !stride_ok(y_row_stride))
+    return M4Q_ERR_MISALIGNED;
+  DevInfo dev;
+  m4q::KvOpsParams p{};
+  rc = ready(&dev, &p.status);
+  if (rc != M4Q_OK) return rc;
+  p.q = {static_cast<const __half*>(X), x_head_stride, x_row_stride};
+  p.qo = static_cast<__half*>(Y);
+  p.qo_hs = y_head_stride;
+  p.qo_rs = y_row_stride;
+  p.H = (int)H;
+  p.M = (int)M;
+  p.D = (int)D;
+  p.pos = pos;
+  p.freqs = freqs;
+  p.rot = (int)rot;
+  p.interleaved = layout == M4Q_ROPE_INTERLEAVED;
+  p.mscale = mscale;
+  p.nsm = dev.sms;
+  return done(m4q::launch_rope_kv(p, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, const void* V, int64_t v_head_stride,
+                 int64_t v_row_stride, int64_t Hkv, int64_t M, int64_t D, const int32_t* pos, const int64_t* freqs,
+                 int64_t rot, int layout, float mscale, const int32_t* slots, void* Kc, void* Vc, int kv_codec,
+                 int64_t B, int64_t C, const void* Q, int64_t q_head_stride, int64_t q_row_stride, int64_t H,
+                 void* Qout, m4q_stream_t stream) {
+  if (!K || !V || !slots || !Kc || !Vc || (Q && (!Qout || !freqs))) return M4Q_ERR_INVALID_ARG;
+  int rc = check_cache(kv_codec, B, Hkv, C, D);
+  if (rc != M4Q_OK) return rc;
+  if (M < 1 || M > INT32_MAX || (Q && H < 1) || (Q ? H : 0) + 2 * Hkv > 65535) return M4Q_ERR_INVALID_ARG;
+  if (freqs) {
+    rc = check_turn(pos, D, rot, layout, mscale);
+    if (rc != M4Q_OK) return rc;
+  }
+  if (!aligned16(K) || !aligned16(V) || !aligned16(Kc) || !aligned16(Vc) || !aligned_to(slots, 4) ||
+      !stride_ok(k_head_stride) || !stride_ok(k_row_stride) || !stride_ok(v_head_stride) || !stride_ok(v_row_stride) ||
+      (freqs && (!aligned_to(pos, 4) || !aligned_to(freqs, 8))) ||
+      (Q && (!aligned16(Q) || !aligned16(Qout) || !stride_ok(q_head_stride) || !stride_ok(q_row_stride))))
+    return M4Q_ERR_MISALIGNED;
+  DevInfo dev;
+  m4q::KvOpsParams p{};
+  rc = ready(&dev, &p.status);
+  if (rc != M4Q_OK) return rc;
+  if (Q) {
+    p.q = {static_cast<const __half*>(Q), q_head_stride, q_row_stride};
+    p.qo = static_cast<__half*>(Qout);
+    p.qo_hs = M * D;
+    p.qo_rs = D;
+    p.H = (int)H;
+  }
+  p.k = {static_cast<const __half*>(K), k_head_stride, k_row_stride};
+  p.v = {static_cast<const __half*>(V), v_head_stride, v_row_stride};
+  p.Hkv = (int)Hkv;
+  p.M = (int)M;
+  p.D = (int)D;
+  if (freqs) {
+    p.pos = pos;
+    p.freqs = freqs;
+    p.rot = (int)rot;
+    p.interleaved = layout == M4Q_ROPE_INTERLEAVED;
+    p.mscale = mscale;
+  }
+  p.slots = slots;
+  p.kc = static_cast<uint8_t*>(Kc);
+  p.vc = static_cast<uint8_t*>(Vc);
+  p.B = (int)B;
+  p.C = (int)C;
+  p.nsm = dev.sms;
+  return done(m4q::launch_rope_kv(p, kv_codec == M4Q_Q8_0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int m4q_kv_read(const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t Hkv, int64_t C, int64_t D,
+                const int32_t* slots, int64_t n, void* Kout, void* Vout, m4q_stream_t stream) {
+  if (!slots || (!Kc) != (!Kout) || (!Vc) != (!Vout) || (!Kc && !Vc)) return M4Q_ERR_INVALID_ARG;
+  int rc = check_cache(kv_codec, B, Hkv, C, D);
+  if (rc != M4Q_OK) return rc;
+  if (n < 1 || n > INT32_MAX) return M4Q_ERR_INVALID_ARG;
+  if ((Kc && (!aligned16(Kc) || !aligned16(Kout))) || (Vc && (!aligned16(Vc) || !aligned16(Vout))) ||
+      !aligned_to(slots, 4))
+    return M4Q_ERR_MISALIGNED;
+  DevInfo dev;
+  m4q::KvReadParams p{};
+  rc = ready(&dev, &p.status);
+  if (rc != M4Q_OK) return rc;
+  p.kc = static_cast<const uint8_t*>(Kc);
+  p.vc = static_cast<const uint8_t*>(Vc);
+  p.ko = static_cast<__half*>(Kout);
+  p.vo = static_cast<__half*>(Vout);
+  p.slots = slots;
+  p.B = (int)B;
+  p.Hkv = (int)Hkv;
+  p.C = (int)C;
+  p.D = (int)D;
+  p.n = (int)n;
+  return done(m4q::launch_kv_read(p, kv_codec == M4Q_Q8_0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t m4q_attention_tree_workspace(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C,
+                                    int64_t D) {
+  (void)kv_codec; (void)B; (void)H; (void)Hkv; (void)N; (void)C; (void)D;
+  return 0;
+}
+
+int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t H, int64_t Hkv,
+                       int64_t N, int64_t C, int64_t D, const int32_t* past, const int32_t* parents, float scale,
+                       void* O, void* workspace, size_t workspace_bytes, m4q_stream_t stream) {
+  (void)workspace_bytes;
+  if (!Q || !Kc || !Vc || !past || !parents || !O) return M4Q_ERR_INVALID_ARG;
+  int rc = check_cache(kv_codec, B, Hkv, C, D);
+  if (rc != M4Q_OK) return rc;
+  if (H < 1 || N < 1 || N > 256 || H > 65535 || B > INT32_MAX / (N * H) || !(scale - scale == 0.f))
+    return M4Q_ERR_INVALID_ARG;
+  if (H % Hkv != 0) return M4Q_ERR_BAD_SHAPE;
+  if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) || !aligned_to(past, 4) ||
+      !aligned_to(parents, 4) || (workspace && !aligned16(workspace)))
+    return M4Q_ERR_MISALIGNED;
+  DevInfo dev;
+  m4q::TreeParams p{};
+  rc = ready(&dev, &p.status);
+  if (rc != M4Q_OK) return rc;
+  p.q = static_cast<const __half*>(Q);
+  p.k = static_cast<const uint8_t*>(Kc);
+  p.v = static_cast<const uint8_t*>(Vc);
+  p.o = static_cast<__half*>(O);
+  p.past = past;
+  p.parents = parents;
+  p.B = (int)B;
+  p.H = (int)H;
+  p.Hkv = (int)Hkv;
+  p.G = (int)(H / Hkv);
+  p.N = (int)N;
+  p.C = (int)C;
+  p.D = (int)D;
+  p.row_bytes = kv_codec == M4Q_KV_F16 ? 2 * D : D / 32 * 34;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.nsm = dev.sms;
+  return done(m4q::launch_attention_tree(p, kv_codec == M4Q_Q8_0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int m4q_norm_residual(const void* h, const void* R, int res_type, const void* w_post, const void* gate, int gate_rows,
+                      const void* w_pre, int64_t M, int64_t D, float res_scale, float branch_scale, float eps,
+                      void* R_out, void* Y, m4q_stream_t stream) {
+  if (!R || (res_type != M4Q_RES_F16 && res_type != M4Q_RES_F32)) return M4Q_ERR_INVALID_ARG;
+  if (!h && (w_post || gate)) return M4Q_ERR_INVALID_ARG;
+  if ((!w_pre) != (!Y) || (!R_out && !Y)) return M4Q_ERR_INVALID_ARG;
+  if (M < 1 || M > INT32_MAX || D < 8 || D > 32768) return M4Q_ERR_INVALID_ARG;
+  if (!(res_scale - res_scale == 0.f) || !(branch_scale - branch_scale == 0.f) || !(eps >= 0.f) ||
+      !(eps - eps == 0.f))
+    return M4Q_ERR_INVALID_ARG;
+  if (D % 8 != 0) return M4Q_ERR_BAD_SHAPE;
+  if (!aligned16(h) || !aligned16(R) || !aligned16(w_post) || !aligned16(gate) || !aligned16(w_pre) ||
+      !aligned16(R_out) || !aligned16(Y))
+    return M4Q_ERR_MISALIGNED;
+  DevInfo dev;
+  m4q::NormParams p{};
+  const int rc = ready(&dev, &p.status);
+  if (rc != M4Q_OK) return rc;
+  p.h = static_cast<const __half*>(h);
+  p.r = R;
+  p.w_post = static_cast<const __half*>(w_post);
+  p.gate = static_cast<const __half*>(gate);
+  p.w_pre = static_cast<const __half*>(w_pre);
+  p.r_out = R_out;
+  p.y = static_cast<__half*>(Y);
+  p.M = M;
+  p.D = (int)D;
+  p.gate_rows = gate_rows ? 1 : 0;
+  p.res_scale = res_scale;
+  p.branch_scale = branch_scale;
+  p.eps = eps;
+  return done(m4q::launch_norm_residual(p, res_type == M4Q_RES_F32, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int m4q_check_finite(const void* x, int64_t n, m4q_stream_t stream) {

@@ -132,6 +132,75 @@ cudaError_t launch_kv_q8_stage(const void* k, const void* v, long long rows, int
 cudaError_t launch_attention_tc(const AttnParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                 const CUtensorMap& tm_v, cudaStream_t s);
 
+// kv_ops.cu: rotary positions and the KV cache's rows (fp16, or Q8_0 blocks
+// along D), D = 64 or 128.
+struct RowsView {         // fp16 rows [heads][M] of D values, strides in elements
+  const __half* p;
+  long long hs, rs;
+};
+struct KvOpsParams {
+  RowsView q, k, v;       // Q rows (H of them a token, may be 0), K and V rows (Hkv, may be 0)
+  __half* qo;             // rotated Q, strides qo_hs, qo_rs
+  long long qo_hs, qo_rs;
+  int H, Hkv, M, D;
+  const int32_t* pos;     // [M]
+  const int64_t* freqs;   // [rot / 2] turns per position in units of 2^-64, or null: no rotation
+  int rot, interleaved;
+  float mscale;
+  const int32_t* slots;   // [M] cache row b C + j of each token; outside [0, B C): not written
+  uint8_t* kc;            // caches [B][Hkv][C] rows
+  uint8_t* vc;
+  int B, C;
+  uint32_t* status;
+  int nsm;
+};
+cudaError_t launch_rope_kv(const KvOpsParams& p, bool q8, cudaStream_t s);
+struct KvReadParams {
+  const uint8_t* kc;      // caches [B][Hkv][C] rows; either may be null
+  const uint8_t* vc;
+  __half* ko;             // [Hkv][n][D]
+  __half* vo;
+  const int32_t* slots;   // [n]
+  int B, Hkv, C, D, n;
+  uint32_t* status;
+};
+cudaError_t launch_kv_read(const KvReadParams& p, bool q8, cudaStream_t s);
+
+// norm.cu: residual update and the norms on both sides of a block, one row of
+// D values (D % 8 == 0) a group of warps.
+struct NormParams {
+  const __half* h;        // block output [M][D], or null: the residual is only normalised
+  const void* r;          // residual stream [M][D], fp16 or fp32
+  const __half* w_post;   // [D] or null
+  const __half* gate;     // [D], [M][D] (gate_rows), or null
+  const __half* w_pre;    // [D] or null (then no y)
+  void* r_out;            // null: not written
+  __half* y;
+  long long M;
+  int D;
+  int gate_rows;
+  float res_scale, branch_scale, eps;
+  uint32_t* status;
+};
+cudaError_t launch_norm_residual(const NormParams& p, bool res32, cudaStream_t s);
+
+// attention_tree.cu: attention of N drafted nodes of each of B sequences over
+// its cache [Hkv][C] rows of D values.
+struct TreeParams {
+  const __half* q;        // [H][B N][D]
+  const uint8_t* k;       // [B][Hkv][C] rows
+  const uint8_t* v;
+  __half* o;              // [B N][H D]
+  const int32_t* past;    // [B]
+  const int32_t* parents; // [B][N]
+  int B, H, Hkv, G, N, C, D;
+  long long row_bytes;    // bytes of one cache row
+  float scale_log2;       // softmax scale * log2(e)
+  uint32_t* status;
+  int nsm;
+};
+cudaError_t launch_attention_tree(const TreeParams& p, bool q8, cudaStream_t s);
+
 // misc.cu
 // Status bit of a failed bounds check (the kernels' kErrBounds), and the
 // bounds-checked build switch (-DM4Q_BOUNDS=1).

@@ -883,22 +883,62 @@ int m4q_kv_read(const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t
   return done(m4q::launch_kv_read(p, kv_codec == M4Q_Q8_0, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// How a tree attention call is laid out: persistent CTAs, and the workspace of
+// the pieces that an even split of the key tiles leaves.
+struct TreePlan {
+  int rtiles, ws_rows, grid;
+  bool split;          // with a workspace
+  size_t ws_ml, ws_o, ws_bytes;
+};
+
+constexpr int kTreeLeast = 2;   // key tiles a CTA takes at least
+
+TreePlan tree_plan(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C, int64_t D, int sms) {
+  TreePlan t;
+  const int64_t rows = N * (H / Hkv);
+  t.rtiles = (int)((rows + 127) / 128);
+  t.ws_rows = (int)(rows < 128 ? rows : 128);
+  const int64_t seqs = B < m4q::kTreeSeqs ? B : m4q::kTreeSeqs;
+  const int64_t items = seqs * Hkv * t.rtiles, tiles = (C + 127) / 128;
+  const int64_t most = items * tiles;
+  t.split = tiles > kTreeLeast;
+  const int64_t want = t.split ? (most + kTreeLeast - 1) / kTreeLeast : items;
+  t.grid = (int)(want < sms ? want : sms);
+  t.ws_ml = ((m4q::kTreeSeqs + 1) * sizeof(int) + 255) / 256 * 256;
+  t.ws_o = t.ws_ml + ((size_t)2 * t.grid * t.ws_rows * sizeof(float2) + 255) / 256 * 256;
+  t.ws_bytes = t.split ? t.ws_o + (size_t)2 * t.grid * t.ws_rows * D * sizeof(float) : 0;
+  return t;
+}
+
+int check_tree(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C, int64_t D) {
+  const int rc = check_cache(kv_codec, B, Hkv, C, D);
+  if (rc != M4Q_OK) return rc;
+  if (H < 1 || N < 1 || N > 256 || H > 65535 || B > INT32_MAX / (N * H)) return M4Q_ERR_INVALID_ARG;
+  return H % Hkv == 0 ? M4Q_OK : M4Q_ERR_BAD_SHAPE;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t m4q_attention_tree_workspace(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C,
                                     int64_t D) {
-  (void)kv_codec; (void)B; (void)H; (void)Hkv; (void)N; (void)C; (void)D;
-  return 0;
+  if (check_tree(kv_codec, B, H, Hkv, N, C, D) != M4Q_OK) return 0;
+  DevInfo dev;
+  if (current_device_info(&dev) != M4Q_OK) return 0;
+  return tree_plan(B, H, Hkv, N, C, D, dev.sms).ws_bytes;
 }
 
 int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t H, int64_t Hkv,
                        int64_t N, int64_t C, int64_t D, const int32_t* past, const int32_t* parents, float scale,
                        void* O, void* workspace, size_t workspace_bytes, m4q_stream_t stream) {
-  (void)workspace_bytes;
-  if (!Q || !Kc || !Vc || !past || !parents || !O) return M4Q_ERR_INVALID_ARG;
-  int rc = check_cache(kv_codec, B, Hkv, C, D);
+  if (!Q || !Kc || !Vc || !past || !parents || !O || !(scale - scale == 0.f)) return M4Q_ERR_INVALID_ARG;
+  int rc = check_tree(kv_codec, B, H, Hkv, N, C, D);
   if (rc != M4Q_OK) return rc;
-  if (H < 1 || N < 1 || N > 256 || H > 65535 || B > INT32_MAX / (N * H) || !(scale - scale == 0.f))
-    return M4Q_ERR_INVALID_ARG;
-  if (H % Hkv != 0) return M4Q_ERR_BAD_SHAPE;
   if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) || !aligned_to(past, 4) ||
       !aligned_to(parents, 4) || (workspace && !aligned16(workspace)))
     return M4Q_ERR_MISALIGNED;
@@ -906,23 +946,44 @@ int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_cod
   m4q::TreeParams p{};
   rc = ready(&dev, &p.status);
   if (rc != M4Q_OK) return rc;
-  p.q = static_cast<const __half*>(Q);
-  p.k = static_cast<const uint8_t*>(Kc);
-  p.v = static_cast<const uint8_t*>(Vc);
-  p.o = static_cast<__half*>(O);
-  p.past = past;
-  p.parents = parents;
-  p.B = (int)B;
+  TreePlan t = tree_plan(B, H, Hkv, N, C, D, dev.sms);
+  if (!workspace || workspace_bytes < t.ws_bytes) t.split = false;
+  p.q_rows = B * N;
+  p.B_all = (int)B;
   p.H = (int)H;
   p.Hkv = (int)Hkv;
   p.G = (int)(H / Hkv);
   p.N = (int)N;
   p.C = (int)C;
   p.D = (int)D;
-  p.row_bytes = kv_codec == M4Q_KV_F16 ? 2 * D : D / 32 * 34;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.nsm = dev.sms;
-  return done(m4q::launch_attention_tree(p, kv_codec == M4Q_Q8_0, reinterpret_cast<cudaStream_t>(stream)));
+  p.rtiles = t.rtiles;
+  p.split = t.split ? 1 : 0;
+  p.least = kTreeLeast;
+  p.ws_rows = t.ws_rows;
+  if (t.split) {
+    char* ws = static_cast<char*>(workspace);
+    p.ws_pre = reinterpret_cast<int*>(ws);
+    p.ws_ml = reinterpret_cast<float2*>(ws + t.ws_ml);
+    p.ws_o = reinterpret_cast<float*>(ws + t.ws_o);
+  }
+  const bool q8 = kv_codec == M4Q_Q8_0;
+  CUtensorMap tm_k{}, tm_v{};
+  if (!q8 && (!encode_kv(&tm_k, Kc, B * Hkv, C, D) || !encode_kv(&tm_v, Vc, B * Hkv, C, D))) return M4Q_ERR_CUDA;
+  const int64_t row = q8 ? D / 32 * 34 : 2 * D;
+  for (int64_t b0 = 0; b0 < B; b0 += m4q::kTreeSeqs) {
+    p.b0 = (int)b0;
+    p.B = (int)(B - b0 < m4q::kTreeSeqs ? B - b0 : m4q::kTreeSeqs);
+    p.q = static_cast<const __half*>(Q) + b0 * N * D;
+    p.k = static_cast<const uint8_t*>(Kc) + b0 * Hkv * C * row;
+    p.v = static_cast<const uint8_t*>(Vc) + b0 * Hkv * C * row;
+    p.o = static_cast<__half*>(O) + b0 * N * H * D;
+    p.past = past + b0;
+    p.parents = parents + b0 * N;
+    rc = done(m4q::launch_attention_tree(p, q8, tm_k, tm_v, t.grid, reinterpret_cast<cudaStream_t>(stream)));
+    if (rc != M4Q_OK) return rc;
+  }
+  return M4Q_OK;
 }
 
 int m4q_norm_residual(const void* h, const void* R, int res_type, const void* w_post, const void* gate, int gate_rows,

@@ -1,99 +1,934 @@
 // attention_tree.cu -- attention of drafted trees of tokens (or of single new
-// tokens, trees of one node) over a batch of KV caches, fp16 or Q8_0.
+// tokens, trees of one node) over a batch of KV caches, fp16 or Q8_0, on the
+// tcgen05 tensor cores.
 //
-// Node i of sequence b sees the keys j < past[b] of its cache and, at rows
-// past[b] + a, its ancestors a and itself.  One warp takes one (sequence,
-// head, node) and walks its keys with an online softmax.
+//   O_i = sum_j softmax_j(scale Q_i . K_j) V_j
+// over the keys j < past[b] and, at rows past[b] + a, node i's ancestors a and
+// itself.  The lengths and the trees are read on the device, so that a captured
+// call follows them.
+//
+// Work.  The rows of one (sequence, KV head) are its N nodes times the G query
+// heads of the group, r = i G + g; an item is 128 of them, and its work is a
+// walk over tiles of 128 keys.  The tiles of all items of the call form one
+// sequence, cut into equal runs, one for each persistent CTA (one an SM): a
+// ragged batch loads every SM alike whatever its lengths.  A run that covers a
+// whole item writes its output; pieces of an item go to the workspace as
+// (O, max, sum) and a second kernel joins them.  Without a workspace the CTAs
+// take whole items.
+//
+// A decode step reads each key once for few rows, so HBM should bound it: per
+// SM 23 bytes a clock, i.e. a tile of 128 fp16 keys (K and V, D = 128, 64 KB)
+// in about 2800 clocks and one of Q8_0 in 1500.  A 128-row tcgen05 tile pair
+// (S = Q K^T and O += P V) takes about 1000, whatever part of its rows is used,
+// so that one kernel serves 1 to 128 rows an item alike.
+//
+// Warps (640 threads):
+//   0, 1    one lane each issues the MMAs of tile team 0 or 1 (tiles of even
+//           and odd number): S into the team's TMEM buffer, then, when the
+//           softmax has put P over it, O_team += P V;
+//   2, 3    copies: fp16 caches by TMA into the swizzled K (warp 2) and V
+//           (warp 3) stages; Q8_0 rows as they lie (warp 2, 1-D bulk copies)
+//           into a raw ring;
+//   4-11    softmax, one team of four warps a tile parity, one thread a row:
+//           row maximum, P = 2^(s - m) against a reference m that is raised
+//           only when the maximum passes it by 2^8 (O is then rescaled in
+//           TMEM), fp32 row sum, P rounded to fp16;
+//   12-19   per run: Q into swizzled shared memory; Q8_0: each raw tile
+//           decoded to fp16 (RNE(q d), the weights' exact decode) in the
+//           swizzled stages; in tiles that hold keys which some row does not
+//           see, non-finite V values are replaced by zero and noted.
+// The two teams have their own O and reference, so the only ties between them
+// are the shared K/V stages; they are joined when a run of an item ends.
+//
+// Masks.  Tiles below past[b] have none.  In the others each row has 128
+// visibility bits, from its ancestors' bits; scores of unseen keys are replaced
+// before the maximum and their P is zero.  P = 0 does not silence a NaN or an
+// infinity in V (0 x inf), hence the replacement above; where a row does see
+// such a value it is added to the row's result at the end.
+//
+// Every wait is bounded in time; on expiry the CTA records the failure in the
+// status word and returns.
+#include <algorithm>
+
 #include "kv_common.cuh"
 #include "launch.h"
+#include "tc_attn.cuh"
 
 namespace m4q {
 
 namespace {
 
+constexpr int kTile = 128;      // rows of an item, keys of a tile
+constexpr int kSeqs = kTreeSeqs;   // sequences of one launch
+constexpr float kRaise = 8.f;   // reference kept while the row maximum stays within 2^8 of it
+constexpr int kThreads = 640;
+
 template <int D, bool Q8>
-__device__ __forceinline__ void load_row(const uint8_t* base, long long row, int lane, float (&x)[D / 32]) {
-  if constexpr (Q8) {
-    const uint8_t* r = base + row * (D / 32 * 34);
+struct TreeCfg {
+  static constexpr int kRow = Q8 ? D / 32 * 34 : 2 * D;
+  static constexpr int kTileBytes = kTile * D * 2;     // an fp16 tile: D / 64 panels of [128][128 B]
+  static constexpr int kKS = Q8 ? 2 : D == 128 ? 3 : 6;
+  static constexpr int kVS = Q8 ? 2 : D == 128 ? 2 : 5;
+  static constexpr int kRS = Q8 ? (D == 128 ? 3 : 8) : 0;       // raw ring (K, V, K, ...)
+  static constexpr int kRaw = kTile * kRow + 32;       // a tile, its 16-byte shift, and the decode's overread
+  static constexpr int kBars = 2 * kKS + 4 * kVS + 2 * kRS + 12;
+  static constexpr int kFixed = 8 * 256 * 4            // ancestor bits [8][team][128]
+                                + 2 * 2 * kTile * 8    // (m, l) [parity][team][128]
+                                + 2 * 8 * 4 * 4        // noted V rows [parity][warp][masked tile]
+                                + (kSeqs + 4) * 4      // tile prefix
+                                + kBars * 8 + 16;
+  static constexpr int kSmem =
+      1024 + (1 + kKS + kVS) * kTileBytes + kRS * kRaw + kFixed;
+  static constexpr uint32_t kOCol = 256;               // O of team t at kOCol + t D, S/P at 128 t
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(kRaw % 16 == 0, "bulk copy alignment");
+};
+
+// A run of tiles of one item.
+struct Seg {
+  int b, hk, rt;     // sequence, KV head, row tile
+  int k0, k1, nk;    // tiles [k0, k1) of the item's nk
+  int past;          // keys that every node sees
+};
+
+// The CTA's share of the call's tiles (or of its items, without a split).
+struct Share {
+  long long at, end;
+};
+
+__device__ __forceinline__ int clamp_past(const TreeParams& p, int b) { return min(max(__ldg(p.past + b), 0), p.C); }
+
+__device__ __forceinline__ Share tree_share(const TreeParams& p, const int* pre) {
+  const long long hr = (long long)p.Hkv * p.rtiles;
+  Share s;
+  if (p.split) {
+    const long long units = hr * pre[p.B];
+    const long long g = min((long long)gridDim.x, max(1ll, units / p.least));
+    const long long c = blockIdx.x;
+    s.at = c < g ? units * c / g : units;
+    s.end = c < g ? units * (c + 1) / g : units;
+  } else {
+    const long long items = hr * p.B;
+    s.at = items * blockIdx.x / gridDim.x;
+    s.end = items * (blockIdx.x + 1) / gridDim.x;
+  }
+  return s;
+}
+
+__device__ __forceinline__ bool tree_next(const TreeParams& p, const int* pre, Share& s, Seg& g) {
+  if (s.at >= s.end) return false;
+  const long long hr = (long long)p.Hkv * p.rtiles;
+  long long item;
+  if (p.split) {
+    int lo = 0, hi = p.B - 1;   // last b with hr pre[b] <= at
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (hr * pre[mid] <= s.at) lo = mid;
+      else hi = mid - 1;
+    }
+    g.b = lo;
+    g.nk = pre[lo + 1] - pre[lo];
+    const long long rem = s.at - hr * pre[lo];
+    item = rem / g.nk;
+    g.k0 = (int)(rem % g.nk);
+    g.k1 = (int)min((long long)g.nk, g.k0 + (s.end - s.at));
+    s.at += g.k1 - g.k0;
+  } else {
+    g.b = (int)(s.at / hr);
+    item = s.at % hr;
+    g.nk = pre[g.b + 1] - pre[g.b];
+    g.k0 = 0;
+    g.k1 = g.nk;
+    ++s.at;
+  }
+  g.hk = (int)(item / p.rtiles);
+  g.rt = (int)(item % p.rtiles);
+  g.past = clamp_past(p, g.b);
+  return true;
+}
+
+// First tile of an item with keys that some row does not see (at least the
+// last one, where unused nodes are dealt with).
+__device__ __forceinline__ int first_masked(const Seg& g) { return min(g.past / kTile, g.nk - 1); }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Bits 0..31: the keys kq .. kq + 31 that a row sees; anc: the row's ancestor
+// bits, one word every 256 words.
+__device__ __forceinline__ uint32_t seen32(const uint32_t* anc, int kq, int past, int C) {
+  const int rel = kq - past;
+  uint32_t v;
+  if (rel <= -32) v = 0xFFFFFFFFu;
+  else if (rel < 0) v = ((1u << -rel) - 1u) | (anc[0] << -rel);
+  else {
+    const int w = rel >> 5, s = rel & 31;
+    const uint32_t lo = w < 8 ? anc[256 * w] : 0u, hi = w + 1 < 8 ? anc[256 * (w + 1)] : 0u;
+    v = __funnelshift_r(lo, hi, s);
+  }
+  const int n = C - kq;
+  if (n < 32) v = n <= 0 ? 0u : v & ((1u << n) - 1u);
+  return v;
+}
+
+// Non-finite halves of an fp16 pair cleared; true if there were any.
+__device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
+  const bool lo = (w & 0x7C00u) == 0x7C00u, hi = (w & 0x7C000000u) == 0x7C000000u;
+  if (lo) w &= 0xFFFF0000u;
+  if (hi) w &= 0x0000FFFFu;
+  return lo || hi;
+}
+
+// Decode a raw Q8_0 tile (rows of D / 32 blocks, the first row `sh` bytes in)
+// into the swizzled fp16 tile; thread t of 256 takes row t % 128 of blocks
+// 2 u + t / 128.  A warp reads 32 consecutive rows of one block column: rows
+// of 136 bytes as five 8-byte words from the boundary at or before the block
+// (34 words apart, so a half-warp covers every bank once), rows of 68 bytes
+// as 4-byte words (17 apart).  With `clean`, non-finite values become zero and
+// the rows that held them are returned as the warp's 32 bits.
+template <int D>
+__device__ __forceinline__ uint32_t decode_tile(uint8_t* dst, const uint8_t* raw, int t, const DecK& K, bool clean) {
+  constexpr int RB = D / 32 * 34;
+  const int row = t & 127, h = t >> 7;
+  bool any = false;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) {
-      const float d = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(r + 34 * b)));
-      x[b] = __half2float(__float2half_rn((float)(int8_t)r[34 * b + 2 + lane] * d));
+  for (int u = 0; u < D / 64; ++u) {
+    const int blk = 2 * u + h, off = row * RB + 34 * blk;
+    uint32_t w[9];
+    if constexpr (RB % 8 == 0) {
+      const uint2* src = reinterpret_cast<const uint2*>(raw + (off & ~7));
+      uint32_t a[10];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const uint2 x = src[i];
+        a[2 * i] = x.x;
+        a[2 * i + 1] = x.y;
+      }
+      // the block starts 4 (u & 1) + 2 h bytes into the first word
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        const uint32_t b0 = (u & 1) ? a[i + 1] : a[i], b1 = (u & 1) ? (i < 8 ? a[i + 2] : 0u) : a[i + 1];
+        w[i] = h ? __funnelshift_r(b0, b1, 16) : b0;
+      }
+    } else {
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(raw + (off & ~3));
+      uint32_t a[10];
+#pragma unroll
+      for (int i = 0; i < 9; ++i) a[i] = src[i];
+      a[9] = h ? src[9] : 0u;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) w[i] = h ? __funnelshift_r(a[i], a[i + 1], 16) : a[i];
+    }
+    const uint32_t d2 = dup_scale(u16_at(w, 0));
+    uint32_t v[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v[q] = q8_pair(spread_pair(w, 2 + 2 * q), d2, K);
+    if (clean) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) any |= clear_nonfinite(v[q]);
+    }
+    uint8_t* base = dst + (blk >> 1) * (kTile * 128) + row * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(base + (((4 * (blk & 1) + i) ^ (row & 7)) << 4)) =
+          make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+  return clean ? __ballot_sync(0xffffffffu, any) : 0u;
+}
+
+// The same clearing of an fp16 tile that has landed.
+template <int D>
+__device__ __forceinline__ uint32_t clean_tile(uint8_t* tile, int t) {
+  const int row = t & 127, h = t >> 7;
+  bool any = false;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    const int ch = h * (D / 16) + c;   // 16-byte chunk of the row
+    uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+    uint4 v = *at;
+    bool bad = clear_nonfinite(v.x);
+    bad |= clear_nonfinite(v.y);
+    bad |= clear_nonfinite(v.z);
+    bad |= clear_nonfinite(v.w);
+    if (bad) *at = v;
+    any |= bad;
+  }
+  return __ballot_sync(0xffffffffu, any);
+}
+
+// Value c of a V row in global memory.
+template <int D, bool Q8>
+__device__ __forceinline__ float value_at(const TreeParams& p, const Seg& g, int key, int c) {
+  if (!in_bounds(key >= 0 && key < p.C && c >= 0 && c < D, p.status, kSiteTreeKV)) return 0.f;
+  const uint8_t* row = p.v + (((long long)g.b * p.Hkv + g.hk) * p.C + key) * TreeCfg<D, Q8>::kRow;
+  if constexpr (Q8) {
+    const uint8_t* blk = row + 34 * (c >> 5);
+    const __half d = __ushort_as_half(*reinterpret_cast<const unsigned short*>(blk));
+    return __half2float(__hmul(__int2half_rn((int)(int8_t)blk[2 + (c & 31)]), d));
+  } else {
+    return __half2float(reinterpret_cast<const __half*>(row)[c]);
+  }
+}
+
+// Non-finite values of the V rows that were cleared and that this row sees,
+// added to its columns c0 .. c0 + 15.
+template <int D, bool Q8>
+__device__ __noinline__ void add_nonfinite(const TreeParams& p, const Seg& g, const uint32_t* noted,
+                                           const uint32_t* anc, int c0, float (&x)[16]) {
+  const int jm = first_masked(g);
+  for (int mt = 0; mt < 4; ++mt) {
+    const int j = jm + mt;
+    if (j < g.k0 || j >= g.k1) continue;
+    for (int q = 0; q < 4; ++q) {
+      const int kq = j * kTile + 32 * q;
+      uint32_t bits = (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32(anc, kq, g.past, p.C);
+      while (bits) {
+        const int key = kq + __ffs(bits) - 1;
+        bits &= bits - 1;
+        for (int c = 0; c < 16; ++c) {
+          const float v = value_at<D, Q8>(p, g, key, c0 + c);
+          if (!(v - v == 0.f)) x[c] += v;
+        }
+      }
+    }
+  }
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const TreeParams p) {
+  using Cfg = TreeCfg<D, Q8>;
+  constexpr int KS = Cfg::kKS, VS = Cfg::kVS, RS = Cfg::kRS > 0 ? Cfg::kRS : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* qs = smem_align<1024>(smem_raw);
+  uint8_t* kst = qs + Cfg::kTileBytes;
+  uint8_t* vst = kst + KS * Cfg::kTileBytes;
+  uint8_t* raws = vst + VS * Cfg::kTileBytes;
+  uint32_t* anc_all = reinterpret_cast<uint32_t*>(raws + Cfg::kRS * Cfg::kRaw);   // [8][256]
+  float2* ml = reinterpret_cast<float2*>(anc_all + 8 * 256);                      // [parity][team][128]
+  uint32_t* noted = reinterpret_cast<uint32_t*>(ml + 4 * kTile);                  // [parity][8 warps][4]
+  int* pre = reinterpret_cast<int*>(noted + 64);                                  // [kSeqs + 1]
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(pre + kSeqs + 4);  // [KS] K of a tile in its stage
+  uint64_t* k_empty = k_full + KS;     // [KS] S done with it
+  uint64_t* v_full = k_empty + KS;     // [VS] V of a tile in its stage
+  uint64_t* v_raw = v_full + VS;       // [VS] (fp16) V of a masked tile, not yet cleared (v_full: the others')
+  uint64_t* v_clean = v_raw + VS;      // [VS] (fp16) V of a masked tile, cleared
+  uint64_t* v_empty = v_clean + VS;    // [VS] P V done with it
+  uint64_t* r_full = v_empty + VS;     // [RS] raw tile landed
+  uint64_t* r_empty = r_full + Cfg::kRS;
+  uint64_t* s_full = r_empty + Cfg::kRS;   // [2] S of a team's tile in TMEM
+  uint64_t* p_full = s_full + 2;       // [2] its P written
+  uint64_t* pv_done = p_full + 2;      // [2] its P V done
+  uint64_t* q_full = pv_done + 2;      // Q of a run written
+  uint64_t* q_empty = q_full + 1;      // both teams' S of a run done
+  uint64_t* ml_rdy = q_empty + 1;      // softmax: (m, l) of a run written
+  uint64_t* nf_rdy = ml_rdy + 1;       // preparation of a run's tiles done (noted rows final)
+  uint64_t* o_free = nf_rdy + 1;       // softmax: O of a run read out
+  uint64_t* drain = o_free + 1;        // both issuers: every MMA complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(&k_full[i], Q8 ? 8 : 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(&v_full[i], Q8 ? 8 : 1);
+      mbar_init(&v_raw[i], 1);
+      mbar_init(&v_clean[i], 8);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < Cfg::kRS; ++i) {
+      mbar_init(&r_full[i], 1);
+      mbar_init(&r_empty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(q_empty, 2);
+    mbar_init(ml_rdy, 8);
+    mbar_init(nf_rdy, 8);
+    mbar_init(o_free, 8);
+    mbar_init(drain, 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  pdl_wait();   // every global access below comes after the previous kernel
+  if (warp == 3) {
+    // tiles of each sequence, and their prefix sums
+    int sum = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int n = 0;
+      if (b < p.B) n = (min((long long)clamp_past(p, b) + p.N, (long long)p.C) + kTile - 1) / kTile;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += up;
+      }
+      if (b < p.B) pre[b + 1] = sum + n;
+      sum += __shfl_sync(0xffffffffu, n, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{abort_flag, p.status, 2000000000ull};
+  // a wait that may last a whole run (a million keys take about 10 ms); it ends
+  // at once when another wait gives up
+  const WaitCtl run_ctl{abort_flag, p.status, 30000000000ull};
+  if (p.split && blockIdx.x == 0 && warp == 2)
+    for (int b = lane; b <= p.B; b += 32) p.ws_pre[b] = pre[b];
+  Share share = tree_share(p, pre);
+  Seg sg;
+
+  if (warp < 2) {
+    // ------------------------------------------------------------ MMA issuers
+    if (lane == 0) {
+      const int team = warp;
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, kTile);
+      constexpr uint32_t idesc_o = idesc_f16_f32(128, D) | (1u << 16);   // B (V) N-major
+      const uint64_t qd = sdesc_sw128_kmajor(smem_u32(qs));
+      const uint64_t kd = sdesc_sw128_kmajor(smem_u32(kst));
+      const uint64_t vd = sdesc_sw128_nmajor(smem_u32(vst), kTile * 128);
+      const uint32_t scol = tmem + 128 * team, ocol = tmem + Cfg::kOCol + D * team;
+      uint32_t full_ph = 0, clean_ph = 0;   // phase bits of v_full and v_clean of each stage
+      bool ok = true;
+      int g = 0, nt = 0;          // tiles of the CTA, tiles of the team
+      for (int w = 0; ok && tree_next(p, pre, share, sg); ++w) {
+        const int jm = first_masked(sg);
+        bool first = true;
+        ok = mbar_wait(q_full, w & 1, ctl);
+        for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g) {
+          const int vs = g % VS;
+          const bool wants_clean = !Q8 && j >= jm;
+          uint64_t* v_ready = wants_clean ? &v_clean[vs] : &v_full[vs];
+          const uint32_t v_ph = ((wants_clean ? clean_ph : full_ph) >> vs) & 1u;
+          (wants_clean ? clean_ph : full_ph) ^= 1u << vs;
+          if ((g & 1) != team) continue;
+          const int ks = g % KS;
+          ok = mbar_wait(&k_full[ks], (g / KS) & 1, ctl);
+          if (nt > 0) ok = ok && mbar_wait(&pv_done[team], (nt - 1) & 1, ctl);   // S and P share columns
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kds = kd + (uint64_t)(ks * (Cfg::kTileBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kTile * 128 >> 4) + 2 * (kk & 3);
+            mma_ss_f16(scol, qd + off, kds + off, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[team]);
+          tc_commit(&k_empty[ks]);
+          ok = mbar_wait(v_ready, v_ph, ctl) && mbar_wait(&p_full[team], nt & 1, ctl);
+          if (first && w > 0) ok = ok && mbar_wait(o_free, (w - 1) & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vds = vd + (uint64_t)(vs * (Cfg::kTileBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc_mma_ts_f16(ocol, scol + 8 * kk, vds + (uint32_t)(kk * (2048 >> 4)), idesc_o,
+                          (kk > 0 || !first) ? 1u : 0u);
+          tc_commit(&v_empty[vs]);
+          tc_commit(&pv_done[team]);
+          first = false;
+          ++nt;
+        }
+        if (ok) tc_commit(q_empty);   // this team's S of the run are done with Q
+      }
+      tc_commit(drain);
+      mbar_wait_drain(drain, 0, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0 && (!Q8 || warp == 2)) {
+      bool ok = true;
+      int n = 0;          // copies issued
+      const int ns = Q8 ? RS : warp == 2 ? KS : VS;
+      uint64_t* full = Q8 ? r_full : warp == 2 ? k_full : v_full;
+      uint64_t* empty = Q8 ? r_empty : warp == 2 ? k_empty : v_empty;
+      uint8_t* ring = Q8 ? raws : warp == 2 ? kst : vst;
+      const CUtensorMap* map = warp == 2 ? &tm_k : &tm_v;
+      uint32_t full_ph = 0, raw_ph = 0;     // (fp16 V) phases that have been armed, by stage
+      if (!Q8) tma_prefetch_desc(map);
+      while (ok && tree_next(p, pre, share, sg)) {
+        const int jm = first_masked(sg);
+        const long long head = (long long)sg.b * p.Hkv + sg.hk;
+        const int last = (int)min((long long)sg.past + p.N, (long long)p.C);   // rows in use
+        for (int j = sg.k0; j < sg.k1 && ok; ++j)
+#pragma unroll 1
+          for (int kv = 0; kv < (Q8 ? 2 : 1); ++kv, ++n) {
+            const int sl = n % ns;
+            if (n >= ns && !mbar_wait_idle(&empty[sl], ((n / ns) - 1) & 1, ctl, 128)) { ok = false; break; }
+            if constexpr (Q8) {
+              // whole 16-byte units around the tile's rows in use (the cache is
+              // a multiple of 16 bytes)
+              const long long a = (head * p.C + (long long)j * kTile) * Cfg::kRow;
+              const long long e = (head * p.C + min((long long)(j + 1) * kTile, (long long)last)) * Cfg::kRow;
+              const long long a16 = a & ~15ll, e16 = (e + 15) & ~15ll;
+              if (in_bounds(a16 >= 0 && e16 > a16 && e16 - a16 <= Cfg::kRaw &&
+                                e16 <= (long long)(p.B_all - p.b0) * p.Hkv * p.C * Cfg::kRow,
+                            p.status, kSiteTreeKV)) {
+                mbar_arrive_expect_tx(&full[sl], (uint32_t)(e16 - a16));
+                bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + a16, (uint32_t)(e16 - a16), &full[sl]);
+              }
+            } else {
+              // V of a masked tile goes by way of the clearing warps
+              const bool raw = warp == 3 && j >= jm;
+              uint64_t* bar = raw ? &v_raw[sl] : &full[sl];
+              (raw ? raw_ph : full_ph) ^= 1u << sl;
+              mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
+#pragma unroll
+              for (int pn = 0; pn < D / 64; ++pn)
+                if (in_bounds(j >= 0 && (long long)j * kTile < p.C && head >= 0 && head < (long long)p.B * p.Hkv, p.status,
+                              kSiteTreeKV))
+                  tma_load_3d(ring + sl * Cfg::kTileBytes + pn * (kTile * 128), map, bar, 64 * pn, j * kTile,
+                              (int)(head + (long long)p.b0 * p.Hkv));
+            }
+          }
+      }
+      // after a failure, wait for the copies in flight before the CTA can leave
+      if (!ok && Q8)
+        for (int i = n > ns ? n - ns : 0; i < n; ++i) mbar_wait_drain(&full[i % ns], (i / ns) & 1, 100000000ull);
+      if (!ok && !Q8)   // the last armed phase of a barrier (of one never armed, the phase before its first)
+        for (int i = 0; i < ns; ++i) {
+          mbar_wait_drain(&full[i], ((full_ph >> i) & 1) ^ 1, 100000000ull);
+          if (warp == 3) mbar_wait_drain(&v_raw[i], ((raw_ph >> i) & 1) ^ 1, 100000000ull);
+        }
+    }
+    __syncwarp();
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ softmax
+    const int team = (warp - 4) >> 2;
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t scol = tmem + lanes + 128 * team, ocol = tmem + lanes + Cfg::kOCol + D * team;
+    uint32_t* anc = anc_all + 128 * team + r;   // this row's bits: word i at anc[256 i]
+    const float sc = p.scale_log2;
+    const bool hi = sc >= 0.f;                  // the max of sc s is sc max s, or sc min s when sc < 0
+    const int R = p.N * p.G;
+    bool ok = true;
+    int g = 0, n0 = 0, n1 = 0;                  // tiles of the CTA, of team 0, of team 1
+    bool fresh = true;                          // the CTA's first run
+    for (int w = 0; ok && tree_next(p, pre, share, sg); ++w) {
+      const int row = sg.rt * kTile + r;
+      const bool valid = row < R;
+      const bool busy = sg.rt * kTile + 32 * (warp & 3) < R;   // the warp has a row
+      const int node = valid ? row / p.G : 0;
+      const int jm = first_masked(sg);
+      bool used = true;
+      if (busy && sg.k1 > jm) {
+        // ancestors of this row's node: a walk up its parents, each lower
+        const int* par = p.parents + (long long)sg.b * p.N;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) anc[256 * i] = 0u;
+        for (int a = node; a >= 0;) {
+          anc[256 * (a >> 5)] |= 1u << (a & 31);
+          const int up = __ldg(par + a);
+          if (up < -1 || up >= a) used = false;
+          a = used ? up : -1;
+        }
+        if (!used) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) anc[256 * i] = 0u;
+        }
+        __syncwarp();
+      }
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int j = sg.k0; j < sg.k1; ++j, ++g) {
+        if ((g & 1) != team) {
+          (team ? n0 : n1)++;
+          continue;
+        }
+        int& nt = team ? n1 : n0;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[team], nt & 1, ctl));
+        ++nt;
+        if (!ok) break;
+        if (!busy) {
+          mbar_arrive_warp(&p_full[team]);
+          continue;
+        }
+        tc_fence_after();
+        const bool masked = j >= jm;
+        uint32_t vis[4];
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) vis[q] = seen32(anc, j * kTile + 32 * q, sg.past, p.C);
+        }
+        // extreme raw score of the row's visible keys
+        float t = hi ? -INFINITY : INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[64];
+          tmem_ld64_wait(scol + 64 * half, v);
+          float x[4] = {t, t, t, t};
+          if (masked) {
+            const float none = hi ? -INFINITY : INFINITY;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              const float s = (vis[2 * half + (e >> 5)] >> (e & 31)) & 1u ? __uint_as_float(v[e]) : none;
+              x[e & 3] = hi ? fmaxf(x[e & 3], s) : fminf(x[e & 3], s);
+            }
+          } else if (hi) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e & 3] = fminf(x[e & 3], __uint_as_float(v[e]));
+          }
+          t = hi ? fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) : fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+        }
+        // the tile's maximum; -inf when the row sees no key of it
+        const float mu = (t == INFINITY || t == -INFINITY) ? -INFINITY : t * sc;
+        const float mj = mu > m + kRaise || m == -INFINITY ? fmaxf(mu, m) : m;
+        const bool raise = mj > m && !first && m != -INFINITY;
+        if (__any_sync(0xffffffffu, raise)) {
+          // the team's earlier P V are done (its next S waits for them)
+          const float a = raise ? ex2(m - mj) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16_wait(ocol + 16 * c, v);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * a);
+            tmem_st16(ocol + 16 * c, v);
+          }
+        }
+        if (mj != m) l *= m == -INFINITY ? 0.f : ex2(m - mj);
+        m = mj;
+        const float muse = mj == -INFINITY ? 0.f : mj;
+        const unsigned long long sc2 = pack2(sc, sc), nm2 = pack2(-muse, -muse);
+        unsigned long long s2 = 0ull;
+        // chunks of 16 keys, the next load in flight; P of keys 16 c .. + 15 to
+        // columns 8 c .. + 7, whose scores have been read
+        uint32_t v[2][16];
+        tmem_ld16_async(scol, v[0]);
+        tmem_wait_ld_tied(v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (c < 7) tmem_ld16_async(scol + 16 * (c + 1), v[(c + 1) & 1]);
+          const uint32_t (&x)[16] = v[c & 1];
+          uint32_t wv[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float a0, a1;
+            unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, nm2), a0, a1);
+            float p0 = ex2(a0), p1 = ex2(a1);
+            if (masked) {
+              p0 = (vis[c >> 1] >> (16 * (c & 1) + e)) & 1u ? p0 : 0.f;
+              p1 = (vis[c >> 1] >> (16 * (c & 1) + e + 1)) & 1u ? p1 : 0.f;
+            }
+            s2 = add2(s2, pack2(p0, p1));
+            const __half2 hh = __floats2half2_rn(p0, p1);
+            wv[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+          }
+          tmem_st8(scol + 8 * c, wv);
+          if (c < 7) tmem_wait_ld_tied(v[(c + 1) & 1]);
+        }
+        float sum0, sum1;
+        unpack2(s2, sum0, sum1);
+        l += sum0 + sum1;
+        first = false;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive_warp(&p_full[team]);
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- end of a run
+      const int par = w & 1;
+      ml[(par * 2 + team) * kTile + r] = make_float2(m, l);
+      mbar_arrive_warp(ml_rdy);
+      const int g0 = g - (sg.k1 - sg.k0);
+      bool got = mbar_wait(ml_rdy, par, ctl) && mbar_wait(nf_rdy, par, ctl);
+      if (n0 > 0) got = got && mbar_wait(&pv_done[0], (n0 - 1) & 1, ctl);
+      if (n1 > 0) got = got && mbar_wait(&pv_done[1], (n1 - 1) & 1, ctl);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      if (busy) {
+        // tiles of this run by team (a team without one has no O)
+        const bool has0 = sg.k1 - sg.k0 > 1 || !(g0 & 1), has1 = sg.k1 - sg.k0 > 1 || (g0 & 1);
+        const float2 a = ml[(par * 2 + 0) * kTile + r], b = ml[(par * 2 + 1) * kTile + r];
+        const float M = fmaxf(a.x, b.x);
+        const float w0 = a.x == M ? 1.f : ex2(a.x - M), w1 = b.x == M ? 1.f : ex2(b.x - M);
+        const float L = a.y * w0 + b.y * w1;
+        const bool whole = sg.k0 == 0 && sg.k1 == sg.nk;
+        // a whole item is divided by its sum (a row without a key is zero)
+        const float inv = !whole ? 1.f : L > 0.f ? 1.f / L : L;
+        const float f0 = w0 * inv, f1 = w1 * inv;
+        const uint32_t* nt = noted + par * 32;
+        const bool anynf = sg.k1 > jm && __any_sync(0xffffffffu, nt[lane] != 0u);
+        const bool head_ok = in_bounds(node < p.N, p.status, kSiteTreeO);
+        __half* orow = p.o + ((long long)sg.b * p.N + node) * p.H * D +
+                       (long long)(sg.hk * p.G + (valid ? row % p.G : 0)) * D;
+        const long long slot = (2ll * blockIdx.x + (fresh ? 0 : 1)) * p.ws_rows + r;
+        const bool store = valid && head_ok;
+        const bool ws_ok = in_bounds(whole || !valid || (p.split && r < p.ws_rows), p.status, kSiteTreeWs);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          const int col = team * (D / 2) + 16 * c;
+          uint32_t v0[16], v1[16];
+          tmem_ld16_wait(tmem + lanes + Cfg::kOCol + col, v0);
+          tmem_ld16_wait(tmem + lanes + Cfg::kOCol + D + col, v1);
+          float x[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            x[q] = (has0 ? __uint_as_float(v0[q]) * f0 : 0.f) + (has1 ? __uint_as_float(v1[q]) * f1 : 0.f);
+          if (anynf) {
+            if (valid && used) add_nonfinite<D, Q8>(p, sg, nt, anc, col, x);
+            __syncwarp();
+          }
+          if (whole) {
+            uint32_t hv[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const __half2 hh = __floats2half2_rn(x[2 * q], x[2 * q + 1]);
+              hv[q] = used ? *reinterpret_cast<const uint32_t*>(&hh) : 0u;
+            }
+            if (store) {
+              *reinterpret_cast<uint4*>(orow + col) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+              *reinterpret_cast<uint4*>(orow + col + 8) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+            }
+          } else if (store && ws_ok) {
+            float4* dst = reinterpret_cast<float4*>(p.ws_o + slot * D + col);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+          }
+        }
+        // the piece that holds the tree tells of an unused node by a sum of -1
+        if (!whole && store && ws_ok && team == 0) p.ws_ml[slot] = make_float2(M, used ? L : -1.f);
+      }
+      fresh = false;
+      tc_fence_before();
+      mbar_arrive_warp(o_free);
     }
   } else {
+    // ------------------------------------------------------------ Q, decode, clearing
+    const int t = threadIdx.x - 12 * 32;        // 0 .. 255
+    const int pw = warp - 12;
+    const int R = p.N * p.G;
+    const DecK K = make_deck();
+    bool ok = true;
+    int g = 0, rn = 0;
+    uint32_t raw_ph = 0;                        // phase bits of v_raw of each stage
+    for (int w = 0; ok && tree_next(p, pre, share, sg); ++w) {
+      const int jm = first_masked(sg);
+      ok = __all_sync(0xffffffffu, w == 0 || mbar_wait_idle(q_empty, (w - 1) & 1, run_ctl, 64));
+      if (!ok) break;
+      uint32_t* nt = noted + (w & 1) * 32 + pw * 4;
+      if (lane < 4) nt[lane] = 0u;
+      __syncwarp();
+      // Q rows, 16 bytes a thread and step, D / 8 neighbours a row
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
-      x[b] = __half2float(reinterpret_cast<const __half*>(base)[row * D + 32 * b + lane]);
+      for (int i = 0; i < kTile * (D / 8) / 256; ++i) {
+        const int idx = t + 256 * i, rr = idx / (D / 8), ch = idx % (D / 8);
+        const int row = sg.rt * kTile + rr;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < R) {
+          const int node = row / p.G, h = sg.hk * p.G + row % p.G;
+          if (in_bounds(node < p.N && h < p.H, p.status, kSiteTreeQ))
+            v = __ldg(reinterpret_cast<const uint4*>(p.q + ((long long)h * p.q_rows + (long long)sg.b * p.N + node) * D) + ch);
+        }
+        *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kTile * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(q_full);
+      const long long head = (long long)sg.b * p.Hkv + sg.hk;
+      for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g) {
+        const int ks = g % KS, vs = g % VS;
+        if constexpr (Q8) {
+          const int sh = (int)(((head * p.C + (long long)j * kTile) * Cfg::kRow) & 15);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++rn) {
+            const int rs = rn % RS;
+            uint64_t* empty = kv ? &v_empty[vs] : &k_empty[ks];
+            const int ns = kv ? VS : KS;
+            bool go = mbar_wait(&r_full[rs], (rn / RS) & 1, ctl);
+            if (g >= ns) go = go && mbar_wait(empty, ((g / ns) - 1) & 1, ctl);
+            ok = __all_sync(0xffffffffu, go);
+            if (!ok) break;
+            uint8_t* dst = kv ? vst + vs * Cfg::kTileBytes : kst + ks * Cfg::kTileBytes;
+            const bool clean = kv && j >= jm;
+            const uint32_t bits = decode_tile<D>(dst, raws + rs * Cfg::kRaw + sh, t, K, clean);
+            if (clean && lane == 0) nt[j - jm] = bits;
+            fence_proxy_async_smem();
+            mbar_arrive_warp(kv ? &v_full[vs] : &k_full[ks]);
+            mbar_arrive_warp(&r_empty[rs]);
+          }
+        } else if (j >= jm) {
+          ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
+          if (!ok) break;
+          raw_ph ^= 1u << vs;
+          const uint32_t bits = clean_tile<D>(vst + vs * Cfg::kTileBytes, t);
+          if (lane == 0) nt[j - jm] = bits;
+          fence_proxy_async_smem();
+          mbar_arrive_warp(&v_clean[vs]);
+        }
+      }
+      // The notes of run w + 1 go where those of run w - 1 were: their readers
+      // are done once O of run w - 1 is free.  Waited for here, before the
+      // arrival that lets run w end, so that o_free is at most one phase ahead.
+      if (ok && w >= 1) ok = __all_sync(0xffffffffu, mbar_wait_idle(o_free, (w - 1) & 1, ctl, 64));
+      if (ok) mbar_arrive_warp(nf_rdy);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D, bool Q8>
-__global__ void __launch_bounds__(128) tree_simple_kernel(const TreeParams p) {
-  pdl_launch_dependents();
+// Joins the pieces of the items that were cut: row r of an item whose tiles
+// went to CTAs c0 .. c1 is sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
+// W warps a row, warp k taking pieces k, k + W, ...
+template <int D, int W>
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int grid) {
+  constexpr int kRows = 8 / W;       // rows a CTA
+  constexpr int E = D / 32;          // values a lane
+  __shared__ float red_o[8][D];
+  __shared__ float red_l[8];
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long w = ((long long)blockIdx.x * 128 + threadIdx.x) >> 5;
-  if (w >= (long long)p.B * p.N * p.H) return;
-  const int h = (int)(w % p.H), i = (int)(w / p.H % p.N), b = (int)(w / p.H / p.N);
-  const int* parents = p.parents + (long long)b * p.N;
-  const int past = min(max(p.past[b], 0), p.C);
-  // the walk to the context: a node is unused if it or an ancestor is
-  bool used = true;
-  for (int a = i; a >= 0;) {
-    const int q = parents[a];
-    used = used && q >= -1 && q < a;
-    if (!used) break;
-    a = q;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = warp % W;
+  const int blocks = (p.ws_rows + kRows - 1) / kRows;
+  const long long item = blockIdx.x / blocks;
+  const int r = (int)(blockIdx.x % blocks) * kRows + warp / W;
+  const long long hr = (long long)p.Hkv * p.rtiles;
+  const int b = (int)(item / hr);
+  const int hk = (int)(item % hr / p.rtiles), row = (int)(item % p.rtiles) * kTile + r;
+  const int before = __ldg(p.ws_pre + b), nk = __ldg(p.ws_pre + b + 1) - before;
+  const long long units = hr * __ldg(p.ws_pre + p.B);
+  const long long n = min((long long)grid, max(1ll, units / p.least));
+  const long long u0 = hr * before + (item % hr) * nk, u1 = u0 + nk;
+  const int c0 = (int)(((u0 + 1) * n - 1) / units), c1 = (int)((u1 * n - 1) / units);
+  if (c0 == c1) return;              // not cut: its CTA wrote the output
+  const bool live = r < p.ws_rows && row < p.N * p.G;
+  auto slot = [&](int c) { return (2ll * c + (c > c0 || units * c0 / n == u0 ? 0 : 1)) * p.ws_rows + r; };
+  float M = -INFINITY, L = 0.f;
+  bool unused = false;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  if (live && in_bounds(c0 >= 0 && c1 < grid && c0 <= c1, p.status, kSiteTreeWs)) {
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float2 v = p.ws_ml[slot(c)];
+      M = fmaxf(M, v.x);
+      unused |= v.y == -1.f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    unused = __any_sync(0xffffffffu, unused);
+#pragma unroll 4
+    for (int c = c0 + k; c <= c1; c += W) {
+      const long long s = slot(c);
+      const float2 v = p.ws_ml[s];
+      const float f = v.x == M ? 1.f : ex2(v.x - M);
+      const float* src = p.ws_o + s * D + E * lane;
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(src);
+        x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
+      } else {
+        const float2 q = *reinterpret_cast<const float2*>(src);
+        x[0] = q.x; x[1] = q.y;
+      }
+      L += f * v.y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += f * x[e];
+    }
   }
-  const __half* qrow = p.q + ((long long)h * p.B * p.N + (long long)b * p.N + i) * D;
-  float q[D / 32], acc[D / 32], l = 0.f, top = -INFINITY;
+  if constexpr (W > 1) {
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    q[c] = __half2float(qrow[32 * c + lane]);
-    acc[c] = 0.f;
+    for (int e = 0; e < E; ++e) red_o[warp][E * lane + e] = acc[e];
+    if (lane == 0) red_l[warp] = L;
+    __syncthreads();
+    if (k != 0) return;
+    L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      L += red_l[warp + i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += red_o[warp + i][E * lane + e];
+    }
   }
-  const long long head = ((long long)b * p.Hkv + h / p.G) * p.C;
-  auto step = [&](long long j) {
-    float k[D / 32], v[D / 32];
-    load_row<D, Q8>(p.k, head + j, lane, k);
-    load_row<D, Q8>(p.v, head + j, lane, v);
-    float s = 0.f;
+  if (!live || !in_bounds(row / p.G < p.N, p.status, kSiteTreeO)) return;
+  const float inv = L > 0.f ? 1.f / L : L;
+  __half* orow = p.o + ((long long)b * p.N + row / p.G) * p.H * D + (long long)(hk * p.G + row % p.G) * D + E * lane;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) s += q[c] * k[c];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.scale_log2;
-    const float now = fmaxf(top, s), a = exp2f(top - now), e = exp2f(s - now);
-    l = l * a + e;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc[c] = acc[c] * a + e * v[c];
-    top = now;
-  };
-  if (used) {
-    for (int j = 0; j < past; ++j) step(j);
-    for (int a = i; a >= 0; a = parents[a])
-      if (past + a < p.C) step(past + a);
-  }
-  __half* o = p.o + ((long long)b * p.N + i) * p.H * D + (long long)h * D;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) o[32 * c + lane] = __float2half_rn(l > 0.f || l != l ? acc[c] / l : 0.f);
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__half2*>(orow + e) =
+        unused ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(acc[e] * inv, acc[e + 1] * inv);
 }
 
-}  // namespace
-
-cudaError_t launch_attention_tree(const TreeParams& p, bool q8, cudaStream_t s) {
-  const long long warps = (long long)p.B * p.N * p.H;
+template <typename... KArgs, typename... Args>
+cudaError_t launch_tree_kernel(void (*kern)(KArgs...), unsigned grid, unsigned block, int smem, cudaStream_t s,
+                               const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)((warps + 3) / 4), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  if (p.D == 64) return cudaLaunchKernelEx(&cfg, q8 ? tree_simple_kernel<64, true> : tree_simple_kernel<64, false>, p);
-  return cudaLaunchKernelEx(&cfg, q8 ? tree_simple_kernel<128, true> : tree_simple_kernel<128, false>, p);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D, bool Q8>
+cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
+                        cudaStream_t s) {
+  auto kern = tree_kernel<D, Q8>;
+  std::atomic<unsigned long long>& configured = attr_flag<std::integer_sequence<int, 5, D, Q8>>();
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeCfg<D, Q8>::kSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  e = launch_tree_kernel(kern, (unsigned)grid, kThreads, TreeCfg<D, Q8>::kSmem, s, tm_k, tm_v, p);
+  if (e != cudaSuccess || !p.split) return e;
+  // warps a row: enough for the pieces an item is likely to have
+  const long long items = (long long)p.B * p.Hkv * p.rtiles;
+  if (grid >= 8 * items) return launch_tree_kernel(tree_join_kernel<D, 8>, (unsigned)(items * p.ws_rows), 256, 0, s, p, grid);
+  if (grid >= 3 * items)
+    return launch_tree_kernel(tree_join_kernel<D, 4>, (unsigned)(items * ((p.ws_rows + 1) / 2)), 256, 0, s, p, grid);
+  return launch_tree_kernel(tree_join_kernel<D, 1>, (unsigned)(items * ((p.ws_rows + 7) / 8)), 256, 0, s, p, grid);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tree(const TreeParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                  int grid, cudaStream_t s) {
+  if (p.D == 64) return q8 ? launch_tree<64, true>(p, tm_k, tm_v, grid, s) : launch_tree<64, false>(p, tm_k, tm_v, grid, s);
+  return q8 ? launch_tree<128, true>(p, tm_k, tm_v, grid, s) : launch_tree<128, false>(p, tm_k, tm_v, grid, s);
 }
 
 }  // namespace m4q

@@ -185,21 +185,33 @@ struct NormParams {
 cudaError_t launch_norm_residual(const NormParams& p, bool res32, cudaStream_t s);
 
 // attention_tree.cu: attention of N drafted nodes of each of B sequences over
-// its cache [Hkv][C] rows of D values.
+// its cache [Hkv][C] rows of D values.  One launch takes up to kTreeSeqs
+// sequences (their tile counts stay in shared memory): sequences b0 .. b0 +
+// B - 1 of the B_all of a call; the pointers are those of sequence b0.
+constexpr int kTreeSeqs = 256;
 struct TreeParams {
-  const __half* q;        // [H][B N][D]
+  const __half* q;        // [H][q_rows][D], row b N + i
   const uint8_t* k;       // [B][Hkv][C] rows
   const uint8_t* v;
   __half* o;              // [B N][H D]
   const int32_t* past;    // [B]
   const int32_t* parents; // [B][N]
-  int B, H, Hkv, G, N, C, D;
-  long long row_bytes;    // bytes of one cache row
+  long long q_rows;       // B_all N
+  int B, B_all, b0, H, Hkv, G, N, C, D;
   float scale_log2;       // softmax scale * log2(e)
+  int rtiles;             // row tiles of an item's sequence and KV head: ceil(N G / 128)
+  int split;              // tiles are dealt out evenly over the CTAs, pieces of items joined
+  int least;              // tiles a CTA takes at least
+  int ws_rows;            // rows of a piece: min(N G, 128)
+  int* ws_pre;            // [kTreeSeqs + 1] tile prefix sums, written by the first kernel
+  float2* ws_ml;          // [2 grid][ws_rows] (max, sum) of a piece
+  float* ws_o;            // [2 grid][ws_rows][D] its unnormalised O
   uint32_t* status;
-  int nsm;
 };
-cudaError_t launch_attention_tree(const TreeParams& p, bool q8, cudaStream_t s);
+// tm_k, tm_v: [B_all Hkv][C][D] of fp16 caches, boxes of [1][128 keys][64 d],
+// 128-byte swizzle (not read for Q8_0).
+cudaError_t launch_attention_tree(const TreeParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                  int grid, cudaStream_t s);
 
 // misc.cu
 // Status bit of a failed bounds check (the kernels' kErrBounds), and the

@@ -432,66 +432,116 @@ def attention(q, k, v, kv_codec: int, hkv: int, t: int, q_offset: int | None = N
     return out
 
 
+# The serving calls below run once or several times a layer for a few tokens,
+# where the binding's own time counts: checks take the short way where they
+# pass and the long one (which raises) where they do not.
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _need(t, dtype, what):
+    """_require, short where it passes."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _require(t, dtype, what)
+
+
 def _one_device(first, *others):
     """All tensors live on the current device (the library launches there)."""
-    import torch
-    dev = first.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError("tensors are on %s, but cuda:%d is the current device" % (dev, torch.cuda.current_device()))
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors are on %s and %s" % (dev, t.device))
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors are on %s and %s" % (first.device, t.device))
+    if dev != _t().cuda.current_device():
+        raise ValueError("tensors are on %s, but cuda:%d is the current device"
+                         % (first.device, _t().cuda.current_device()))
 
 
-def _allocate(shape, dtype, device, stream):
-    """A new tensor that belongs to `stream` (the current one if None)."""
-    import torch
+def _allocate(shape, dtype, like, stream):
+    """A new tensor on `like`'s device that belongs to `stream` (the current
+    one if None)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _t().empty(shape, dtype=dtype, device=like.device)
+    with _t().cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _raw_stream(stream):
+    """The stream's handle (the current stream's if None, without a Stream
+    object in between)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _t()._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
 
 
 def _ints(t, dtype, n, what):
-    _require(t, dtype, what)
+    _need(t, dtype, what)
     if t.numel() != n:
         raise ValueError("%s holds %d values, expected %d" % (what, t.numel(), n))
+
+
+def _halfs(t, shape, what):
+    """A caller's contiguous fp16 result of exactly this many values."""
+    _need(t, _t().float16, what)
+    n = 1
+    for s in shape:
+        n *= s
+    if t.numel() != n:
+        raise ValueError("%s holds %d elements, expected %d for shape %s" % (what, t.numel(), n, tuple(shape)))
+    return t
 
 
 def _head_rows(x, what):
     """fp16 rows [heads, M, D] with unit-stride values, any head and row
     strides; returns (heads, M, D, head stride, row stride)."""
-    import torch
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.float16:
+    if not isinstance(x, _t().Tensor) or x.dtype is not _torch.float16:
         raise TypeError("%s must be a torch.float16 tensor" % what)
-    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
+    if x.dim() != 3:
+        raise ValueError("%s must be [heads, M, D]" % what)
+    (h, n, d), (hs, rs, one) = x.shape, x.stride()
+    if one != 1 and d > 1:
         raise ValueError("%s must be [heads, M, D] with unit-stride rows" % what)
     if not x.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % what)
-    h, n, d = x.shape
-    return h, n, d, x.stride(0) if h > 1 else 0, x.stride(1) if n > 1 else 0
+    return h, n, d, hs if h > 1 else 0, rs if n > 1 else 0
 
 
 def _cache_shape(kc, vc, kv_codec):
     """(B, Hkv, C, D) of a pair of caches [B, Hkv, C, row] (or [Hkv, C, row]:
     one sequence)."""
-    import torch
-    if kv_codec not in (KV_F16, Q8_0):
+    if kv_codec == KV_F16:
+        dtype = _t().float16
+    elif kv_codec == Q8_0:
+        dtype = _t().uint8
+    else:
         raise M4QError(ERR_UNSUPPORTED_CODEC, "KV cache")
+    shape = None
     for t, what in ((kc, "kc"), (vc, "vc")):
         if t is not None:
-            _require(t, torch.float16 if kv_codec == KV_F16 else torch.uint8, what)
-            if t.dim() not in (3, 4):
-                raise ValueError("%s must be [B, Hkv, C, row] or [Hkv, C, row]" % what)
-    some = kc if kc is not None else vc
-    if kc is not None and vc is not None and kc.shape != vc.shape:
-        raise ValueError("kc and vc must have one shape")
-    shape = tuple(some.shape) if some.dim() == 4 else (1,) + tuple(some.shape)
-    row = shape[3]
+            _need(t, dtype, what)
+            if shape is not None and t.shape != shape:
+                raise ValueError("kc and vc must have one shape")
+            shape = t.shape
+    if len(shape) == 4:
+        b, hkv, c, row = shape
+    elif len(shape) == 3:
+        b, (hkv, c, row) = 1, shape
+    else:
+        raise ValueError("a cache must be [B, Hkv, C, row] or [Hkv, C, row]")
     d = row if kv_codec == KV_F16 else row // 34 * 32
     if d not in (64, 128) or (kv_codec != KV_F16 and row % 34):
         raise ValueError("cache rows of %d are not fp16 or Q8_0 rows of 64 or 128 values" % row)
-    return shape[0], shape[1], shape[2], d
+    return b, hkv, c, d
 
 
 def rope_freqs(rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
@@ -508,9 +558,8 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, facto
 
 
 def _turn_args(pos, freqs, m_):
-    import torch
-    _ints(pos, torch.int32, m_, "pos")
-    _require(freqs, torch.int64, "freqs")
+    _ints(pos, _t().int32, m_, "pos")
+    _need(freqs, _torch.int64, "freqs")
     return 2 * freqs.numel()
 
 
@@ -519,27 +568,30 @@ def rope(x, pos, freqs, layout: int = ROPE_HALF, mscale: float = 1.0, out=None, 
     [H, M, D] turned by pos int32 [M].  x may have any head and row strides
     that are multiples of 8.  out (fp16 [H, M, D], rows that do not overlap)
     may be x itself."""
-    import torch
     h, m_, d, hs, rs = _head_rows(x, "x")
     rot = _turn_args(pos, freqs, m_)
     if out is None:
-        out = _allocate((h, m_, d), torch.float16, x.device, stream)
-    oh, om, od, ohs, ors = _head_rows(out, "out")
-    if (oh, om, od) != (h, m_, d):
-        raise ValueError("out must be [%d, %d, %d]" % (h, m_, d))
-    steps = sorted(((ohs, oh), (ors, om))) if oh > 1 and om > 1 else [(max(ohs, ors), max(oh, om))]
-    reach = d
-    for step, count in steps:
-        if count > 1 and step < reach:
-            raise ValueError("out's rows overlap")
-        reach = step * count
-    if out.data_ptr() == x.data_ptr() and (hs, rs) != (ohs, ors):
-        raise ValueError("out starts where x does, with other strides")
+        out = _allocate((h, m_, d), _torch.float16, x, stream)
+        ohs, ors = m_ * d, d
+    else:
+        oh, om, od, ohs, ors = _head_rows(out, "out")
+        if (oh, om, od) != (h, m_, d):
+            raise ValueError("out must be [%d, %d, %d]" % (h, m_, d))
+        reach = d   # rows in order of their step: each starts past the ones before
+        for step, count in sorted(((ohs, oh), (ors, om))):
+            if count > 1:
+                if step < reach:
+                    raise ValueError("out's rows overlap")
+                reach = step * count
+        if out.data_ptr() == x.data_ptr() and (hs, rs) != (ohs, ors):
+            raise ValueError("out starts where x does, with other strides")
     _one_device(x, pos, freqs, out)
     if h == 0 or m_ == 0:
         return out
-    _check(load().m4q_rope(x.data_ptr(), hs, rs, h, m_, d, pos.data_ptr(), freqs.data_ptr(), rot, layout, mscale,
-                           out.data_ptr(), ohs, ors, _stream_ptr(stream)), "m4q_rope")
+    rc = load().m4q_rope(x.data_ptr(), hs, rs, h, m_, d, pos.data_ptr(), freqs.data_ptr(), rot, layout, mscale,
+                         out.data_ptr(), ohs, ors, _raw_stream(stream))
+    if rc:
+        raise M4QError(rc, "m4q_rope")
     return out
 
 
@@ -549,68 +601,76 @@ def kv_write(k, v, kc, vc, kv_codec: int, slots, pos=None, freqs=None, layout: i
     [B, Hkv, C, row] at slots int32 [M] (b * C + j; outside the cache: not
     written), k turned by pos and freqs when given.  With q fp16 [H, M, D] the
     queries are turned in the same launch and returned as q_out [H, M, D]."""
-    import torch
     hkv, m_, d, khs, krs = _head_rows(k, "k")
     vh, vm, vd, vhs, vrs = _head_rows(v, "v")
     b, ch, c, cd = _cache_shape(kc, vc, kv_codec)
-    if (vh, vm, vd) != (hkv, m_, d) or (ch, cd) != (hkv, d):
+    if kc is None or vc is None:
+        raise ValueError("both caches are written")
+    if vh != hkv or vm != m_ or vd != d or ch != hkv or cd != d:
         raise ValueError("k, v and the caches must agree on heads, rows and D")
-    _ints(slots, torch.int32, m_, "slots")
-    rot = 0
+    _ints(slots, _torch.int32, m_, "slots")
+    rot, h, qhs, qrs, p_pos, p_freqs, p_q, p_qo = 0, 0, 0, 0, None, None, None, None
     if freqs is not None:
         if pos is None:
             raise ValueError("freqs needs pos")
         rot = _turn_args(pos, freqs, m_)
-    h, qhs, qrs = 0, 0, 0
+        p_pos, p_freqs = pos.data_ptr(), freqs.data_ptr()
     if q is not None:
         if freqs is None:
             raise ValueError("q needs freqs")
         h, qm, qd, qhs, qrs = _head_rows(q, "q")
-        if (qm, qd) != (m_, d):
+        if qm != m_ or qd != d or h == 0:
             raise ValueError("q must be [H, %d, %d]" % (m_, d))
+        p_q = q.data_ptr()
         if q_out is None:
-            q_out = _allocate((h, m_, d), torch.float16, q.device, stream)
-        _result(q_out, (h, m_, d), q.device, "q_out")
-        if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
-            raise ValueError("q_out starts where q does, with other strides")
-    _one_device(k, v, kc, vc, slots, pos, freqs, q, q_out if q is not None else None)
+            q_out = _allocate((h, m_, d), _torch.float16, q, stream)
+            p_qo = q_out.data_ptr()
+        else:
+            _halfs(q_out, (h, m_, d), "q_out")
+            p_qo = q_out.data_ptr()
+            if p_qo == p_q and not q.is_contiguous():
+                raise ValueError("q_out starts where q does, with other strides")
+        _one_device(k, v, kc, vc, slots, pos, freqs, q, q_out)
+    else:
+        q_out = None
+        _one_device(k, v, kc, vc, slots, pos if rot else None, freqs)
     if m_ == 0:
         return q_out
-    if q is not None and h == 0:
-        raise ValueError("q has no heads")
-    _check(load().m4q_kv_write(k.data_ptr(), khs, krs, v.data_ptr(), vhs, vrs, hkv, m_, d,
-                               pos.data_ptr() if freqs is not None else None,
-                               freqs.data_ptr() if freqs is not None else None, rot, layout, mscale,
-                               slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, c,
-                               q.data_ptr() if q is not None else None, qhs, qrs, h,
-                               q_out.data_ptr() if q is not None else None, _stream_ptr(stream)), "m4q_kv_write")
-    return q_out if q is not None else None
+    rc = load().m4q_kv_write(k.data_ptr(), khs, krs, v.data_ptr(), vhs, vrs, hkv, m_, d, p_pos, p_freqs, rot, layout,
+                             mscale, slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, c, p_q, qhs, qrs, h,
+                             p_qo, _raw_stream(stream))
+    if rc:
+        raise M4QError(rc, "m4q_kv_write")
+    return q_out
 
 
 def kv_read(kc, vc, kv_codec: int, slots, k_out=None, v_out=None, stream=None):
     """(k, v): the cache rows slots int32 [n] of every KV head as fp16 [Hkv, n,
     D] (a slot outside the cache: zeros).  kc or vc may be None (and so its
     result)."""
-    import torch
     if kc is None and vc is None:
         raise ValueError("kc or vc is needed")
     b, hkv, c, d = _cache_shape(kc, vc, kv_codec)
     n = slots.numel()
-    _ints(slots, torch.int32, n, "slots")
-    outs = []
-    for cache, out, what in ((kc, k_out, "k_out"), (vc, v_out, "v_out")):
-        if cache is None:
-            outs.append(None)
-            continue
-        if out is None:
-            out = _allocate((hkv, n, d), torch.float16, cache.device, stream)
-        outs.append(_result(out, (hkv, n, d), cache.device, what))
-    _one_device(slots, kc, vc, *outs)
+    _ints(slots, _torch.int32, n, "slots")
+    shape = (hkv, n, d)
+    pk = pv = pko = pvo = None
+    if kc is None:
+        k_out = None
+    else:
+        k_out = _allocate(shape, _torch.float16, kc, stream) if k_out is None else _halfs(k_out, shape, "k_out")
+        pk, pko = kc.data_ptr(), k_out.data_ptr()
+    if vc is None:
+        v_out = None
+    else:
+        v_out = _allocate(shape, _torch.float16, vc, stream) if v_out is None else _halfs(v_out, shape, "v_out")
+        pv, pvo = vc.data_ptr(), v_out.data_ptr()
+    _one_device(slots, kc, vc, k_out, v_out)
     if n:
-        p = [t.data_ptr() if t is not None else None for t in (kc, vc, outs[0], outs[1])]
-        _check(load().m4q_kv_read(p[0], p[1], kv_codec, b, hkv, c, d, slots.data_ptr(), n, p[2], p[3],
-                                  _stream_ptr(stream)), "m4q_kv_read")
-    return outs[0], outs[1]
+        rc = load().m4q_kv_read(pk, pv, kv_codec, b, hkv, c, d, slots.data_ptr(), n, pko, pvo, _raw_stream(stream))
+        if rc:
+            raise M4QError(rc, "m4q_kv_read")
+    return k_out, v_out
 
 
 def attention_tree(q, kc, vc, kv_codec: int, past, parents, scale: float | None = None, out=None, workspace=None,
@@ -622,36 +682,45 @@ def attention_tree(q, kc, vc, kv_codec: int, past, parents, scale: float | None 
     used node: unused, a zero row) and itself, at rows past + node.  N = 1 is
     one new token a sequence.  The workspace is allocated here when not given;
     workspace=False runs without one (no key split)."""
-    import torch
-    _require(q, torch.float16, "q")
+    _need(q, _t().float16, "q")
+    if kc is None or vc is None:
+        raise ValueError("both caches are read")
     b, hkv, c, d = _cache_shape(kc, vc, kv_codec)
-    if kc is None or vc is None or q.dim() != 3 or q.shape[2] != d:
-        raise ValueError("q must be [H, B * N, %d], with both caches" % d)
-    h, rows = q.shape[0], q.shape[1]
-    if rows % b:
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [H, B * N, %d]" % d)
+    h, rows, _ = q.shape
+    if b == 0 or rows % b:
         raise ValueError("q holds %d rows, not a whole number for %d sequences" % (rows, b))
     n = rows // b
-    _ints(past, torch.int32, b, "past")
-    _ints(parents, torch.int32, rows, "parents")
+    _ints(past, _torch.int32, b, "past")
+    _ints(parents, _torch.int32, rows, "parents")
     if scale is None:
-        scale = float(d) ** -0.5
+        scale = d ** -0.5
     if out is None:
-        out = _allocate((rows, h * d), torch.float16, q.device, stream)
-    _result(out, (rows, h * d), q.device)
-    _one_device(q, kc, vc, past, parents, out, workspace if workspace is not False else None)
+        out = _allocate((rows, h * d), _torch.float16, q, stream)
+    else:
+        _halfs(out, (rows, h * d), "out")
     if rows == 0 or h == 0:
         return out
     lib = load()
+    p_ws, n_ws = None, 0
     if workspace is None:
-        need = int(lib.m4q_attention_tree_workspace(kv_codec, b, h, hkv, n, c, d))
-        workspace = _allocate((need,), torch.uint8, q.device, stream) if need else None
+        n_ws = lib.m4q_attention_tree_workspace(kv_codec, b, h, hkv, n, c, d)
+        if n_ws:
+            workspace = _allocate((n_ws,), _torch.uint8, q, stream)
+            p_ws = workspace.data_ptr()
     elif workspace is False:
         workspace = None
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib.m4q_attention_tree(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, h, hkv, n, c, d,
-                                  past.data_ptr(), parents.data_ptr(), float(scale), out.data_ptr(), ws_ptr, ws_bytes,
-                                  _stream_ptr(stream)), "m4q_attention_tree")
+    else:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        p_ws, n_ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _one_device(q, kc, vc, past, parents, out, workspace)
+    rc = lib.m4q_attention_tree(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, h, hkv, n, c, d,
+                                past.data_ptr(), parents.data_ptr(), scale, out.data_ptr(), p_ws, n_ws,
+                                _raw_stream(stream))
+    if rc:
+        raise M4QError(rc, "m4q_attention_tree")
     return out
 
 
@@ -663,44 +732,47 @@ def norm_residual(h, r, w_pre, w_post=None, gate=None, res_scale: float = 1.0, b
     Without w_post the branch is not normalised; with h None r is only
     normalised (r_new is r); with w_pre None there is no y.  r_out may be r,
     out may be h."""
-    import torch
-    if not isinstance(r, torch.Tensor) or r.dtype not in (torch.float16, torch.float32):
+    f16 = _t().float16
+    res32 = getattr(r, "dtype", None) is _torch.float32
+    if not isinstance(r, _torch.Tensor) or not (res32 or r.dtype is f16):
         raise TypeError("r must be an fp16 or fp32 CUDA tensor")
-    _require(r, r.dtype, "r")
-    if r.dim() < 1:
+    _need(r, r.dtype, "r")
+    shape = r.shape
+    if len(shape) < 1:
         raise ValueError("r needs a last dimension")
-    d = r.shape[-1]
-    m_ = r.numel() // d if d else 0
+    d, total = shape[-1], r.numel()
+    m_ = total // d if d else 0
     if h is None and (w_post is not None or gate is not None or r_out is not None):
         raise ValueError("w_post, gate and r_out need h")
     if h is None and w_pre is None:
         raise ValueError("nothing to compute")
-    for t, n, what in ((h, m_ * d, "h"), (w_post, d, "w_post"), (w_pre, d, "w_pre")):
-        if t is not None:
-            _require(t, torch.float16, what)
-            if t.numel() != n:
-                raise ValueError("%s holds %d values, expected %d" % (what, t.numel(), n))
+    p_h = p_wpost = p_wpre = p_gate = p_y = p_ro = y = None
     gate_rows = 0
+    if h is not None:
+        p_h = _halfs(h, (total,), "h").data_ptr()
+    if w_post is not None:
+        p_wpost = _halfs(w_post, (d,), "w_post").data_ptr()
     if gate is not None:
-        _require(gate, torch.float16, "gate")
-        if gate.numel() not in (d, m_ * d):
-            raise ValueError("gate must hold D or M * D values")
         gate_rows = int(gate.numel() != d)
-    y = None
+        p_gate = _halfs(gate, (total if gate_rows else d,), "gate").data_ptr()
     if w_pre is not None:
-        y = _allocate(r.shape, torch.float16, r.device, stream) if out is None else _result(out, r.shape, r.device)
+        p_wpre = _halfs(w_pre, (d,), "w_pre").data_ptr()
+        y = _allocate(shape, f16, r, stream) if out is None else _halfs(out, shape, "out")
+        p_y = y.data_ptr()
     if h is not None:
         if r_out is None:
-            r_out = _allocate(r.shape, r.dtype, r.device, stream)
-        _require(r_out, r.dtype, "r_out")
-        if r_out.numel() != m_ * d:
-            raise ValueError("r_out must hold %d values" % (m_ * d))
+            r_out = _allocate(shape, r.dtype, r, stream)
+        else:
+            _need(r_out, r.dtype, "r_out")
+            if r_out.numel() != total:
+                raise ValueError("r_out must hold %d values" % total)
+        p_ro = r_out.data_ptr()
     _one_device(r, h, w_pre, w_post, gate, y, r_out)
     if m_:
-        p = [t.data_ptr() if t is not None else None for t in (h, r, w_post, gate, w_pre, r_out, y)]
-        _check(load().m4q_norm_residual(p[0], p[1], RES_F32 if r.dtype == torch.float32 else RES_F16, p[2], p[3],
-                                        gate_rows, p[4], m_, d, res_scale, branch_scale, eps, p[5], p[6],
-                                        _stream_ptr(stream)), "m4q_norm_residual")
+        rc = load().m4q_norm_residual(p_h, r.data_ptr(), RES_F32 if res32 else RES_F16, p_wpost, p_gate, gate_rows,
+                                      p_wpre, m_, d, res_scale, branch_scale, eps, p_ro, p_y, _raw_stream(stream))
+        if rc:
+            raise M4QError(rc, "m4q_norm_residual")
     return y, r_out if h is not None else r
 
 

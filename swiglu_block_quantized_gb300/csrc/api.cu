@@ -892,7 +892,7 @@ namespace {
 struct TreePlan {
   int rtiles, ws_rows, grid;
   bool split;          // with a workspace
-  size_t ws_ml, ws_o, ws_bytes;
+  size_t ws_o, ws_bytes;
 };
 
 constexpr int kTreeLeast = 2;   // key tiles a CTA takes at least
@@ -908,8 +908,7 @@ TreePlan tree_plan(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C, int6
   t.split = tiles > kTreeLeast;
   const int64_t want = t.split ? (most + kTreeLeast - 1) / kTreeLeast : items;
   t.grid = (int)(want < sms ? want : sms);
-  t.ws_ml = ((m4q::kTreeSeqs + 1) * sizeof(int) + 255) / 256 * 256;
-  t.ws_o = t.ws_ml + ((size_t)2 * t.grid * t.ws_rows * sizeof(float2) + 255) / 256 * 256;
+  t.ws_o = ((size_t)2 * t.grid * t.ws_rows * sizeof(float2) + 255) / 256 * 256;
   t.ws_bytes = t.split ? t.ws_o + (size_t)2 * t.grid * t.ws_rows * D * sizeof(float) : 0;
   return t;
 }
@@ -963,8 +962,7 @@ int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_cod
   p.ws_rows = t.ws_rows;
   if (t.split) {
     char* ws = static_cast<char*>(workspace);
-    p.ws_pre = reinterpret_cast<int*>(ws);
-    p.ws_ml = reinterpret_cast<float2*>(ws + t.ws_ml);
+    p.ws_ml = reinterpret_cast<float2*>(ws);
     p.ws_o = reinterpret_cast<float*>(ws + t.ws_o);
   }
   const bool q8 = kv_codec == M4Q_Q8_0;

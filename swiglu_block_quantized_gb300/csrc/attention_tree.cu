@@ -48,19 +48,15 @@
 //
 // Every wait is bounded in time; on expiry the CTA records the failure in the
 // status word and returns.
+// Items of at most 32 rows go to attention_few.cu.
 #include <algorithm>
 
-#include "kv_common.cuh"
-#include "launch.h"
-#include "tc_attn.cuh"
+#include "tree_common.cuh"
 
 namespace m4q {
 
 namespace {
 
-constexpr int kTile = 128;      // rows of an item, keys of a tile
-constexpr int kSeqs = kTreeSeqs;   // sequences of one launch
-constexpr float kRaise = 8.f;   // reference kept while the row maximum stays within 2^8 of it
 constexpr int kThreads = 640;
 
 template <int D, bool Q8>
@@ -75,7 +71,7 @@ struct TreeCfg {
   static constexpr int kFixed = 8 * 256 * 4            // ancestor bits [8][team][128]
                                 + 2 * 2 * kTile * 8    // (m, l) [parity][team][128]
                                 + 2 * 8 * 4 * 4        // noted V rows [parity][warp][masked tile]
-                                + (kSeqs + 4) * 4      // tile prefix
+                                + (int)sizeof(TreeSched) + 8
                                 + kBars * 8 + 16;
   static constexpr int kSmem =
       1024 + (1 + kKS + kVS) * kTileBytes + kRS * kRaw + kFixed;
@@ -84,198 +80,8 @@ struct TreeCfg {
   static_assert(kRaw % 16 == 0, "bulk copy alignment");
 };
 
-// A run of tiles of one item.
-struct Seg {
-  int b, hk, rt;     // sequence, KV head, row tile
-  int k0, k1, nk;    // tiles [k0, k1) of the item's nk
-  int past;          // keys that every node sees
-};
-
-// The CTA's share of the call's tiles (or of its items, without a split).
-struct Share {
-  long long at, end;
-};
-
-__device__ __forceinline__ int clamp_past(const TreeParams& p, int b) { return min(max(__ldg(p.past + b), 0), p.C); }
-
-__device__ __forceinline__ Share tree_share(const TreeParams& p, const int* pre) {
-  const long long hr = (long long)p.Hkv * p.rtiles;
-  Share s;
-  if (p.split) {
-    const long long units = hr * pre[p.B];
-    const long long g = min((long long)gridDim.x, max(1ll, units / p.least));
-    const long long c = blockIdx.x;
-    s.at = c < g ? units * c / g : units;
-    s.end = c < g ? units * (c + 1) / g : units;
-  } else {
-    const long long items = hr * p.B;
-    s.at = items * blockIdx.x / gridDim.x;
-    s.end = items * (blockIdx.x + 1) / gridDim.x;
-  }
-  return s;
-}
-
-__device__ __forceinline__ bool tree_next(const TreeParams& p, const int* pre, Share& s, Seg& g) {
-  if (s.at >= s.end) return false;
-  const long long hr = (long long)p.Hkv * p.rtiles;
-  long long item;
-  if (p.split) {
-    int lo = 0, hi = p.B - 1;   // last b with hr pre[b] <= at
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (hr * pre[mid] <= s.at) lo = mid;
-      else hi = mid - 1;
-    }
-    g.b = lo;
-    g.nk = pre[lo + 1] - pre[lo];
-    const long long rem = s.at - hr * pre[lo];
-    item = rem / g.nk;
-    g.k0 = (int)(rem % g.nk);
-    g.k1 = (int)min((long long)g.nk, g.k0 + (s.end - s.at));
-    s.at += g.k1 - g.k0;
-  } else {
-    g.b = (int)(s.at / hr);
-    item = s.at % hr;
-    g.nk = pre[g.b + 1] - pre[g.b];
-    g.k0 = 0;
-    g.k1 = g.nk;
-    ++s.at;
-  }
-  g.hk = (int)(item / p.rtiles);
-  g.rt = (int)(item % p.rtiles);
-  g.past = clamp_past(p, g.b);
-  return true;
-}
-
-// First tile of an item with keys that some row does not see (at least the
-// last one, where unused nodes are dealt with).
-__device__ __forceinline__ int first_masked(const Seg& g) { return min(g.past / kTile, g.nk - 1); }
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-// Bits 0..31: the keys kq .. kq + 31 that a row sees; anc: the row's ancestor
-// bits, one word every 256 words.
-__device__ __forceinline__ uint32_t seen32(const uint32_t* anc, int kq, int past, int C) {
-  const int rel = kq - past;
-  uint32_t v;
-  if (rel <= -32) v = 0xFFFFFFFFu;
-  else if (rel < 0) v = ((1u << -rel) - 1u) | (anc[0] << -rel);
-  else {
-    const int w = rel >> 5, s = rel & 31;
-    const uint32_t lo = w < 8 ? anc[256 * w] : 0u, hi = w + 1 < 8 ? anc[256 * (w + 1)] : 0u;
-    v = __funnelshift_r(lo, hi, s);
-  }
-  const int n = C - kq;
-  if (n < 32) v = n <= 0 ? 0u : v & ((1u << n) - 1u);
-  return v;
-}
-
-// Non-finite halves of an fp16 pair cleared; true if there were any.
-__device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
-  const bool lo = (w & 0x7C00u) == 0x7C00u, hi = (w & 0x7C000000u) == 0x7C000000u;
-  if (lo) w &= 0xFFFF0000u;
-  if (hi) w &= 0x0000FFFFu;
-  return lo || hi;
-}
-
-// Decode a raw Q8_0 tile (rows of D / 32 blocks, the first row `sh` bytes in)
-// into the swizzled fp16 tile; thread t of 256 takes row t % 128 of blocks
-// 2 u + t / 128.  A warp reads 32 consecutive rows of one block column: rows
-// of 136 bytes as five 8-byte words from the boundary at or before the block
-// (34 words apart, so a half-warp covers every bank once), rows of 68 bytes
-// as 4-byte words (17 apart).  With `clean`, non-finite values become zero and
-// the rows that held them are returned as the warp's 32 bits.
-template <int D>
-__device__ __forceinline__ uint32_t decode_tile(uint8_t* dst, const uint8_t* raw, int t, const DecK& K, bool clean) {
-  constexpr int RB = D / 32 * 34;
-  const int row = t & 127, h = t >> 7;
-  bool any = false;
-#pragma unroll
-  for (int u = 0; u < D / 64; ++u) {
-    const int blk = 2 * u + h, off = row * RB + 34 * blk;
-    uint32_t w[9];
-    if constexpr (RB % 8 == 0) {
-      const uint2* src = reinterpret_cast<const uint2*>(raw + (off & ~7));
-      uint32_t a[10];
-#pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        const uint2 x = src[i];
-        a[2 * i] = x.x;
-        a[2 * i + 1] = x.y;
-      }
-      // the block starts 4 (u & 1) + 2 h bytes into the first word
-#pragma unroll
-      for (int i = 0; i < 9; ++i) {
-        const uint32_t b0 = (u & 1) ? a[i + 1] : a[i], b1 = (u & 1) ? (i < 8 ? a[i + 2] : 0u) : a[i + 1];
-        w[i] = h ? __funnelshift_r(b0, b1, 16) : b0;
-      }
-    } else {
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(raw + (off & ~3));
-      uint32_t a[10];
-#pragma unroll
-      for (int i = 0; i < 9; ++i) a[i] = src[i];
-      a[9] = h ? src[9] : 0u;
-#pragma unroll
-      for (int i = 0; i < 9; ++i) w[i] = h ? __funnelshift_r(a[i], a[i + 1], 16) : a[i];
-    }
-    const uint32_t d2 = dup_scale(u16_at(w, 0));
-    uint32_t v[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) v[q] = q8_pair(spread_pair(w, 2 + 2 * q), d2, K);
-    if (clean) {
-#pragma unroll
-      for (int q = 0; q < 16; ++q) any |= clear_nonfinite(v[q]);
-    }
-    uint8_t* base = dst + (blk >> 1) * (kTile * 128) + row * 128;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(base + (((4 * (blk & 1) + i) ^ (row & 7)) << 4)) =
-          make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  }
-  return clean ? __ballot_sync(0xffffffffu, any) : 0u;
-}
-
-// The same clearing of an fp16 tile that has landed.
-template <int D>
-__device__ __forceinline__ uint32_t clean_tile(uint8_t* tile, int t) {
-  const int row = t & 127, h = t >> 7;
-  bool any = false;
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    const int ch = h * (D / 16) + c;   // 16-byte chunk of the row
-    uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-    uint4 v = *at;
-    bool bad = clear_nonfinite(v.x);
-    bad |= clear_nonfinite(v.y);
-    bad |= clear_nonfinite(v.z);
-    bad |= clear_nonfinite(v.w);
-    if (bad) *at = v;
-    any |= bad;
-  }
-  return __ballot_sync(0xffffffffu, any);
-}
-
-// Value c of a V row in global memory.
-template <int D, bool Q8>
-__device__ __forceinline__ float value_at(const TreeParams& p, const Seg& g, int key, int c) {
-  if (!in_bounds(key >= 0 && key < p.C && c >= 0 && c < D, p.status, kSiteTreeKV)) return 0.f;
-  const uint8_t* row = p.v + (((long long)g.b * p.Hkv + g.hk) * p.C + key) * TreeCfg<D, Q8>::kRow;
-  if constexpr (Q8) {
-    const uint8_t* blk = row + 34 * (c >> 5);
-    const __half d = __ushort_as_half(*reinterpret_cast<const unsigned short*>(blk));
-    return __half2float(__hmul(__int2half_rn((int)(int8_t)blk[2 + (c & 31)]), d));
-  } else {
-    return __half2float(reinterpret_cast<const __half*>(row)[c]);
-  }
-}
-
 // Non-finite values of the V rows that were cleared and that this row sees,
-// added to its columns c0 .. c0 + 15.
+// added to its columns c0 .. c0 + 15 (Q8_0: positions of a decoded row).
 template <int D, bool Q8>
 __device__ __noinline__ void add_nonfinite(const TreeParams& p, const Seg& g, const uint32_t* noted,
                                            const uint32_t* anc, int c0, float (&x)[16]) {
@@ -285,12 +91,13 @@ __device__ __noinline__ void add_nonfinite(const TreeParams& p, const Seg& g, co
     if (j < g.k0 || j >= g.k1) continue;
     for (int q = 0; q < 4; ++q) {
       const int kq = j * kTile + 32 * q;
-      uint32_t bits = (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32(anc, kq, g.past, p.C);
+      uint32_t bits = (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32<8>(anc, 256, kq, g.past, p.C);
       while (bits) {
         const int key = kq + __ffs(bits) - 1;
         bits &= bits - 1;
         for (int c = 0; c < 16; ++c) {
-          const float v = value_at<D, Q8>(p, g, key, c0 + c);
+          const int at = c0 + c;
+          const float v = value_at<D, Q8>(p, g, key, Q8 ? (at & ~31) + q8_code_at((at >> 5) & 1, at & 31) : at);
           if (!(v - v == 0.f)) x[c] += v;
         }
       }
@@ -312,8 +119,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* anc_all = reinterpret_cast<uint32_t*>(raws + Cfg::kRS * Cfg::kRaw);   // [8][256]
   float2* ml = reinterpret_cast<float2*>(anc_all + 8 * 256);                      // [parity][team][128]
   uint32_t* noted = reinterpret_cast<uint32_t*>(ml + 4 * kTile);                  // [parity][8 warps][4]
-  int* pre = reinterpret_cast<int*>(noted + 64);                                  // [kSeqs + 1]
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(pre + kSeqs + 4);  // [KS] K of a tile in its stage
+  TreeSched* sched = reinterpret_cast<TreeSched*>(noted + 64);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sched) +
+                                                  (sizeof(TreeSched) + 7) / 8 * 8);   // [KS] K of a tile in its stage
   uint64_t* k_empty = k_full + KS;     // [KS] S done with it
   uint64_t* v_full = k_empty + KS;     // [VS] V of a tile in its stage
   uint64_t* v_raw = v_full + VS;       // [VS] (fp16) V of a masked tile, not yet cleared (v_full: the others')
@@ -369,23 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_launch_dependents();
   pdl_wait();   // every global access below comes after the previous kernel
-  if (warp == 3) {
-    // tiles of each sequence, and their prefix sums
-    int sum = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int b = b0 + lane;
-      int n = 0;
-      if (b < p.B) n = (min((long long)clamp_past(p, b) + p.N, (long long)p.C) + kTile - 1) / kTile;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) n += up;
-      }
-      if (b < p.B) pre[b + 1] = sum + n;
-      sum += __shfl_sync(0xffffffffu, n, 31);
-    }
-    if (lane == 0) pre[0] = 0;
-  }
+  if (warp == 3) tree_schedule(p, sched, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -394,9 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a wait that may last a whole run (a million keys take about 10 ms); it ends
   // at once when another wait gives up
   const WaitCtl run_ctl{abort_flag, p.status, 30000000000ull};
-  if (p.split && blockIdx.x == 0 && warp == 2)
-    for (int b = lane; b <= p.B; b += 32) p.ws_pre[b] = pre[b];
-  Share share = tree_share(p, pre);
+  TreeWalk walk = tree_begin(sched);
   Seg sg;
 
   if (warp < 2) {
@@ -412,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t full_ph = 0, clean_ph = 0;   // phase bits of v_full and v_clean of each stage
       bool ok = true;
       int g = 0, nt = 0;          // tiles of the CTA, tiles of the team
-      for (int w = 0; ok && tree_next(p, pre, share, sg); ++w) {
+      for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
         const int jm = first_masked(sg);
         bool first = true;
         ok = mbar_wait(q_full, w & 1, ctl);
@@ -466,9 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t* empty = Q8 ? r_empty : warp == 2 ? k_empty : v_empty;
       uint8_t* ring = Q8 ? raws : warp == 2 ? kst : vst;
       const CUtensorMap* map = warp == 2 ? &tm_k : &tm_v;
-      uint32_t full_ph = 0, raw_ph = 0;     // (fp16 V) phases that have been armed, by stage
+      uint32_t full_ph = 0, raw_ph = 0;     // phases that have been armed, by stage
       if (!Q8) tma_prefetch_desc(map);
-      while (ok && tree_next(p, pre, share, sg)) {
+      while (ok && tree_next(p, sched, walk, sg)) {
         const int jm = first_masked(sg);
         const long long head = (long long)sg.b * p.Hkv + sg.hk;
         const int last = (int)min((long long)sg.past + p.N, (long long)p.C);   // rows in use
@@ -476,19 +266,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int kv = 0; kv < (Q8 ? 2 : 1); ++kv, ++n) {
             const int sl = n % ns;
-            if (n >= ns && !mbar_wait_idle(&empty[sl], ((n / ns) - 1) & 1, ctl, 128)) { ok = false; break; }
+            if (n >= ns && !mbar_wait_idle(&empty[sl], ((n / ns) - 1) & 1, ctl, 32)) { ok = false; break; }
             if constexpr (Q8) {
-              // whole 16-byte units around the tile's rows in use (the cache is
-              // a multiple of 16 bytes)
-              const long long a = (head * p.C + (long long)j * kTile) * Cfg::kRow;
-              const long long e = (head * p.C + min((long long)(j + 1) * kTile, (long long)last)) * Cfg::kRow;
-              const long long a16 = a & ~15ll, e16 = (e + 15) & ~15ll;
-              if (in_bounds(a16 >= 0 && e16 > a16 && e16 - a16 <= Cfg::kRaw &&
-                                e16 <= (long long)(p.B_all - p.b0) * p.Hkv * p.C * Cfg::kRow,
-                            p.status, kSiteTreeKV)) {
-                mbar_arrive_expect_tx(&full[sl], (uint32_t)(e16 - a16));
-                bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + a16, (uint32_t)(e16 - a16), &full[sl]);
-              }
+              long long at;
+              uint32_t bytes;
+              raw_span(head, p.C, Cfg::kRow, j, last, at, bytes);
+              full_ph ^= 1u << sl;
+              mbar_arrive_expect_tx(&full[sl], bytes);
+              if (in_bounds(at >= 0 && bytes > 0 && bytes <= (uint32_t)Cfg::kRaw &&
+                                at + bytes <= (long long)(p.B_all - p.b0) * p.Hkv * p.C * Cfg::kRow,
+                            p.status, kSiteTreeKV))
+                bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + at, bytes, &full[sl]);
             } else {
               // V of a masked tile goes by way of the clearing warps
               const bool raw = warp == 3 && j >= jm;
@@ -504,13 +292,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
       }
-      // after a failure, wait for the copies in flight before the CTA can leave
-      if (!ok && Q8)
-        for (int i = n > ns ? n - ns : 0; i < n; ++i) mbar_wait_drain(&full[i % ns], (i / ns) & 1, 100000000ull);
-      if (!ok && !Q8)   // the last armed phase of a barrier (of one never armed, the phase before its first)
+      if (!ok)   // copies in flight land before the CTA can leave: the last armed phase of each barrier
         for (int i = 0; i < ns; ++i) {
           mbar_wait_drain(&full[i], ((full_ph >> i) & 1) ^ 1, 100000000ull);
-          if (warp == 3) mbar_wait_drain(&v_raw[i], ((raw_ph >> i) & 1) ^ 1, 100000000ull);
+          if (!Q8 && warp == 3) mbar_wait_drain(&v_raw[i], ((raw_ph >> i) & 1) ^ 1, 100000000ull);
         }
     }
     __syncwarp();
@@ -527,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int g = 0, n0 = 0, n1 = 0;                  // tiles of the CTA, of team 0, of team 1
     bool fresh = true;                          // the CTA's first run
-    for (int w = 0; ok && tree_next(p, pre, share, sg); ++w) {
+    for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
       const int row = sg.rt * kTile + r;
       const bool valid = row < R;
       const bool busy = sg.rt * kTile + 32 * (warp & 3) < R;   // the warp has a row
@@ -535,20 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int jm = first_masked(sg);
       bool used = true;
       if (busy && sg.k1 > jm) {
-        // ancestors of this row's node: a walk up its parents, each lower
-        const int* par = p.parents + (long long)sg.b * p.N;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) anc[256 * i] = 0u;
-        for (int a = node; a >= 0;) {
-          anc[256 * (a >> 5)] |= 1u << (a & 31);
-          const int up = __ldg(par + a);
-          if (up < -1 || up >= a) used = false;
-          a = used ? up : -1;
-        }
-        if (!used) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) anc[256 * i] = 0u;
-        }
+        used = ancestors<8>(p.parents + (long long)sg.b * p.N, node, anc, 256);
         __syncwarp();
       }
       float m = -INFINITY, l = 0.f;
@@ -559,7 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         int& nt = team ? n1 : n0;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[team], nt & 1, ctl));
+        // warps without a row stay out of the others' way while they wait
+        ok = __all_sync(0xffffffffu, busy ? mbar_wait(&s_full[team], nt & 1, ctl)
+                                          : mbar_wait_idle(&s_full[team], nt & 1, ctl, 256));
         ++nt;
         if (!ok) break;
         if (!busy) {
@@ -571,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t vis[4];
         if (masked) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) vis[q] = seen32(anc, j * kTile + 32 * q, sg.past, p.C);
+          for (int q = 0; q < 4; ++q) vis[q] = seen32<8>(anc, 256, j * kTile + 32 * q, sg.past, p.C);
         }
         // extreme raw score of the row's visible keys
         float t = hi ? -INFINITY : INFINITY;
@@ -696,21 +470,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (valid && used) add_nonfinite<D, Q8>(p, sg, nt, anc, col, x);
             __syncwarp();
           }
-          if (whole) {
-            uint32_t hv[8];
+          if (store && ws_ok) {
+            if constexpr (Q8) {
+              // decoded order: positions 4 i, 4 i + 2 and 4 i + 1, 4 i + 3 hold neighbours
+              const int odd = (col >> 5) & 1, pos0 = col & 31, at = col & ~31;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const __half2 hh = __floats2half2_rn(x[2 * q], x[2 * q + 1]);
-              hv[q] = used ? *reinterpret_cast<const uint32_t*>(&hh) : 0u;
-            }
-            if (store) {
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float a0 = used ? x[4 * i + k] : 0.f, a1 = used ? x[4 * i + k + 2] : 0.f;
+                  const int i4 = pos0 + 4 * i;
+                  const int e = odd ? i4 + 2 * k : i4 > 0 ? i4 - 2 + 2 * k : 30 * k;
+                  if (whole) *reinterpret_cast<__half2*>(orow + at + e) = __floats2half2_rn(a0, a1);
+                  else *reinterpret_cast<float2*>(p.ws_o + slot * D + at + e) = make_float2(a0, a1);
+                }
+            } else if (whole) {
+              uint32_t hv[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const __half2 hh = __floats2half2_rn(x[2 * q], x[2 * q + 1]);
+                hv[q] = used ? *reinterpret_cast<const uint32_t*>(&hh) : 0u;
+              }
               *reinterpret_cast<uint4*>(orow + col) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
               *reinterpret_cast<uint4*>(orow + col + 8) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-            }
-          } else if (store && ws_ok) {
-            float4* dst = reinterpret_cast<float4*>(p.ws_o + slot * D + col);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.ws_o + slot * D + col);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+              for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            }
           }
         }
         // the piece that holds the tree tells of an unused node by a sum of -1
@@ -729,25 +516,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int g = 0, rn = 0;
     uint32_t raw_ph = 0;                        // phase bits of v_raw of each stage
-    for (int w = 0; ok && tree_next(p, pre, share, sg); ++w) {
+    for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
       const int jm = first_masked(sg);
       ok = __all_sync(0xffffffffu, w == 0 || mbar_wait_idle(q_empty, (w - 1) & 1, run_ctl, 64));
       if (!ok) break;
       uint32_t* nt = noted + (w & 1) * 32 + pw * 4;
       if (lane < 4) nt[lane] = 0u;
       __syncwarp();
-      // Q rows, 16 bytes a thread and step, D / 8 neighbours a row
+      // Q rows (Q8_0: in the decoded blocks' order), a block of 32 values a step
 #pragma unroll
-      for (int i = 0; i < kTile * (D / 8) / 256; ++i) {
-        const int idx = t + 256 * i, rr = idx / (D / 8), ch = idx % (D / 8);
+      for (int i = 0; i < kTile * (D / 32) / 256; ++i) {
+        const int u = t + 256 * i, rr = u / (D / 32), blk = u % (D / 32);
         const int row = sg.rt * kTile + rr;
-        uint4 v = make_uint4(0, 0, 0, 0);
+        uint4 q[4] = {}, o[4];
         if (row < R) {
           const int node = row / p.G, h = sg.hk * p.G + row % p.G;
-          if (in_bounds(node < p.N && h < p.H, p.status, kSiteTreeQ))
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + ((long long)h * p.q_rows + (long long)sg.b * p.N + node) * D) + ch);
+          if (in_bounds(node < p.N && h < p.H, p.status, kSiteTreeQ)) {
+            const uint4* src =
+                reinterpret_cast<const uint4*>(p.q + ((long long)h * p.q_rows + (long long)sg.b * p.N + node) * D) + 4 * blk;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) q[c] = __ldg(src + c);
+          }
         }
-        *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kTile * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+        if constexpr (Q8) order_block(q, blk & 1, o);
+        else
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[c] = q[c];
+        uint8_t* base = qs + (blk >> 1) * (kTile * 128) + rr * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(base + (((4 * (blk & 1) + c) ^ (rr & 7)) << 4)) = o[c];
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full);
@@ -767,8 +564,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             uint8_t* dst = kv ? vst + vs * Cfg::kTileBytes : kst + ks * Cfg::kTileBytes;
             const bool clean = kv && j >= jm;
-            const uint32_t bits = decode_tile<D>(dst, raws + rs * Cfg::kRaw + sh, t, K, clean);
-            if (clean && lane == 0) nt[j - jm] = bits;
+            const int row = t & 127;
+            bool any = false;
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
+              const int blk = 2 * u + (t >> 7);
+              uint32_t v[16];
+              decode_block<D>(raws + rs * Cfg::kRaw + sh, row, blk, K, v);
+              if (clean) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) any |= clear_nonfinite(v[q]);
+              }
+              uint8_t* base = dst + (blk >> 1) * (kTile * 128) + row * 128;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(base + (((4 * (blk & 1) + i) ^ (row & 7)) << 4)) =
+                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+            if (clean) {
+              const uint32_t bits = __ballot_sync(0xffffffffu, any);
+              if (lane == 0) nt[j - jm] = bits;
+            }
             fence_proxy_async_smem();
             mbar_arrive_warp(kv ? &v_full[vs] : &k_full[ks]);
             mbar_arrive_warp(&r_empty[rs]);
@@ -777,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
           if (!ok) break;
           raw_ph ^= 1u << vs;
-          const uint32_t bits = clean_tile<D>(vst + vs * Cfg::kTileBytes, t);
+          const uint32_t bits = clean_tile<D, 256>(vst + vs * Cfg::kTileBytes, t);
           if (lane == 0) nt[j - jm] = bits;
           fence_proxy_async_smem();
           mbar_arrive_warp(&v_clean[vs]);
@@ -817,14 +633,35 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
   const long long hr = (long long)p.Hkv * p.rtiles;
   const int b = (int)(item / hr);
   const int hk = (int)(item % hr / p.rtiles), row = (int)(item % p.rtiles) * kTile + r;
-  const int before = __ldg(p.ws_pre + b), nk = __ldg(p.ws_pre + b + 1) - before;
-  const long long units = hr * __ldg(p.ws_pre + p.B);
-  const long long n = min((long long)grid, max(1ll, units / p.least));
-  const long long u0 = hr * before + (item % hr) * nk, u1 = u0 + nk;
-  const int c0 = (int)(((u0 + 1) * n - 1) / units), c1 = (int)((u1 * n - 1) / units);
+  // the sequences' tiles, as tree_schedule counts them
+  __shared__ int sums[3];
+  if (warp == 0) {
+    int before = 0, all = 0, mine = 0;
+    for (int i = lane; i < p.B; i += 32) {
+      const int past = min(max(__ldg(p.past + i), 0), p.C);
+      const int n = (int)((min((long long)past + p.N, (long long)p.C) + kTile - 1) / kTile);
+      all += n;
+      before += i < b ? n : 0;
+      mine += i == b ? n : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    }
+    if (lane == 0) sums[0] = before, sums[1] = mine, sums[2] = all;
+  }
+  __syncthreads();
+  const int nk = sums[1];
+  const long long units = hr * sums[2];
+  const Deal dl = deal(units, tree_shares(p, units, grid));
+  const long long u0 = hr * sums[0] + (item % hr) * nk, u1 = u0 + nk;
+  const int c0 = deal_owner(dl, u0), c1 = deal_owner(dl, u1 - 1);
   if (c0 == c1) return;              // not cut: its CTA wrote the output
   const bool live = r < p.ws_rows && row < p.N * p.G;
-  auto slot = [&](int c) { return (2ll * c + (c > c0 || units * c0 / n == u0 ? 0 : 1)) * p.ws_rows + r; };
+  const bool at_start = deal_start(dl, c0) == u0;   // the first piece is its CTA's first run
+  auto slot = [&](int c) { return (2ll * c + (c > c0 || at_start ? 0 : 1)) * p.ws_rows + r; };
   float M = -INFINITY, L = 0.f;
   bool unused = false;
   float acc[E];
@@ -883,38 +720,20 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
         unused ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_tree_kernel(void (*kern)(KArgs...), unsigned grid, unsigned block, int smem, cudaStream_t s,
-                               const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(block, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D, bool Q8>
 cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
                         cudaStream_t s) {
   auto kern = tree_kernel<D, Q8>;
-  std::atomic<unsigned long long>& configured = attr_flag<std::integer_sequence<int, 5, D, Q8>>();
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = allow_smem<std::integer_sequence<int, 5, D, Q8>>(kern, TreeCfg<D, Q8>::kSmem);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeCfg<D, Q8>::kSmem);
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(bit);
-  }
   e = launch_tree_kernel(kern, (unsigned)grid, kThreads, TreeCfg<D, Q8>::kSmem, s, tm_k, tm_v, p);
-  if (e != cudaSuccess || !p.split) return e;
+  return e != cudaSuccess || !p.split ? e : launch_tree_join<D>(p, grid, s);
+}
+
+}  // namespace
+
+template <int D>
+cudaError_t launch_tree_join(const TreeParams& p, int grid, cudaStream_t s) {
   // warps a row: enough for the pieces an item is likely to have
   const long long items = (long long)p.B * p.Hkv * p.rtiles;
   if (grid >= 8 * items) return launch_tree_kernel(tree_join_kernel<D, 8>, (unsigned)(items * p.ws_rows), 256, 0, s, p, grid);
@@ -922,11 +741,14 @@ cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tm_k, const CUte
     return launch_tree_kernel(tree_join_kernel<D, 4>, (unsigned)(items * ((p.ws_rows + 1) / 2)), 256, 0, s, p, grid);
   return launch_tree_kernel(tree_join_kernel<D, 1>, (unsigned)(items * ((p.ws_rows + 7) / 8)), 256, 0, s, p, grid);
 }
-
-}  // namespace
+template cudaError_t launch_tree_join<64>(const TreeParams&, int, cudaStream_t);
+template cudaError_t launch_tree_join<128>(const TreeParams&, int, cudaStream_t);
 
 cudaError_t launch_attention_tree(const TreeParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                   int grid, cudaStream_t s) {
+  // few rows: keys on the MMA's 128 lanes instead of rows (a 128-row tile costs
+  // the same for any of them)
+  if (p.N * p.G <= 32) return launch_attention_few(p, q8, tm_k, tm_v, grid, s);
   if (p.D == 64) return q8 ? launch_tree<64, true>(p, tm_k, tm_v, grid, s) : launch_tree<64, false>(p, tm_k, tm_v, grid, s);
   return q8 ? launch_tree<128, true>(p, tm_k, tm_v, grid, s) : launch_tree<128, false>(p, tm_k, tm_v, grid, s);
 }

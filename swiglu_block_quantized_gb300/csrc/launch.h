@@ -203,7 +203,6 @@ struct TreeParams {
   int split;              // tiles are dealt out evenly over the CTAs, pieces of items joined
   int least;              // tiles a CTA takes at least
   int ws_rows;            // rows of a piece: min(N G, 128)
-  int* ws_pre;            // [kTreeSeqs + 1] tile prefix sums, written by the first kernel
   float2* ws_ml;          // [2 grid][ws_rows] (max, sum) of a piece
   float* ws_o;            // [2 grid][ws_rows][D] its unnormalised O
   uint32_t* status;
@@ -212,6 +211,9 @@ struct TreeParams {
 // 128-byte swizzle (not read for Q8_0).
 cudaError_t launch_attention_tree(const TreeParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                   int grid, cudaStream_t s);
+// attention_few.cu: the same for N G <= 32 rows an item
+cudaError_t launch_attention_few(const TreeParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                 int grid, cudaStream_t s);
 
 // misc.cu
 // Status bit of a failed bounds check (the kernels' kErrBounds), and the

@@ -1,0 +1,359 @@
+// tree_common.cuh -- what the kernels of m4q_attention_tree share: the even
+// split of all key tiles over the CTAs, the masks of the tiles that hold a
+// tree, the decode of raw Q8_0 tiles and the handling of non-finite values.
+#pragma once
+
+#include "kv_common.cuh"
+#include "launch.h"
+#include "tc_attn.cuh"
+
+namespace m4q {
+
+constexpr int kTile = 128;         // keys of a tile
+constexpr float kRaise = 8.f;      // reference kept while a row's maximum stays within 2^8 of it
+
+// ------------------------------------------------------------------ schedule
+//
+// The tiles of all items (row tile, KV head, sequence: rt fastest) form one
+// sequence of units, unit u of CTA c's run [start(c), start(c + 1)), start(c) =
+// c base + min(c, rem).  Without a split the items are dealt out the same way.
+
+// A run of tiles of one item.
+struct Seg {
+  int b, hk, rt;     // sequence, KV head, row tile
+  int k0, k1, nk;    // tiles [k0, k1) of the item's nk
+  int past;          // keys that every node sees
+};
+
+// In shared memory: keys and tiles of each sequence, and where the CTA starts.
+struct TreeSched {
+  int past[kTreeSeqs];
+  int pre[kTreeSeqs + 1];
+  int b, item, k;
+  int left;          // units (or, without a split, items) of this CTA
+};
+
+// n units over g shares: share c starts at c base + min(c, rem).
+struct Deal {
+  long long base, rem;
+};
+__device__ __forceinline__ Deal deal(long long n, int g) {
+  Deal d;
+  if (n < (1ll << 31)) {   // 32-bit division: the 64-bit one costs a few hundred clocks
+    d.base = (unsigned)n / (unsigned)g;
+    d.rem = (unsigned)n % (unsigned)g;
+  } else {
+    d.base = n / g;
+    d.rem = n % g;
+  }
+  return d;
+}
+__device__ __forceinline__ long long deal_start(const Deal& d, long long c) { return c * d.base + min(c, d.rem); }
+// The share that holds unit u.
+__device__ __forceinline__ int deal_owner(const Deal& d, long long u) {
+  const long long cut = d.rem * (d.base + 1);
+  if (u < cut) return (int)(cut < (1ll << 31) ? (unsigned)u / (unsigned)(d.base + 1) : u / (d.base + 1));
+  const long long v = u - cut;
+  return (int)(d.rem + (v < (1ll << 31) && d.base < (1ll << 31) ? (unsigned)v / (unsigned)d.base : v / d.base));
+}
+// CTAs that take part: as many as have `least` tiles each.
+__device__ __forceinline__ int tree_shares(const TreeParams& p, long long units, int grid) {
+  return (int)min((long long)grid, max(1ll, units < (1ll << 31) ? (long long)((unsigned)units / (unsigned)p.least)
+                                                                : units / p.least));
+}
+
+// Filled by one warp; the CTA synchronises before anyone reads.
+__device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s, int lane) {
+  int sum = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int n = 0;
+    if (b < p.B) {
+      const int past = min(max(__ldg(p.past + b), 0), p.C);
+      s->past[b] = past;
+      n = (int)((min((long long)past + p.N, (long long)p.C) + kTile - 1) / kTile);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += up;
+    }
+    if (b < p.B) s->pre[b + 1] = sum + n;
+    sum += __shfl_sync(0xffffffffu, n, 31);
+  }
+  if (lane == 0) s->pre[0] = 0;
+  __syncwarp();
+  const int hr = p.Hkv * p.rtiles;
+  const long long n = p.split ? (long long)hr * sum : (long long)hr * p.B;
+  const int shares = p.split ? tree_shares(p, n, (int)gridDim.x) : (int)gridDim.x;
+  const Deal d = deal(n, shares);
+  const long long c = blockIdx.x;
+  const long long at = c < shares ? deal_start(d, c) : n, end = c < shares ? deal_start(d, c + 1) : n;
+  if (p.split) {
+    // last sequence whose units start at or before `at`
+    int b = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const bool le = b0 + lane < p.B && (long long)hr * s->pre[b0 + lane] <= at;
+      b += __popc(__ballot_sync(0xffffffffu, le));
+    }
+    b = max(b - 1, 0);
+    const int nk = s->pre[b + 1] - s->pre[b];
+    const long long rem = at - (long long)hr * s->pre[b];
+    if (lane == 0) {
+      s->b = b;
+      s->item = rem < (1ll << 31) ? (int)((unsigned)rem / (unsigned)nk) : (int)(rem / nk);
+      s->k = (int)(rem - (long long)s->item * nk);
+      s->left = (int)(end - at);
+    }
+  } else if (lane == 0) {
+    s->b = (int)(at / hr);
+    s->item = (int)(at % hr);
+    s->k = 0;
+    s->left = (int)(end - at);
+  }
+}
+
+// Each role walks the CTA's runs with a copy of this.
+struct TreeWalk {
+  int b, item, k, left;
+};
+__device__ __forceinline__ TreeWalk tree_begin(const TreeSched* s) { return TreeWalk{s->b, s->item, s->k, s->left}; }
+__device__ __forceinline__ bool tree_next(const TreeParams& p, const TreeSched* s, TreeWalk& w, Seg& g) {
+  if (w.left <= 0) return false;
+  g.b = w.b;
+  g.nk = s->pre[w.b + 1] - s->pre[w.b];
+  g.past = s->past[w.b];
+  g.hk = p.rtiles == 1 ? w.item : w.item / p.rtiles;
+  g.rt = w.item - g.hk * p.rtiles;
+  g.k0 = w.k;
+  g.k1 = p.split ? min(g.nk, w.k + w.left) : g.nk;
+  w.left -= p.split ? g.k1 - g.k0 : 1;
+  w.k = 0;   // a run that stops inside an item is the CTA's last
+  if (++w.item == p.Hkv * p.rtiles) {
+    w.item = 0;
+    ++w.b;
+  }
+  return true;
+}
+
+// First tile of an item with keys that some row does not see (at least the
+// last one, where unused nodes are dealt with).  At most 3 tiles follow it.
+__device__ __forceinline__ int first_masked(const Seg& g) { return min(g.past / kTile, g.nk - 1); }
+
+// ------------------------------------------------------------------ masks
+
+// Ancestor bits of a node, itself included, 32 nodes a word, word i stored at
+// anc[i stride]; 0 and false when it, or one of its ancestors, is not used.
+template <int WORDS>
+__device__ __forceinline__ bool ancestors(const int* parents, int node, uint32_t* anc, int stride) {
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) anc[i * stride] = 0u;
+  bool used = true;
+  for (int a = node; a >= 0;) {   // each parent is lower than its child: at most N steps
+    anc[(a >> 5) * stride] |= 1u << (a & 31);
+    const int up = __ldg(parents + a);
+    if (up < -1 || up >= a) used = false;
+    a = used ? up : -1;
+  }
+  if (!used) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) anc[i * stride] = 0u;
+  }
+  return used;
+}
+
+// Bits 0..31: which of the keys kq .. kq + 31 a row sees, from its ancestor bits.
+template <int WORDS>
+__device__ __forceinline__ uint32_t seen32(const uint32_t* anc, int stride, int kq, int past, int C) {
+  const int rel = kq - past;
+  uint32_t v;
+  if (rel <= -32) v = 0xFFFFFFFFu;
+  else if (rel < 0) v = ((1u << -rel) - 1u) | (anc[0] << -rel);
+  else {
+    const int w = rel >> 5, s = rel & 31;
+    const uint32_t lo = w < WORDS ? anc[w * stride] : 0u, hi = w + 1 < WORDS ? anc[(w + 1) * stride] : 0u;
+    v = __funnelshift_r(lo, hi, s);
+  }
+  const int n = C - kq;
+  if (n < 32) v = n <= 0 ? 0u : v & ((1u << n) - 1u);
+  return v;
+}
+
+// ------------------------------------------------------------------ non-finite values
+
+// Non-finite halves of an fp16 pair cleared; true if there were any.
+__device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
+  const bool lo = (w & 0x7C00u) == 0x7C00u, hi = (w & 0x7C000000u) == 0x7C000000u;
+  if (lo) w &= 0xFFFF0000u;
+  if (hi) w &= 0x0000FFFFu;
+  return lo || hi;
+}
+
+// Clear an fp16 tile that has landed (D / 64 panels of [128 keys][128 B],
+// swizzled): thread t of T takes row t % 128 and D / 8 / (T / 128) of its
+// 16-byte chunks.  Returns the warp's 32 rows that held non-finite values.
+template <int D, int T>
+__device__ __forceinline__ uint32_t clean_tile(uint8_t* tile, int t) {
+  constexpr int kEach = D / 8 / (T / 128);
+  const int row = t & 127, h = t >> 7;
+  bool any = false;
+#pragma unroll 4
+  for (int c = 0; c < kEach; ++c) {
+    const int ch = h * kEach + c;
+    uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+    uint4 v = *at;
+    bool bad = clear_nonfinite(v.x);
+    bad |= clear_nonfinite(v.y);
+    bad |= clear_nonfinite(v.z);
+    bad |= clear_nonfinite(v.w);
+    if (bad) *at = v;
+    any |= bad;
+  }
+  return __ballot_sync(0xffffffffu, any);
+}
+
+// Value c of a V row in global memory.
+template <int D, bool Q8>
+__device__ __forceinline__ float value_at(const TreeParams& p, const Seg& g, int key, int c) {
+  if (!in_bounds(key >= 0 && key < p.C && c >= 0 && c < D, p.status, kSiteTreeKV)) return 0.f;
+  const uint8_t* row = p.v + (((long long)g.b * p.Hkv + g.hk) * p.C + key) * (Q8 ? D / 32 * 34 : 2 * D);
+  if constexpr (Q8) {
+    const uint8_t* blk = row + 34 * (c >> 5);
+    const __half d = __ushort_as_half(*reinterpret_cast<const unsigned short*>(blk));
+    return __half2float(__hmul(__int2half_rn((int)(int8_t)blk[2 + (c & 31)]), d));
+  } else {
+    return __half2float(reinterpret_cast<const __half*>(row)[c]);
+  }
+}
+
+// ------------------------------------------------------------------ Q8_0 tiles
+
+// Raw tiles are decoded a block at a time, four code bytes of a word to two
+// fp16 pairs (bytes 0 and 2, 1 and 3: no byte permutes).  A block of an even
+// column starts on a word: its first two codes share a word with the scale and
+// its last two with the next block, so these four form word 0; the other 28
+// are words 1 to 7 as they lie.  A block of an odd column starts in the middle
+// of a word and its codes are words 0 to 7.  So the decoded row holds the
+// block's values in this order; Q rows are put in the same order, and the
+// columns of O come out in it.
+__host__ __device__ constexpr int q8_code_at(int odd, int pos) {
+  const int i = pos >> 2, j = pos & 3, byte = j == 1 ? 2 : j == 2 ? 1 : j;
+  return odd ? 4 * i + byte : i > 0 ? 4 * i - 2 + byte : byte < 2 ? byte : 28 + byte;
+}
+
+// Block `blk` of row `row` of a raw tile (rows of D / 32 blocks) as 16 fp16
+// pairs in that order, each value RNE(q d).  Rows of 136 bytes are read as
+// 8-byte words (34 words apart: a half-warp's 16 rows cover every bank once),
+// rows of 68 bytes as 4-byte words (17 apart).
+template <int D>
+__device__ __forceinline__ void decode_block(const uint8_t* raw, int row, int blk, const DecK& K, uint32_t (&v)[16]) {
+  constexpr int RB = D / 32 * 34;
+  const int off = row * RB + 34 * blk;
+  uint32_t w[9];   // the words that hold the block
+  if constexpr (RB % 8 == 0) {
+    const uint2* src = reinterpret_cast<const uint2*>(raw + (off & ~7));
+    uint32_t a[10];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const uint2 x = src[i];
+      a[2 * i] = x.x;
+      a[2 * i + 1] = x.y;
+    }
+    if (blk & 2) {
+#pragma unroll
+      for (int i = 0; i < 9; ++i) w[i] = a[i + 1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 9; ++i) w[i] = a[i];
+    }
+  } else {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(raw + (off & ~3));
+#pragma unroll
+    for (int i = 0; i < 9; ++i) w[i] = src[i];
+  }
+  uint32_t d2;
+  if (blk & 1) {
+    d2 = __byte_perm(w[0], 0u, 0x3232);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = w[i + 1];
+  } else {
+    d2 = __byte_perm(w[0], 0u, 0x1010);
+    w[0] = __byte_perm(w[0], w[8], 0x5432);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q8_word(w[i], d2, K, v[2 * i], v[2 * i + 1]);
+}
+
+// 32 fp16 values of a Q row's block to the order of decode_block.
+__device__ __forceinline__ void order_block(const uint4 (&q)[4], int odd, uint4 (&out)[4]) {
+  const uint32_t s[16] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w,
+                          q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
+  uint32_t o[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int e0 = q8_code_at(0, 2 * k), e1 = q8_code_at(0, 2 * k + 1);
+    const int f0 = q8_code_at(1, 2 * k), f1 = q8_code_at(1, 2 * k + 1);
+    const uint32_t e = __byte_perm(s[e0 >> 1], s[e1 >> 1], ((e0 & 1) ? 0x32u : 0x10u) | ((e1 & 1) ? 0x7600u : 0x5400u));
+    const uint32_t f = __byte_perm(s[f0 >> 1], s[f1 >> 1], ((f0 & 1) ? 0x32u : 0x10u) | ((f1 & 1) ? 0x7600u : 0x5400u));
+    o[k] = odd ? f : e;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+}
+
+// 1-D bulk copy; addresses and size multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The whole 16-byte units around the rows [j kTile, min(that + kTile, last))
+// of a head of the raw cache: first byte and size (the cache is a multiple of
+// 16 bytes).
+__device__ __forceinline__ void raw_span(long long head, int C, int row_bytes, int j, int last, long long& at,
+                                         uint32_t& bytes) {
+  const long long a = (head * C + (long long)j * kTile) * row_bytes;
+  const long long e = (head * C + min((long long)(j + 1) * kTile, (long long)last)) * row_bytes;
+  at = a & ~15ll;
+  bytes = (uint32_t)(((e + 15) & ~15ll) - at);
+}
+
+// Joins the pieces of the items that were cut (attention_tree.cu).
+template <int D>
+cudaError_t launch_tree_join(const TreeParams& p, int grid, cudaStream_t s);
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_tree_kernel(void (*kern)(KArgs...), unsigned grid, unsigned block, int smem, cudaStream_t s,
+                               const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Once per kernel and device: its dynamic shared memory.
+template <typename Tag, typename Kern>
+cudaError_t allow_smem(Kern kern, int bytes) {
+  std::atomic<unsigned long long>& configured = attr_flag<Tag>();
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  return cudaSuccess;
+}
+
+}  // namespace m4q

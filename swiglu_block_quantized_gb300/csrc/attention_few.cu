@@ -19,10 +19,15 @@
 // maxima, raise the references and rescale O^T and the sums.  Row sums stay in
 // the threads (one partial sum a key lane and row) until the run ends.
 //
+// Tiles go to two teams in turn, each with its own P^T, O^T, references and sums,
+// joined when a run ends: a tile's chain from scores to P takes about 2500 clocks
+// whatever its size (barriers, TMEM loads, the fence before the MMA reads P), and
+// two of them overlap.
+//
 // Warps: 0 issues the S MMAs (four TMEM buffers ahead), 1 the P V MMAs, 2 and 3
-// the copies, 4-7 are the softmax (lane = key), the others prepare (Q, the Q8_0
-// decode, the clearing of non-finite V), as in attention_tree.cu, whose notes
-// on masks, schedule and pieces hold here.
+// the copies, 4-11 are the softmax teams (lane = key), the others prepare (Q, the
+// clearing of non-finite V; Q8_0: eight decode K tiles and eight V tiles), as in
+// attention_tree.cu, whose notes on masks, schedule and pieces hold here.
 #include <algorithm>
 
 #include "tree_common.cuh"
@@ -41,17 +46,20 @@ struct FewCfg {
   static constexpr int kKS = Q8 ? 2 : D == 128 ? 3 : 6;
   static constexpr int kVS = Q8 ? 2 : D == 128 ? 3 : 6;
   static constexpr int kRaw = kTile * kRow + 32;       // a raw tile, its 16-byte shift, and the decode's overread
-  static constexpr int kRS = Q8 ? (D == 128 ? 4 : 12) : 0;
-  static constexpr int kPrep = Q8 ? 16 : 4;            // preparing warps
-  static constexpr int kPerMatrix = Q8 && D == 64 ? 8 : kPrep;   // of them, those that decode one K or V tile
-  static constexpr int kThreads = 32 * (8 + kPrep);
-  static constexpr int kBars = 2 * kKS + 4 * kVS + 2 * kRS + 8 + 4 + 6;
-  static constexpr int kFixed = (int)sizeof(TreeSched) + 2 * kPrep * 16 + 4 * 32 * 4 + 4 * N * 4 + 5 * N * 4 +
-                                kBars * 8 + 64;
+  static constexpr int kRS = Q8 ? (D == 64 ? 12 : NC == 1 ? 4 : 3) : 0;
+  static constexpr int kPrep = Q8 ? 16 : 4;            // preparing warps: Q8_0: 8 for K tiles, 8 for V tiles
+  static constexpr int kThreads = 32 * (12 + kPrep);
+  static constexpr int kBars = 2 * kKS + 4 * kVS + 2 * kRS + 8 + 4 + 7;
+  static constexpr int kFixed = (int)sizeof(TreeSched) + 2 * 8 * 16   // schedule, noted rows
+                                + 8 * 32 * 4                          // ancestor bits by warp
+                                + 2 * 4 * N * 4 + 4 * N * 4           // wmax, mref and fac by team
+                                + 4 * N * 8                           // (m, l) [parity][team]
+                                + 8 * 2 * N * 4 + 8 * N * 4           // factors and output rows by warp
+                                + 2 * 8 + kBars * 8 + 64;
   static constexpr int kSmem = 1024 + kQBytes + 2 * kPBytes + (kKS + kVS) * kTileBytes + kRS * kRaw + kFixed;
-  static constexpr uint32_t kOCol = 4 * N;             // S^T buffers at N i, then O^T
+  static constexpr uint32_t kOCol = 4 * N;             // S^T buffers at N i, then O^T of the teams
   static constexpr uint32_t kCols = NC == 1 ? 128 : 256;
-  static_assert(5 * N <= (int)kCols, "TMEM budget");
+  static_assert(6 * N <= (int)kCols, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kRaw % 16 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "alignment");
 };
@@ -69,27 +77,62 @@ __device__ __forceinline__ bool vote_or(uint32_t id, uint32_t count, bool pred) 
   return r != 0;
 }
 
+// 8 consecutive 32-bit TMEM columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Sum of the non-finite values at d of the cleared V rows that a row sees (0 if
+// there is none).
+template <int D, bool Q8>
+__device__ __noinline__ float few_nonfinite(const TreeParams& p, const Seg& g, const uint32_t* noted, uint32_t anc,
+                                            int d) {
+  const int jm = first_masked(g);
+  float z = 0.f;
+  for (int mt = 0; mt < 4; ++mt) {
+    if (jm + mt < g.k0 || jm + mt >= g.k1) continue;
+    for (int q = 0; q < 4; ++q) {
+      const int kq = (jm + mt) * kTile + 32 * q;
+      uint32_t bits = (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32<1>(&anc, 0, kq, g.past, p.C);
+      while (bits) {
+        const int k = kq + __ffs(bits) - 1;
+        bits &= bits - 1;
+        const float v = value_at<D, Q8>(p, g, k, d);
+        if (!(v - v == 0.f)) z += v;
+      }
+    }
+  }
+  return z;
+}
+
 template <int D, bool Q8, int NC>
 __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const TreeParams p) {
   using Cfg = FewCfg<D, Q8, NC>;
   constexpr int N = Cfg::N, KS = Cfg::kKS, VS = Cfg::kVS, RS = Cfg::kRS > 0 ? Cfg::kRS : 1;
-  constexpr int PW = Cfg::kPrep, PM = Cfg::kPerMatrix;
+  constexpr int PW = Cfg::kPrep, PM = 8;   // warps that decode one tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_align<1024>(smem_raw);
   uint8_t* ps = qs + Cfg::kQBytes;                     // [2] P^T
   uint8_t* kst = ps + 2 * Cfg::kPBytes;
   uint8_t* vst = kst + KS * Cfg::kTileBytes;
   uint8_t* raws = vst + VS * Cfg::kTileBytes;
-  uint32_t* noted = reinterpret_cast<uint32_t*>(raws + Cfg::kRS * Cfg::kRaw);   // [parity][PW][4]
-  uint32_t* anc_all = noted + 2 * PW * 4;              // [warp][32] ancestor bits of a row
-  float* wmax = reinterpret_cast<float*>(anc_all + 4 * 32);   // [warp][N] column maxima, or sums
-  float* mref = wmax + 4 * N;                          // [N] references
-  float* fac = mref + N;                               // [N] rescale factors
-  float* linv = fac + N;                               // [N] output factors
-  int* unused_all = reinterpret_cast<int*>(linv + N);  // [parity][N] row of an unused node
-  TreeSched* sched = reinterpret_cast<TreeSched*>(unused_all + 2 * N);
+  uint32_t* noted = reinterpret_cast<uint32_t*>(raws + Cfg::kRS * Cfg::kRaw);   // [parity][8 warps][4]
+  uint32_t* anc_all = noted + 2 * 8 * 4;               // [warp][32] ancestor bits of a row
+  float* wmax_all = reinterpret_cast<float*>(anc_all + 8 * 32);   // [team][warp][N] column maxima, or sums
+  float* mref_all = wmax_all + 2 * 4 * N;              // [team][N] references
+  float* fac_all = mref_all + 2 * N;                   // [team][N] rescale factors
+  float2* ml = reinterpret_cast<float2*>(fac_all + 2 * N);        // [parity][team][N]
+  float* wf_all = reinterpret_cast<float*>(ml + 4 * N);           // [warp][team][N] output factors
+  int* off_all = reinterpret_cast<int*>(wf_all + 8 * 2 * N);      // [warp][N] output row of D values
+  uint32_t* unused_s = reinterpret_cast<uint32_t*>(off_all + 8 * N);       // [parity] rows of unused nodes
+  TreeSched* sched = reinterpret_cast<TreeSched*>(unused_s + 4);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sched) + (sizeof(TreeSched) + 7) / 8 * 8);
   uint64_t* k_empty = k_full + KS;     // [KS] S^T done with it
   uint64_t* v_full = k_empty + KS;     // [VS] V of a tile in its stage
@@ -107,7 +150,8 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
   uint64_t* o_done = q_empty + 1;      // P V of a run done
   uint64_t* o_free = o_done + 1;       // O^T of a run read out
   uint64_t* nf_rdy = o_free + 1;       // preparation of a run done (noted rows final)
-  uint64_t* drain = nf_rdy + 1;        // both issuers: every MMA complete
+  uint64_t* ml_rdy = nf_rdy + 1;       // both teams' (m, l) of a run
+  uint64_t* drain = ml_rdy + 1;        // both issuers: every MMA complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -138,7 +182,8 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
     mbar_init(q_full, PW);
     mbar_init(q_empty, 1);
     mbar_init(o_done, 1);
-    mbar_init(o_free, 4);
+    mbar_init(o_free, 8);
+    mbar_init(ml_rdy, 2);
     mbar_init(nf_rdy, PW);
     mbar_init(drain, 2);
     *abort_flag = 0;
@@ -213,15 +258,15 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
             full_ph ^= 1u << vs;
           }
           ok = ok && mbar_wait(&p_full[pb], (g >> 1) & 1, ctl);
-          if (j == sg.k0 && w > 0) ok = ok && mbar_wait(o_free, (w - 1) & 1, ctl);
+          if (j == sg.k0 && w > 0) ok = ok && mbar_wait(o_free, (w - 1) & 1, ctl);   // of both teams
           if (!ok) break;
           tc_fence_after();
           const uint64_t vds = vd + (uint64_t)(vs * (Cfg::kTileBytes >> 4));
           const uint64_t pds = pd + (uint64_t)(pb * (Cfg::kPBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ss_f16(tmem + Cfg::kOCol, vds + (uint32_t)(kk * (2048 >> 4)),
-                       pds + (kk >> 2) * (N * 128 >> 4) + 2 * (kk & 3), idesc, (kk > 0 || j > sg.k0) ? 1u : 0u);
+            mma_ss_f16(tmem + Cfg::kOCol + N * pb, vds + (uint32_t)(kk * (2048 >> 4)),
+                       pds + (kk >> 2) * (N * 128 >> 4) + 2 * (kk & 3), idesc, (kk > 0 || j > sg.k0 + 1) ? 1u : 0u);
           tc_commit(&v_empty[vs]);
           tc_commit(&p_free[pb]);
         }
@@ -284,14 +329,19 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
         }
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ softmax
-    const int sw = warp - 4;                       // = warp & 3: TMEM lanes 32 sw ..
+    const int team = (warp - 4) >> 2, sw = warp & 3;   // sw: TMEM lanes 32 sw ..
     const int key = 32 * sw + lane;                // this thread's key of a tile, and its d of O^T
     const uint32_t lanes = (uint32_t)(32 * sw) << 16;
-    uint32_t* anc = anc_all + 32 * sw;             // each warp has a copy: [row]
+    const uint32_t bar = 1 + team;                 // named barrier of the team
+    const uint32_t ocol = tmem + lanes + Cfg::kOCol + N * team;
+    uint32_t* anc = anc_all + 32 * (warp - 4);     // each warp has a copy: [row]
+    float* wmax = wmax_all + team * 4 * N;
+    float* mref = mref_all + team * N;
+    float* fac = fac_all + team * N;
     // P^T: row n, key: panel key / 64, 16-byte chunk ((key % 64) / 8) ^ (n % 8)
-    uint8_t* pbase = ps + (key >> 6) * (N * 128) + (key & 7) * 2;
+    uint8_t* pdst = ps + team * Cfg::kPBytes + (key >> 6) * (N * 128) + (key & 7) * 2;
     const int pchunk = (key & 63) >> 3;
     const float sc = p.scale_log2;
     const int R = p.N * p.G;                       // rows, at most N
@@ -300,80 +350,88 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
     bool fresh = true;                             // the CTA's first run
     int g = 0;
     for (int w = 0; !stop && tree_next(p, sched, walk, sg); ++w) {
-      const int jm = first_masked(sg);
-      int* unused_s = unused_all + (w & 1) * N;
+      const int jm = first_masked(sg), par = w & 1;
       if (sg.k1 > jm) {
         // the tree's bits, lane = row (nodes are at most 32: one word)
         uint32_t bits = 0;
         bool used = true;
         if (lane < R) used = ancestors<1>(p.parents + (long long)sg.b * p.N, lane / p.G, &bits, 1);
         anc[lane] = bits;
-        if (sw == 0 && lane < N) unused_s[lane] = used ? 0 : 1;
+        const uint32_t un = __ballot_sync(0xffffffffu, !used);
+        if (warp == 4 && lane == 0) unused_s[par] = un;
         __syncwarp();
       }
       float l[N];
 #pragma unroll
       for (int n = 0; n < N; ++n) l[n] = 0.f;
       for (int j = sg.k0; j < sg.k1; ++j, ++g) {
-        const int sb = g & 3, pb = g & 1;
-        const bool first = j == sg.k0;
-        bad = bad || !mbar_wait(&s_full[sb], (g >> 2) & 1, ctl);
-        bad = __any_sync(0xffffffffu, bad);
+        if ((g & 1) != team) continue;
+        const int sb = g & 3;
+        const bool first = j < sg.k0 + 2;          // the team's first tile of the run
+        // S^T, and the team's previous P V (its P^T is overwritten below, its
+        // O^T when references rise)
+        bool got = mbar_wait(&s_full[sb], (g >> 2) & 1, ctl);
+        if (g >= 2) got = got && mbar_wait(&p_free[team], ((g >> 1) - 1) & 1, ctl);
+        bad = !__all_sync(0xffffffffu, got);
         const uint32_t scol = tmem + lanes + N * sb;
-        const bool masked = j >= jm;
         uint32_t vis = 0xFFFFFFFFu;                // rows that see this key
-        if (masked) {
+        if (j >= jm) {
           const int kabs = j * kTile + key, rel = kabs - sg.past;
-          vis = 0u;
-          if (kabs < p.C) {
-            if (rel < 0) vis = 0xFFFFFFFFu;
-            else if (rel < 32)
+          if (rel >= 0 || kabs >= p.C) {
+            vis = 0u;
+            if (kabs < p.C && rel < 32)
               for (int n = 0; n < R; ++n) vis |= ((anc[n] >> rel) & 1u) << n;
           }
         }
-        bool above = first;
-        float x[N];
-        if (!bad) {
-          tc_fence_after();
+        const bool masked = __any_sync(0xffffffffu, vis != 0xFFFFFFFFu);
+        // x: the thread's scaled scores of 16 rows (masked: -inf)
+        auto scores = [&](int c, float (&x)[16]) {
+          uint32_t v[16];
+          tmem_ld16_wait(scol + 16 * c, v);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            uint32_t v[16];
-            tmem_ld16_wait(scol + 16 * c, v);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[16 * c + e] = __uint_as_float(v[e]) * sc;
-          }
+          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]) * sc;
           if (masked) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) x[n] = (vis >> n) & 1u ? x[n] : -INFINITY;
+            for (int e = 0; e < 16; ++e) x[e] = (vis >> (16 * c + e)) & 1u ? x[e] : -INFINITY;
           }
+        };
+        float x[16];
+        bool above = first;
+        if (!bad) {
+          tc_fence_after();
           if (!first) {
             float top = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < N; n += 4) {
-              const float4 m4 = *reinterpret_cast<const float4*>(mref + n);
-              top = fmaxf(top, fmaxf(fmaxf(x[n] - m4.x, x[n + 1] - m4.y), fmaxf(x[n + 2] - m4.z, x[n + 3] - m4.w)));
+            for (int c = 0; c < NC; ++c) {
+              scores(c, x);
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 m4 = *reinterpret_cast<const float4*>(mref + 16 * c + e);
+                top = fmaxf(top, fmaxf(fmaxf(x[e] - m4.x, x[e + 1] - m4.y), fmaxf(x[e + 2] - m4.z, x[e + 3] - m4.w)));
+              }
             }
             above = top > kRaise;   // a row without a reference yet has -inf: a key that it sees is above
           }
-          tc_fence_before();
         }
         // the warps go on, or leave, together (a named barrier has no time limit)
-        if (vote_or(1, 128, above || bad)) {
-          // ------------------------------------------------ raise references
-          // column maxima over the tile's keys
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            float t = bad ? -INFINITY : x[n];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-            if (lane == (n & 31)) wmax[sw * N + n] = t;
-          }
-          // O^T holds the run's earlier tiles: their P V have to be done
-          if (!first && !bad) bad = !mbar_wait(&p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, ctl);
-          if (vote_or(1, 128, bad)) {
+        if (vote_or(bar, 128, above || bad)) {
+          if (vote_or(bar, 128, bad)) {
             stop = true;
             break;
           }
+          // column maxima over the tile's keys
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c) {
+            scores(c, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float t = x[e];
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+              if (lane == e) wmax[sw * N + 16 * c + e] = t;
+            }
+          }
+          vote_or(bar, 128, false);
           if (sw == 0 && lane < N) {
             const float t = fmaxf(fmaxf(wmax[lane], wmax[N + lane]), fmaxf(wmax[2 * N + lane], wmax[3 * N + lane]));
             const float m = first ? -INFINITY : mref[lane];
@@ -381,46 +439,47 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
             fac[lane] = m == -INFINITY ? 0.f : ex2(m - nm);
             mref[lane] = nm;
           }
-          vote_or(1, 128, false);
+          vote_or(bar, 128, false);
           if (!first) {
-            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < NC; ++c) {
               uint32_t v[16];
-              tmem_ld16_wait(tmem + lanes + Cfg::kOCol + 16 * c, v);
+              tmem_ld16_wait(ocol + 16 * c, v);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const float f = fac[16 * c + e];
                 v[e] = f == 1.f ? v[e] : __float_as_uint(__uint_as_float(v[e]) * f);
               }
-              tmem_st16(tmem + lanes + Cfg::kOCol + 16 * c, v);
+              tmem_st16(ocol + 16 * c, v);
             }
             tmem_wait_st();
-            tc_fence_before();
 #pragma unroll
             for (int n = 0; n < N; ++n) l[n] *= fac[n];
           }
+          if (NC == 1) scores(0, x);
         }
-        // P^T over the buffer of tile g - 2
-        if (g >= 2) bad = !__all_sync(0xffffffffu, mbar_wait(&p_free[pb], ((g >> 1) - 1) & 1, ctl));
-        if (!bad) {
-          uint8_t* dst = pbase + pb * Cfg::kPBytes;
+        // P^T = 2^(x - m); a masked key's x is -inf, also where the reference is
 #pragma unroll
-          for (int n = 0; n < N; n += 4) {
-            const float4 m4 = *reinterpret_cast<const float4*>(mref + n);
+        for (int c = 0; c < NC; ++c) {
+          if (NC > 1) scores(c, x);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(mref + 16 * c + e);
             const float m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // a masked key's x is -inf, also where the reference is
-              const float pv = x[n + e] == -INFINITY ? 0.f : ex2(x[n + e] - m[e]);
-              l[n + e] += pv;
-              *reinterpret_cast<__half*>(dst + (n + e) * 128 + ((pchunk ^ ((n + e) & 7)) << 4)) = __float2half_rn(pv);
+            for (int i = 0; i < 4; ++i) {
+              float pv = ex2(x[e + i] - m[i]);
+              if (masked) pv = x[e + i] == -INFINITY ? 0.f : pv;
+              l[16 * c + e + i] += pv;
+              *reinterpret_cast<__half*>(pdst + (16 * c + e + i) * 128 + ((pchunk ^ ((e + i) & 7)) << 4)) =
+                  __float2half_rn(pv);
             }
           }
-          fence_proxy_async_smem();
-          mbar_arrive_warp(&s_free[sb]);
-          mbar_arrive_warp(&p_full[pb]);
         }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive_warp(&s_free[sb]);
+        mbar_arrive_warp(&p_full[team]);
       }
       if (stop) break;
       // ---------------------------------------------------------- end of a run
@@ -432,77 +491,91 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
         if (lane == (n & 31)) wmax[sw * N + n] = t;
       }
-      const int par = w & 1;
-      bad = bad || !(mbar_wait(o_done, par, ctl) && mbar_wait(nf_rdy, par, ctl));
-      if (vote_or(1, 128, bad)) {
+      vote_or(bar, 128, false);
+      const int len = sg.k1 - sg.k0, g0 = g - len;
+      // a team without a tile of the run has no O^T and no references
+      const bool has0 = len > 1 || !(g0 & 1), has1 = len > 1 || (g0 & 1), mine = team ? has1 : has0;
+      if (sw == 0) {
+        if (lane < N)
+          ml[(par * 2 + team) * N + lane] =
+              mine ? make_float2(mref[lane], wmax[lane] + wmax[N + lane] + wmax[2 * N + lane] + wmax[3 * N + lane])
+                   : make_float2(-INFINITY, 0.f);
+        mbar_arrive_warp(ml_rdy);
+      }
+      const bool got = mbar_wait(ml_rdy, par, ctl) && mbar_wait(o_done, par, ctl) && mbar_wait(nf_rdy, par, ctl);
+      bad = !__all_sync(0xffffffffu, got);
+      if (vote_or(bar, 128, bad)) {
         stop = true;
         break;
       }
       tc_fence_after();
-      const bool whole = sg.k0 == 0 && sg.k1 == sg.nk;
-      const bool tree = sg.k1 > jm;
-      const long long slot = (2ll * blockIdx.x + (fresh ? 0 : 1)) * p.ws_rows;
-      if (sw == 0 && lane < N) {
-        const float L = wmax[lane] + wmax[N + lane] + wmax[2 * N + lane] + wmax[3 * N + lane];
-        const bool un = tree && unused_s[lane];
+      const bool whole = sg.k0 == 0 && sg.k1 == sg.nk, tree = sg.k1 > jm;
+      const uint32_t unused = tree ? unused_s[par] : 0u;
+      float* wf = wf_all + (warp - 4) * 2 * N;
+      int* off = off_all + (warp - 4) * N;
+      if (lane < N) {
+        const float2 a = ml[par * 2 * N + lane], b = ml[(par * 2 + 1) * N + lane];
+        const float M = fmaxf(a.x, b.x);
+        const float w0 = a.x == M ? 1.f : ex2(a.x - M), w1 = b.x == M ? 1.f : ex2(b.x - M);
+        const float L = a.y * w0 + b.y * w1;
         // a whole item is divided by its sum (a row without a key is zero)
-        linv[lane] = !whole ? 1.f : L > 0.f ? 1.f / L : L;
-        if (!whole && lane < R && in_bounds(p.split && lane < p.ws_rows, p.status, kSiteTreeWs))
-          p.ws_ml[slot + lane] = make_float2(mref[lane], un ? -1.f : L);
+        const float inv = !whole ? 1.f : L > 0.f ? 1.f / L : L;
+        wf[lane] = w0 * inv;
+        wf[N + lane] = w1 * inv;
+        const int node = lane / p.G, h = sg.hk * p.G + lane - node * p.G;
+        const int piece = (2 * blockIdx.x + (fresh ? 0 : 1)) * p.ws_rows + lane;
+        off[lane] = whole ? (sg.b * p.N + node) * p.H + h : piece;   // B N H fits 31 bits
+        if (warp == 4 && !whole && lane < R && in_bounds(p.split && lane < p.ws_rows, p.status, kSiteTreeWs))
+          p.ws_ml[piece] = make_float2(M, (unused >> lane) & 1u ? -1.f : L);
       }
-      uint32_t some = 0;
-      if (tree)
-        for (int i = lane; i < PW * 4; i += 32) some |= noted[par * PW * 4 + i];
-      const bool anynf = __any_sync(0xffffffffu, some != 0u);
-      vote_or(1, 128, false);   // linv is written
+      __syncwarp();
+      // each team takes half of the rows; lane = d
       const int d = Q8 ? (key & ~31) + q8_code_at((key >> 5) & 1, key & 31) : key;
-#pragma unroll 1
-      for (int c = 0; c < NC; ++c) {
-        uint32_t v[16];
-        tmem_ld16_wait(tmem + lanes + Cfg::kOCol + 16 * c, v);
-        if (key < D) {
+      uint32_t v0[8 * NC], v1[8 * NC];
+      const int nb = 8 * NC * team;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int n = 16 * c + e;
-            if (n >= R) break;
-            float o = __uint_as_float(v[e]) * linv[n];
-            const bool un = tree && unused_s[n];
-            if (anynf && !un) {
-              // non-finite values of cleared V rows that this row sees
-              for (int mt = 0; mt < 4; ++mt)
-                for (int q = 0; q < 4; ++q) {
-                  if (jm + mt < sg.k0 || jm + mt >= sg.k1) continue;
-                  const int kq = (jm + mt) * kTile + 32 * q;
-                  uint32_t bits = 0;
-                  for (int i = q; i < PW; i += 4) bits |= noted[par * PW * 4 + 4 * i + mt];
-                  bits &= seen32<1>(anc + n, 0, kq, sg.past, p.C);
-                  while (bits) {
-                    const int k = kq + __ffs(bits) - 1;
-                    bits &= bits - 1;
-                    const float z = value_at<D, Q8>(p, sg, k, d);
-                    if (!(z - z == 0.f)) o += z;
-                  }
-                }
-            }
-            const int node = n / p.G, h = sg.hk * p.G + n % p.G;
+      for (int c = 0; c < NC; ++c) {
+        tmem_ld8(tmem + lanes + Cfg::kOCol + nb + 8 * c, v0 + 8 * c);
+        tmem_ld8(tmem + lanes + Cfg::kOCol + N + nb + 8 * c, v1 + 8 * c);
+      }
+      if (key < D) {
+#pragma unroll
+        for (int e = 0; e < 8 * NC; ++e) {
+          const int n = nb + e;
+          if (n < R) {
+            const float o = (has0 ? __uint_as_float(v0[e]) * wf[n] : 0.f) + (has1 ? __uint_as_float(v1[e]) * wf[N + n] : 0.f);
             if (whole) {
-              if (in_bounds(node < p.N && h < p.H, p.status, kSiteTreeO))
-                p.o[((long long)sg.b * p.N + node) * p.H * D + (long long)h * D + d] = __float2half_rn(un ? 0.f : o);
+              if (in_bounds(n / p.G < p.N, p.status, kSiteTreeO))
+                p.o[(long long)off[n] * D + d] = __float2half_rn((unused >> n) & 1u ? 0.f : o);
             } else if (in_bounds(p.split && n < p.ws_rows, p.status, kSiteTreeWs)) {
-              p.ws_o[(slot + n) * D + d] = o;
+              p.ws_o[(long long)off[n] * D + d] = o;
             }
           }
         }
-        __syncwarp();
       }
+      uint32_t some = 0;
+      if (tree) some = noted[par * 32 + lane];
+      if (__any_sync(0xffffffffu, some != 0u) && key < D) {
+        // non-finite values of cleared V rows, added for the rows that see them
+        for (int e = 0; e < 8 * NC; ++e) {
+          const int n = nb + e;
+          if (n >= R || ((unused >> n) & 1u)) continue;
+          const float z = few_nonfinite<D, Q8>(p, sg, noted + par * 32, anc[n], d);
+          if (z == 0.f) continue;
+          if (whole) p.o[(long long)off[n] * D + d] = __float2half_rn(__half2float(p.o[(long long)off[n] * D + d]) + z);
+          else p.ws_o[(long long)off[n] * D + d] += z;
+        }
+      }
+      __syncwarp();
       fresh = false;
       tc_fence_before();
       mbar_arrive_warp(o_free);
     }
   } else {
     // ------------------------------------------------------------ Q, decode, clearing
-    const int t = threadIdx.x - 8 * 32;         // 0 .. 32 PW - 1
-    const int pw = warp - 8;
+    const int t = threadIdx.x - 12 * 32;        // 0 .. 32 PW - 1
+    const int pw = warp - 12;
+    const int kv = Q8 ? pw >> 3 : 1;            // Q8_0: this warp decodes K (0) or V (1) tiles
     const int R = p.N * p.G;
     const DecK K = make_deck();
     bool ok = true;
@@ -512,8 +585,9 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       const int jm = first_masked(sg);
       ok = __all_sync(0xffffffffu, w == 0 || mbar_wait_idle(q_empty, (w - 1) & 1, run_ctl, 64));
       if (!ok) break;
-      uint32_t* nt = noted + (w & 1) * PW * 4 + pw * 4;
-      if (lane < 4) nt[lane] = 0u;
+      uint32_t* nt = noted + (w & 1) * 32 + (pw & 7) * 4;
+      if (kv == 1 && lane < 4) nt[lane] = 0u;
+      if (!Q8 && lane < 4) nt[16 + lane] = 0u;   // (four warps: the other four's notes stay empty)
       __syncwarp();
       // Q rows (Q8_0: in the decoded blocks' order), a block of 32 values a thread
       for (int u = t; u < N * (D / 32); u += 32 * PW) {
@@ -543,36 +617,37 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
         const int ks = g % KS, vs = g % VS;
         if constexpr (Q8) {
           const int sh = (int)(((head * p.C + (long long)j * kTile) * Cfg::kRow) & 15);
-          // D = 128: all warps decode K, then V; D = 64: one half each
-          const int row = t & 127, blk = D == 128 ? t >> 7 : (t >> 7) & 1;
-#pragma unroll 1
-          for (int kv = D == 128 ? 0 : t >> 8; kv < 2; kv += D == 128 ? 1 : 2) {
-            const int rn = 2 * g + kv, rs = rn % RS;
-            const int ns = kv ? VS : KS;
-            bool go = mbar_wait(&r_full[rs], (rn / RS) & 1, ctl);
-            if (g >= ns) go = go && mbar_wait(kv ? &v_empty[vs] : &k_empty[ks], ((g / ns) - 1) & 1, ctl);
-            ok = __all_sync(0xffffffffu, go);
-            if (!ok) break;
-            uint8_t* dst = kv ? vst + vs * Cfg::kTileBytes : kst + ks * Cfg::kTileBytes;
+          const int rn = 2 * g + kv, rs = rn % RS, ns = kv ? VS : KS;
+          bool go = mbar_wait(&r_full[rs], (rn / RS) & 1, ctl);
+          if (g >= ns) go = go && mbar_wait(kv ? &v_empty[vs] : &k_empty[ks], ((g / ns) - 1) & 1, ctl);
+          ok = __all_sync(0xffffffffu, go);
+          if (!ok) break;
+          uint8_t* dst = kv ? vst + vs * Cfg::kTileBytes : kst + ks * Cfg::kTileBytes;
+          const int row = t & 127;
+          const bool clean = kv && j >= jm;
+          bool any = false;
+#pragma unroll
+          for (int u = 0; u < D / 64; ++u) {
+            const int blk = 2 * u + ((t >> 7) & 1);
             uint32_t v[16];
             decode_block<D>(raws + rs * Cfg::kRaw + sh, row, blk, K, v);
-            if (kv && j >= jm) {
-              bool any = false;
+            if (clean) {
 #pragma unroll
               for (int q = 0; q < 16; ++q) any |= clear_nonfinite(v[q]);
-              const uint32_t bits = __ballot_sync(0xffffffffu, any);
-              if (lane == 0) nt[j - jm] = bits;
             }
             uint8_t* base = dst + (blk >> 1) * (kTile * 128) + row * 128;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(base + (((4 * (blk & 1) + i) ^ (row & 7)) << 4)) =
                   make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            fence_proxy_async_smem();
-            mbar_arrive_warp(kv ? &v_full[vs] : &k_full[ks]);
-            mbar_arrive_warp(&r_empty[rs]);
-            if (D == 64) break;
           }
+          if (clean) {
+            const uint32_t bits = __ballot_sync(0xffffffffu, any);
+            if (lane == 0) nt[j - jm] = bits;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive_warp(kv ? &v_full[vs] : &k_full[ks]);
+          mbar_arrive_warp(&r_empty[rs]);
         } else if (j >= jm) {
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
           if (!ok) break;

@@ -4,18 +4,23 @@
 // With few rows the 128 lanes of a tcgen05 tile are best given to the keys:
 //   S^T = K Q^T       M = 128 keys, N = 16 or 32 rows: lane = key
 //   O^T += V^T P^T    M = D (two copies of 64 when D = 64), N = rows: lane = d
-// so that the softmax of a tile is 16 or 32 values a thread whatever the mask,
-// and the MMAs shrink with N.  K is the A operand as it lies ([key][D],
-// K-major), V is the A operand as it lies ([key][D], M-major), Q and P are the
-// small B operands in shared memory.  What is left is the stream of the cache:
-// HBM should bound the fp16 kernel, and for Q8_0 the decode (about 2.4
-// instructions a value, 640 issue slots of a scheduler for a tile of 128 keys at
-// D = 128, against 1500 clocks of HBM time).
+// so that the softmax of a tile is a few values a thread whatever the mask, and
+// the MMAs shrink with N.  V is the A operand as it lies ([key][D], M-major), P
+// the small K-major B operand in shared memory.  (O += P V with P as a 128-row A
+// operand took 122 us against 107 where this was measured, 32 sequences of one
+// token: most of those rows are nobody's, and reading them costs the shared
+// memory that the decode needs.)
+// What is left is the stream of the cache: HBM should bound the fp16 kernel. For
+// Q8_0 the shared memory comes close: a tile of 128 keys at D = 128 is 1500 clocks
+// of HBM time, and with both decoded tiles in shared memory its copy, decode and
+// MMAs move 198 KB there, 1550 clocks. So K is decoded into TMEM instead (lane =
+// key, the A operand from there), which leaves 134 KB; V has to be read across
+// its keys and stays in shared memory.
 //
 // A row's reference maximum is kept while its scores stay within 2^8 of it, so
 // the usual tile needs no maximum across the keys: each thread forms its
 // exponents against the reference and the four warps vote (one barrier) whether
-// one is above 8.  If so (always in a run's first tile) they find the column
+// one is above 8.  If so (always in a run's first tile) they find the rows'
 // maxima, raise the references and rescale O^T and the sums.  Row sums stay in
 // the threads (one partial sum a key lane and row) until the run ends.
 //
@@ -43,23 +48,24 @@ struct FewCfg {
   static constexpr int kTileBytes = kTile * D * 2;     // an fp16 tile: D / 64 panels of [128][128 B]
   static constexpr int kQBytes = N * D * 2;            // D / 64 panels of [N][128 B]
   static constexpr int kPBytes = N * kTile * 2;        // two panels (64 keys) of [N][128 B]
-  static constexpr int kKS = Q8 ? 2 : D == 128 ? 3 : 6;
-  static constexpr int kVS = Q8 ? 2 : D == 128 ? 3 : 6;
+  static constexpr int kKS = Q8 ? 3 : D == 128 ? 3 : 6;   // K stages (Q8_0: in TMEM)
+  static constexpr int kVS = D == 128 ? 3 : 6;
   static constexpr int kRaw = kTile * kRow + 32;       // a raw tile, its 16-byte shift, and the decode's overread
-  static constexpr int kRS = Q8 ? (D == 64 ? 12 : NC == 1 ? 4 : 3) : 0;
-  static constexpr int kPrep = Q8 ? 16 : 4;            // preparing warps: Q8_0: 8 for K tiles, 8 for V tiles
+  static constexpr int kRS = Q8 ? (D == 64 ? 10 : NC == 1 ? 6 : 5) : 0;
+  static constexpr int kPrep = Q8 ? (NC == 1 ? 16 : 8) : 4;   // preparing warps: Q8_0: half for K tiles, half for V tiles
   static constexpr int kThreads = 32 * (12 + kPrep);
   static constexpr int kBars = 2 * kKS + 4 * kVS + 2 * kRS + 8 + 4 + 7;
   static constexpr int kFixed = (int)sizeof(TreeSched) + 2 * 8 * 16   // schedule, noted rows
                                 + 8 * 32 * 4                          // ancestor bits by warp
                                 + 2 * 4 * N * 4 + 4 * N * 4           // wmax, mref and fac by team
                                 + 4 * N * 8                           // (m, l) [parity][team]
-                                + 8 * 2 * N * 4 + 8 * N * 4           // factors and output rows by warp
                                 + 2 * 8 + kBars * 8 + 64;
-  static constexpr int kSmem = 1024 + kQBytes + 2 * kPBytes + (kKS + kVS) * kTileBytes + kRS * kRaw + kFixed;
+  static constexpr int kSmem = 1024 + kQBytes + 2 * kPBytes + ((Q8 ? 0 : kKS) + kVS) * kTileBytes + kRS * kRaw + kFixed;
   static constexpr uint32_t kOCol = 4 * N;             // S^T buffers at N i, then O^T of the teams
-  static constexpr uint32_t kCols = NC == 1 ? 128 : 256;
-  static_assert(6 * N <= (int)kCols, "TMEM budget");
+  static constexpr uint32_t kKCol = 6 * N;             // Q8_0: K stages of D / 2 columns
+  static constexpr uint32_t kUsed = kKCol + (Q8 ? kKS * D / 2 : 0);
+  static constexpr uint32_t kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kRaw % 16 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "alignment");
 };
@@ -77,32 +83,58 @@ __device__ __forceinline__ bool vote_or(uint32_t id, uint32_t count, bool pred) 
   return r != 0;
 }
 
-// 8 consecutive 32-bit TMEM columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
+// Sums (or maxima) of N values over the warp: halves of the rows change lanes,
+// N / 2 + N / 4 + ... shuffles instead of 5 N.  Returned: row `lane` (N = 32) or
+// lane / 2 (N = 16).
+template <int N, bool MAX>
+__device__ __forceinline__ float reduce_rows(float (&l)[N], int lane) {
+#pragma unroll
+  for (int h = N / 2, bit = 16; h >= 1; h /= 2, bit /= 2) {
+#pragma unroll
+    for (int n = 0; n < h; ++n) {
+      const float keep = lane & bit ? l[n + h] : l[n], give = lane & bit ? l[n] : l[n + h];
+      const float got = __shfl_xor_sync(0xffffffffu, give, bit);
+      l[n] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  if constexpr (N == 16) {
+    const float got = __shfl_xor_sync(0xffffffffu, l[0], 1);
+    return MAX ? fmaxf(l[0], got) : l[0] + got;
+  }
+  return l[0];
+}
+
+// 4 consecutive 32-bit TMEM columns of this thread's lane: loaded and waited
+// for, or stored.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&v)[4]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
 // Sum of the non-finite values at d of the cleared V rows that a row sees (0 if
 // there is none).
 template <int D, bool Q8>
-__device__ __noinline__ float few_nonfinite(const TreeParams& p, const Seg& g, const uint32_t* noted, uint32_t anc,
-                                            int d) {
+__device__ __noinline__ float few_nonfinite(const TreeParams& p, Seg g, const uint32_t* noted, uint32_t anc, int d) {
   const int jm = first_masked(g);
   float z = 0.f;
+#pragma unroll 1
   for (int mt = 0; mt < 4; ++mt) {
     if (jm + mt < g.k0 || jm + mt >= g.k1) continue;
+#pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       const int kq = (jm + mt) * kTile + 32 * q;
       uint32_t bits = (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32<1>(&anc, 0, kq, g.past, p.C);
       while (bits) {
-        const int k = kq + __ffs(bits) - 1;
+        const float v = value_at<D, Q8>(p, g, kq + __ffs(bits) - 1, d);
         bits &= bits - 1;
-        const float v = value_at<D, Q8>(p, g, k, d);
         if (!(v - v == 0.f)) z += v;
       }
     }
@@ -116,12 +148,12 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
                const TreeParams p) {
   using Cfg = FewCfg<D, Q8, NC>;
   constexpr int N = Cfg::N, KS = Cfg::kKS, VS = Cfg::kVS, RS = Cfg::kRS > 0 ? Cfg::kRS : 1;
-  constexpr int PW = Cfg::kPrep, PM = 8;   // warps that decode one tile
+  constexpr int PW = Cfg::kPrep, PM = PW / 2;   // warps that decode one tile (Q8_0)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_align<1024>(smem_raw);
   uint8_t* ps = qs + Cfg::kQBytes;                     // [2] P^T
   uint8_t* kst = ps + 2 * Cfg::kPBytes;
-  uint8_t* vst = kst + KS * Cfg::kTileBytes;
+  uint8_t* vst = kst + (Q8 ? 0 : KS) * Cfg::kTileBytes;
   uint8_t* raws = vst + VS * Cfg::kTileBytes;
   uint32_t* noted = reinterpret_cast<uint32_t*>(raws + Cfg::kRS * Cfg::kRaw);   // [parity][8 warps][4]
   uint32_t* anc_all = noted + 2 * 8 * 4;               // [warp][32] ancestor bits of a row
@@ -129,9 +161,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
   float* mref_all = wmax_all + 2 * 4 * N;              // [team][N] references
   float* fac_all = mref_all + 2 * N;                   // [team][N] rescale factors
   float2* ml = reinterpret_cast<float2*>(fac_all + 2 * N);        // [parity][team][N]
-  float* wf_all = reinterpret_cast<float*>(ml + 4 * N);           // [warp][team][N] output factors
-  int* off_all = reinterpret_cast<int*>(wf_all + 8 * 2 * N);      // [warp][N] output row of D values
-  uint32_t* unused_s = reinterpret_cast<uint32_t*>(off_all + 8 * N);       // [parity] rows of unused nodes
+  uint32_t* unused_s = reinterpret_cast<uint32_t*>(ml + 4 * N);                // [parity] rows of unused nodes
   TreeSched* sched = reinterpret_cast<TreeSched*>(unused_s + 4);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sched) + (sizeof(TreeSched) + 7) / 8 * 8);
   uint64_t* k_empty = k_full + KS;     // [KS] S^T done with it
@@ -214,19 +244,28 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       const uint64_t kd = sdesc_sw128_kmajor(smem_u32(kst));
       bool ok = true;
       int g = 0;
+      Ring<KS> kr;
       for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
         ok = mbar_wait(q_full, w & 1, ctl);
-        for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g) {
-          const int ks = g % KS, sb = g & 3;
-          ok = mbar_wait(&k_full[ks], (g / KS) & 1, ctl);
+        for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g, kr.step()) {
+          const int ks = kr.at, sb = g & 3;
+          ok = mbar_wait(&k_full[ks], kr.ph, ctl);
           if (g >= 4) ok = ok && mbar_wait(&s_free[sb], ((g >> 2) - 1) & 1, ctl);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t kds = kd + (uint64_t)(ks * (Cfg::kTileBytes >> 4));
+          if constexpr (Q8) {
+            const uint32_t kcol = tmem + Cfg::kKCol + ks * (D / 2);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss_f16(tmem + N * sb, kds + (kk >> 2) * (kTile * 128 >> 4) + 2 * (kk & 3),
-                       qd + (kk >> 2) * (N * 128 >> 4) + 2 * (kk & 3), idesc, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_ts_f16(tmem + N * sb, kcol + 8 * kk, qd + (kk >> 2) * (N * 128 >> 4) + 2 * (kk & 3), idesc,
+                            kk > 0 ? 1u : 0u);
+          } else {
+            const uint64_t kds = kd + (uint64_t)(ks * (Cfg::kTileBytes >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss_f16(tmem + N * sb, kds + (kk >> 2) * (kTile * 128 >> 4) + 2 * (kk & 3),
+                         qd + (kk >> 2) * (N * 128 >> 4) + 2 * (kk & 3), idesc, kk > 0 ? 1u : 0u);
+          }
           tc_commit(&s_full[sb]);
           tc_commit(&k_empty[ks]);
         }
@@ -246,10 +285,11 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       uint32_t full_ph = 0, clean_ph = 0;   // phase bits of v_full and v_clean of each stage
       bool ok = true;
       int g = 0;
+      Ring<VS> vr;
       for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
         const int jm = first_masked(sg);
-        for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g) {
-          const int vs = g % VS, pb = g & 1;
+        for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g, vr.step()) {
+          const int vs = vr.at, pb = g & 1;
           if (!Q8 && j >= jm) {
             ok = mbar_wait(&v_clean[vs], (clean_ph >> vs) & 1, ctl);
             clean_ph ^= 1u << vs;
@@ -340,11 +380,14 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
     float* wmax = wmax_all + team * 4 * N;
     float* mref = mref_all + team * N;
     float* fac = fac_all + team * N;
-    // P^T: row n, key: panel key / 64, 16-byte chunk ((key % 64) / 8) ^ (n % 8)
+    // P: row n, key: panel key / 64, 16-byte chunk ((key % 64) / 8) ^ (n % 8)
     uint8_t* pdst = ps + team * Cfg::kPBytes + (key >> 6) * (N * 128) + (key & 7) * 2;
     const int pchunk = (key & 63) >> 3;
     const float sc = p.scale_log2;
     const int R = p.N * p.G;                       // rows, at most N
+    // whole groups of 4 are computed; the P of later rows, whatever the buffer
+    // holds, reaches only their own columns of O^T
+    const int RU = (R + 3) & ~3;
     bool bad = false;                              // a wait gave up
     bool stop = false;
     bool fresh = true;                             // the CTA's first run
@@ -368,8 +411,8 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
         if ((g & 1) != team) continue;
         const int sb = g & 3;
         const bool first = j < sg.k0 + 2;          // the team's first tile of the run
-        // S^T, and the team's previous P V (its P^T is overwritten below, its
-        // O^T when references rise)
+        // S^T, and the team's previous P V (its P is overwritten below, its O
+        // rescaled when references rise)
         bool got = mbar_wait(&s_full[sb], (g >> 2) & 1, ctl);
         if (g >= 2) got = got && mbar_wait(&p_free[team], ((g >> 1) - 1) & 1, ctl);
         bad = !__all_sync(0xffffffffu, got);
@@ -380,35 +423,36 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
           if (rel >= 0 || kabs >= p.C) {
             vis = 0u;
             if (kabs < p.C && rel < 32)
+#pragma unroll 1
               for (int n = 0; n < R; ++n) vis |= ((anc[n] >> rel) & 1u) << n;
           }
         }
         const bool masked = __any_sync(0xffffffffu, vis != 0xFFFFFFFFu);
-        // x: the thread's scaled scores of 16 rows (masked: -inf)
-        auto scores = [&](int c, float (&x)[16]) {
-          uint32_t v[16];
-          tmem_ld16_wait(scol + 16 * c, v);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]) * sc;
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = (vis >> (16 * c + e)) & 1u ? x[e] : -INFINITY;
-          }
-        };
-        float x[16];
+        // x: the thread's scaled scores (masked: -inf)
+        float x[N];
         bool above = first;
         if (!bad) {
           tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            uint32_t v[16];
+            tmem_ld16_wait(scol + 16 * c, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[16 * c + e] = __uint_as_float(v[e]) * sc;
+          }
+          tc_fence_before();
+          mbar_arrive_warp(&s_free[sb]);
+          if (masked) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) x[n] = (vis >> n) & 1u ? x[n] : -INFINITY;
+          }
           if (!first) {
             float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              scores(c, x);
-#pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 m4 = *reinterpret_cast<const float4*>(mref + 16 * c + e);
-                top = fmaxf(top, fmaxf(fmaxf(x[e] - m4.x, x[e + 1] - m4.y), fmaxf(x[e + 2] - m4.z, x[e + 3] - m4.w)));
-              }
+            for (int n = 0; n < N; n += 4) {
+              if (n >= RU) break;
+              const float4 m4 = *reinterpret_cast<const float4*>(mref + n);
+              top = fmaxf(top, fmaxf(fmaxf(x[n] - m4.x, x[n + 1] - m4.y), fmaxf(x[n + 2] - m4.z, x[n + 3] - m4.w)));
             }
             above = top > kRaise;   // a row without a reference yet has -inf: a key that it sees is above
           }
@@ -419,20 +463,13 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
             stop = true;
             break;
           }
-          // column maxima over the tile's keys
-#pragma unroll 1
-          for (int c = 0; c < NC; ++c) {
-            scores(c, x);
+          // row maxima over the tile's keys
+          float t[N];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float t = x[e];
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-              if (lane == e) wmax[sw * N + 16 * c + e] = t;
-            }
-          }
+          for (int n = 0; n < N; ++n) t[n] = x[n];
+          wmax[sw * N + (NC == 1 ? lane >> 1 : lane)] = reduce_rows<N, true>(t, lane);
           vote_or(bar, 128, false);
-          if (sw == 0 && lane < N) {
+          if (sw == 0 && lane < RU) {
             const float t = fmaxf(fmaxf(wmax[lane], wmax[N + lane]), fmaxf(wmax[2 * N + lane], wmax[3 * N + lane]));
             const float m = first ? -INFINITY : mref[lane];
             const float nm = t > m + kRaise || m == -INFINITY ? fmaxf(m, t) : m;
@@ -442,61 +479,48 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
           vote_or(bar, 128, false);
           if (!first) {
 #pragma unroll 1
-            for (int c = 0; c < NC; ++c) {
-              uint32_t v[16];
-              tmem_ld16_wait(ocol + 16 * c, v);
+            for (int n = 0; n < RU; n += 4) {
+              uint32_t v[4];
+              tmem_ld4(ocol + n, v);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float f = fac[16 * c + e];
-                v[e] = f == 1.f ? v[e] : __float_as_uint(__uint_as_float(v[e]) * f);
-              }
-              tmem_st16(ocol + 16 * c, v);
+              for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fac[n + e]);
+              tmem_st4(ocol + n, v);
             }
             tmem_wait_st();
+            tc_fence_before();
 #pragma unroll
-            for (int n = 0; n < N; ++n) l[n] *= fac[n];
-          }
-          if (NC == 1) scores(0, x);
-        }
-        // P^T = 2^(x - m); a masked key's x is -inf, also where the reference is
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          if (NC > 1) scores(c, x);
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 m4 = *reinterpret_cast<const float4*>(mref + 16 * c + e);
-            const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float pv = ex2(x[e + i] - m[i]);
-              if (masked) pv = x[e + i] == -INFINITY ? 0.f : pv;
-              l[16 * c + e + i] += pv;
-              *reinterpret_cast<__half*>(pdst + (16 * c + e + i) * 128 + ((pchunk ^ ((e + i) & 7)) << 4)) =
-                  __float2half_rn(pv);
+            for (int n = 0; n < N; ++n) {
+              if (n >= RU) break;
+              l[n] *= fac[n];
             }
+          }
+        }
+        // P = 2^(x - m); a masked key's x is -inf, also where the reference is
+#pragma unroll
+        for (int n = 0; n < N; n += 4) {
+          if (n >= RU) break;
+          const float4 m4 = *reinterpret_cast<const float4*>(mref + n);
+          const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float pv = x[n + i] == -INFINITY ? 0.f : ex2(x[n + i] - m[i]);
+            l[n + i] += pv;
+            *reinterpret_cast<__half*>(pdst + (n + i) * 128 + ((pchunk ^ ((n + i) & 7)) << 4)) = __float2half_rn(pv);
           }
         }
         fence_proxy_async_smem();
-        tc_fence_before();
-        mbar_arrive_warp(&s_free[sb]);
         mbar_arrive_warp(&p_full[team]);
       }
       if (stop) break;
       // ---------------------------------------------------------- end of a run
       // sums over the 128 key lanes
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        float t = l[n];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (lane == (n & 31)) wmax[sw * N + n] = t;
-      }
+      wmax[sw * N + (NC == 1 ? lane >> 1 : lane)] = reduce_rows<N, false>(l, lane);
       vote_or(bar, 128, false);
       const int len = sg.k1 - sg.k0, g0 = g - len;
       // a team without a tile of the run has no O^T and no references
       const bool has0 = len > 1 || !(g0 & 1), has1 = len > 1 || (g0 & 1), mine = team ? has1 : has0;
       if (sw == 0) {
-        if (lane < N)
+        if (lane < RU)
           ml[(par * 2 + team) * N + lane] =
               mine ? make_float2(mref[lane], wmax[lane] + wmax[N + lane] + wmax[2 * N + lane] + wmax[3 * N + lane])
                    : make_float2(-INFINITY, 0.f);
@@ -511,62 +535,50 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       tc_fence_after();
       const bool whole = sg.k0 == 0 && sg.k1 == sg.nk, tree = sg.k1 > jm;
       const uint32_t unused = tree ? unused_s[par] : 0u;
-      float* wf = wf_all + (warp - 4) * 2 * N;
-      int* off = off_all + (warp - 4) * N;
-      if (lane < N) {
+      // lane n: the factors of row n's two O^T columns, and where the row goes
+      float f0 = 0.f, f1 = 0.f;
+      int at = 0;
+      if (lane < R) {
         const float2 a = ml[par * 2 * N + lane], b = ml[(par * 2 + 1) * N + lane];
         const float M = fmaxf(a.x, b.x);
         const float w0 = a.x == M ? 1.f : ex2(a.x - M), w1 = b.x == M ? 1.f : ex2(b.x - M);
         const float L = a.y * w0 + b.y * w1;
         // a whole item is divided by its sum (a row without a key is zero)
         const float inv = !whole ? 1.f : L > 0.f ? 1.f / L : L;
-        wf[lane] = w0 * inv;
-        wf[N + lane] = w1 * inv;
+        f0 = w0 * inv;
+        f1 = w1 * inv;
         const int node = lane / p.G, h = sg.hk * p.G + lane - node * p.G;
-        const int piece = (2 * blockIdx.x + (fresh ? 0 : 1)) * p.ws_rows + lane;
-        off[lane] = whole ? (sg.b * p.N + node) * p.H + h : piece;   // B N H fits 31 bits
-        if (warp == 4 && !whole && lane < R && in_bounds(p.split && lane < p.ws_rows, p.status, kSiteTreeWs))
+        const int piece = (2 * (int)blockIdx.x + (fresh ? 0 : 1)) * p.ws_rows + lane;
+        at = whole ? (sg.b * p.N + node) * p.H + h : piece;   // B N H fits 31 bits
+        if (warp == 4 && !whole && in_bounds(p.split && lane < p.ws_rows, p.status, kSiteTreeWs))
           p.ws_ml[piece] = make_float2(M, (unused >> lane) & 1u ? -1.f : L);
       }
-      __syncwarp();
-      // each team takes half of the rows; lane = d
+      const bool anynf = __any_sync(0xffffffffu, tree && noted[par * 32 + lane] != 0u);
+      // lane = d; the teams take groups of four rows in turn
       const int d = Q8 ? (key & ~31) + q8_code_at((key >> 5) & 1, key & 31) : key;
-      uint32_t v0[8 * NC], v1[8 * NC];
-      const int nb = 8 * NC * team;
+#pragma unroll 1
+      for (int n0 = 4 * team; n0 < R; n0 += 8) {
+        uint32_t v0[4], v1[4];
+        tmem_ld4(tmem + lanes + Cfg::kOCol + n0, v0);
+        tmem_ld4(tmem + lanes + Cfg::kOCol + N + n0, v1);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        tmem_ld8(tmem + lanes + Cfg::kOCol + nb + 8 * c, v0 + 8 * c);
-        tmem_ld8(tmem + lanes + Cfg::kOCol + N + nb + 8 * c, v1 + 8 * c);
-      }
-      if (key < D) {
-#pragma unroll
-        for (int e = 0; e < 8 * NC; ++e) {
-          const int n = nb + e;
-          if (n < R) {
-            const float o = (has0 ? __uint_as_float(v0[e]) * wf[n] : 0.f) + (has1 ? __uint_as_float(v1[e]) * wf[N + n] : 0.f);
-            if (whole) {
-              if (in_bounds(n / p.G < p.N, p.status, kSiteTreeO))
-                p.o[(long long)off[n] * D + d] = __float2half_rn((unused >> n) & 1u ? 0.f : o);
-            } else if (in_bounds(p.split && n < p.ws_rows, p.status, kSiteTreeWs)) {
-              p.ws_o[(long long)off[n] * D + d] = o;
-            }
+        for (int e = 0; e < 4; ++e) {
+          const int n = n0 + e;
+          const float a = __shfl_sync(0xffffffffu, f0, n & 31), b = __shfl_sync(0xffffffffu, f1, n & 31);
+          const int row = __shfl_sync(0xffffffffu, at, n & 31);
+          float o = (has0 ? __uint_as_float(v0[e]) * a : 0.f) + (has1 ? __uint_as_float(v1[e]) * b : 0.f);
+          if (n >= R || key >= D) continue;
+          if (anynf) o += few_nonfinite<D, Q8>(p, sg, noted + par * 32, anc[n], d);
+          if ((unused >> n) & 1u) o = 0.f;
+          const long long i = (long long)row * D + d;
+          if (whole) {
+            if (in_bounds(row < p.B * p.N * p.H, p.status, kSiteTreeO)) p.o[i] = __float2half_rn(o);
+          } else if (in_bounds(p.split && row < 2 * (int)gridDim.x * p.ws_rows, p.status, kSiteTreeWs)) {
+            p.ws_o[i] = o;
           }
         }
+        __syncwarp();
       }
-      uint32_t some = 0;
-      if (tree) some = noted[par * 32 + lane];
-      if (__any_sync(0xffffffffu, some != 0u) && key < D) {
-        // non-finite values of cleared V rows, added for the rows that see them
-        for (int e = 0; e < 8 * NC; ++e) {
-          const int n = nb + e;
-          if (n >= R || ((unused >> n) & 1u)) continue;
-          const float z = few_nonfinite<D, Q8>(p, sg, noted + par * 32, anc[n], d);
-          if (z == 0.f) continue;
-          if (whole) p.o[(long long)off[n] * D + d] = __float2half_rn(__half2float(p.o[(long long)off[n] * D + d]) + z);
-          else p.ws_o[(long long)off[n] * D + d] += z;
-        }
-      }
-      __syncwarp();
       fresh = false;
       tc_fence_before();
       mbar_arrive_warp(o_free);
@@ -575,19 +587,26 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
     // ------------------------------------------------------------ Q, decode, clearing
     const int t = threadIdx.x - 12 * 32;        // 0 .. 32 PW - 1
     const int pw = warp - 12;
-    const int kv = Q8 ? pw >> 3 : 1;            // Q8_0: this warp decodes K (0) or V (1) tiles
+    const int kv = Q8 ? pw / PM : 1;            // Q8_0: this warp decodes K (0) or V (1) tiles
+    const bool odd = PM == 8 && ((pw >> 2) & 1);   // of 8 warps, the second four take the odd blocks
     const int R = p.N * p.G;
     const DecK K = make_deck();
     bool ok = true;
     int g = 0;
     uint32_t raw_ph = 0;                        // phase bits of v_raw of each stage
+    Ring<KS> kr;
+    Ring<VS> vr;
+    Ring<RS> rr;
+    if (Q8 && kv) rr.step();
     for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
       const int jm = first_masked(sg);
       ok = __all_sync(0xffffffffu, w == 0 || mbar_wait_idle(q_empty, (w - 1) & 1, run_ctl, 64));
       if (!ok) break;
-      uint32_t* nt = noted + (w & 1) * 32 + (pw & 7) * 4;
-      if (kv == 1 && lane < 4) nt[lane] = 0u;
-      if (!Q8 && lane < 4) nt[16 + lane] = 0u;   // (four warps: the other four's notes stay empty)
+      uint32_t* nt = noted + (w & 1) * 32 + (Q8 ? pw & (PM - 1) : pw) * 4;
+      if (kv == 1 && lane < 4) {
+        nt[lane] = 0u;
+        if (!Q8 || PM == 4) nt[16 + lane] = 0u;   // (four warps: the other four's notes stay empty)
+      }
       __syncwarp();
       // Q rows (Q8_0: in the decoded blocks' order), a block of 32 values a thread
       for (int u = t; u < N * (D / 32); u += 32 * PW) {
@@ -613,46 +632,68 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full);
       const long long head = (long long)sg.b * p.Hkv + sg.hk;
-      for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g) {
-        const int ks = g % KS, vs = g % VS;
+      for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g, kr.step(), vr.step()) {
+        const int ks = kr.at, vs = vr.at;
         if constexpr (Q8) {
           const int sh = (int)(((head * p.C + (long long)j * kTile) * Cfg::kRow) & 15);
-          const int rn = 2 * g + kv, rs = rn % RS, ns = kv ? VS : KS;
-          bool go = mbar_wait(&r_full[rs], (rn / RS) & 1, ctl);
-          if (g >= ns) go = go && mbar_wait(kv ? &v_empty[vs] : &k_empty[ks], ((g / ns) - 1) & 1, ctl);
+          const int rs = rr.at;
+          bool go = mbar_wait(&r_full[rs], rr.ph, ctl);
+          if (kv == 0 ? g >= KS : g >= VS) go = go && mbar_wait(kv ? &v_empty[vs] : &k_empty[ks], (kv ? vr.ph : kr.ph) ^ 1u, ctl);
           ok = __all_sync(0xffffffffu, go);
           if (!ok) break;
-          uint8_t* dst = kv ? vst + vs * Cfg::kTileBytes : kst + ks * Cfg::kTileBytes;
+          const uint8_t* src = raws + rs * Cfg::kRaw + sh;
           const int row = t & 127;
-          const bool clean = kv && j >= jm;
-          bool any = false;
-#pragma unroll
-          for (int u = 0; u < D / 64; ++u) {
-            const int blk = 2 * u + ((t >> 7) & 1);
+          if (kv == 0) {
+            // K: to the lanes and columns of its TMEM stage (warp % 4 = 32-row group)
+            tc_fence_after();
+            const uint32_t kcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + Cfg::kKCol + ks * (D / 2);
             uint32_t v[16];
-            decode_block<D>(raws + rs * Cfg::kRaw + sh, row, blk, K, v);
-            if (clean) {
-#pragma unroll
-              for (int q = 0; q < 16; ++q) any |= clear_nonfinite(v[q]);
+            if (!odd) {
+              decode_block<D, 0>(src, row, K, v);
+              tmem_st16(kcol, v);
+              if constexpr (D == 128) {
+                decode_block<D, 2>(src, row, K, v);
+                tmem_st16(kcol + 32, v);
+              }
             }
-            uint8_t* base = dst + (blk >> 1) * (kTile * 128) + row * 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(base + (((4 * (blk & 1) + i) ^ (row & 7)) << 4)) =
-                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (odd || PM == 4) {
+              decode_block<D, 1>(src, row, K, v);
+              tmem_st16(kcol + 16, v);
+              if constexpr (D == 128) {
+                decode_block<D, 3>(src, row, K, v);
+                tmem_st16(kcol + 48, v);
+              }
+            }
+            mbar_arrive_warp(&r_empty[rs]);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive_warp(&k_full[ks]);
+          } else {
+            uint8_t* dst = vst + vs * Cfg::kTileBytes;
+            if (!odd) {
+              decode_to_tile<D, 0>(dst, src, row, K);
+              if constexpr (D == 128) decode_to_tile<D, 2>(dst, src, row, K);
+            }
+            if (odd || PM == 4) {
+              decode_to_tile<D, 1>(dst, src, row, K);
+              if constexpr (D == 128) decode_to_tile<D, 3>(dst, src, row, K);
+            }
+            if (j >= jm) {   // this thread's blocks
+              const bool any = PM == 4 ? clean_chunks(dst, row, 0, D / 8, 0) : clean_chunks(dst, row, odd ? 4 : 0, D / 16, 4);
+              const uint32_t bits = __ballot_sync(0xffffffffu, any);
+              if (lane == 0) nt[j - jm] = bits;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive_warp(&v_full[vs]);
+            mbar_arrive_warp(&r_empty[rs]);
           }
-          if (clean) {
-            const uint32_t bits = __ballot_sync(0xffffffffu, any);
-            if (lane == 0) nt[j - jm] = bits;
-          }
-          fence_proxy_async_smem();
-          mbar_arrive_warp(kv ? &v_full[vs] : &k_full[ks]);
-          mbar_arrive_warp(&r_empty[rs]);
+          rr.step();   // K and V tiles alternate in the raw ring
+          rr.step();
         } else if (j >= jm) {
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
           if (!ok) break;
           raw_ph ^= 1u << vs;
-          const uint32_t bits = clean_tile<D, 32 * PW>(vst + vs * Cfg::kTileBytes, t);
+          const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t, 0, D / 8, 0));
           if (lane == 0) nt[j - jm] = bits;
           fence_proxy_async_smem();
           mbar_arrive_warp(&v_clean[vs]);

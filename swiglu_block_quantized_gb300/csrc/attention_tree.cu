@@ -83,24 +83,18 @@ struct TreeCfg {
 // Non-finite values of the V rows that were cleared and that this row sees,
 // added to its columns c0 .. c0 + 15 (Q8_0: positions of a decoded row).
 template <int D, bool Q8>
-__device__ __noinline__ void add_nonfinite(const TreeParams& p, const Seg& g, const uint32_t* noted,
+__device__ __noinline__ void add_nonfinite(const TreeParams& p, Seg g, const uint32_t* noted,
                                            const uint32_t* anc, int c0, float (&x)[16]) {
   const int jm = first_masked(g);
+#pragma unroll 1
   for (int mt = 0; mt < 4; ++mt) {
     const int j = jm + mt;
     if (j < g.k0 || j >= g.k1) continue;
+#pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       const int kq = j * kTile + 32 * q;
-      uint32_t bits = (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32<8>(anc, 256, kq, g.past, p.C);
-      while (bits) {
-        const int key = kq + __ffs(bits) - 1;
-        bits &= bits - 1;
-        for (int c = 0; c < 16; ++c) {
-          const int at = c0 + c;
-          const float v = value_at<D, Q8>(p, g, key, Q8 ? (at & ~31) + q8_code_at((at >> 5) & 1, at & 31) : at);
-          if (!(v - v == 0.f)) x[c] += v;
-        }
-      }
+      add_values<D, Q8>(p, g, kq, (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32<8>(anc, 256, kq, g.past, p.C),
+                        c0, x);
     }
   }
 }
@@ -467,37 +461,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 16; ++q)
             x[q] = (has0 ? __uint_as_float(v0[q]) * f0 : 0.f) + (has1 ? __uint_as_float(v1[q]) * f1 : 0.f);
           if (anynf) {
-            if (valid && used) add_nonfinite<D, Q8>(p, sg, nt, anc, col, x);
+            if (valid && used) {   // (a copy: an array whose address is taken lives in memory)
+              float y[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) y[q] = x[q];
+              add_nonfinite<D, Q8>(p, sg, nt, anc, col, y);
+#pragma unroll
+              for (int q = 0; q < 16; ++q) x[q] = y[q];
+            }
             __syncwarp();
           }
           if (store && ws_ok) {
-            if constexpr (Q8) {
-              // decoded order: positions 4 i, 4 i + 2 and 4 i + 1, 4 i + 3 hold neighbours
-              const int odd = (col >> 5) & 1, pos0 = col & 31, at = col & ~31;
+            if (!used) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float a0 = used ? x[4 * i + k] : 0.f, a1 = used ? x[4 * i + k + 2] : 0.f;
-                  const int i4 = pos0 + 4 * i;
-                  const int e = odd ? i4 + 2 * k : i4 > 0 ? i4 - 2 + 2 * k : 30 * k;
-                  if (whole) *reinterpret_cast<__half2*>(orow + at + e) = __floats2half2_rn(a0, a1);
-                  else *reinterpret_cast<float2*>(p.ws_o + slot * D + at + e) = make_float2(a0, a1);
-                }
-            } else if (whole) {
-              uint32_t hv[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const __half2 hh = __floats2half2_rn(x[2 * q], x[2 * q + 1]);
-                hv[q] = used ? *reinterpret_cast<const uint32_t*>(&hh) : 0u;
-              }
-              *reinterpret_cast<uint4*>(orow + col) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-              *reinterpret_cast<uint4*>(orow + col + 8) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.ws_o + slot * D + col);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+              for (int q = 0; q < 16; ++q) x[q] = 0.f;
             }
+            store_columns<D, Q8>(x, col, whole, orow, p.ws_o + slot * D);
           }
         }
         // the piece that holds the tree tells of an unused node by a sum of -1
@@ -563,26 +542,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, go);
             if (!ok) break;
             uint8_t* dst = kv ? vst + vs * Cfg::kTileBytes : kst + ks * Cfg::kTileBytes;
-            const bool clean = kv && j >= jm;
             const int row = t & 127;
-            bool any = false;
-#pragma unroll
-            for (int u = 0; u < D / 64; ++u) {
-              const int blk = 2 * u + (t >> 7);
-              uint32_t v[16];
-              decode_block<D>(raws + rs * Cfg::kRaw + sh, row, blk, K, v);
-              if (clean) {
-#pragma unroll
-                for (int q = 0; q < 16; ++q) any |= clear_nonfinite(v[q]);
-              }
-              uint8_t* base = dst + (blk >> 1) * (kTile * 128) + row * 128;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(base + (((4 * (blk & 1) + i) ^ (row & 7)) << 4)) =
-                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            const uint8_t* src = raws + rs * Cfg::kRaw + sh;
+            if (t < 128) {
+              decode_to_tile<D, 0>(dst, src, row, K);
+              if constexpr (D == 128) decode_to_tile<D, 2>(dst, src, row, K);
+            } else {
+              decode_to_tile<D, 1>(dst, src, row, K);
+              if constexpr (D == 128) decode_to_tile<D, 3>(dst, src, row, K);
             }
-            if (clean) {
-              const uint32_t bits = __ballot_sync(0xffffffffu, any);
+            if (kv && j >= jm) {   // this thread's blocks
+              const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(dst, row, 4 * (t >> 7), D / 16, 4));
               if (lane == 0) nt[j - jm] = bits;
             }
             fence_proxy_async_smem();
@@ -593,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
           if (!ok) break;
           raw_ph ^= 1u << vs;
-          const uint32_t bits = clean_tile<D, 256>(vst + vs * Cfg::kTileBytes, t);
+          const uint32_t bits =
+              __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t & 127, (t >> 7) * (D / 16), D / 16, 0));
           if (lane == 0) nt[j - jm] = bits;
           fence_proxy_async_smem();
           mbar_arrive_warp(&v_clean[vs]);
@@ -627,19 +598,20 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
   __shared__ float red_l[8];
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = warp % W;
-  const int blocks = (p.ws_rows + kRows - 1) / kRows;
-  const long long item = blockIdx.x / blocks;
-  const int r = (int)(blockIdx.x % blocks) * kRows + warp / W;
-  const long long hr = (long long)p.Hkv * p.rtiles;
-  const int b = (int)(item / hr);
-  const int hk = (int)(item % hr / p.rtiles), row = (int)(item % p.rtiles) * kTile + r;
+  const unsigned blocks = (p.ws_rows + kRows - 1) / kRows;
+  const unsigned item = blockIdx.x / blocks;
+  const int r = (int)(blockIdx.x - item * blocks) * kRows + warp / W;
+  const unsigned hr = (unsigned)p.Hkv * p.rtiles;
+  const int b = (int)(item / hr), sub = (int)(item - b * hr);
+  const int hk = sub / p.rtiles, row = (sub - hk * p.rtiles) * kTile + r;
   // the sequences' tiles, as tree_schedule counts them
   __shared__ int sums[3];
   if (warp == 0) {
     int before = 0, all = 0, mine = 0;
+#pragma unroll 1
     for (int i = lane; i < p.B; i += 32) {
       const int past = min(max(__ldg(p.past + i), 0), p.C);
-      const int n = (int)((min((long long)past + p.N, (long long)p.C) + kTile - 1) / kTile);
+      const int n = tiles_of(p, past);
       all += n;
       before += i < b ? n : 0;
       mine += i == b ? n : 0;
@@ -653,11 +625,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
     if (lane == 0) sums[0] = before, sums[1] = mine, sums[2] = all;
   }
   __syncthreads();
-  const int nk = sums[1];
-  const long long units = hr * sums[2];
+  const unsigned nk = sums[1], units = hr * sums[2];
   const Deal dl = deal(units, tree_shares(p, units, grid));
-  const long long u0 = hr * sums[0] + (item % hr) * nk, u1 = u0 + nk;
-  const int c0 = deal_owner(dl, u0), c1 = deal_owner(dl, u1 - 1);
+  const unsigned u0 = hr * sums[0] + sub * nk;
+  const int c0 = deal_owner(dl, u0), c1 = deal_owner(dl, u0 + nk - 1);
   if (c0 == c1) return;              // not cut: its CTA wrote the output
   const bool live = r < p.ws_rows && row < p.N * p.G;
   const bool at_start = deal_start(dl, c0) == u0;   // the first piece is its CTA's first run
@@ -668,6 +639,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   if (live && in_bounds(c0 >= 0 && c1 < grid && c0 <= c1, p.status, kSiteTreeWs)) {
+#pragma unroll 1
     for (int c = c0 + lane; c <= c1; c += 32) {
       const float2 v = p.ws_ml[slot(c)];
       M = fmaxf(M, v.x);

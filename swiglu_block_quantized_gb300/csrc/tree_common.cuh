@@ -33,45 +33,44 @@ struct TreeSched {
   int left;          // units (or, without a split, items) of this CTA
 };
 
-// n units over g shares: share c starts at c base + min(c, rem).
+// n units over g shares: share c starts at c base + min(c, rem).  Unit counts fit
+// 31 bits (the host sees to it): a 64-bit division is a thousand bytes of code and
+// some hundred clocks, in a kernel whose short calls are bound by both.
 struct Deal {
-  long long base, rem;
+  unsigned base, rem;
 };
-__device__ __forceinline__ Deal deal(long long n, int g) {
+__device__ __forceinline__ Deal deal(unsigned n, unsigned g) {
   Deal d;
-  if (n < (1ll << 31)) {   // 32-bit division: the 64-bit one costs a few hundred clocks
-    d.base = (unsigned)n / (unsigned)g;
-    d.rem = (unsigned)n % (unsigned)g;
-  } else {
-    d.base = n / g;
-    d.rem = n % g;
-  }
+  d.base = n / g;
+  d.rem = n - d.base * g;
   return d;
 }
-__device__ __forceinline__ long long deal_start(const Deal& d, long long c) { return c * d.base + min(c, d.rem); }
+__device__ __forceinline__ unsigned deal_start(const Deal& d, unsigned c) { return c * d.base + min(c, d.rem); }
 // The share that holds unit u.
-__device__ __forceinline__ int deal_owner(const Deal& d, long long u) {
-  const long long cut = d.rem * (d.base + 1);
-  if (u < cut) return (int)(cut < (1ll << 31) ? (unsigned)u / (unsigned)(d.base + 1) : u / (d.base + 1));
-  const long long v = u - cut;
-  return (int)(d.rem + (v < (1ll << 31) && d.base < (1ll << 31) ? (unsigned)v / (unsigned)d.base : v / d.base));
+__device__ __forceinline__ int deal_owner(const Deal& d, unsigned u) {
+  const unsigned cut = d.rem * (d.base + 1);
+  return (int)(u < cut ? u / (d.base + 1) : d.rem + (u - cut) / d.base);
 }
 // CTAs that take part: as many as have `least` tiles each.
-__device__ __forceinline__ int tree_shares(const TreeParams& p, long long units, int grid) {
-  return (int)min((long long)grid, max(1ll, units < (1ll << 31) ? (long long)((unsigned)units / (unsigned)p.least)
-                                                                : units / p.least));
+__device__ __forceinline__ unsigned tree_shares(const TreeParams& p, unsigned units, unsigned grid) {
+  return min(grid, max(1u, units / (unsigned)p.least));
+}
+// Tiles of a sequence.
+__device__ __forceinline__ int tiles_of(const TreeParams& p, int past) {
+  return (int)((unsigned)(min(past, p.C - p.N) + p.N + kTile - 1) / kTile);
 }
 
 // Filled by one warp; the CTA synchronises before anyone reads.
 __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s, int lane) {
   int sum = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
     int n = 0;
     if (b < p.B) {
       const int past = min(max(__ldg(p.past + b), 0), p.C);
       s->past[b] = past;
-      n = (int)((min((long long)past + p.N, (long long)p.C) + kTile - 1) / kTile);
+      n = tiles_of(p, past);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -83,32 +82,34 @@ __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s,
   }
   if (lane == 0) s->pre[0] = 0;
   __syncwarp();
-  const int hr = p.Hkv * p.rtiles;
-  const long long n = p.split ? (long long)hr * sum : (long long)hr * p.B;
-  const int shares = p.split ? tree_shares(p, n, (int)gridDim.x) : (int)gridDim.x;
+  const unsigned hr = (unsigned)p.Hkv * p.rtiles;
+  const unsigned n = p.split ? hr * sum : hr * p.B;
+  const unsigned shares = p.split ? tree_shares(p, n, gridDim.x) : gridDim.x;
   const Deal d = deal(n, shares);
-  const long long c = blockIdx.x;
-  const long long at = c < shares ? deal_start(d, c) : n, end = c < shares ? deal_start(d, c + 1) : n;
+  const unsigned c = blockIdx.x;
+  const unsigned at = c < shares ? deal_start(d, c) : n, end = c < shares ? deal_start(d, c + 1) : n;
+  unsigned b = 0, each = 1, rem = at;
   if (p.split) {
     // last sequence whose units start at or before `at`
-    int b = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const bool le = b0 + lane < p.B && (long long)hr * s->pre[b0 + lane] <= at;
+      const bool le = b0 + lane < p.B && hr * s->pre[b0 + lane] <= at;
       b += __popc(__ballot_sync(0xffffffffu, le));
     }
-    b = max(b - 1, 0);
-    const int nk = s->pre[b + 1] - s->pre[b];
-    const long long rem = at - (long long)hr * s->pre[b];
-    if (lane == 0) {
-      s->b = b;
-      s->item = rem < (1ll << 31) ? (int)((unsigned)rem / (unsigned)nk) : (int)(rem / nk);
-      s->k = (int)(rem - (long long)s->item * nk);
-      s->left = (int)(end - at);
-    }
-  } else if (lane == 0) {
-    s->b = (int)(at / hr);
-    s->item = (int)(at % hr);
-    s->k = 0;
+    b = max(b, 1u) - 1;
+    each = s->pre[b + 1] - s->pre[b];
+    rem = at - hr * s->pre[b];
+  }
+  unsigned item = rem / each;
+  const unsigned k = rem - item * each;
+  if (!p.split) {
+    b = item / hr;
+    item -= b * hr;
+  }
+  if (lane == 0) {
+    s->b = (int)b;
+    s->item = (int)item;
+    s->k = (int)k;
     s->left = (int)(end - at);
   }
 }
@@ -189,17 +190,15 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
   return lo || hi;
 }
 
-// Clear an fp16 tile that has landed (D / 64 panels of [128 keys][128 B],
-// swizzled): thread t of T takes row t % 128 and D / 8 / (T / 128) of its
-// 16-byte chunks.  Returns the warp's 32 rows that held non-finite values.
-template <int D, int T>
-__device__ __forceinline__ uint32_t clean_tile(uint8_t* tile, int t) {
-  constexpr int kEach = D / 8 / (T / 128);
-  const int row = t & 127, h = t >> 7;
+// Clear `count` 16-byte chunks of row `row` of an fp16 tile (D / 64 panels of
+// [128 keys][128 B], swizzled), from chunk `first`, skipping `skip` after every
+// four.  True if there were non-finite values.  (Only for tiles with masks: kept
+// short, out of the way of the decode.)
+static __device__ __noinline__ bool clean_chunks(uint8_t* tile, int row, int first, int count, int skip) {
   bool any = false;
-#pragma unroll 4
-  for (int c = 0; c < kEach; ++c) {
-    const int ch = h * kEach + c;
+#pragma unroll 1
+  for (int c = 0; c < count; ++c) {
+    const int ch = first + c + (c >> 2) * skip;
     uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
     uint4 v = *at;
     bool bad = clear_nonfinite(v.x);
@@ -209,7 +208,7 @@ __device__ __forceinline__ uint32_t clean_tile(uint8_t* tile, int t) {
     if (bad) *at = v;
     any |= bad;
   }
-  return __ballot_sync(0xffffffffu, any);
+  return any;
 }
 
 // Value c of a V row in global memory.
@@ -241,17 +240,66 @@ __host__ __device__ constexpr int q8_code_at(int odd, int pos) {
   return odd ? 4 * i + byte : i > 0 ? 4 * i - 2 + byte : byte < 2 ? byte : 28 + byte;
 }
 
-// Block `blk` of row `row` of a raw tile (rows of D / 32 blocks) as 16 fp16
-// pairs in that order, each value RNE(q d).  Rows of 136 bytes are read as
-// 8-byte words (34 words apart: a half-warp's 16 rows cover every bank once),
-// rows of 68 bytes as 4-byte words (17 apart).
-template <int D>
-__device__ __forceinline__ void decode_block(const uint8_t* raw, int row, int blk, const DecK& K, uint32_t (&v)[16]) {
-  constexpr int RB = D / 32 * 34;
-  const int off = row * RB + 34 * blk;
+// Non-finite values of the V rows kq + i, i in `bits`, added to columns c0 ..
+// c0 + 15 (positions of a decoded row).
+template <int D, bool Q8>
+__device__ __forceinline__ void add_values(const TreeParams& p, const Seg& g, int kq, uint32_t bits, int c0,
+                                           float (&x)[16]) {
+  while (bits) {
+    const int key = kq + __ffs(bits) - 1;
+    bits &= bits - 1;
+#pragma unroll 1
+    for (int c = 0; c < 16; ++c) {
+      const int at = c0 + c;
+      const float v = value_at<D, Q8>(p, g, key, Q8 ? (at & ~31) + q8_code_at((at >> 5) & 1, at & 31) : at);
+      if (!(v - v == 0.f)) x[c] += v;
+    }
+  }
+}
+
+// Columns col .. col + 15 (positions) of a row, to fp16 output or fp32 piece.
+template <int D, bool Q8>
+__device__ __forceinline__ void store_columns(const float (&x)[16], int col, bool whole, __half* orow, float* wrow) {
+  if constexpr (Q8) {
+    // decoded order: positions 4 i, 4 i + 2 and 4 i + 1, 4 i + 3 hold neighbours
+    const int odd = (col >> 5) & 1, pos0 = col & 31, at = col & ~31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float a = x[4 * i + k], b = x[4 * i + k + 2];
+        const int i4 = pos0 + 4 * i;
+        const int e = odd ? i4 + 2 * k : i4 > 0 ? i4 - 2 + 2 * k : 30 * k;
+        if (whole) *reinterpret_cast<__half2*>(orow + at + e) = __floats2half2_rn(a, b);
+        else *reinterpret_cast<float2*>(wrow + at + e) = make_float2(a, b);
+      }
+  } else if (whole) {
+    uint32_t h[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const __half2 hh = __floats2half2_rn(x[2 * q], x[2 * q + 1]);
+      h[q] = *reinterpret_cast<const uint32_t*>(&hh);
+    }
+    *reinterpret_cast<uint4*>(orow + col) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(orow + col + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+  } else {
+    float4* dst = reinterpret_cast<float4*>(wrow + col);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+  }
+}
+
+// Block BLK of row `row` of a raw tile (rows of D / 32 blocks) as 16 fp16 pairs
+// in that order, each value RNE(q d).  Rows of 136 bytes are read as 8-byte
+// words (34 words apart: a half-warp's 16 rows cover every bank once), rows of
+// 68 bytes as 4-byte words (17 apart).  The block is a template argument: with a
+// runtime one the two word orders become selects, half as many instructions again.
+template <int D, int BLK>
+__device__ __forceinline__ void decode_block(const uint8_t* raw, int row, const DecK& K, uint32_t (&v)[16]) {
+  constexpr int RB = D / 32 * 34, kWord = (34 * BLK) & ~3;   // the block's first word
   uint32_t w[9];   // the words that hold the block
   if constexpr (RB % 8 == 0) {
-    const uint2* src = reinterpret_cast<const uint2*>(raw + (off & ~7));
+    const uint2* src = reinterpret_cast<const uint2*>(raw + row * RB + (kWord & ~7));
     uint32_t a[10];
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
@@ -259,29 +307,30 @@ __device__ __forceinline__ void decode_block(const uint8_t* raw, int row, int bl
       a[2 * i] = x.x;
       a[2 * i + 1] = x.y;
     }
-    if (blk & 2) {
 #pragma unroll
-      for (int i = 0; i < 9; ++i) w[i] = a[i + 1];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 9; ++i) w[i] = a[i];
-    }
+    for (int i = 0; i < 9; ++i) w[i] = a[i + ((kWord >> 2) & 1)];
   } else {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(raw + (off & ~3));
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(raw + row * RB + kWord);
 #pragma unroll
     for (int i = 0; i < 9; ++i) w[i] = src[i];
   }
-  uint32_t d2;
-  if (blk & 1) {
-    d2 = __byte_perm(w[0], 0u, 0x3232);
+  const uint32_t d2 = __byte_perm(w[0], 0u, BLK & 1 ? 0x3232 : 0x1010);
+  if constexpr (BLK % 2 == 0) w[0] = __byte_perm(w[0], w[8], 0x5432);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = w[i + 1];
-  } else {
-    d2 = __byte_perm(w[0], 0u, 0x1010);
-    w[0] = __byte_perm(w[0], w[8], 0x5432);
-  }
+  for (int i = 0; i < 8; ++i) q8_word(w[i + (BLK & 1)], d2, K, v[2 * i], v[2 * i + 1]);
+}
+
+// Block BLK decoded and written to the swizzled fp16 tile (D / 64 panels of
+// [128][128 B]).
+template <int D, int BLK>
+__device__ __forceinline__ void decode_to_tile(uint8_t* dst, const uint8_t* raw, int row, const DecK& K) {
+  uint32_t v[16];
+  decode_block<D, BLK>(raw, row, K, v);
+  uint8_t* base = dst + (BLK >> 1) * (kTile * 128) + row * 128;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q8_word(w[i], d2, K, v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(base + (((4 * (BLK & 1) + i) ^ (row & 7)) << 4)) =
+        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
 // 32 fp16 values of a Q row's block to the order of decode_block.
@@ -300,6 +349,19 @@ __device__ __forceinline__ void order_block(const uint4 (&q)[4], int odd, uint4 
 #pragma unroll
   for (int i = 0; i < 4; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
 }
+
+// A place in a ring of N stages and the parity of its pass.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++at == N) {
+      at = 0;
+      ph ^= 1u;
+    }
+  }
+};
 
 // 1-D bulk copy; addresses and size multiples of 16 bytes.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

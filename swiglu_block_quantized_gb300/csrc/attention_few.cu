@@ -31,7 +31,7 @@
 //
 // Warps: 0 issues the S MMAs (four TMEM buffers ahead), 1 the P V MMAs, 2 and 3
 // the copies, 4-11 are the softmax teams (lane = key), the others prepare (Q, the
-// clearing of non-finite V; Q8_0: eight decode K tiles and eight V tiles), as in
+// clearing of non-finite V; Q8_0: groups of four decode K or V tiles), as in
 // attention_tree.cu, whose notes on masks, schedule and pieces hold here.
 #include <algorithm>
 
@@ -52,7 +52,8 @@ struct FewCfg {
   static constexpr int kVS = D == 128 ? 3 : 6;
   static constexpr int kRaw = kTile * kRow + 32;       // a raw tile, its 16-byte shift, and the decode's overread
   static constexpr int kRS = Q8 ? (D == 64 ? 10 : NC == 1 ? 6 : 5) : 0;
-  static constexpr int kPrep = Q8 ? (NC == 1 ? 16 : 8) : 4;   // preparing warps: Q8_0: half for K tiles, half for V tiles
+  static constexpr int kGroups = Q8 && NC == 1 ? 2 : 1;  // Q8_0: groups of 4 warps that take K (and V) tiles in turn
+  static constexpr int kPrep = Q8 ? 8 * kGroups : 4;   // preparing warps
   static constexpr int kThreads = 32 * (12 + kPrep);
   static constexpr int kBars = 2 * kKS + 4 * kVS + 2 * kRS + 8 + 4 + 7;
   static constexpr int kFixed = (int)sizeof(TreeSched) + 2 * 8 * 16   // schedule, noted rows
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
                const TreeParams p) {
   using Cfg = FewCfg<D, Q8, NC>;
   constexpr int N = Cfg::N, KS = Cfg::kKS, VS = Cfg::kVS, RS = Cfg::kRS > 0 ? Cfg::kRS : 1;
-  constexpr int PW = Cfg::kPrep, PM = PW / 2;   // warps that decode one tile (Q8_0)
+  constexpr int PW = Cfg::kPrep, PG = Cfg::kGroups;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_align<1024>(smem_raw);
   uint8_t* ps = qs + Cfg::kQBytes;                     // [2] P^T
@@ -188,18 +189,18 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) {
-      mbar_init(&k_full[i], Q8 ? PM : 1);
+      mbar_init(&k_full[i], Q8 ? 4 : 1);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < VS; ++i) {
-      mbar_init(&v_full[i], Q8 ? PM : 1);
+      mbar_init(&v_full[i], Q8 ? 4 : 1);
       mbar_init(&v_raw[i], 1);
       mbar_init(&v_clean[i], PW);
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < Cfg::kRS; ++i) {
       mbar_init(&r_full[i], 1);
-      mbar_init(&r_empty[i], PM);
+      mbar_init(&r_empty[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -587,8 +588,10 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
     // ------------------------------------------------------------ Q, decode, clearing
     const int t = threadIdx.x - 12 * 32;        // 0 .. 32 PW - 1
     const int pw = warp - 12;
-    const int kv = Q8 ? pw / PM : 1;            // Q8_0: this warp decodes K (0) or V (1) tiles
-    const bool odd = PM == 8 && ((pw >> 2) & 1);   // of 8 warps, the second four take the odd blocks
+    // Q8_0: group pw / 4 decodes K (the first PG groups) or V tiles, those with
+    // g % PG = turn: a group's waits and hand-overs, some 800 clocks a tile, pass
+    // while the other works
+    const int kv = Q8 ? pw / (4 * PG) : 1, turn = Q8 ? (pw >> 2) % PG : 0;
     const int R = p.N * p.G;
     const DecK K = make_deck();
     bool ok = true;
@@ -602,10 +605,11 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       const int jm = first_masked(sg);
       ok = __all_sync(0xffffffffu, w == 0 || mbar_wait_idle(q_empty, (w - 1) & 1, run_ctl, 64));
       if (!ok) break;
-      uint32_t* nt = noted + (w & 1) * 32 + (Q8 ? pw & (PM - 1) : pw) * 4;
+      // notes of this warp's 32 rows, by masked tile (the V groups')
+      uint32_t* nt = noted + (w & 1) * 32 + (4 * turn + (pw & 3)) * 4;
       if (kv == 1 && lane < 4) {
         nt[lane] = 0u;
-        if (!Q8 || PM == 4) nt[16 + lane] = 0u;   // (four warps: the other four's notes stay empty)
+        if (PG == 1) nt[16 + lane] = 0u;
       }
       __syncwarp();
       // Q rows (Q8_0: in the decoded blocks' order), a block of 32 values a thread
@@ -635,9 +639,13 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g, kr.step(), vr.step()) {
         const int ks = kr.at, vs = vr.at;
         if constexpr (Q8) {
-          const int sh = (int)(((head * p.C + (long long)j * kTile) * Cfg::kRow) & 15);
           const int rs = rr.at;
-          bool go = mbar_wait(&r_full[rs], rr.ph, ctl);
+          const uint32_t rph = rr.ph;
+          rr.step();   // K and V tiles alternate in the raw ring
+          rr.step();
+          if (PG > 1 && (g & 1) != turn) continue;
+          const int sh = (int)(((head * p.C + (long long)j * kTile) * Cfg::kRow) & 15);
+          bool go = mbar_wait(&r_full[rs], rph, ctl);
           if (kv == 0 ? g >= KS : g >= VS) go = go && mbar_wait(kv ? &v_empty[vs] : &k_empty[ks], (kv ? vr.ph : kr.ph) ^ 1u, ctl);
           ok = __all_sync(0xffffffffu, go);
           if (!ok) break;
@@ -648,21 +656,15 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
             tc_fence_after();
             const uint32_t kcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + Cfg::kKCol + ks * (D / 2);
             uint32_t v[16];
-            if (!odd) {
-              decode_block<D, 0>(src, row, K, v);
-              tmem_st16(kcol, v);
-              if constexpr (D == 128) {
-                decode_block<D, 2>(src, row, K, v);
-                tmem_st16(kcol + 32, v);
-              }
-            }
-            if (odd || PM == 4) {
-              decode_block<D, 1>(src, row, K, v);
-              tmem_st16(kcol + 16, v);
-              if constexpr (D == 128) {
-                decode_block<D, 3>(src, row, K, v);
-                tmem_st16(kcol + 48, v);
-              }
+            decode_block<D, 0>(src, row, K, v);
+            tmem_st16(kcol, v);
+            decode_block<D, 1>(src, row, K, v);
+            tmem_st16(kcol + 16, v);
+            if constexpr (D == 128) {
+              decode_block<D, 2>(src, row, K, v);
+              tmem_st16(kcol + 32, v);
+              decode_block<D, 3>(src, row, K, v);
+              tmem_st16(kcol + 48, v);
             }
             mbar_arrive_warp(&r_empty[rs]);
             tmem_wait_st();
@@ -670,25 +672,20 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
             mbar_arrive_warp(&k_full[ks]);
           } else {
             uint8_t* dst = vst + vs * Cfg::kTileBytes;
-            if (!odd) {
-              decode_to_tile<D, 0>(dst, src, row, K);
-              if constexpr (D == 128) decode_to_tile<D, 2>(dst, src, row, K);
+            decode_to_tile<D, 0>(dst, src, row, K);
+            decode_to_tile<D, 1>(dst, src, row, K);
+            if constexpr (D == 128) {
+              decode_to_tile<D, 2>(dst, src, row, K);
+              decode_to_tile<D, 3>(dst, src, row, K);
             }
-            if (odd || PM == 4) {
-              decode_to_tile<D, 1>(dst, src, row, K);
-              if constexpr (D == 128) decode_to_tile<D, 3>(dst, src, row, K);
-            }
-            if (j >= jm) {   // this thread's blocks
-              const bool any = PM == 4 ? clean_chunks(dst, row, 0, D / 8, 0) : clean_chunks(dst, row, odd ? 4 : 0, D / 16, 4);
-              const uint32_t bits = __ballot_sync(0xffffffffu, any);
+            if (j >= jm) {
+              const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(dst, row, 0, D / 8, 0));
               if (lane == 0) nt[j - jm] = bits;
             }
             fence_proxy_async_smem();
             mbar_arrive_warp(&v_full[vs]);
             mbar_arrive_warp(&r_empty[rs]);
           }
-          rr.step();   // K and V tiles alternate in the raw ring
-          rr.step();
         } else if (j >= jm) {
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
           if (!ok) break;

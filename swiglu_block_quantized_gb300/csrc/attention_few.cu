@@ -49,7 +49,7 @@ struct FewCfg {
   static constexpr int kQBytes = N * D * 2;            // D / 64 panels of [N][128 B]
   static constexpr int kPBytes = N * kTile * 2;        // two panels (64 keys) of [N][128 B]
   static constexpr int kKS = Q8 ? 3 : D == 128 ? 3 : 6;   // K stages (Q8_0: in TMEM)
-  static constexpr int kVS = D == 128 ? 3 : 6;
+  static constexpr int kVS = D == 128 ? 3 : Q8 ? 4 : 6;
   static constexpr int kRaw = kTile * kRow + 32;       // a raw tile, its 16-byte shift, and the decode's overread
   static constexpr int kRS = Q8 ? (D == 64 ? 10 : NC == 1 ? 6 : 5) : 0;
   static constexpr int kGroups = Q8 && NC == 1 ? 2 : 1;  // Q8_0: groups of 4 warps that take K (and V) tiles in turn
@@ -68,6 +68,7 @@ struct FewCfg {
   static constexpr uint32_t kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(kUsed <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(kGroups == 1 || (kRS / 2 >= kKS && kRS / 2 >= kVS), "a raw slot is used again after its stage");
   static_assert(kRaw % 16 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "alignment");
 };
 
@@ -645,8 +646,12 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
           rr.step();
           if (PG > 1 && (g & 1) != turn) continue;
           const int sh = (int)(((head * p.C + (long long)j * kTile) * Cfg::kRow) & 15);
-          bool go = mbar_wait(&r_full[rs], rph, ctl);
-          if (kv == 0 ? g >= KS : g >= VS) go = go && mbar_wait(kv ? &v_empty[vs] : &k_empty[ks], (kv ? vr.ph : kr.ph) ^ 1u, ctl);
+          // The stage first: its last tile's MMAs are done, so the raw slot's last
+          // tile (the other group's, perhaps, and no later one: static_assert) has
+          // landed, and the slot's parity can only mean this tile.
+          bool go = true;
+          if (kv == 0 ? g >= KS : g >= VS) go = mbar_wait(kv ? &v_empty[vs] : &k_empty[ks], (kv ? vr.ph : kr.ph) ^ 1u, ctl);
+          go = go && mbar_wait(&r_full[rs], rph, ctl);
           ok = __all_sync(0xffffffffu, go);
           if (!ok) break;
           const uint8_t* src = raws + rs * Cfg::kRaw + sh;

@@ -890,7 +890,7 @@ namespace {
 // How a tree attention call is laid out: persistent CTAs, and the workspace of
 // the pieces that an even split of the key tiles leaves.
 struct TreePlan {
-  int rtiles, ws_rows, grid;
+  int rtiles, ws_rows, grid, seqs;
   bool split;          // with a workspace
   size_t ws_o, ws_bytes;
 };
@@ -902,8 +902,13 @@ TreePlan tree_plan(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C, int6
   const int64_t rows = N * (H / Hkv);
   t.rtiles = (int)((rows + 127) / 128);
   t.ws_rows = (int)(rows < 128 ? rows : 128);
-  const int64_t seqs = B < m4q::kTreeSeqs ? B : m4q::kTreeSeqs;
-  const int64_t items = seqs * Hkv * t.rtiles, tiles = (C + 127) / 128;
+  const int64_t tiles = (C + 127) / 128;
+  // sequences a launch: its unit count fits 31 bits (check_tree: that of one does)
+  const int64_t fit = INT32_MAX / (Hkv * t.rtiles * tiles);
+  int64_t seqs = B < m4q::kTreeSeqs ? B : m4q::kTreeSeqs;
+  if (seqs > fit) seqs = fit;
+  t.seqs = (int)seqs;
+  const int64_t items = seqs * Hkv * t.rtiles;
   const int64_t most = items * tiles;
   t.split = tiles > kTreeLeast;
   const int64_t want = t.split ? (most + kTreeLeast - 1) / kTreeLeast : items;
@@ -917,7 +922,8 @@ int check_tree(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64
   const int rc = check_cache(kv_codec, B, Hkv, C, D);
   if (rc != M4Q_OK) return rc;
   if (H < 1 || N < 1 || N > 256 || H > 65535 || B > INT32_MAX / (N * H)) return M4Q_ERR_INVALID_ARG;
-  return H % Hkv == 0 ? M4Q_OK : M4Q_ERR_BAD_SHAPE;
+  if (H % Hkv != 0) return M4Q_ERR_BAD_SHAPE;
+  return (N * (H / Hkv) + 127) / 128 * Hkv <= INT32_MAX / ((C + 127) / 128) ? M4Q_OK : M4Q_ERR_BAD_SHAPE;
 }
 
 }  // namespace
@@ -968,13 +974,12 @@ int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_cod
   const bool q8 = kv_codec == M4Q_Q8_0;
   CUtensorMap tm_k{}, tm_v{};
   if (!q8 && (!encode_kv(&tm_k, Kc, B * Hkv, C, D) || !encode_kv(&tm_v, Vc, B * Hkv, C, D))) return M4Q_ERR_CUDA;
-  const int64_t row = q8 ? D / 32 * 34 : 2 * D;
-  for (int64_t b0 = 0; b0 < B; b0 += m4q::kTreeSeqs) {
+  p.k = static_cast<const uint8_t*>(Kc);
+  p.v = static_cast<const uint8_t*>(Vc);
+  for (int64_t b0 = 0; b0 < B; b0 += t.seqs) {
     p.b0 = (int)b0;
-    p.B = (int)(B - b0 < m4q::kTreeSeqs ? B - b0 : m4q::kTreeSeqs);
+    p.B = (int)(B - b0 < t.seqs ? B - b0 : t.seqs);
     p.q = static_cast<const __half*>(Q) + b0 * N * D;
-    p.k = static_cast<const uint8_t*>(Kc) + b0 * Hkv * C * row;
-    p.v = static_cast<const uint8_t*>(Vc) + b0 * Hkv * C * row;
     p.o = static_cast<__half*>(O) + b0 * N * H * D;
     p.past = past + b0;
     p.parents = parents + b0 * N;

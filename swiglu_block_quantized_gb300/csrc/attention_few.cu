@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       if (!Q8) tma_prefetch_desc(map);
       while (ok && tree_next(p, sched, walk, sg)) {
         const int jm = first_masked(sg);
-        const long long head = (long long)sg.b * p.Hkv + sg.hk;
+        const long long head = (long long)(p.b0 + sg.b) * p.Hkv + sg.hk;
         const int last = (int)min((long long)sg.past + p.N, (long long)p.C);   // rows in use
         for (int j = sg.k0; j < sg.k1 && ok; ++j)
 #pragma unroll 1
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
               full_ph ^= 1u << sl;
               mbar_arrive_expect_tx(&full[sl], bytes);
               if (in_bounds(at >= 0 && bytes > 0 && bytes <= (uint32_t)Cfg::kRaw &&
-                                at + bytes <= (long long)(p.B_all - p.b0) * p.Hkv * p.C * Cfg::kRow,
+                                at + bytes <= (long long)p.B_all * p.Hkv * p.C * Cfg::kRow,
                             p.status, kSiteTreeKV))
                 bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + at, bytes, &full[sl]);
             } else {
@@ -357,10 +357,10 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
               mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
 #pragma unroll
               for (int pn = 0; pn < D / 64; ++pn)
-                if (in_bounds(j >= 0 && (long long)j * kTile < p.C && head >= 0 && head < (long long)p.B * p.Hkv, p.status,
+                if (in_bounds(j >= 0 && (long long)j * kTile < p.C && head >= 0 && head < (long long)p.B_all * p.Hkv, p.status,
                               kSiteTreeKV))
                   tma_load_3d(ring + sl * Cfg::kTileBytes + pn * (kTile * 128), map, bar, 64 * pn, j * kTile,
-                              (int)(head + (long long)p.b0 * p.Hkv));
+                              (int)head);
             }
           }
       }
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full);
-      const long long head = (long long)sg.b * p.Hkv + sg.hk;
+      const long long head = (long long)(p.b0 + sg.b) * p.Hkv + sg.hk;
       for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g, kr.step(), vr.step()) {
         const int ks = kr.at, vs = vr.at;
         if constexpr (Q8) {

@@ -19,8 +19,10 @@
 // A decode step reads each key once for few rows, so HBM should bound it: per
 // SM 23 bytes a clock, i.e. a tile of 128 fp16 keys (K and V, D = 128, 64 KB)
 // in about 2800 clocks and one of Q8_0 in 1500.  A 128-row tcgen05 tile pair
-// (S = Q K^T and O += P V) takes about 1000, whatever part of its rows is used,
-// so that one kernel serves 1 to 128 rows an item alike.
+// (S = Q K^T and O += P V) takes about 1000, whatever part of its rows is used.
+// Items of at most 32 rows go to attention_few.cu.  (Pairs of row tiles that share
+// each copied and decoded key tile, for more than 128 rows, took 86 us against 74
+// for 256 rows over 32K Q8_0 keys: both teams then wait for the same tile.)
 //
 // Warps (640 threads):
 //   0, 1    one lane each issues the MMAs of tile team 0 or 1 (tiles of even
@@ -48,7 +50,6 @@
 //
 // Every wait is bounded in time; on expiry the CTA records the failure in the
 // status word and returns.
-// Items of at most 32 rows go to attention_few.cu.
 #include <algorithm>
 
 #include "tree_common.cuh"
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!Q8) tma_prefetch_desc(map);
       while (ok && tree_next(p, sched, walk, sg)) {
         const int jm = first_masked(sg);
-        const long long head = (long long)sg.b * p.Hkv + sg.hk;
+        const long long head = (long long)(p.b0 + sg.b) * p.Hkv + sg.hk;
         const int last = (int)min((long long)sg.past + p.N, (long long)p.C);   // rows in use
         for (int j = sg.k0; j < sg.k1 && ok; ++j)
 #pragma unroll 1
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               full_ph ^= 1u << sl;
               mbar_arrive_expect_tx(&full[sl], bytes);
               if (in_bounds(at >= 0 && bytes > 0 && bytes <= (uint32_t)Cfg::kRaw &&
-                                at + bytes <= (long long)(p.B_all - p.b0) * p.Hkv * p.C * Cfg::kRow,
+                                at + bytes <= (long long)p.B_all * p.Hkv * p.C * Cfg::kRow,
                             p.status, kSiteTreeKV))
                 bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + at, bytes, &full[sl]);
             } else {
@@ -279,10 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
 #pragma unroll
               for (int pn = 0; pn < D / 64; ++pn)
-                if (in_bounds(j >= 0 && (long long)j * kTile < p.C && head >= 0 && head < (long long)p.B * p.Hkv, p.status,
+                if (in_bounds(j >= 0 && (long long)j * kTile < p.C && head >= 0 && head < (long long)p.B_all * p.Hkv, p.status,
                               kSiteTreeKV))
                   tma_load_3d(ring + sl * Cfg::kTileBytes + pn * (kTile * 128), map, bar, 64 * pn, j * kTile,
-                              (int)(head + (long long)p.b0 * p.Hkv));
+                              (int)head);
             }
           }
       }
@@ -300,8 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t scol = tmem + lanes + 128 * team, ocol = tmem + lanes + Cfg::kOCol + D * team;
     uint32_t* anc = anc_all + 128 * team + r;   // this row's bits: word i at anc[256 i]
-    const float sc = p.scale_log2;
-    const bool hi = sc >= 0.f;                  // the max of sc s is sc max s, or sc min s when sc < 0
+    // positive: a negative scale turns Q's signs, and a scale of zero is one that
+    // no score survives (an unseen key's -inf has to stay -inf)
+    const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
     const int R = p.N * p.G;
     bool ok = true;
     int g = 0, n0 = 0, n1 = 0;                  // tiles of the CTA, of team 0, of team 1
@@ -336,36 +338,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const bool masked = j >= jm;
-        uint32_t vis[4];
         if (masked) {
+          // scores of unseen keys, whatever they are, become -inf
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t vis = seen32<8>(anc, 256, j * kTile + 32 * (c >> 1), sg.past, p.C) >> (16 * (c & 1));
+            uint32_t v[16];
+            tmem_ld16_wait(scol + 16 * c, v);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) vis[q] = seen32<8>(anc, 256, j * kTile + 32 * q, sg.past, p.C);
+            for (int e = 0; e < 16; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0xFF800000u;
+            tmem_st16(scol + 16 * c, v);
+          }
+          tmem_wait_st();
         }
-        // extreme raw score of the row's visible keys
-        float t = hi ? -INFINITY : INFINITY;
+        // the row's largest raw score
+        float t = -INFINITY;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t v[64];
           tmem_ld64_wait(scol + 64 * half, v);
           float x[4] = {t, t, t, t};
-          if (masked) {
-            const float none = hi ? -INFINITY : INFINITY;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              const float s = (vis[2 * half + (e >> 5)] >> (e & 31)) & 1u ? __uint_as_float(v[e]) : none;
-              x[e & 3] = hi ? fmaxf(x[e & 3], s) : fminf(x[e & 3], s);
-            }
-          } else if (hi) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 64; ++e) x[e & 3] = fminf(x[e & 3], __uint_as_float(v[e]));
-          }
-          t = hi ? fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) : fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+          for (int e = 0; e < 64; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
+          t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         }
         // the tile's maximum; -inf when the row sees no key of it
-        const float mu = (t == INFINITY || t == -INFINITY) ? -INFINITY : t * sc;
+        const float mu = t == INFINITY ? -INFINITY : t * sc;   // (an infinite score gives NaN in the end)
         const float mj = mu > m + kRaise || m == -INFINITY ? fmaxf(mu, m) : m;
         const bool raise = mj > m && !first && m != -INFINITY;
         if (__any_sync(0xffffffffu, raise)) {
@@ -399,11 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; e += 2) {
             float a0, a1;
             unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, nm2), a0, a1);
-            float p0 = ex2(a0), p1 = ex2(a1);
-            if (masked) {
-              p0 = (vis[c >> 1] >> (16 * (c & 1) + e)) & 1u ? p0 : 0.f;
-              p1 = (vis[c >> 1] >> (16 * (c & 1) + e + 1)) & 1u ? p1 : 0.f;
-            }
+            const float p0 = ex2(a0), p1 = ex2(a1);
             s2 = add2(s2, pack2(p0, p1));
             const __half2 hh = __floats2half2_rn(p0, p1);
             wv[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
@@ -492,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pw = warp - 12;
     const int R = p.N * p.G;
     const DecK K = make_deck();
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     bool ok = true;
     int g = 0, rn = 0;
     uint32_t raw_ph = 0;                        // phase bits of v_raw of each stage
@@ -521,13 +516,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[c] = q[c];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {   // signs of a negative scale
+          o[c].x ^= flip;
+          o[c].y ^= flip;
+          o[c].z ^= flip;
+          o[c].w ^= flip;
+        }
         uint8_t* base = qs + (blk >> 1) * (kTile * 128) + rr * 128;
 #pragma unroll
         for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(base + (((4 * (blk & 1) + c) ^ (rr & 7)) << 4)) = o[c];
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full);
-      const long long head = (long long)sg.b * p.Hkv + sg.hk;
+      const long long head = (long long)(p.b0 + sg.b) * p.Hkv + sg.hk;
       for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g) {
         const int ks = g % KS, vs = g % VS;
         if constexpr (Q8) {

@@ -187,11 +187,12 @@ cudaError_t launch_norm_residual(const NormParams& p, bool res32, cudaStream_t s
 // attention_tree.cu: attention of N drafted nodes of each of B sequences over
 // its cache [Hkv][C] rows of D values.  One launch takes up to kTreeSeqs
 // sequences (their tile counts stay in shared memory): sequences b0 .. b0 +
-// B - 1 of the B_all of a call; the pointers are those of sequence b0.
+// B - 1 of the B_all of a call; the pointers are those of sequence b0, but for the
+// caches', which are the call's.
 constexpr int kTreeSeqs = 256;
 struct TreeParams {
   const __half* q;        // [H][q_rows][D], row b N + i
-  const uint8_t* k;       // [B][Hkv][C] rows
+  const uint8_t* k;       // [B_all][Hkv][C] rows
   const uint8_t* v;
   __half* o;              // [B N][H D]
   const int32_t* past;    // [B]

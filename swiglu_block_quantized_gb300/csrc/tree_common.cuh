@@ -215,7 +215,7 @@ static __device__ __noinline__ bool clean_chunks(uint8_t* tile, int row, int fir
 template <int D, bool Q8>
 __device__ __forceinline__ float value_at(const TreeParams& p, const Seg& g, int key, int c) {
   if (!in_bounds(key >= 0 && key < p.C && c >= 0 && c < D, p.status, kSiteTreeKV)) return 0.f;
-  const uint8_t* row = p.v + (((long long)g.b * p.Hkv + g.hk) * p.C + key) * (Q8 ? D / 32 * 34 : 2 * D);
+  const uint8_t* row = p.v + (((long long)(p.b0 + g.b) * p.Hkv + g.hk) * p.C + key) * (Q8 ? D / 32 * 34 : 2 * D);
   if constexpr (Q8) {
     const uint8_t* blk = row + 34 * (c >> 5);
     const __half d = __ushort_as_half(*reinterpret_cast<const unsigned short*>(blk));

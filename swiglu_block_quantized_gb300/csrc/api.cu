@@ -910,7 +910,7 @@ TreePlan tree_plan(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C, int6
   t.seqs = (int)seqs;
   const int64_t items = seqs * Hkv * t.rtiles;
   const int64_t most = items * tiles;
-  t.split = tiles > kTreeLeast;
+  t.split = tiles > m4q::kTreeWhole;
   const int64_t want = t.split ? (most + kTreeLeast - 1) / kTreeLeast : items;
   t.grid = (int)(want < sms ? want : sms);
   t.ws_o = ((size_t)2 * t.grid * t.ws_rows * sizeof(float2) + 255) / 256 * 256;

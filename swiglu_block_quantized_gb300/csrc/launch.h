@@ -190,6 +190,9 @@ cudaError_t launch_norm_residual(const NormParams& p, bool res32, cudaStream_t s
 // B - 1 of the B_all of a call; the pointers are those of sequence b0, but for the
 // caches', which are the call's.
 constexpr int kTreeSeqs = 256;
+// Where no item has more key tiles than this, CTAs take whole items: joining pieces
+// costs about as much as six tiles (8 items of 3 tiles: 9.6 us against 14.7).
+constexpr int kTreeWhole = 6;
 struct TreeParams {
   const __half* q;        // [H][q_rows][D], row b N + i
   const uint8_t* k;       // [B_all][Hkv][C] rows
@@ -202,6 +205,7 @@ struct TreeParams {
   float scale_log2;       // softmax scale * log2(e)
   int rtiles;             // row tiles of an item's sequence and KV head: ceil(N G / 128)
   int split;              // tiles are dealt out evenly over the CTAs, pieces of items joined
+                          // (unless, on the device, every item is short: kTreeWhole)
   int least;              // tiles a CTA takes at least
   int ws_rows;            // rows of a piece: min(N G, 128)
   float2* ws_ml;          // [2 grid][ws_rows] (max, sum) of a piece

@@ -31,6 +31,7 @@ struct TreeSched {
   int pre[kTreeSeqs + 1];
   int b, item, k;
   int left;          // units (or, without a split, items) of this CTA
+  int split;         // whether items are cut
 };
 
 // n units over g shares: share c starts at c base + min(c, rem).  Unit counts fit
@@ -62,7 +63,7 @@ __device__ __forceinline__ int tiles_of(const TreeParams& p, int past) {
 
 // Filled by one warp; the CTA synchronises before anyone reads.
 __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s, int lane) {
-  int sum = 0;
+  int sum = 0, most = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
@@ -72,6 +73,7 @@ __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s,
       s->past[b] = past;
       n = tiles_of(p, past);
     }
+    most = max(most, n);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, n, o);
@@ -81,15 +83,16 @@ __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s,
     sum += __shfl_sync(0xffffffffu, n, 31);
   }
   if (lane == 0) s->pre[0] = 0;
+  const bool split = p.split && __any_sync(0xffffffffu, most > kTreeWhole);
   __syncwarp();
   const unsigned hr = (unsigned)p.Hkv * p.rtiles;
-  const unsigned n = p.split ? hr * sum : hr * p.B;
-  const unsigned shares = p.split ? tree_shares(p, n, gridDim.x) : gridDim.x;
+  const unsigned n = split ? hr * sum : hr * p.B;
+  const unsigned shares = split ? tree_shares(p, n, gridDim.x) : gridDim.x;
   const Deal d = deal(n, shares);
   const unsigned c = blockIdx.x;
   const unsigned at = c < shares ? deal_start(d, c) : n, end = c < shares ? deal_start(d, c + 1) : n;
   unsigned b = 0, each = 1, rem = at;
-  if (p.split) {
+  if (split) {
     // last sequence whose units start at or before `at`
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -102,7 +105,7 @@ __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s,
   }
   unsigned item = rem / each;
   const unsigned k = rem - item * each;
-  if (!p.split) {
+  if (!split) {
     b = item / hr;
     item -= b * hr;
   }
@@ -111,6 +114,7 @@ __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s,
     s->item = (int)item;
     s->k = (int)k;
     s->left = (int)(end - at);
+    s->split = split;
   }
 }
 
@@ -127,8 +131,8 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, const TreeSched* 
   g.hk = p.rtiles == 1 ? w.item : w.item / p.rtiles;
   g.rt = w.item - g.hk * p.rtiles;
   g.k0 = w.k;
-  g.k1 = p.split ? min(g.nk, w.k + w.left) : g.nk;
-  w.left -= p.split ? g.k1 - g.k0 : 1;
+  g.k1 = s->split ? min(g.nk, w.k + w.left) : g.nk;
+  w.left -= s->split ? g.k1 - g.k0 : 1;
   w.k = 0;   // a run that stops inside an item is the CTA's last
   if (++w.item == p.Hkv * p.rtiles) {
     w.item = 0;

@@ -457,14 +457,16 @@ def _need(t, dtype, what):
 
 
 def _one_device(first, *others):
-    """All tensors live on the current device (the library launches there)."""
+    """All tensors live on the current device (the library launches there);
+    returns its index."""
     dev = first.get_device()
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensors are on %s and %s" % (first.device, t.device))
-    if dev != _t().cuda.current_device():
+    if dev != _torch._C._cuda_getDevice():
         raise ValueError("tensors are on %s, but cuda:%d is the current device"
-                         % (first.device, _t().cuda.current_device()))
+                         % (first.device, _torch.cuda.current_device()))
+    return dev
 
 
 def _allocate(shape, dtype, like, stream):
@@ -476,12 +478,12 @@ def _allocate(shape, dtype, like, stream):
         return _torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _raw_stream(stream):
-    """The stream's handle (the current stream's if None, without a Stream
-    object in between)."""
+def _raw_stream(stream, dev):
+    """The stream's handle (device dev's current stream's if None, without a
+    Stream object in between)."""
     if stream is not None:
         return stream.cuda_stream
-    return _t()._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
+    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _ints(t, dtype, n, what):
@@ -490,14 +492,11 @@ def _ints(t, dtype, n, what):
         raise ValueError("%s holds %d values, expected %d" % (what, t.numel(), n))
 
 
-def _halfs(t, shape, what):
-    """A caller's contiguous fp16 result of exactly this many values."""
+def _halfs(t, n, what):
+    """A caller's contiguous fp16 tensor of exactly n values."""
     _need(t, _t().float16, what)
-    n = 1
-    for s in shape:
-        n *= s
     if t.numel() != n:
-        raise ValueError("%s holds %d elements, expected %d for shape %s" % (what, t.numel(), n, tuple(shape)))
+        raise ValueError("%s holds %d elements, expected %d" % (what, t.numel(), n))
     return t
 
 
@@ -526,12 +525,14 @@ def _cache_shape(kc, vc, kv_codec):
     else:
         raise M4QError(ERR_UNSUPPORTED_CODEC, "KV cache")
     shape = None
-    for t, what in ((kc, "kc"), (vc, "vc")):
-        if t is not None:
-            _need(t, dtype, what)
-            if shape is not None and t.shape != shape:
-                raise ValueError("kc and vc must have one shape")
-            shape = t.shape
+    if kc is not None:
+        _need(kc, dtype, "kc")
+        shape = kc.shape
+    if vc is not None:
+        _need(vc, dtype, "vc")
+        if shape is not None and vc.shape != shape:
+            raise ValueError("kc and vc must have one shape")
+        shape = vc.shape
     if len(shape) == 4:
         b, hkv, c, row = shape
     elif len(shape) == 3:
@@ -585,11 +586,11 @@ def rope(x, pos, freqs, layout: int = ROPE_HALF, mscale: float = 1.0, out=None, 
                 reach = step * count
         if out.data_ptr() == x.data_ptr() and (hs, rs) != (ohs, ors):
             raise ValueError("out starts where x does, with other strides")
-    _one_device(x, pos, freqs, out)
+    dev = _one_device(x, pos, freqs, out)
     if h == 0 or m_ == 0:
         return out
     rc = load().m4q_rope(x.data_ptr(), hs, rs, h, m_, d, pos.data_ptr(), freqs.data_ptr(), rot, layout, mscale,
-                         out.data_ptr(), ohs, ors, _raw_stream(stream))
+                         out.data_ptr(), ohs, ors, _raw_stream(stream, dev))
     if rc:
         raise M4QError(rc, "m4q_rope")
     return out
@@ -626,19 +627,19 @@ def kv_write(k, v, kc, vc, kv_codec: int, slots, pos=None, freqs=None, layout: i
             q_out = _allocate((h, m_, d), _torch.float16, q, stream)
             p_qo = q_out.data_ptr()
         else:
-            _halfs(q_out, (h, m_, d), "q_out")
+            _halfs(q_out, h * m_ * d, "q_out")
             p_qo = q_out.data_ptr()
             if p_qo == p_q and not q.is_contiguous():
                 raise ValueError("q_out starts where q does, with other strides")
-        _one_device(k, v, kc, vc, slots, pos, freqs, q, q_out)
+        dev = _one_device(k, v, kc, vc, slots, pos, freqs, q, q_out)
     else:
         q_out = None
-        _one_device(k, v, kc, vc, slots, pos if rot else None, freqs)
+        dev = _one_device(k, v, kc, vc, slots, pos if rot else None, freqs)
     if m_ == 0:
         return q_out
     rc = load().m4q_kv_write(k.data_ptr(), khs, krs, v.data_ptr(), vhs, vrs, hkv, m_, d, p_pos, p_freqs, rot, layout,
                              mscale, slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, c, p_q, qhs, qrs, h,
-                             p_qo, _raw_stream(stream))
+                             p_qo, _raw_stream(stream, dev))
     if rc:
         raise M4QError(rc, "m4q_kv_write")
     return q_out
@@ -653,21 +654,22 @@ def kv_read(kc, vc, kv_codec: int, slots, k_out=None, v_out=None, stream=None):
     b, hkv, c, d = _cache_shape(kc, vc, kv_codec)
     n = slots.numel()
     _ints(slots, _torch.int32, n, "slots")
-    shape = (hkv, n, d)
+    shape, total = (hkv, n, d), hkv * n * d
     pk = pv = pko = pvo = None
     if kc is None:
         k_out = None
     else:
-        k_out = _allocate(shape, _torch.float16, kc, stream) if k_out is None else _halfs(k_out, shape, "k_out")
+        k_out = _allocate(shape, _torch.float16, kc, stream) if k_out is None else _halfs(k_out, total, "k_out")
         pk, pko = kc.data_ptr(), k_out.data_ptr()
     if vc is None:
         v_out = None
     else:
-        v_out = _allocate(shape, _torch.float16, vc, stream) if v_out is None else _halfs(v_out, shape, "v_out")
+        v_out = _allocate(shape, _torch.float16, vc, stream) if v_out is None else _halfs(v_out, total, "v_out")
         pv, pvo = vc.data_ptr(), v_out.data_ptr()
-    _one_device(slots, kc, vc, k_out, v_out)
+    dev = _one_device(slots, kc, vc, k_out, v_out)
     if n:
-        rc = load().m4q_kv_read(pk, pv, kv_codec, b, hkv, c, d, slots.data_ptr(), n, pko, pvo, _raw_stream(stream))
+        rc = load().m4q_kv_read(pk, pv, kv_codec, b, hkv, c, d, slots.data_ptr(), n, pko, pvo,
+                                _raw_stream(stream, dev))
         if rc:
             raise M4QError(rc, "m4q_kv_read")
     return k_out, v_out
@@ -699,7 +701,7 @@ def attention_tree(q, kc, vc, kv_codec: int, past, parents, scale: float | None 
     if out is None:
         out = _allocate((rows, h * d), _torch.float16, q, stream)
     else:
-        _halfs(out, (rows, h * d), "out")
+        _halfs(out, rows * h * d, "out")
     if rows == 0 or h == 0:
         return out
     lib = load()
@@ -715,10 +717,10 @@ def attention_tree(q, kc, vc, kv_codec: int, past, parents, scale: float | None 
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
         p_ws, n_ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _one_device(q, kc, vc, past, parents, out, workspace)
+    dev = _one_device(q, kc, vc, past, parents, out, workspace)
     rc = lib.m4q_attention_tree(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, h, hkv, n, c, d,
                                 past.data_ptr(), parents.data_ptr(), scale, out.data_ptr(), p_ws, n_ws,
-                                _raw_stream(stream))
+                                _raw_stream(stream, dev))
     if rc:
         raise M4QError(rc, "m4q_attention_tree")
     return out
@@ -749,15 +751,15 @@ def norm_residual(h, r, w_pre, w_post=None, gate=None, res_scale: float = 1.0, b
     p_h = p_wpost = p_wpre = p_gate = p_y = p_ro = y = None
     gate_rows = 0
     if h is not None:
-        p_h = _halfs(h, (total,), "h").data_ptr()
+        p_h = _halfs(h, total, "h").data_ptr()
     if w_post is not None:
-        p_wpost = _halfs(w_post, (d,), "w_post").data_ptr()
+        p_wpost = _halfs(w_post, d, "w_post").data_ptr()
     if gate is not None:
         gate_rows = int(gate.numel() != d)
-        p_gate = _halfs(gate, (total if gate_rows else d,), "gate").data_ptr()
+        p_gate = _halfs(gate, total if gate_rows else d, "gate").data_ptr()
     if w_pre is not None:
-        p_wpre = _halfs(w_pre, (d,), "w_pre").data_ptr()
-        y = _allocate(shape, f16, r, stream) if out is None else _halfs(out, shape, "out")
+        p_wpre = _halfs(w_pre, d, "w_pre").data_ptr()
+        y = _allocate(shape, f16, r, stream) if out is None else _halfs(out, total, "out")
         p_y = y.data_ptr()
     if h is not None:
         if r_out is None:
@@ -767,10 +769,11 @@ def norm_residual(h, r, w_pre, w_post=None, gate=None, res_scale: float = 1.0, b
             if r_out.numel() != total:
                 raise ValueError("r_out must hold %d values" % total)
         p_ro = r_out.data_ptr()
-    _one_device(r, h, w_pre, w_post, gate, y, r_out)
+    dev = _one_device(r, h, w_pre, w_post, gate, y, r_out)
     if m_:
         rc = load().m4q_norm_residual(p_h, r.data_ptr(), RES_F32 if res32 else RES_F16, p_wpost, p_gate, gate_rows,
-                                      p_wpre, m_, d, res_scale, branch_scale, eps, p_ro, p_y, _raw_stream(stream))
+                                      p_wpre, m_, d, res_scale, branch_scale, eps, p_ro, p_y,
+                                      _raw_stream(stream, dev))
         if rc:
             raise M4QError(rc, "m4q_norm_residual")
     return y, r_out if h is not None else r

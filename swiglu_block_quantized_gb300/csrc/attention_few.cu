@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
     tmem_alloc(tmem_slot, Cfg::kCols);
     tmem_relinquish();
   }
-  pdl_launch_dependents();
   pdl_wait();   // every global access below comes after the previous kernel
+  pdl_launch_dependents();   // after it: see join_span
   if (warp == 3) tree_schedule(p, sched, lane);
   tc_fence_before();
   __syncthreads();
@@ -718,6 +718,73 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
   }
 }
 
+// Joins the pieces of the items that were cut: W warps a row, warp k taking pieces
+// k, k + W, ..., a lane D / 32 values.
+template <int D, int W>
+__global__ void __launch_bounds__(256) few_join_kernel(const TreeParams p, int grid) {
+  constexpr int kRows = 8 / W;       // rows a CTA
+  constexpr int E = D / 32;          // values a lane
+  __shared__ float red_o[8][D];
+  __shared__ float2 red_ml[8];
+  __shared__ int sums[4];
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = warp % W;
+  const unsigned blocks = (p.ws_rows + kRows - 1) / kRows;
+  const unsigned item = blockIdx.x / blocks;
+  const int row = (int)(blockIdx.x - item * blocks) * kRows + warp / W;
+  const int b = (int)(item / p.Hkv), hk = (int)item - b * p.Hkv;
+  const JoinSpan js = join_span(p, b, hk, grid, sums);
+  pdl_wait();
+  if (!js.cut) return;
+  JoinSum<E> acc;
+  acc.clear();
+  bool unused = false;
+  const bool live = row < p.ws_rows && row < p.N * p.G;
+  if (live && in_bounds(js.c1 < (unsigned)grid && js.c0 <= js.c1, p.status, kSiteTreeWs)) {
+#pragma unroll 4
+    for (unsigned c = js.c0 + k; c <= js.c1; c += W) {
+      const long long s = js.slot(c) * p.ws_rows + row;
+      const float2 v = __ldcg(p.ws_ml + s);
+      const float* src = p.ws_o + s * D + E * lane;
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
+        x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
+      } else {
+        const float2 q = __ldcg(reinterpret_cast<const float2*>(src));
+        x[0] = q.x; x[1] = q.y;
+      }
+      unused |= v.y == -1.f;
+      acc.add(v.x, v.y, x);
+    }
+  }
+  if constexpr (W > 1) {
+    if (k > 0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) red_o[warp][E * lane + e] = acc.o[e];
+      if (lane == 0) red_ml[warp] = make_float2(acc.m, unused ? -1.f : acc.l);
+    }
+    __syncthreads();
+    if (k != 0) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = red_o[warp + i][E * lane + e];
+      const float2 v = red_ml[warp + i];
+      unused |= v.y == -1.f;
+      acc.add(v.x, v.y, x);
+    }
+  }
+  if (!live || !in_bounds(row / p.G < p.N, p.status, kSiteTreeO)) return;
+  const float inv = acc.l > 0.f ? 1.f / acc.l : acc.l;
+  __half* orow = p.o + ((long long)b * p.N + row / p.G) * p.H * D + (long long)(hk * p.G + row % p.G) * D + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__half2*>(orow + e) =
+        unused ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(acc.o[e] * inv, acc.o[e + 1] * inv);
+}
+
 template <int D, bool Q8, int NC>
 cudaError_t launch_few(const TreeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
                        cudaStream_t s) {
@@ -726,7 +793,14 @@ cudaError_t launch_few(const TreeParams& p, const CUtensorMap& tm_k, const CUten
   cudaError_t e = allow_smem<std::integer_sequence<int, 6, D, Q8, NC>>(kern, Cfg::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_tree_kernel(kern, (unsigned)grid, Cfg::kThreads, Cfg::kSmem, s, tm_k, tm_v, p);
-  return e != cudaSuccess || !p.split ? e : launch_tree_join<D>(p, grid, s);
+  if (e != cudaSuccess || !p.split) return e;
+  // Warps a row by the pieces that an item is likely to have.
+  const long long items = (long long)p.B * p.Hkv;
+  if (grid >= 24 * items)
+    return launch_tree_kernel(few_join_kernel<D, 8>, (unsigned)(items * p.ws_rows), 256, 0, s, p, grid);
+  if (grid >= 6 * items)
+    return launch_tree_kernel(few_join_kernel<D, 4>, (unsigned)(items * ((p.ws_rows + 1) / 2)), 256, 0, s, p, grid);
+  return launch_tree_kernel(few_join_kernel<D, 1>, (unsigned)(items * ((p.ws_rows + 7) / 8)), 256, 0, s, p, grid);
 }
 
 template <int D, bool Q8>

@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  pdl_launch_dependents();
   pdl_wait();   // every global access below comes after the previous kernel
+  pdl_launch_dependents();   // after it: see join_span
   if (warp == 3) tree_schedule(p, sched, lane);
   tc_fence_before();
   __syncthreads();
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool head_ok = in_bounds(node < p.N, p.status, kSiteTreeO);
         __half* orow = p.o + ((long long)sg.b * p.N + node) * p.H * D +
                        (long long)(sg.hk * p.G + (valid ? row % p.G : 0)) * D;
-        const long long slot = (2ll * blockIdx.x + (fresh ? 0 : 1)) * p.ws_rows + r;
+        const long long slot = 2ll * blockIdx.x + (fresh ? 0 : 1);
         const bool store = valid && head_ok;
         const bool ws_ok = in_bounds(whole || !valid || (p.split && r < p.ws_rows), p.status, kSiteTreeWs);
 #pragma unroll 1
@@ -470,11 +470,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int q = 0; q < 16; ++q) x[q] = 0.f;
             }
-            store_columns<D, Q8>(x, col, whole, orow, p.ws_o + slot * D);
+            if (whole) {
+              store_columns<D, Q8>(x, col, orow);
+            } else {   // [column / 4][row][4]: neighbouring lanes, neighbouring rows
+              float4* piece = reinterpret_cast<float4*>(p.ws_o) + (slot * (D / 4) + col / 4) * p.ws_rows + r;
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                piece[q * p.ws_rows] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            }
           }
         }
         // the piece that holds the tree tells of an unused node by a sum of -1
-        if (!whole && store && ws_ok && team == 0) p.ws_ml[slot] = make_float2(M, used ? L : -1.f);
+        if (!whole && store && ws_ok && team == 0) p.ws_ml[slot * p.ws_rows + r] = make_float2(M, used ? L : -1.f);
       }
       fresh = false;
       tc_fence_before();
@@ -589,112 +596,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of the items that were cut: row r of an item whose tiles
-// went to CTAs c0 .. c1 is sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
-// W warps a row, warp k taking pieces k, k + W, ...
-template <int D, int W>
-__global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int grid) {
-  constexpr int kRows = 8 / W;       // rows a CTA
-  constexpr int E = D / 32;          // values a lane
-  __shared__ float red_o[8][D];
-  __shared__ float red_l[8];
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = warp % W;
-  const unsigned blocks = (p.ws_rows + kRows - 1) / kRows;
-  const unsigned item = blockIdx.x / blocks;
-  const int r = (int)(blockIdx.x - item * blocks) * kRows + warp / W;
-  const unsigned hr = (unsigned)p.Hkv * p.rtiles;
-  const int b = (int)(item / hr), sub = (int)(item - b * hr);
-  const int hk = sub / p.rtiles, row = (sub - hk * p.rtiles) * kTile + r;
-  // the sequences' tiles, as tree_schedule counts them
+// Joins the pieces of the items that were cut.  A CTA takes 32 rows (lanes) and
+// 32 columns (warps: 4 each) of an item, a block of a decoded row, which goes to
+// its own order on the way out; W groups of 8 warps share its pieces.
+template <int D, bool Q8, int W>
+__global__ void __launch_bounds__(256 * W) tree_join_kernel(const TreeParams p, int grid) {
+  constexpr int kPitch = 40;   // halves
+  __shared__ float4 red_o[W > 1 ? W - 1 : 1][256];
+  __shared__ float2 red_ml[W > 1 ? W - 1 : 1][256];
+  __shared__ __align__(16) __half out[32 * kPitch];
   __shared__ int sums[4];
-  if (warp == 0) {
-    int before = 0, all = 0, mine = 0, most = 0;
-#pragma unroll 1
-    for (int i = lane; i < p.B; i += 32) {
-      const int past = min(max(__ldg(p.past + i), 0), p.C);
-      const int n = tiles_of(p, past);
-      all += n;
-      most = max(most, n);
-      before += i < b ? n : 0;
-      mine += i == b ? n : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      all += __shfl_xor_sync(0xffffffffu, all, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-      mine += __shfl_xor_sync(0xffffffffu, mine, o);
-      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    if (lane == 0) sums[0] = before, sums[1] = mine, sums[2] = all, sums[3] = most;
-  }
-  __syncthreads();
-  if (sums[3] <= kTreeWhole) return;   // no item was cut
-  const unsigned nk = sums[1], units = hr * sums[2];
-  const Deal dl = deal(units, tree_shares(p, units, grid));
-  const unsigned u0 = hr * sums[0] + sub * nk;
-  const int c0 = deal_owner(dl, u0), c1 = deal_owner(dl, u0 + nk - 1);
-  if (c0 == c1) return;              // not cut: its CTA wrote the output
-  const bool live = r < p.ws_rows && row < p.N * p.G;
-  const bool at_start = deal_start(dl, c0) == u0;   // the first piece is its CTA's first run
-  auto slot = [&](int c) { return (2ll * c + (c > c0 || at_start ? 0 : 1)) * p.ws_rows + r; };
-  float M = -INFINITY, L = 0.f;
+  pdl_launch_dependents();
+  const int t = threadIdx.x & 255, k = threadIdx.x >> 8, lane = t & 31, warp = t >> 5;
+  const unsigned blocks = (p.ws_rows + 31) / 32 * (D / 32), hr = (unsigned)p.Hkv * p.rtiles;
+  const unsigned item = blockIdx.x / blocks, part = blockIdx.x - item * blocks;
+  const int blk = part % (D / 32), r0 = (int)(part / (D / 32)) * 32, r = r0 + lane;
+  const int b = (int)(item / hr), sub = (int)(item - b * hr), hk = sub / p.rtiles, row0 = (sub - hk * p.rtiles) * kTile;
+  const JoinSpan js = join_span(p, b, sub, grid, sums);
+  pdl_wait();
+  if (!js.cut) return;
+  JoinSum<4> acc;
+  acc.clear();
   bool unused = false;
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (live && in_bounds(c0 >= 0 && c1 < grid && c0 <= c1, p.status, kSiteTreeWs)) {
-#pragma unroll 1
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const float2 v = p.ws_ml[slot(c)];
-      M = fmaxf(M, v.x);
-      unused |= v.y == -1.f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    unused = __any_sync(0xffffffffu, unused);
+  if (r < p.ws_rows && row0 + r < p.N * p.G && in_bounds(js.c1 < (unsigned)grid && js.c0 <= js.c1, p.status, kSiteTreeWs)) {
 #pragma unroll 4
-    for (int c = c0 + k; c <= c1; c += W) {
-      const long long s = slot(c);
-      const float2 v = p.ws_ml[s];
-      const float f = v.x == M ? 1.f : ex2(v.x - M);
-      const float* src = p.ws_o + s * D + E * lane;
-      float x[E];
-      if constexpr (E == 4) {
-        const float4 q = *reinterpret_cast<const float4*>(src);
-        x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
-      } else {
-        const float2 q = *reinterpret_cast<const float2*>(src);
-        x[0] = q.x; x[1] = q.y;
-      }
-      L += f * v.y;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += f * x[e];
+    for (unsigned c = js.c0 + k; c <= js.c1; c += W) {
+      const long long s = js.slot(c);
+      const float2 v = __ldcg(p.ws_ml + s * p.ws_rows + r);
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(p.ws_o) + (s * (D / 4) + 8 * blk + warp) * p.ws_rows + r);
+      const float x[4] = {q.x, q.y, q.z, q.w};
+      unused |= v.y == -1.f;
+      acc.add(v.x, v.y, x);
     }
   }
   if constexpr (W > 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) red_o[warp][E * lane + e] = acc[e];
-    if (lane == 0) red_l[warp] = L;
+    if (k > 0) {
+      red_o[k - 1][t] = make_float4(acc.o[0], acc.o[1], acc.o[2], acc.o[3]);
+      red_ml[k - 1][t] = make_float2(acc.m, unused ? -1.f : acc.l);
+    }
     __syncthreads();
-    if (k != 0) return;
-    L = 0.f;
+    if (k > 0) return;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      L += red_l[warp + i];
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += red_o[warp + i][E * lane + e];
+    for (int i = 0; i < W - 1; ++i) {
+      const float4 q = red_o[i][t];
+      const float2 v = red_ml[i][t];
+      const float x[4] = {q.x, q.y, q.z, q.w};
+      unused |= v.y == -1.f;
+      acc.add(v.x, v.y, x);
     }
   }
-  if (!live || !in_bounds(row / p.G < p.N, p.status, kSiteTreeO)) return;
-  const float inv = L > 0.f ? 1.f / L : L;
-  __half* orow = p.o + ((long long)b * p.N + row / p.G) * p.H * D + (long long)(hk * p.G + row % p.G) * D + E * lane;
+  const float inv = unused ? 0.f : acc.l > 0.f ? 1.f / acc.l : acc.l;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<__half2*>(orow + e) =
-        unused ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < 4; ++e) {
+    const int pos = 4 * warp + e;
+    out[lane * kPitch + (Q8 ? q8_code_at(blk & 1, pos) : pos)] = __float2half_rn(unused ? 0.f : acc.o[e] * inv);
+  }
+  if constexpr (W > 1) named_bar_sync(1, 256);
+  else __syncthreads();
+  // 8 lanes a row, 8 bytes each
+  const int rr = t >> 3, row = row0 + r0 + rr;
+  if (r0 + rr >= p.ws_rows || row >= p.N * p.G) return;
+  const int node = row / p.G;
+  if (!in_bounds(node < p.N, p.status, kSiteTreeO)) return;
+  __half* orow = p.o + ((long long)b * p.N + node) * p.H * D + (long long)(hk * p.G + row - node * p.G) * D;
+  *reinterpret_cast<uint2*>(orow + 32 * blk + 4 * (t & 7)) = *reinterpret_cast<const uint2*>(out + rr * kPitch + 4 * (t & 7));
 }
 
 template <int D, bool Q8>
@@ -704,23 +669,15 @@ cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tm_k, const CUte
   cudaError_t e = allow_smem<std::integer_sequence<int, 5, D, Q8>>(kern, TreeCfg<D, Q8>::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_tree_kernel(kern, (unsigned)grid, kThreads, TreeCfg<D, Q8>::kSmem, s, tm_k, tm_v, p);
-  return e != cudaSuccess || !p.split ? e : launch_tree_join<D>(p, grid, s);
+  if (e != cudaSuccess || !p.split) return e;
+  // Groups of warps by the pieces that an item is likely to have.
+  const long long items = (long long)p.B * p.Hkv * p.rtiles;
+  const unsigned parts = (unsigned)(items * ((p.ws_rows + 31) / 32) * (D / 32));
+  return grid > 4 * items ? launch_tree_kernel(tree_join_kernel<D, Q8, 4>, parts, 1024, 0, s, p, grid)
+                          : launch_tree_kernel(tree_join_kernel<D, Q8, 1>, parts, 256, 0, s, p, grid);
 }
 
 }  // namespace
-
-template <int D>
-cudaError_t launch_tree_join(const TreeParams& p, int grid, cudaStream_t s) {
-  // Warps a row, by the pieces an item is likely to have (10 pieces, 2048 rows of
-  // 128: one call 68.4 us with 4 warps a row, 72.2 with 8).
-  const long long items = (long long)p.B * p.Hkv * p.rtiles;
-  if (grid >= 24 * items) return launch_tree_kernel(tree_join_kernel<D, 8>, (unsigned)(items * p.ws_rows), 256, 0, s, p, grid);
-  if (grid >= 6 * items)
-    return launch_tree_kernel(tree_join_kernel<D, 4>, (unsigned)(items * ((p.ws_rows + 1) / 2)), 256, 0, s, p, grid);
-  return launch_tree_kernel(tree_join_kernel<D, 1>, (unsigned)(items * ((p.ws_rows + 7) / 8)), 256, 0, s, p, grid);
-}
-template cudaError_t launch_tree_join<64>(const TreeParams&, int, cudaStream_t);
-template cudaError_t launch_tree_join<128>(const TreeParams&, int, cudaStream_t);
 
 cudaError_t launch_attention_tree(const TreeParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                   int grid, cudaStream_t s) {

@@ -261,9 +261,9 @@ __device__ __forceinline__ void add_values(const TreeParams& p, const Seg& g, in
   }
 }
 
-// Columns col .. col + 15 (positions) of a row, to fp16 output or fp32 piece.
+// Columns col .. col + 15 (positions) of a row, to the fp16 output.
 template <int D, bool Q8>
-__device__ __forceinline__ void store_columns(const float (&x)[16], int col, bool whole, __half* orow, float* wrow) {
+__device__ __forceinline__ void store_columns(const float (&x)[16], int col, __half* orow) {
   if constexpr (Q8) {
     // decoded order: positions 4 i, 4 i + 2 and 4 i + 1, 4 i + 3 hold neighbours
     const int odd = (col >> 5) & 1, pos0 = col & 31, at = col & ~31;
@@ -271,13 +271,11 @@ __device__ __forceinline__ void store_columns(const float (&x)[16], int col, boo
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float a = x[4 * i + k], b = x[4 * i + k + 2];
         const int i4 = pos0 + 4 * i;
         const int e = odd ? i4 + 2 * k : i4 > 0 ? i4 - 2 + 2 * k : 30 * k;
-        if (whole) *reinterpret_cast<__half2*>(orow + at + e) = __floats2half2_rn(a, b);
-        else *reinterpret_cast<float2*>(wrow + at + e) = make_float2(a, b);
+        *reinterpret_cast<__half2*>(orow + at + e) = __floats2half2_rn(x[4 * i + k], x[4 * i + k + 2]);
       }
-  } else if (whole) {
+  } else {
     uint32_t h[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -286,10 +284,6 @@ __device__ __forceinline__ void store_columns(const float (&x)[16], int col, boo
     }
     *reinterpret_cast<uint4*>(orow + col) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4*>(orow + col + 8) = make_uint4(h[4], h[5], h[6], h[7]);
-  } else {
-    float4* dst = reinterpret_cast<float4*>(wrow + col);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
   }
 }
 
@@ -386,9 +380,76 @@ __device__ __forceinline__ void raw_span(long long head, int C, int row_bytes, i
   bytes = (uint32_t)(((e + 15) & ~15ll) - at);
 }
 
-// Joins the pieces of the items that were cut (attention_tree.cu).
-template <int D>
-cudaError_t launch_tree_join(const TreeParams& p, int grid, cudaStream_t s);
+// Pieces of the items that were cut.  Row r of item (sequence b, head hk, row
+// tile rt), whose tiles went to CTAs c0 .. c1, is
+//   sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
+// A CTA has at most two pieces, of its first run (slot 2 c) and of its last
+// (2 c + 1).
+struct JoinSpan {
+  unsigned c0, c1;
+  bool cut;        // else its one CTA wrote the output
+  bool at_start;   // the piece of c0 is of its first run
+  __device__ __forceinline__ long long slot(unsigned c) const { return 2ll * c + (c > c0 || at_start ? 0 : 1); }
+};
+
+// The pieces of the item `sub` of sequence b (all threads of a CTA call).  Reads
+// the lengths only, and is called before the wait for the kernel that writes the
+// pieces: that kernel lets this one start after its own wait, when the lengths
+// are final.
+__device__ __forceinline__ JoinSpan join_span(const TreeParams& p, int b, unsigned sub, unsigned grid, int (&sums)[4]) {
+  if (threadIdx.x < 32) {   // the sequences' tiles, as tree_schedule counts them
+    int before = 0, all = 0, mine = 0, most = 0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < p.B; i += 32) {
+      const int past = min(max(__ldcg(p.past + i), 0), p.C);
+      const int n = tiles_of(p, past);
+      all += n;
+      most = max(most, n);
+      before += i < b ? n : 0;
+      mine += i == b ? n : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    if (threadIdx.x == 0) sums[0] = before, sums[1] = mine, sums[2] = all, sums[3] = most;
+  }
+  __syncthreads();
+  JoinSpan j{0, 0, false, false};
+  if (sums[3] <= kTreeWhole) return j;   // no item was cut
+  const unsigned hr = (unsigned)p.Hkv * p.rtiles, nk = sums[1], units = hr * sums[2];
+  const Deal dl = deal(units, tree_shares(p, units, grid));
+  const unsigned u0 = hr * sums[0] + sub * nk;
+  j.c0 = deal_owner(dl, u0);
+  j.c1 = deal_owner(dl, u0 + nk - 1);
+  j.cut = j.c0 != j.c1;
+  j.at_start = deal_start(dl, j.c0) == u0;
+  return j;
+}
+
+// A row's sums over pieces taken one after the other: E columns, relative to the
+// largest reference so far.
+template <int E>
+struct JoinSum {
+  float m, l, o[E];
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+  }
+  __device__ __forceinline__ void add(float mc, float lc, const float (&x)[E]) {
+    const float top = fmaxf(m, mc);
+    const float a = m == top ? 1.f : ex2(m - top), f = mc == top ? 1.f : ex2(mc - top);
+    m = top;
+    l = l * a + lc * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * a + x[e] * f;
+  }
+};
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_tree_kernel(void (*kern)(KArgs...), unsigned grid, unsigned block, int smem, cudaStream_t s,

@@ -727,7 +727,6 @@ __global__ void __launch_bounds__(256) few_join_kernel(const TreeParams p, int g
   __shared__ float red_o[8][D];
   __shared__ float2 red_ml[8];
   __shared__ int sums[4];
-  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = warp % W;
   const unsigned blocks = (p.ws_rows + kRows - 1) / kRows;
   const unsigned item = blockIdx.x / blocks;

@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
               decode_to_tile<D, 3>(dst, src, row, K);
             }
             if (j >= jm) {
-              const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(dst, row, 0, D / 8, 0));
+              const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(dst, row, 0, D / 8));
               if (lane == 0) nt[j - jm] = bits;
             }
             fence_proxy_async_smem();
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
           if (!ok) break;
           raw_ph ^= 1u << vs;
-          const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t, 0, D / 8, 0));
+          const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t, 0, D / 8));
           if (lane == 0) nt[j - jm] = bits;
           fence_proxy_async_smem();
           mbar_arrive_warp(&v_clean[vs]);

@@ -68,7 +68,7 @@ struct TreeCfg {
   static constexpr int kVS = Q8 ? 2 : D == 128 ? 2 : 5;
   static constexpr int kRS = Q8 ? (D == 128 ? 3 : 8) : 0;       // raw ring (K, V, K, ...)
   static constexpr int kRaw = kTile * kRow + 32;       // a tile, its 16-byte shift, and the decode's overread
-  static constexpr int kBars = 2 * kKS + 4 * kVS + 2 * kRS + 12;
+  static constexpr int kBars = 2 * kKS + 4 * kVS + 3 * kRS + 12;
   static constexpr int kFixed = 8 * 256 * 4            // ancestor bits [8][team][128]
                                 + 2 * 2 * kTile * 8    // (m, l) [parity][team][128]
                                 + 2 * 8 * 4 * 4        // noted V rows [parity][warp][masked tile]
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_raw = v_full + VS;       // [VS] (fp16) V of a masked tile, not yet cleared (v_full: the others')
   uint64_t* v_clean = v_raw + VS;      // [VS] (fp16) V of a masked tile, cleared
   uint64_t* v_empty = v_clean + VS;    // [VS] P V done with it
-  uint64_t* r_full = v_empty + VS;     // [RS] raw tile landed
-  uint64_t* r_empty = r_full + Cfg::kRS;
+  uint64_t* r_full = v_empty + VS;     // [2][RS] raw tile (K, V) landed in a slot
+  uint64_t* r_empty = r_full + 2 * Cfg::kRS;
   uint64_t* s_full = r_empty + Cfg::kRS;   // [2] S of a team's tile in TMEM
   uint64_t* p_full = s_full + 2;       // [2] its P written
   uint64_t* pv_done = p_full + 2;      // [2] its P V done
@@ -139,18 +139,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) {
-      mbar_init(&k_full[i], Q8 ? 8 : 1);
+      mbar_init(&k_full[i], Q8 ? 4 : 1);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < VS; ++i) {
-      mbar_init(&v_full[i], Q8 ? 8 : 1);
+      mbar_init(&v_full[i], Q8 ? 4 : 1);
       mbar_init(&v_raw[i], 1);
       mbar_init(&v_clean[i], 8);
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < Cfg::kRS; ++i) {
       mbar_init(&r_full[i], 1);
-      mbar_init(&r_empty[i], 8);
+      mbar_init(&r_full[Cfg::kRS + i], 1);
+      mbar_init(&r_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -197,41 +198,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t full_ph = 0, clean_ph = 0;   // phase bits of v_full and v_clean of each stage
       bool ok = true;
       int g = 0, nt = 0;          // tiles of the CTA, tiles of the team
+      Ring<KS> kr;
+      Ring<VS> vr;
       for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
         const int jm = first_masked(sg);
-        bool first = true;
+        // The team's next tile of the run: its stages and barriers.  Looked up while
+        // the softmax has the last one: after P V it would cost 500 to 700 clocks of
+        // a chain of 5000.
+        struct {
+          int ks, vs;
+          uint32_t k_ph, v_ph;
+          uint64_t* v_ready;
+        } at;
+        int j = sg.k0;
+        auto look = [&]() {
+          for (; j < sg.k1;) {
+            const bool wants_clean = !Q8 && j >= jm, mine = (g & 1) == team;
+            at.ks = kr.at;
+            at.k_ph = kr.ph;
+            at.vs = vr.at;
+            at.v_ready = wants_clean ? &v_clean[vr.at] : &v_full[vr.at];
+            at.v_ph = ((wants_clean ? clean_ph : full_ph) >> vr.at) & 1u;
+            (wants_clean ? clean_ph : full_ph) ^= 1u << vr.at;
+            ++j, ++g;
+            kr.step();
+            vr.step();
+            if (mine) return true;
+          }
+          return false;
+        };
+        bool first = true, more = look();
         ok = mbar_wait(q_full, w & 1, ctl);
-        for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g) {
-          const int vs = g % VS;
-          const bool wants_clean = !Q8 && j >= jm;
-          uint64_t* v_ready = wants_clean ? &v_clean[vs] : &v_full[vs];
-          const uint32_t v_ph = ((wants_clean ? clean_ph : full_ph) >> vs) & 1u;
-          (wants_clean ? clean_ph : full_ph) ^= 1u << vs;
-          if ((g & 1) != team) continue;
-          const int ks = g % KS;
-          ok = mbar_wait(&k_full[ks], (g / KS) & 1, ctl);
+        while (ok && more) {
+          ok = mbar_wait(&k_full[at.ks], at.k_ph, ctl);
           if (nt > 0) ok = ok && mbar_wait(&pv_done[team], (nt - 1) & 1, ctl);   // S and P share columns
           if (!ok) break;
           tc_fence_after();
-          const uint64_t kds = kd + (uint64_t)(ks * (Cfg::kTileBytes >> 4));
+          const uint64_t kds = kd + (uint64_t)(at.ks * (Cfg::kTileBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (kTile * 128 >> 4) + 2 * (kk & 3);
             mma_ss_f16(scol, qd + off, kds + off, idesc_s, kk > 0 ? 1u : 0u);
           }
           tc_commit(&s_full[team]);
-          tc_commit(&k_empty[ks]);
-          ok = mbar_wait(v_ready, v_ph, ctl) && mbar_wait(&p_full[team], nt & 1, ctl);
+          tc_commit(&k_empty[at.ks]);
+          const int vs = at.vs;
+          const uint64_t vds = vd + (uint64_t)(vs * (Cfg::kTileBytes >> 4));
+          uint64_t* v_ready = at.v_ready;
+          const uint32_t v_ph = at.v_ph;
+          more = look();
+          ok = mbar_wait(v_ready, v_ph, ctl);
           if (first && w > 0) ok = ok && mbar_wait(o_free, (w - 1) & 1, ctl);
+          ok = ok && mbar_wait(&p_full[team], nt & 1, ctl);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t vds = vd + (uint64_t)(vs * (Cfg::kTileBytes >> 4));
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
             tc_mma_ts_f16(ocol, scol + 8 * kk, vds + (uint32_t)(kk * (2048 >> 4)), idesc_o,
                           (kk > 0 || !first) ? 1u : 0u);
-          tc_commit(&v_empty[vs]);
           tc_commit(&pv_done[team]);
+          tc_commit(&v_empty[vs]);
           first = false;
           ++nt;
         }
@@ -266,12 +292,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               long long at;
               uint32_t bytes;
               raw_span(head, p.C, Cfg::kRow, j, last, at, bytes);
-              full_ph ^= 1u << sl;
-              mbar_arrive_expect_tx(&full[sl], bytes);
+              uint64_t* bar = &full[kv * RS + sl];
+              full_ph ^= 1u << (kv * RS + sl);
+              mbar_arrive_expect_tx(bar, bytes);
               if (in_bounds(at >= 0 && bytes > 0 && bytes <= (uint32_t)Cfg::kRaw &&
                                 at + bytes <= (long long)p.B_all * p.Hkv * p.C * Cfg::kRow,
                             p.status, kSiteTreeKV))
-                bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + at, bytes, &full[sl]);
+                bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + at, bytes, bar);
             } else {
               // V of a masked tile goes by way of the clearing warps
               const bool raw = warp == 3 && j >= jm;
@@ -288,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       }
       if (!ok)   // copies in flight land before the CTA can leave: the last armed phase of each barrier
-        for (int i = 0; i < ns; ++i) {
+        for (int i = 0; i < (Q8 ? 2 * ns : ns); ++i) {
           mbar_wait_drain(&full[i], ((full_ph >> i) & 1) ^ 1, 100000000ull);
           if (!Q8 && warp == 3) mbar_wait_drain(&v_raw[i], ((raw_ph >> i) & 1) ^ 1, 100000000ull);
         }
@@ -495,8 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const DecK K = make_deck();
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     bool ok = true;
-    int g = 0, rn = 0;
-    uint32_t raw_ph = 0;                        // phase bits of v_raw of each stage
+    int g = 0;
+    // Q8_0: warps 12-15 decode K tiles, 16-19 V tiles: the waits of one pass while
+    // the other works
+    const int kv = pw >> 2;
+    uint32_t raw_ph = 0;                        // phase bits of v_raw, or of r_full, of each stage
     for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
       const int jm = first_masked(sg);
       ok = __all_sync(0xffffffffu, w == 0 || mbar_wait_idle(q_empty, (w - 1) & 1, run_ctl, 64));
@@ -538,42 +568,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_warp(q_full);
       const long long head = (long long)(p.b0 + sg.b) * p.Hkv + sg.hk;
       for (int j = sg.k0; j < sg.k1 && ok; ++j, ++g) {
-        const int ks = g % KS, vs = g % VS;
+        [[maybe_unused]] const int ks = g % KS, vs = g % VS;
         if constexpr (Q8) {
+          const int n = 2 * g + kv, rs = n % RS;
           const int sh = (int)(((head * p.C + (long long)j * kTile) * Cfg::kRow) & 15);
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++rn) {
-            const int rs = rn % RS;
-            uint64_t* empty = kv ? &v_empty[vs] : &k_empty[ks];
-            const int ns = kv ? VS : KS;
-            bool go = mbar_wait(&r_full[rs], (rn / RS) & 1, ctl);
-            if (g >= ns) go = go && mbar_wait(empty, ((g / ns) - 1) & 1, ctl);
-            ok = __all_sync(0xffffffffu, go);
-            if (!ok) break;
-            uint8_t* dst = kv ? vst + vs * Cfg::kTileBytes : kst + ks * Cfg::kTileBytes;
-            const int row = t & 127;
-            const uint8_t* src = raws + rs * Cfg::kRaw + sh;
-            if (t < 128) {
-              decode_to_tile<D, 0>(dst, src, row, K);
-              if constexpr (D == 128) decode_to_tile<D, 2>(dst, src, row, K);
-            } else {
-              decode_to_tile<D, 1>(dst, src, row, K);
-              if constexpr (D == 128) decode_to_tile<D, 3>(dst, src, row, K);
-            }
-            if (kv && j >= jm) {   // this thread's blocks
-              const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(dst, row, 4 * (t >> 7), D / 16, 4));
-              if (lane == 0) nt[j - jm] = bits;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive_warp(kv ? &v_full[vs] : &k_full[ks]);
-            mbar_arrive_warp(&r_empty[rs]);
+          bool go = mbar_wait(&r_full[kv * RS + rs], (raw_ph >> rs) & 1, ctl);
+          raw_ph ^= 1u << rs;
+          const int st = kv ? vs : ks, ns = kv ? VS : KS;
+          if (g >= ns) go = go && mbar_wait(kv ? &v_empty[st] : &k_empty[st], ((g / ns) - 1) & 1, ctl);
+          ok = __all_sync(0xffffffffu, go);
+          if (!ok) break;
+          uint8_t* dst = (kv ? vst : kst) + st * Cfg::kTileBytes;
+          const int row = t & 127;
+          const uint8_t* src = raws + rs * Cfg::kRaw + sh;
+          decode_to_tile<D, 0>(dst, src, row, K);
+          decode_to_tile<D, 1>(dst, src, row, K);
+          if constexpr (D == 128) {
+            decode_to_tile<D, 2>(dst, src, row, K);
+            decode_to_tile<D, 3>(dst, src, row, K);
           }
+          if (kv && j >= jm) {
+            const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(dst, row, 0, D / 8));
+            if (lane == 0) nt[j - jm] = bits;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive_warp(kv ? &v_full[st] : &k_full[st]);
+          mbar_arrive_warp(&r_empty[rs]);
         } else if (j >= jm) {
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
           if (!ok) break;
           raw_ph ^= 1u << vs;
           const uint32_t bits =
-              __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t & 127, (t >> 7) * (D / 16), D / 16, 0));
+              __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t & 127, (t >> 7) * (D / 16), D / 16));
           if (lane == 0) nt[j - jm] = bits;
           fence_proxy_async_smem();
           mbar_arrive_warp(&v_clean[vs]);

@@ -195,14 +195,13 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
 }
 
 // Clear `count` 16-byte chunks of row `row` of an fp16 tile (D / 64 panels of
-// [128 keys][128 B], swizzled), from chunk `first`, skipping `skip` after every
-// four.  True if there were non-finite values.  (Only for tiles with masks: kept
-// short, out of the way of the decode.)
-static __device__ __noinline__ bool clean_chunks(uint8_t* tile, int row, int first, int count, int skip) {
+// [128 keys][128 B], swizzled), from chunk `first`.  True if there were non-finite
+// values.  (Only for tiles with masks: kept short, out of the way of the decode.)
+static __device__ __noinline__ bool clean_chunks(uint8_t* tile, int row, int first, int count) {
   bool any = false;
 #pragma unroll 1
   for (int c = 0; c < count; ++c) {
-    const int ch = first + c + (c >> 2) * skip;
+    const int ch = first + c;
     uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
     uint4 v = *at;
     bool bad = clear_nonfinite(v.x);

@@ -72,19 +72,6 @@ struct FewCfg {
   static_assert(kRaw % 16 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "alignment");
 };
 
-__device__ __forceinline__ bool vote_or(uint32_t id, uint32_t count, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "bar.red.or.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"((uint32_t)pred)
-      : "memory");
-  return r != 0;
-}
-
 // Sums (or maxima) of N values over the warp: halves of the rows change lanes,
 // N / 2 + N / 4 + ... shuffles instead of 5 N.  Returned: row `lane` (N = 32) or
 // lane / 2 (N = 16).

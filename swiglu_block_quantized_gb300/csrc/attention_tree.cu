@@ -58,7 +58,7 @@ namespace m4q {
 
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kSoft = 16;   // softmax warps
 
 template <int D, bool Q8>
 struct TreeCfg {
@@ -68,8 +68,11 @@ struct TreeCfg {
   static constexpr int kVS = Q8 ? 2 : D == 128 ? 2 : 5;
   static constexpr int kRS = Q8 ? (D == 128 ? 3 : 8) : 0;       // raw ring (K, V, K, ...)
   static constexpr int kRaw = kTile * kRow + 32;       // a tile, its 16-byte shift, and the decode's overread
+  static constexpr int kPrep = Q8 ? 8 : 4;             // preparing warps
+  static constexpr int kThreads = 32 * (4 + kSoft + kPrep);
   static constexpr int kBars = 2 * kKS + 4 * kVS + 3 * kRS + 12;
-  static constexpr int kFixed = 8 * 256 * 4            // ancestor bits [8][team][128]
+  static constexpr int kFixed = 8 * kTile * 4          // ancestor bits [8][128]
+                                + 6 * kTile * 4        // maxima [team][half][128], sums [team][128]
                                 + 2 * 2 * kTile * 8    // (m, l) [parity][team][128]
                                 + 2 * 8 * 4 * 4        // noted V rows [parity][warp][masked tile]
                                 + (int)sizeof(TreeSched) + 8
@@ -94,25 +97,27 @@ __device__ __noinline__ void add_nonfinite(const TreeParams& p, Seg g, const uin
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       const int kq = j * kTile + 32 * q;
-      add_values<D, Q8>(p, g, kq, (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32<8>(anc, 256, kq, g.past, p.C),
+      add_values<D, Q8>(p, g, kq, (noted[4 * q + mt] | noted[4 * (q + 4) + mt]) & seen32<8>(anc, kTile, kq, g.past, p.C),
                         c0, x);
     }
   }
 }
 
 template <int D, bool Q8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const TreeParams p) {
   using Cfg = TreeCfg<D, Q8>;
-  constexpr int KS = Cfg::kKS, VS = Cfg::kVS, RS = Cfg::kRS > 0 ? Cfg::kRS : 1;
+  constexpr int PW = Cfg::kPrep, KS = Cfg::kKS, VS = Cfg::kVS, RS = Cfg::kRS > 0 ? Cfg::kRS : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_align<1024>(smem_raw);
   uint8_t* kst = qs + Cfg::kTileBytes;
   uint8_t* vst = kst + KS * Cfg::kTileBytes;
   uint8_t* raws = vst + VS * Cfg::kTileBytes;
-  uint32_t* anc_all = reinterpret_cast<uint32_t*>(raws + Cfg::kRS * Cfg::kRaw);   // [8][256]
-  float2* ml = reinterpret_cast<float2*>(anc_all + 8 * 256);                      // [parity][team][128]
+  uint32_t* anc_all = reinterpret_cast<uint32_t*>(raws + Cfg::kRS * Cfg::kRaw);   // [8][128]
+  float* xmax = reinterpret_cast<float*>(anc_all + 8 * kTile);                    // [team][half][128]
+  float* xsum = xmax + 4 * kTile;                                                 // [team][128]
+  float2* ml = reinterpret_cast<float2*>(xsum + 2 * kTile);                       // [parity][team][128]
   uint32_t* noted = reinterpret_cast<uint32_t*>(ml + 4 * kTile);                  // [parity][8 warps][4]
   TreeSched* sched = reinterpret_cast<TreeSched*>(noted + 64);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sched) +
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < VS; ++i) {
       mbar_init(&v_full[i], Q8 ? 4 : 1);
       mbar_init(&v_raw[i], 1);
-      mbar_init(&v_clean[i], 8);
+      mbar_init(&v_clean[i], PW);
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < Cfg::kRS; ++i) {
@@ -155,14 +160,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(q_full, 8);
+    mbar_init(q_full, PW);
     mbar_init(q_empty, 2);
     mbar_init(ml_rdy, 8);
-    mbar_init(nf_rdy, 8);
-    mbar_init(o_free, 8);
+    mbar_init(nf_rdy, PW);
+    mbar_init(o_free, kSoft);
     mbar_init(drain, 2);
     *abort_flag = 0;
     fence_mbar_init();
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            tc_mma_ts_f16(ocol, scol + 8 * kk, vds + (uint32_t)(kk * (2048 >> 4)), idesc_o,
+            tc_mma_ts_f16(ocol, scol + 64 * (kk >> 2) + 8 * (kk & 3), vds + (uint32_t)(kk * (2048 >> 4)), idesc_o,
                           (kk > 0 || !first) ? 1u : 0u);
           tc_commit(&pv_done[team]);
           tc_commit(&v_empty[vs]);
@@ -321,13 +326,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-  } else if (warp < 12) {
+  } else if (warp < 4 + kSoft) {
     // ------------------------------------------------------------ softmax
-    const int team = (warp - 4) >> 2;
-    const int r = 32 * (warp & 3) + lane;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t scol = tmem + lanes + 128 * team, ocol = tmem + lanes + Cfg::kOCol + D * team;
-    uint32_t* anc = anc_all + 128 * team + r;   // this row's bits: word i at anc[256 i]
+    const int team = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3;
+    const int r = 32 * quad + lane;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t scol = tmem + lanes + 128 * team + 64 * half;               // its 64 keys' scores, then P
+    const uint32_t ocol = tmem + lanes + Cfg::kOCol + D * team + D / 2 * half;   // the columns it rescales
+    uint32_t* anc = anc_all + r;   // this row's bits: word i at anc[128 i]
+    // named barriers: the four warps of these rows, and the two of a team
+    const uint32_t quad_bar = 1 + quad, pair_bar = 5 + 4 * team + quad;
+    float* mine = xmax + (2 * team + half) * kTile + r;
+    const float* others = xmax + (2 * team + 1 - half) * kTile + r;
     // positive: a negative scale turns Q's signs, and a scale of zero is one that
     // no score survives (an unseen key's -inf has to stay -inf)
     const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
@@ -338,13 +348,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
       const int row = sg.rt * kTile + r;
       const bool valid = row < R;
-      const bool busy = sg.rt * kTile + 32 * (warp & 3) < R;   // the warp has a row
+      const bool busy = sg.rt * kTile + 32 * quad < R;   // the warp has a row
       const int node = valid ? row / p.G : 0;
       const int jm = first_masked(sg);
       bool used = true;
       if (busy && sg.k1 > jm) {
-        used = ancestors<8>(p.parents + (long long)sg.b * p.N, node, anc, 256);
-        __syncwarp();
+        named_bar_sync(quad_bar, 128);   // the last run's readers are done
+        if (warp < 8) ancestors<8>(p.parents + (long long)sg.b * p.N, node, anc, kTile);
+        named_bar_sync(quad_bar, 128);
+        used = (anc[(node >> 5) * kTile] >> (node & 31)) & 1u;   // a used node sees itself
       }
       float m = -INFINITY, l = 0.f;
       bool first = true;
@@ -358,37 +370,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, busy ? mbar_wait(&s_full[team], nt & 1, ctl)
                                           : mbar_wait_idle(&s_full[team], nt & 1, ctl, 256));
         ++nt;
-        if (!ok) break;
         if (!busy) {
+          if (!ok) break;
           mbar_arrive_warp(&p_full[team]);
           continue;
         }
         tc_fence_after();
-        const bool masked = j >= jm;
-        if (masked) {
-          // scores of unseen keys, whatever they are, become -inf
+        float t = -INFINITY;   // the half row's largest raw score
+        if (ok) {
+          if (j >= jm) {
+            // scores of unseen keys, whatever they are, become -inf
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            const uint32_t vis = seen32<8>(anc, 256, j * kTile + 32 * (c >> 1), sg.past, p.C) >> (16 * (c & 1));
-            uint32_t v[16];
-            tmem_ld16_wait(scol + 16 * c, v);
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t vis =
+                  seen32<8>(anc, kTile, j * kTile + 64 * half + 32 * (c >> 1), sg.past, p.C) >> (16 * (c & 1));
+              uint32_t v[16];
+              tmem_ld16_wait(scol + 16 * c, v);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0xFF800000u;
-            tmem_st16(scol + 16 * c, v);
+              for (int e = 0; e < 16; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0xFF800000u;
+              tmem_st16(scol + 16 * c, v);
+            }
+            tmem_wait_st();
           }
-          tmem_wait_st();
-        }
-        // the row's largest raw score
-        float t = -INFINITY;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t v[64];
-          tmem_ld64_wait(scol + 64 * half, v);
-          float x[4] = {t, t, t, t};
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v[32];
+            tmem_ld32_wait(scol + 32 * q, v);
+            float x[4] = {t, t, t, t};
 #pragma unroll
-          for (int e = 0; e < 64; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
-          t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            for (int e = 0; e < 32; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
+            t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          }
+          *mine = t;
         }
+        // the two halves go on, or leave, together (a named barrier has no time limit)
+        if (vote_or(pair_bar, 64, !ok)) {
+          ok = false;
+          break;
+        }
+        t = fmaxf(t, *others);
         // the tile's maximum; -inf when the row sees no key of it
         const float mu = t == INFINITY ? -INFINITY : t * sc;   // (an infinite score gives NaN in the end)
         const float mj = mu > m + kRaise || m == -INFINITY ? fmaxf(mu, m) : m;
@@ -397,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the team's earlier P V are done (its next S waits for them)
           const float a = raise ? ex2(m - mj) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
+          for (int c = 0; c < D / 32; ++c) {
             uint32_t v[16];
             tmem_ld16_wait(ocol + 16 * c, v);
 #pragma unroll
@@ -416,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16_async(scol, v[0]);
         tmem_wait_ld_tied(v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c < 7) tmem_ld16_async(scol + 16 * (c + 1), v[(c + 1) & 1]);
+        for (int c = 0; c < 4; ++c) {
+          if (c < 3) tmem_ld16_async(scol + 16 * (c + 1), v[(c + 1) & 1]);
           const uint32_t (&x)[16] = v[c & 1];
           uint32_t wv[8];
 #pragma unroll
@@ -430,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wv[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
           }
           tmem_st8(scol + 8 * c, wv);
-          if (c < 7) tmem_wait_ld_tied(v[(c + 1) & 1]);
+          if (c < 3) tmem_wait_ld_tied(v[(c + 1) & 1]);
         }
         float sum0, sum1;
         unpack2(s2, sum0, sum1);
@@ -440,16 +460,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive_warp(&p_full[team]);
       }
-      if (!ok) break;
       // ---------------------------------------------------------- end of a run
       const int par = w & 1;
-      ml[(par * 2 + team) * kTile + r] = make_float2(m, l);
-      mbar_arrive_warp(ml_rdy);
+      if (half) xsum[team * kTile + r] = l;
+      named_bar_sync(pair_bar, 64);
+      if (!half) {
+        ml[(par * 2 + team) * kTile + r] = make_float2(m, l + xsum[team * kTile + r]);
+        if (ok) mbar_arrive_warp(ml_rdy);
+      }
       const int g0 = g - (sg.k1 - sg.k0);
-      bool got = mbar_wait(ml_rdy, par, ctl) && mbar_wait(nf_rdy, par, ctl);
+      bool got = ok && mbar_wait(ml_rdy, par, ctl) && mbar_wait(nf_rdy, par, ctl);
       if (n0 > 0) got = got && mbar_wait(&pv_done[0], (n0 - 1) & 1, ctl);
       if (n1 > 0) got = got && mbar_wait(&pv_done[1], (n1 - 1) & 1, ctl);
-      ok = __all_sync(0xffffffffu, got);
+      ok = !vote_or(quad_bar, 128, !got);
       if (!ok) break;
       tc_fence_after();
       if (busy) {
@@ -472,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool store = valid && head_ok;
         const bool ws_ok = in_bounds(whole || !valid || (p.split && r < p.ws_rows), p.status, kSiteTreeWs);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          const int col = team * (D / 2) + 16 * c;
+        for (int c = 0; c < D / 64; ++c) {
+          const int col = (2 * team + half) * (D / 4) + 16 * c;
           uint32_t v0[16], v1[16];
           tmem_ld16_wait(tmem + lanes + Cfg::kOCol + col, v0);
           tmem_ld16_wait(tmem + lanes + Cfg::kOCol + D + col, v1);
@@ -508,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // the piece that holds the tree tells of an unused node by a sum of -1
-        if (!whole && store && ws_ok && team == 0) p.ws_ml[slot * p.ws_rows + r] = make_float2(M, used ? L : -1.f);
+        if (!whole && store && ws_ok && team == 0 && half == 0) p.ws_ml[slot * p.ws_rows + r] = make_float2(M, used ? L : -1.f);
       }
       fresh = false;
       tc_fence_before();
@@ -516,14 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ Q, decode, clearing
-    const int t = threadIdx.x - 12 * 32;        // 0 .. 255
-    const int pw = warp - 12;
+    const int t = threadIdx.x - 32 * (4 + kSoft);   // 0 .. 32 PW - 1
+    const int pw = warp - 4 - kSoft;
     const int R = p.N * p.G;
     const DecK K = make_deck();
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     bool ok = true;
     int g = 0;
-    // Q8_0: warps 12-15 decode K tiles, 16-19 V tiles: the waits of one pass while
+    // Q8_0: the first four warps decode K tiles, the others V tiles: the waits of one pass while
     // the other works
     const int kv = pw >> 2;
     uint32_t raw_ph = 0;                        // phase bits of v_raw, or of r_full, of each stage
@@ -532,12 +555,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, w == 0 || mbar_wait_idle(q_empty, (w - 1) & 1, run_ctl, 64));
       if (!ok) break;
       uint32_t* nt = noted + (w & 1) * 32 + pw * 4;
-      if (lane < 4) nt[lane] = 0u;
+      if (lane < 4) {
+        nt[lane] = 0u;
+        if (PW == 4) nt[16 + lane] = 0u;
+      }
       __syncwarp();
       // Q rows (Q8_0: in the decoded blocks' order), a block of 32 values a step
 #pragma unroll
-      for (int i = 0; i < kTile * (D / 32) / 256; ++i) {
-        const int u = t + 256 * i, rr = u / (D / 32), blk = u % (D / 32);
+      for (int i = 0; i < kTile * (D / 32) / (32 * PW); ++i) {
+        const int u = t + 32 * PW * i, rr = u / (D / 32), blk = u % (D / 32);
         const int row = sg.rt * kTile + rr;
         uint4 q[4] = {}, o[4];
         if (row < R) {
@@ -598,8 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));
           if (!ok) break;
           raw_ph ^= 1u << vs;
-          const uint32_t bits =
-              __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t & 127, (t >> 7) * (D / 16), D / 16));
+          const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t, 0, D / 8));
           if (lane == 0) nt[j - jm] = bits;
           fence_proxy_async_smem();
           mbar_arrive_warp(&v_clean[vs]);
@@ -694,7 +719,7 @@ cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& tm_k, const CUte
   auto kern = tree_kernel<D, Q8>;
   cudaError_t e = allow_smem<std::integer_sequence<int, 5, D, Q8>>(kern, TreeCfg<D, Q8>::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_tree_kernel(kern, (unsigned)grid, kThreads, TreeCfg<D, Q8>::kSmem, s, tm_k, tm_v, p);
+  e = launch_tree_kernel(kern, (unsigned)grid, TreeCfg<D, Q8>::kThreads, TreeCfg<D, Q8>::kSmem, s, tm_k, tm_v, p);
   if (e != cudaSuccess || !p.split) return e;
   // Groups of warps by the pieces that an item is likely to have: with 10 of them
   // (2048 rows of 128) a call took 58.0 us with four groups and 61.4 with one, with

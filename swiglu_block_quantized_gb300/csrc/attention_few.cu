@@ -385,9 +385,8 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       const int jm = first_masked(sg), par = w & 1;
       if (sg.k1 > jm) {
         // the tree's bits, lane = row (nodes are at most 32: one word)
-        uint32_t bits = 0;
-        bool used = true;
-        if (lane < R) used = ancestors<1>(p.parents + (long long)sg.b * p.N, lane / p.G, &bits, 1);
+        uint32_t bits;
+        const bool used = ancestors32(p.parents + (long long)sg.b * p.N, p.N, lane < R ? lane / p.G : -1, bits);
         anc[lane] = bits;
         const uint32_t un = __ballot_sync(0xffffffffu, !used);
         if (warp == 4 && lane == 0) unused_s[par] = un;

@@ -74,6 +74,7 @@ struct TreeCfg {
   static constexpr int kFixed = 8 * kTile * 4          // ancestor bits [8][128]
                                 + 6 * kTile * 4        // maxima [team][half][128], sums [team][128]
                                 + 2 * 2 * kTile * 8    // (m, l) [parity][team][128]
+                                + 256 * 2              // parents
                                 + 2 * 8 * 4 * 4        // noted V rows [parity][warp][masked tile]
                                 + (int)sizeof(TreeSched) + 8
                                 + kBars * 8 + 16;
@@ -119,7 +120,10 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
   float* xsum = xmax + 4 * kTile;                                                 // [team][128]
   float2* ml = reinterpret_cast<float2*>(xsum + 2 * kTile);                       // [parity][team][128]
   uint32_t* noted = reinterpret_cast<uint32_t*>(ml + 4 * kTile);                  // [parity][8 warps][4]
-  TreeSched* sched = reinterpret_cast<TreeSched*>(noted + 64);
+  // parents of the run's tree: its writers, one warp for 32 rows, write the same,
+  // and none is a run ahead of another (ml_rdy)
+  int16_t* up = reinterpret_cast<int16_t*>(noted + 64);                           // [256]
+  TreeSched* sched = reinterpret_cast<TreeSched*>(up + 256);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sched) +
                                                   (sizeof(TreeSched) + 7) / 8 * 8);   // [KS] K of a tile in its stage
   uint64_t* k_empty = k_full + KS;     // [KS] S done with it
@@ -234,6 +238,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
         };
         bool first = true, more = look();
         ok = mbar_wait(q_full, w & 1, ctl);
+        if (ok && !more) tc_commit(q_empty);
         while (ok && more) {
           ok = mbar_wait(&k_full[at.ks], at.k_ph, ctl);
           if (nt > 0) ok = ok && mbar_wait(&pv_done[team], (nt - 1) & 1, ctl);   // S and P share columns
@@ -252,6 +257,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
           uint64_t* v_ready = at.v_ready;
           const uint32_t v_ph = at.v_ph;
           more = look();
+          if (!more) tc_commit(q_empty);   // this team's S of the run are done with Q
           ok = mbar_wait(v_ready, v_ph, ctl);
           if (first && w > 0) ok = ok && mbar_wait(o_free, (w - 1) & 1, ctl);
           ok = ok && mbar_wait(&p_full[team], nt & 1, ctl);
@@ -266,7 +272,6 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
           first = false;
           ++nt;
         }
-        if (ok) tc_commit(q_empty);   // this team's S of the run are done with Q
       }
       tc_commit(drain);
       mbar_wait_drain(drain, 0, 200000000ull);
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
       bool used = true;
       if (busy && sg.k1 > jm) {
         named_bar_sync(quad_bar, 128);   // the last run's readers are done
-        if (warp < 8) ancestors<8>(p.parents + (long long)sg.b * p.N, node, anc, kTile);
+        if (warp < 8) ancestors256(p.parents + (long long)sg.b * p.N, p.N, up, node, anc, kTile);
         named_bar_sync(quad_bar, 128);
         used = (anc[(node >> 5) * kTile] >> (node & 31)) & 1u;   // a used node sees itself
       }

@@ -147,24 +147,50 @@ __device__ __forceinline__ int first_masked(const Seg& g) { return min(g.past / 
 
 // ------------------------------------------------------------------ masks
 
-// Ancestor bits of a node, itself included, 32 nodes a word, word i stored at
-// anc[i stride]; 0 and false when it, or one of its ancestors, is not used.
-template <int WORDS>
-__device__ __forceinline__ bool ancestors(const int* parents, int node, uint32_t* anc, int stride) {
-#pragma unroll
-  for (int i = 0; i < WORDS; ++i) anc[i * stride] = 0u;
+// Ancestor bits of each lane's node (-1: none), itself included, for trees of at
+// most 32; 0 and false when it, or one of its ancestors, is not used.  The whole
+// warp calls.  The lanes hold the parents: a step up a tree is a shuffle, not a load
+// that waits for the last one.
+__device__ __forceinline__ bool ancestors32(const int* parents, int n, int node, uint32_t& bits) {
+  const int lane = threadIdx.x & 31;
+  const int up = lane < n ? __ldg(parents + lane) : -2;
+  bits = 0u;
   bool used = true;
-  for (int a = node; a >= 0;) {   // each parent is lower than its child: at most N steps
-    anc[(a >> 5) * stride] |= 1u << (a & 31);
-    const int up = __ldg(parents + a);
-    if (up < -1 || up >= a) used = false;
-    a = used ? up : -1;
+  int a = node;
+  while (__any_sync(0xffffffffu, a >= 0)) {   // each parent is lower than its child: at most n steps
+    const int next = __shfl_sync(0xffffffffu, up, a & 31);
+    if (a >= 0) {
+      bits |= 1u << a;
+      if (next < -1 || next >= a) used = false;
+      a = used ? next : -1;
+    }
   }
-  if (!used) {
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) anc[i * stride] = 0u;
-  }
+  if (!used) bits = 0u;
   return used;
+}
+
+// The same for trees of up to 256, 32 nodes a word, word i stored at anc[i stride];
+// the n parents pass through `up` in shared memory.
+__device__ __forceinline__ void ancestors256(const int* parents, int n, int16_t* up, int node, uint32_t* anc,
+                                             int stride) {
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < n; i += 32) {
+    const int v = __ldg(parents + i);
+    up[i] = (int16_t)(v >= -1 && v < i ? v : -2);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) anc[i * stride] = 0u;
+  __syncwarp();
+  int a = node;
+#pragma unroll 1
+  while (a >= 0) {
+    anc[(a >> 5) * stride] |= 1u << (a & 31);
+    a = up[a];
+  }
+  if (a == -2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) anc[i * stride] = 0u;
+  }
 }
 
 // Bits 0..31: which of the keys kq .. kq + 31 a row sees, from its ancestor bits.

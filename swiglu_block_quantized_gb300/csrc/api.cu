@@ -890,12 +890,11 @@ namespace {
 // How a tree attention call is laid out: persistent CTAs, and the workspace of
 // the pieces that an even split of the key tiles leaves.
 struct TreePlan {
-  int rtiles, ws_rows, grid, seqs;
+  int rtiles, ws_rows, grid, seqs, waves;
   bool split;          // with a workspace
+  m4q::TreeWhole whole;
   size_t ws_o, ws_bytes;
 };
-
-constexpr int kTreeLeast = 2;   // key tiles a CTA takes at least
 
 TreePlan tree_plan(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C, int64_t D, int sms) {
   TreePlan t;
@@ -910,8 +909,11 @@ TreePlan tree_plan(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C, int6
   t.seqs = (int)seqs;
   const int64_t items = seqs * Hkv * t.rtiles;
   const int64_t most = items * tiles;
-  t.split = tiles > m4q::kTreeWhole;
-  const int64_t want = t.split ? (most + kTreeLeast - 1) / kTreeLeast : items;
+  const m4q::TreeWhole whole = rows <= m4q::kTreeFewRows ? m4q::kFewWhole : m4q::kRowsWhole;
+  t.whole = {whole.most, whole.per / (float)sms};
+  t.waves = (int)((items + sms - 1) / sms);
+  t.split = tiles * t.waves > whole.most;
+  const int64_t want = t.split ? (most + m4q::kTreeLeast - 1) / m4q::kTreeLeast : items;
   t.grid = (int)(want < sms ? want : sms);
   t.ws_o = ((size_t)2 * t.grid * t.ws_rows * sizeof(float2) + 255) / 256 * 256;
   t.ws_bytes = t.split ? t.ws_o + (size_t)2 * t.grid * t.ws_rows * D * sizeof(float) : 0;
@@ -964,7 +966,8 @@ int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_cod
   p.scale_log2 = scale * 1.4426950408889634f;
   p.rtiles = t.rtiles;
   p.split = t.split ? 1 : 0;
-  p.least = kTreeLeast;
+  p.whole = t.whole;
+  p.waves = t.waves;
   p.ws_rows = t.ws_rows;
   if (t.split) {
     char* ws = static_cast<char*>(workspace);

@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
             for (int c = 0; c < 4; ++c) {
               const uint32_t vis =
                   seen32<8>(anc, kTile, j * kTile + 64 * half + 32 * (c >> 1), sg.past, p.C) >> (16 * (c & 1));
+              if (__all_sync(0xffffffffu, (vis & 0xFFFFu) == 0xFFFFu)) continue;
               uint32_t v[16];
               tmem_ld16_wait(scol + 16 * c, v);
 #pragma unroll
@@ -741,7 +742,7 @@ cudaError_t launch_attention_tree(const TreeParams& p, bool q8, const CUtensorMa
                                   int grid, cudaStream_t s) {
   // few rows: keys on the MMA's 128 lanes instead of rows (a 128-row tile costs
   // the same for any of them)
-  if (p.N * p.G <= 32) return launch_attention_few(p, q8, tm_k, tm_v, grid, s);
+  if (p.N * p.G <= kTreeFewRows) return launch_attention_few(p, q8, tm_k, tm_v, grid, s);
   if (p.D == 64) return q8 ? launch_tree<64, true>(p, tm_k, tm_v, grid, s) : launch_tree<64, false>(p, tm_k, tm_v, grid, s);
   return q8 ? launch_tree<128, true>(p, tm_k, tm_v, grid, s) : launch_tree<128, false>(p, tm_k, tm_v, grid, s);
 }

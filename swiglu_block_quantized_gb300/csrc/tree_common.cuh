@@ -52,9 +52,14 @@ __device__ __forceinline__ int deal_owner(const Deal& d, unsigned u) {
   const unsigned cut = d.rem * (d.base + 1);
   return (int)(u < cut ? u / (d.base + 1) : d.rem + (u - cut) / d.base);
 }
-// CTAs that take part: as many as have `least` tiles each.
-__device__ __forceinline__ unsigned tree_shares(const TreeParams& p, unsigned units, unsigned grid) {
-  return min(grid, max(1u, units / (unsigned)p.least));
+// CTAs that take part: as many as have kTreeLeast tiles each.
+__device__ __forceinline__ unsigned tree_shares(unsigned units, unsigned grid) {
+  return min(grid, max(1u, units / kTreeLeast));
+}
+// Whether items are cut (TreeWhole), from the longest one's tiles and all tiles: one
+// rounding, so that the kernel and the join agree.
+__device__ __forceinline__ bool tree_cut(const TreeParams& p, int most, unsigned units) {
+  return (float)most * (float)p.waves - (float)p.whole.most > __fmul_rn(p.whole.per, (float)units);
 }
 // Tiles of a sequence.
 __device__ __forceinline__ int tiles_of(const TreeParams& p, int past) {
@@ -83,11 +88,12 @@ __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s,
     sum += __shfl_sync(0xffffffffu, n, 31);
   }
   if (lane == 0) s->pre[0] = 0;
-  const bool split = p.split && __any_sync(0xffffffffu, most > kTreeWhole);
+  most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
   __syncwarp();
   const unsigned hr = (unsigned)p.Hkv * p.rtiles;
+  const bool split = p.split && tree_cut(p, most, hr * sum);
   const unsigned n = split ? hr * sum : hr * p.B;
-  const unsigned shares = split ? tree_shares(p, n, gridDim.x) : gridDim.x;
+  const unsigned shares = split ? tree_shares(n, gridDim.x) : gridDim.x;
   const Deal d = deal(n, shares);
   const unsigned c = blockIdx.x;
   const unsigned at = c < shares ? deal_start(d, c) : n, end = c < shares ? deal_start(d, c + 1) : n;
@@ -459,9 +465,9 @@ __device__ __forceinline__ JoinSpan join_span(const TreeParams& p, int b, unsign
   }
   __syncthreads();
   JoinSpan j{0, 0, false, false};
-  if (sums[3] <= kTreeWhole) return j;   // no item was cut
   const unsigned hr = (unsigned)p.Hkv * p.rtiles, nk = sums[1], units = hr * sums[2];
-  const Deal dl = deal(units, tree_shares(p, units, grid));
+  if (!tree_cut(p, sums[3], units)) return j;   // no item was cut
+  const Deal dl = deal(units, tree_shares(units, grid));
   const unsigned u0 = hr * sums[0] + sub * nk;
   j.c0 = deal_owner(dl, u0);
   j.c1 = deal_owner(dl, u0 + nk - 1);

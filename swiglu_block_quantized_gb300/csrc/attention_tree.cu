@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
           }
           if (kv && j >= jm) {
             const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(dst, row, 0, D / 8));
-            if (lane == 0) nt[j - jm] = bits;
+            if (lane == 0) nt[j - jm] = bits & rows_in_use(p, sg, j * kTile + 32 * (pw & 3));
           }
           fence_proxy_async_smem();
           mbar_arrive_warp(kv ? &v_full[st] : &k_full[st]);
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
           if (!ok) break;
           raw_ph ^= 1u << vs;
           const uint32_t bits = __ballot_sync(0xffffffffu, clean_chunks(vst + vs * Cfg::kTileBytes, t, 0, D / 8));
-          if (lane == 0) nt[j - jm] = bits;
+          if (lane == 0) nt[j - jm] = bits & rows_in_use(p, sg, j * kTile + 32 * (pw & 3));
           fence_proxy_async_smem();
           mbar_arrive_warp(&v_clean[vs]);
         }

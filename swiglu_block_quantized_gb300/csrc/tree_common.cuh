@@ -246,6 +246,14 @@ static __device__ __noinline__ bool clean_chunks(uint8_t* tile, int row, int fir
   return any;
 }
 
+// Which of the rows kq .. kq + 31 are in use.  Those behind hold anything (in a
+// Q8_0 tile what the last one left): nobody sees them, and if they were noted each
+// run's end would look for them (14 us against 22 for 8 nodes over 636 keys).
+__device__ __forceinline__ uint32_t rows_in_use(const TreeParams& p, const Seg& g, int kq) {
+  const int n = min(g.past, p.C - p.N) + p.N - kq;
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // Value c of a V row in global memory.
 template <int D, bool Q8>
 __device__ __forceinline__ float value_at(const TreeParams& p, const Seg& g, int key, int c) {

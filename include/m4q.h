@@ -346,7 +346,8 @@ int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t
  *  - slots: int32 [M], the cache row b * C + j of each token.  A slot outside
  *    [0, B * C) writes nothing (padding).  Two tokens of one call do not share
  *    a slot (not checked: the row would mix both).  Rows that no slot names
- *    are left as they are.
+ *    are left as they are.  The caches overlap neither each other nor K, V, Q
+ *    or Qout (not checked).
  *  - A Q8_0 block of 32 values x: d = max|x| / 127 rounded up to fp16, codes
  *    x / d to the nearest integer, ties to even (none exceeds 127); a block
  *    with an infinity or a NaN decodes to NaN.  K is quantised from the fp32
@@ -412,7 +413,8 @@ size_t m4q_attention_tree_workspace(int kv_codec, int64_t B, int64_t H, int64_t 
  * for each of M rows of D values, rms(x) = sqrt(mean x^2 + eps).
  *  - h: fp16 [M][D], the block's output; R: the residual stream [M][D] in
  *    res_type; R_out: r' in res_type (NULL: not written; may be R); Y: fp16
- *    [M][D] (may be h).
+ *    [M][D] (may be h, not R_out: M4Q_ERR_INVALID_ARG).  No other two arrays
+ *    overlap (not checked).
  *  - w_post, w_pre: fp16 [D].  gate: fp16 [D] (gate_rows 0) or [M][D]
  *    (gate_rows 1), or NULL.
  *  - Sums, r' and products are fp32; r' is rounded where it is stored and y is

@@ -1006,6 +1006,7 @@ int m4q_norm_residual(const void* h, const void* R, int res_type, const void* w_
   if (!aligned16(h) || !aligned16(R) || !aligned16(w_post) || !aligned16(gate) || !aligned16(w_pre) ||
       !aligned16(R_out) || !aligned16(Y))
     return M4Q_ERR_MISALIGNED;
+  if (Y == R_out) return M4Q_ERR_INVALID_ARG;
   DevInfo dev;
   m4q::NormParams p{};
   const int rc = ready(&dev, &p.status);

@@ -29,6 +29,12 @@
 // whatever its size (barriers, TMEM loads, the fence before the MMA reads P), and
 // two of them overlap.
 //
+// Measured: 32 sequences of one token, 4 heads a group, D = 128, over 500 to 8,100
+// Q8_0 keys in 97.5 us (300 MB: 3.1 TB/s), 8 nodes over 300 fp16 keys in 9.6 us.
+// fp16 calls are at HBM when long; Q8_0 is bound by the decode warps' instructions,
+// whose fetch is the second stall after TMEM and shared memory loads (72 KB of
+// code); short calls by the start and end of a run.
+//
 // Warps: 0 issues the S MMAs (four TMEM buffers ahead), 1 the P V MMAs, 2 and 3
 // the copies, 4-11 are the softmax teams (lane = key), the others prepare (Q, the
 // clearing of non-finite V; Q8_0: groups of four decode K or V tiles), as in

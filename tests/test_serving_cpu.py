@@ -160,6 +160,7 @@ def test_norm_residual_refuses(lib):
     assert call(d=68) == m.ERR_BAD_SHAPE
     for kw in (dict(h=ODD), dict(r=ODD), dict(wp=ODD), dict(g=ODD), dict(w=ODD), dict(ro=ODD), dict(y=ODD)):
         assert call(**kw) == m.ERR_MISALIGNED, kw
+    assert call() == m.ERR_INVALID_ARG   # y is r_out
 
 
 # ---------------------------------------------------------------- the binding's refusals

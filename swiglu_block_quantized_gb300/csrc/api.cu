@@ -910,9 +910,9 @@ TreePlan tree_plan(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C, int6
   const int64_t items = seqs * Hkv * t.rtiles;
   const int64_t most = items * tiles;
   const m4q::TreeWhole whole = rows <= m4q::kTreeFewRows ? m4q::kFewWhole : m4q::kRowsWhole;
-  t.whole = {whole.most, whole.per / (float)sms};
+  t.whole = whole;
   t.waves = (int)((items + sms - 1) / sms);
-  t.split = tiles * t.waves > whole.most;
+  t.split = (double)tiles * t.waves > whole.join;
   const int64_t want = t.split ? (most + m4q::kTreeLeast - 1) / m4q::kTreeLeast : items;
   t.grid = (int)(want < sms ? want : sms);
   t.ws_o = ((size_t)2 * t.grid * t.ws_rows * sizeof(float2) + 255) / 256 * 256;
@@ -967,6 +967,7 @@ int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_cod
   p.rtiles = t.rtiles;
   p.split = t.split ? 1 : 0;
   p.whole = t.whole;
+  p.share = 1.f / (float)dev.sms;
   p.waves = t.waves;
   p.ws_rows = t.ws_rows;
   if (t.split) {

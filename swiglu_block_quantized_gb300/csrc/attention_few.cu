@@ -30,7 +30,7 @@
 // two of them overlap.
 //
 // Measured: 32 sequences of one token, 4 heads a group, D = 128, over 500 to 8,100
-// Q8_0 keys in 97.5 us (300 MB: 3.1 TB/s), 8 nodes over 300 fp16 keys in 9.6 us.
+// Q8_0 keys in 96 us (300 MB: 3.1 TB/s), 8 nodes over 300 fp16 keys in 9.6 us.
 // fp16 calls are at HBM when long; Q8_0 is bound by the decode warps' instructions,
 // whose fetch is the second stall after TMEM and shared memory loads (72 KB of
 // code); short calls by the start and end of a run.

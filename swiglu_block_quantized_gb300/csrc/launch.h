@@ -193,17 +193,16 @@ constexpr int kTreeSeqs = 256;
 // Nodes times query heads of a group up to which the kernel with the keys on the
 // MMA's lanes takes a call (attention_few.cu).
 constexpr int kTreeFewRows = 32;
-// Items are cut when the longest, as often as an SM takes one, has more tiles than
-// `most` and `per` times the SM's share of all tiles: otherwise the join, and the
-// second run of a CTA, cost more than they save.  Measured, whole against cut, in us (G = 4, D = 64, fp16): 8
+// Items are cut when the longest, as often as an SM takes one, has `join` tiles
+// more than the SM's share u of all tiles, and u / 2, at most `run`, more on top:
+// otherwise the join, and the second run of a CTA, cost more than they save.  Measured, whole against cut, in us (G = 4, D = 64, fp16): 8
 // sequences of 24 nodes 14.7 / 15.0 with 8 tiles each and 16.9 / 15.9 with 10, one of
 // 64 nodes 10.7 / 10.1 with 4 and 12.9 / 10.4 with 6; few rows: 8 sequences of 4 nodes
 // 16.0 / 17.0 with 16 tiles and 18.3 / 17.8 with 20, one of one 8.6 / 8.3 with 6.
 struct TreeWhole {
-  int most;
-  float per;
+  float join, run;
 };
-constexpr TreeWhole kRowsWhole{4, 1.f}, kFewWhole{6, 1.5f};
+constexpr TreeWhole kRowsWhole{4.f, 0.f}, kFewWhole{6.f, 4.f};
 constexpr int kTreeLeast = 2;   // key tiles a CTA takes at least
 struct TreeParams {
   const __half* q;        // [H][q_rows][D], row b N + i
@@ -218,7 +217,8 @@ struct TreeParams {
   int rtiles;             // row tiles of an item's sequence and KV head: ceil(N G / 128)
   int split;              // tiles are dealt out evenly over the CTAs, pieces of items joined
                           // (unless, on the device, every item is short: tree_cut)
-  TreeWhole whole;        // (`per` of the launch's tiles, not of an SM's share)
+  TreeWhole whole;
+  float share;            // an SM's share of a tile: 1 / SMs
   int waves;              // items an SM takes: ceil(B Hkv rtiles / SMs), of a full launch
   int ws_rows;            // rows of a piece: min(N G, 128)
   float2* ws_ml;          // [2 grid][ws_rows] (max, sum) of a piece

@@ -56,10 +56,12 @@ __device__ __forceinline__ int deal_owner(const Deal& d, unsigned u) {
 __device__ __forceinline__ unsigned tree_shares(unsigned units, unsigned grid) {
   return min(grid, max(1u, units / kTreeLeast));
 }
-// Whether items are cut (TreeWhole), from the longest one's tiles and all tiles: one
-// rounding, so that the kernel and the join agree.
+// Whether items are cut (TreeWhole), from the longest one's tiles and all tiles.
+// The kernel and the join have to agree: every rounding is written out.
 __device__ __forceinline__ bool tree_cut(const TreeParams& p, int most, unsigned units) {
-  return (float)most * (float)p.waves - (float)p.whole.most > __fmul_rn(p.whole.per, (float)units);
+  const float u = __fmul_rn(p.share, (float)units);
+  const float more = __fadd_rn(p.whole.join, fminf(__fmul_rn(0.5f, u), p.whole.run));
+  return __fmul_rn((float)most, (float)p.waves) > __fadd_rn(u, more);
 }
 // Tiles of a sequence.
 __device__ __forceinline__ int tiles_of(const TreeParams& p, int past) {

@@ -17,34 +17,35 @@ enum : uint32_t {
   kSiteTreeWs = 37,      // tree attention: partial result
 };
 
-// Half a Q8_0 block: x[0..15] of this lane and of the lane next to it (lane ^ 1)
-// are the block's 32 values.  Returns the bits of the scale d and 16 code
-// bytes.  d = max|x| / 127 rounded up; q = x / d to the nearest integer, ties
-// to even.  x times the rounded reciprocal of d can land beside an exact tie;
-// the step q + (x - q d) / d, its remainder exact, ends within an fp32 rounding
-// of x / d, so ties are hit and anything farther from one than that is not.  A
-// test for ties with a second round of code only where one is met was slower
-// (39.1 us against 26.6 for 8,000 tokens of 8 + 8 heads written and read back).  The whole warp calls.
-__device__ __forceinline__ uint16_t q8_encode16(const float (&x)[16], uint32_t (&codes)[4]) {
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
-  const float other = __shfl_xor_sync(0xffffffffu, top, 1);
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(other));
+// Larger of two, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
+
+// Eight values of a Q8_0 block whose largest magnitude is `top`.  Returns the bits
+// of the scale d and 8 code bytes.  d = top / 127 rounded up; q = x / d to the
+// nearest integer, ties to even.  x times the rounded reciprocal of d can land
+// beside an exact tie; the step q + (x - q d) / d, its remainder exact, ends within
+// an fp32 rounding of x / d, so ties are hit and anything farther from one than that
+// is not.  A test for ties with a second round of code only where one is met was
+// slower (39.1 us against 26.6 for 8,000 tokens of 8 + 8 heads written and read
+// back).
+__device__ __forceinline__ uint16_t q8_encode8(const float* x, float top, uint32_t (&codes)[2]) {
   const __half dh = __float2half_ru(__fdiv_rn(top, 127.f));
   const uint16_t bits = __half_as_ushort(dh);
   const bool bad = !((bits & 0x7C00u) < 0x7C00u);   // infinity or NaN in the block, or a scale beyond fp16
   const float d = __half2float(dh);
   const float inv = d > 0.f && !bad ? __frcp_rn(d) : 0.f;
   constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
-  float y[16];
+  float y[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const float q = x[i] * inv;
     y[i] = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, d, x[i]), inv, q), kMagic);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const uint32_t a = __byte_perm(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), 0x0040);
     const uint32_t b = __byte_perm(__float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]), 0x0040);
     codes[i] = bad ? 0u : __byte_perm(a, b, 0x5410);

@@ -22,15 +22,16 @@
 // layout, 16 neighbours otherwise, read and written as 16-byte vectors.  A
 // thread keeps one (token, unit), forms its eight sines and cosines once and
 // walks the heads of its chunk with them; the D / 16 threads of a row are
-// neighbours in a warp, so that the exchange of a quantised row (a block's
-// values come from units rot / 2 apart) stays inside the warp.  The next head's
-// vectors are under way while a head is turned and packed (31.5 to 26.6 us for
-// the write and read back below, 25.4 to 24.9 for the rotation).
+// neighbours in a warp.  A quantised row exchanges the largest magnitudes of its
+// vectors there (a block's vectors may come from units rot / 2 apart), not its
+// values (25.5 us against 26.6 for the write and read back below).  The next
+// head's vectors are under way while a head is turned and packed (31.5 to 26.6 us,
+// and 25.4 to 24.9 for the rotation).
 //
 // Bound by memory from a few thousand tokens on, by the launch below that.
 // Measured: 32 heads of 8,192 tokens, 128 values, rotated in 24.9 us (5.4 TB/s
 // of input and output), of 128 tokens in 3.0 us; 8,000 tokens of 8 + 8 heads
-// written to Q8_0 rows and read back in 26.6 us (3.8 TB/s); 32,000 Q8_0 rows of
+// written to Q8_0 rows and read back in 25.5 us (3.9 TB/s); 32,000 Q8_0 rows of
 // 8 heads read back in 17.9 us (5.6 TB/s).
 #include <type_traits>
 
@@ -118,9 +119,9 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
   constexpr int U = D / 16;                  // units (threads) a row
   constexpr int RB = Q8 ? D / 32 * 34 : 2 * D;
   constexpr int kRowsPerWarp = 32 / U;
-  // a warp's rows: fp32 values (16 a lane; the pitch keeps the lanes' 16-byte
-  // accesses apart), then the packed bytes
-  __shared__ __align__(16) float xch[Q8 ? kBlock / 32 : 1][Q8 ? kRowsPerWarp * (D + 4) : 4];
+  // a warp's rows: the largest magnitudes of 8 values each, then the packed bytes
+  constexpr int kTops = D / 8 + 4;
+  __shared__ __align__(16) float tops[Q8 ? kBlock / 32 : 1][Q8 ? kRowsPerWarp * kTops : 4];
   __shared__ __align__(16) uint16_t packed[Q8 ? kBlock / 32 : 1][Q8 ? kRowsPerWarp * RB / 2 : 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = threadIdx.x % U, rw = lane / U;
@@ -190,32 +191,35 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
       unpack8(v0, *reinterpret_cast<float(*)[8]>(x));
       unpack8(v1, *reinterpret_cast<float(*)[8]>(x + 8));
       if (turns) rotate16(x, t, p.interleaved);
-      if (p.rot && !p.interleaved && !isv) {
-        // to the row's own order: lane u takes values 16 u .. 16 u + 15
-        float* xr = &xch[warp][rw * (D + 4)];
-        __syncwarp();
+      // the largest magnitudes of the two vectors' blocks
+      float t0 = 0.f, t1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          *reinterpret_cast<float4*>(xr + lo + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-          *reinterpret_cast<float4*>(xr + hi + i) = make_float4(x[8 + i], x[9 + i], x[10 + i], x[11 + i]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(xr + 16 * u + i);
-          x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
-        }
+      for (int i = 0; i < 8; ++i) {
+        t0 = max_nan(t0, fabsf(x[i]));
+        t1 = max_nan(t1, fabsf(x[8 + i]));
       }
-      uint32_t codes[4];
-      const uint16_t d = q8_encode16(x, codes);
-      // packed row: block u / 2 at byte 34 (u / 2), its half u % 2
-      uint16_t* pr = &packed[warp][rw * (RB / 2) + 17 * (u >> 1)];
+      float* top = &tops[warp][rw * kTops];
       __syncwarp();
-      if (!(u & 1)) pr[0] = d;
+      top[lo >> 3] = t0;
+      top[hi >> 3] = t1;
+      __syncwarp();
+      const float4 b0 = *reinterpret_cast<const float4*>(top + 4 * (lo >> 5));
+      const float4 b1 = *reinterpret_cast<const float4*>(top + 4 * (hi >> 5));
+      uint32_t c0[2], c1[2];
+      const uint16_t d0 = q8_encode8(x, max_nan(max_nan(b0.x, b0.y), max_nan(b0.z, b0.w)), c0);
+      const uint16_t d1 = q8_encode8(x + 8, max_nan(max_nan(b1.x, b1.y), max_nan(b1.z, b1.w)), c1);
+      // packed row: block b at byte 34 b
+      uint16_t* pr = &packed[warp][rw * (RB / 2)];
+      uint16_t* p0 = pr + 17 * (lo >> 5) + ((lo & 31) >> 1);
+      uint16_t* p1 = pr + 17 * (hi >> 5) + ((hi & 31) >> 1);
+      if (!(lo & 31)) p0[0] = d0;
+      if (!(hi & 31)) p1[0] = d1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pr[1 + 8 * (u & 1) + 2 * i] = (uint16_t)codes[i];
-        pr[2 + 8 * (u & 1) + 2 * i] = (uint16_t)(codes[i] >> 16);
+      for (int i = 0; i < 2; ++i) {
+        p0[1 + 2 * i] = (uint16_t)c0[i];
+        p0[2 + 2 * i] = (uint16_t)(c0[i] >> 16);
+        p1[1 + 2 * i] = (uint16_t)c1[i];
+        p1[2 + 2 * i] = (uint16_t)(c1[i] >> 16);
       }
       __syncwarp();
       // the row's threads copy it out in whole 8-byte (D = 128) or 4-byte words

@@ -25,12 +25,17 @@
 // for 256 rows over 32K Q8_0 keys: both teams then wait for the same tile.)
 //
 // Measured: 8 sequences of 24 nodes, 4 heads a group, D = 64, over 1,000 to 8,100
-// fp16 keys in 33.7 us (75.6 MB: 2.2 TB/s), one of 64 nodes, D = 128, over 32,500
+// fp16 keys in 32.8 us (75.6 MB: 2.3 TB/s), one of 64 nodes, D = 128, over 32,500
 // Q8_0 keys in 55.7 us (34 GFLOP: 612 TFLOP/s).  Long calls are at HBM for fp16 at
-// D = 128 (1.38 us a tile and SM, 7.2 TB/s), at 4.5 TB/s for D = 64, and Q8_0 at D =
-// 128 takes 1.3 us a tile; there a team's chain of a tile bounds them (scores 650 to
-// 950 clocks, maxima 500, exponentials 1300, hand-over 350, P V 700), short calls the
-// start (schedule, Q: 3 us), the end of a run (2 us) and the join (3 us).
+// D = 128 (1.38 us a tile and SM, 7.2 TB/s) and at 5.5 TB/s for D = 64 (0.91 us a
+// tile), and Q8_0 at D = 128 takes 1.3 us a tile: there a team's chain of a tile bounds
+// them (scores 650 to 950 clocks, maxima 500, exponentials 1300, hand-over 350, P V
+// 700); short calls the start (schedule, Q: 3 us), the end of a run (2 us) and the
+// join (3 us).
+//
+// TMEM holds two O and, at D = 64, three score buffers: a team's next scores are
+// formed in the third while it works on the last ones, off its chain (1.10 to 0.91
+// us a tile).  At D = 128 there are two, one a team, whose P lies over its S.
 //
 // Warps (fp16 768 threads, Q8_0 896):
 //   0, 1    one lane each issues the MMAs of tile team 0 or 1 (tiles of even
@@ -83,7 +88,8 @@ struct TreeCfg {
   static constexpr int kRaw = kTile * kRow + 32;       // a tile, its 16-byte shift, and the decode's overread
   static constexpr int kPrep = Q8 ? 8 : 4;             // preparing warps
   static constexpr int kThreads = 32 * (4 + kSoft + kPrep);
-  static constexpr int kBars = 2 * kKS + 4 * kVS + 3 * kRS + 12;
+  static constexpr int kSB = D == 64 ? 3 : 2;          // score buffers
+  static constexpr int kBars = 2 * kKS + 4 * kVS + 3 * kRS + 17;
   static constexpr int kFixed = 8 * kTile * 4          // ancestor bits [8][128]
                                 + 6 * kTile * 4        // maxima [team][half][128], sums [team][128]
                                 + 2 * 2 * kTile * 8    // (m, l) [parity][team][128]
@@ -93,7 +99,7 @@ struct TreeCfg {
                                 + kBars * 8 + 16;
   static constexpr int kSmem =
       1024 + (1 + kKS + kVS) * kTileBytes + kRS * kRaw + kFixed;
-  static constexpr uint32_t kOCol = 256;               // O of team t at kOCol + t D, S/P at 128 t
+  static constexpr uint32_t kOCol = 128 * kSB;         // O of team t at kOCol + t D, S/P buffers at 128 i
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kRaw % 16 == 0, "bulk copy alignment");
 };
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const TreeParams p) {
   using Cfg = TreeCfg<D, Q8>;
-  constexpr int PW = Cfg::kPrep, KS = Cfg::kKS, VS = Cfg::kVS, RS = Cfg::kRS > 0 ? Cfg::kRS : 1;
+  constexpr int SB = Cfg::kSB, PW = Cfg::kPrep, KS = Cfg::kKS, VS = Cfg::kVS, RS = Cfg::kRS > 0 ? Cfg::kRS : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_align<1024>(smem_raw);
   uint8_t* kst = qs + Cfg::kTileBytes;
@@ -146,10 +152,10 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
   uint64_t* v_empty = v_clean + VS;    // [VS] P V done with it
   uint64_t* r_full = v_empty + VS;     // [2][RS] raw tile (K, V) landed in a slot
   uint64_t* r_empty = r_full + 2 * Cfg::kRS;
-  uint64_t* s_full = r_empty + Cfg::kRS;   // [2] S of a team's tile in TMEM
-  uint64_t* p_full = s_full + 2;       // [2] its P written
-  uint64_t* pv_done = p_full + 2;      // [2] its P V done
-  uint64_t* q_full = pv_done + 2;      // Q of a run written
+  uint64_t* s_full = r_empty + Cfg::kRS;   // [team][2] S of the team's tile n (n % 2) in TMEM
+  uint64_t* p_full = s_full + 4;       // [team][2] its P written
+  uint64_t* pv_done = p_full + 4;      // [SB] P V of a buffer's tile done
+  uint64_t* q_full = pv_done + 3;      // Q of a run written
   uint64_t* q_empty = q_full + 1;      // both teams' S of a run done
   uint64_t* ml_rdy = q_empty + 1;      // softmax: (m, l) of a run written
   uint64_t* nf_rdy = ml_rdy + 1;       // preparation of a run's tiles done (noted rows final)
@@ -175,11 +181,11 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
       mbar_init(&r_full[Cfg::kRS + i], 1);
       mbar_init(&r_empty[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 8);
-      mbar_init(&pv_done[i], 1);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(&pv_done[i], 1);
     mbar_init(q_full, PW);
     mbar_init(q_empty, 2);
     mbar_init(ml_rdy, 8);
@@ -216,10 +222,10 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
       const uint64_t qd = sdesc_sw128_kmajor(smem_u32(qs));
       const uint64_t kd = sdesc_sw128_kmajor(smem_u32(kst));
       const uint64_t vd = sdesc_sw128_nmajor(smem_u32(vst), kTile * 128);
-      const uint32_t scol = tmem + 128 * team, ocol = tmem + Cfg::kOCol + D * team;
+      const uint32_t ocol = tmem + Cfg::kOCol + D * team;
       uint32_t full_ph = 0, clean_ph = 0;   // phase bits of v_full and v_clean of each stage
       bool ok = true;
-      int g = 0, nt = 0;          // tiles of the CTA, tiles of the team
+      int g = 0;                  // tiles of the CTA
       Ring<KS> kr;
       Ring<VS> vr;
       for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
@@ -227,15 +233,17 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
         // The team's next tile of the run: its stages and barriers.  Looked up while
         // the softmax has the last one: after P V it would cost 500 to 700 clocks of
         // a chain of 5000.
-        struct {
-          int ks, vs;
+        struct Tile {
+          int x, ks, vs;              // number in the CTA, stages
           uint32_t k_ph, v_ph;
           uint64_t* v_ready;
-        } at;
+        };
+        Tile at{};
         int j = sg.k0;
         auto look = [&]() {
           for (; j < sg.k1;) {
             const bool wants_clean = !Q8 && j >= jm, mine = (g & 1) == team;
+            at.x = g;
             at.ks = kr.at;
             at.k_ph = kr.ph;
             at.vs = vr.at;
@@ -249,41 +257,56 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
           }
           return false;
         };
-        bool first = true, more = look();
-        ok = mbar_wait(q_full, w & 1, ctl);
-        if (ok && !more) tc_commit(q_empty);
-        while (ok && more) {
-          ok = mbar_wait(&k_full[at.ks], at.k_ph, ctl);
-          if (nt > 0) ok = ok && mbar_wait(&pv_done[team], (nt - 1) & 1, ctl);   // S and P share columns
-          if (!ok) break;
+        // P V of tile x done (its buffer's x / SB-th use)
+        auto pv_wait = [&](int x) { return x < 0 || mbar_wait(&pv_done[x % SB], (x / SB) & 1, ctl); };
+        // S of the tile looked up, into its buffer, which is free
+        auto scores = [&]() {
+          if (!mbar_wait(&k_full[at.ks], at.k_ph, ctl)) return false;
           tc_fence_after();
           const uint64_t kds = kd + (uint64_t)(at.ks * (Cfg::kTileBytes >> 4));
+          const uint32_t scol = tmem + 128 * (at.x % SB);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (kTile * 128 >> 4) + 2 * (kk & 3);
             mma_ss_f16(scol, qd + off, kds + off, idesc_s, kk > 0 ? 1u : 0u);
           }
-          tc_commit(&s_full[team]);
+          tc_commit(&s_full[2 * team + ((at.x >> 1) & 1)]);
           tc_commit(&k_empty[at.ks]);
-          const int vs = at.vs;
-          const uint64_t vds = vd + (uint64_t)(vs * (Cfg::kTileBytes >> 4));
-          uint64_t* v_ready = at.v_ready;
-          const uint32_t v_ph = at.v_ph;
+          return true;
+        };
+        bool first = true, more = look();
+        ok = mbar_wait(q_full, w & 1, ctl);
+        if (ok && !more) tc_commit(q_empty);
+        if (ok && more && SB == 3) ok = pv_wait(at.x - 3) && scores();
+        while (ok && more) {
+          if (SB == 2) {
+            ok = pv_wait(at.x - 2) && scores();
+            if (!ok) break;
+          }
+          const Tile now = at;
           more = look();
+          if constexpr (SB == 3) {
+            // The next scores, a tile ahead, into the buffer of the other team's last
+            // tile.  Waited for without a next tile too: P V of all tiles go in order,
+            // so that no barrier is ever two phases past a wait for it.
+            ok = pv_wait(now.x - 1) && (!more || scores());
+            if (!ok) break;
+          }
           if (!more) tc_commit(q_empty);   // this team's S of the run are done with Q
-          ok = mbar_wait(v_ready, v_ph, ctl);
+          ok = mbar_wait(now.v_ready, now.v_ph, ctl);
           if (first && w > 0) ok = ok && mbar_wait(o_free, (w - 1) & 1, ctl);
-          ok = ok && mbar_wait(&p_full[team], nt & 1, ctl);
+          ok = ok && mbar_wait(&p_full[2 * team + ((now.x >> 1) & 1)], (now.x >> 2) & 1, ctl);
           if (!ok) break;
           tc_fence_after();
+          const uint64_t vds = vd + (uint64_t)(now.vs * (Cfg::kTileBytes >> 4));
+          const uint32_t scol = tmem + 128 * (now.x % SB);
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
             tc_mma_ts_f16(ocol, scol + 64 * (kk >> 2) + 8 * (kk & 3), vds + (uint32_t)(kk * (2048 >> 4)), idesc_o,
                           (kk > 0 || !first) ? 1u : 0u);
-          tc_commit(&pv_done[team]);
-          tc_commit(&v_empty[vs]);
+          tc_commit(&pv_done[now.x % SB]);
+          tc_commit(&v_empty[now.vs]);
           first = false;
-          ++nt;
         }
       }
       tc_commit(drain);
@@ -349,7 +372,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
     const int team = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3;
     const int r = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    const uint32_t scol = tmem + lanes + 128 * team + 64 * half;               // its 64 keys' scores, then P
+    const uint32_t scol0 = tmem + lanes + 64 * half;                           // buffer 0: its 64 keys' scores, then P
     const uint32_t ocol = tmem + lanes + Cfg::kOCol + D * team + D / 2 * half;   // the columns it rescales
     uint32_t* anc = anc_all + r;   // this row's bits: word i at anc[128 i]
     // named barriers: the four warps of these rows, and the two of a team
@@ -361,7 +384,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
     const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
     const int R = p.N * p.G;
     bool ok = true;
-    int g = 0, n0 = 0, n1 = 0;                  // tiles of the CTA, of team 0, of team 1
+    int g = 0;                                  // tiles of the CTA
     bool fresh = true;                          // the CTA's first run
     for (int w = 0; ok && tree_next(p, sched, walk, sg); ++w) {
       const int row = sg.rt * kTile + r;
@@ -379,18 +402,15 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
       float m = -INFINITY, l = 0.f;
       bool first = true;
       for (int j = sg.k0; j < sg.k1; ++j, ++g) {
-        if ((g & 1) != team) {
-          (team ? n0 : n1)++;
-          continue;
-        }
-        int& nt = team ? n1 : n0;
+        if ((g & 1) != team) continue;
+        const int sp = 2 * team + ((g >> 1) & 1);
+        const uint32_t ph = (g >> 2) & 1, scol = scol0 + 128 * (g % SB);
         // warps without a row stay out of the others' way while they wait
-        ok = __all_sync(0xffffffffu, busy ? mbar_wait(&s_full[team], nt & 1, ctl)
-                                          : mbar_wait_idle(&s_full[team], nt & 1, ctl, 256));
-        ++nt;
+        ok = __all_sync(0xffffffffu, busy ? mbar_wait(&s_full[sp], ph, ctl)
+                                          : mbar_wait_idle(&s_full[sp], ph, ctl, 256));
         if (!busy) {
           if (!ok) break;
-          mbar_arrive_warp(&p_full[team]);
+          mbar_arrive_warp(&p_full[sp]);
           continue;
         }
         tc_fence_after();
@@ -433,7 +453,13 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
         const float mj = mu > m + kRaise || m == -INFINITY ? fmaxf(mu, m) : m;
         const bool raise = mj > m && !first && m != -INFINITY;
         if (__any_sync(0xffffffffu, raise)) {
-          // the team's earlier P V are done (its next S waits for them)
+          // the team's last P V is done (with two buffers S has waited for it; with
+          // three, PV of the buffer's next tile comes after this tile's)
+          if (SB == 3) {
+            mbar_wait(&pv_done[(g - 2) % SB], ((g - 2) / SB) & 1, ctl);
+            __syncwarp();
+            tc_fence_after();
+          }
           const float a = raise ? ex2(m - mj) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -477,7 +503,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
         first = false;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive_warp(&p_full[team]);
+        mbar_arrive_warp(&p_full[sp]);
       }
       // ---------------------------------------------------------- end of a run
       const int par = w & 1;
@@ -489,8 +515,9 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
       }
       const int g0 = g - (sg.k1 - sg.k0);
       bool got = ok && mbar_wait(ml_rdy, par, ctl) && mbar_wait(nf_rdy, par, ctl);
-      if (n0 > 0) got = got && mbar_wait(&pv_done[0], (n0 - 1) & 1, ctl);
-      if (n1 > 0) got = got && mbar_wait(&pv_done[1], (n1 - 1) & 1, ctl);
+      // (of three buffers the last tile's: P V go in order)
+      got = got && mbar_wait(&pv_done[(g - 1) % SB], ((g - 1) / SB) & 1, ctl);
+      if (SB == 2 && g > 1) got = got && mbar_wait(&pv_done[(g - 2) % SB], ((g - 2) / SB) & 1, ctl);
       ok = !vote_or(quad_bar, 128, !got);
       if (!ok) break;
       tc_fence_after();

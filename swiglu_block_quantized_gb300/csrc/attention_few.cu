@@ -42,6 +42,7 @@
 #include <algorithm>
 
 #include "tree_common.cuh"
+#include "tree_rings.h"
 
 namespace m4q {
 
@@ -54,14 +55,15 @@ struct FewCfg {
   static constexpr int kTileBytes = kTile * D * 2;     // an fp16 tile: D / 64 panels of [128][128 B]
   static constexpr int kQBytes = N * D * 2;            // D / 64 panels of [N][128 B]
   static constexpr int kPBytes = N * kTile * 2;        // two panels (64 keys) of [N][128 B]
-  static constexpr int kKS = Q8 ? 3 : D == 128 ? 3 : 6;   // K stages (Q8_0: in TMEM)
-  static constexpr int kVS = D == 128 ? 3 : Q8 ? 4 : 6;
+  static constexpr FewRings kRings = few_rings(D, Q8, NC);
+  static constexpr int kKS = kRings.ks;                // K stages (Q8_0: in TMEM)
+  static constexpr int kVS = kRings.vs;
   static constexpr int kRaw = kTile * kRow + 32;       // a raw tile, its 16-byte shift, and the decode's overread
-  static constexpr int kRS = Q8 ? (D == 64 ? 10 : NC == 1 ? 6 : 5) : 0;
-  static constexpr int kGroups = Q8 && NC == 1 ? 2 : 1;  // Q8_0: groups of 4 warps that take K (and V) tiles in turn
+  static constexpr int kRS = kRings.rs;
+  static constexpr int kGroups = kRings.groups;
   static constexpr int kPrep = Q8 ? 8 * kGroups : 4;   // preparing warps
   static constexpr int kThreads = 32 * (12 + kPrep);
-  static constexpr int kBars = 2 * kKS + 4 * kVS + 2 * kRS + 8 + 4 + 7;
+  static constexpr int kBars = 2 * kKS + 4 * kVS + 3 * kRS + 8 + 4 + 7;
   static constexpr int kFixed = (int)sizeof(TreeSched) + 2 * 8 * 16   // schedule, noted rows
                                 + 8 * 32 * 4                          // ancestor bits by warp
                                 + 2 * 4 * N * 4 + 4 * N * 4           // wmax, mref and fac by team
@@ -74,7 +76,7 @@ struct FewCfg {
   static constexpr uint32_t kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(kUsed <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static_assert(kGroups == 1 || (kRS / 2 >= kKS && kRS / 2 >= kVS), "a raw slot is used again after its stage");
+  static_assert(few_groups_ok(kRings), "a raw slot is used again after its stage");
   static_assert(kRaw % 16 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "alignment");
 };
 
@@ -164,8 +166,8 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
   uint64_t* v_raw = v_full + VS;       // [VS] (fp16) V of a masked tile, not yet cleared
   uint64_t* v_clean = v_raw + VS;      // [VS] (fp16) V of a masked tile, cleared
   uint64_t* v_empty = v_clean + VS;    // [VS] P V done with it
-  uint64_t* r_full = v_empty + VS;     // [RS] raw tile landed
-  uint64_t* r_empty = r_full + Cfg::kRS;
+  uint64_t* r_full = v_empty + VS;     // [2][RS] raw tile (K, V) landed in a slot
+  uint64_t* r_empty = r_full + 2 * Cfg::kRS;
   uint64_t* s_full = r_empty + Cfg::kRS;   // [4] S^T of a tile in TMEM
   uint64_t* s_free = s_full + 4;       // [4] read
   uint64_t* p_full = s_free + 4;       // [2] P^T written
@@ -193,7 +195,8 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < Cfg::kRS; ++i) {
-      mbar_init(&r_full[i], 1);
+      mbar_init(&r_full[few_raw_bar(Cfg::kRS, 0, i)], 1);
+      mbar_init(&r_full[few_raw_bar(Cfg::kRS, 1, i)], 1);
       mbar_init(&r_empty[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
@@ -336,12 +339,13 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
               long long at;
               uint32_t bytes;
               raw_span(head, p.C, Cfg::kRow, j, last, at, bytes);
-              full_ph ^= 1u << sl;
-              mbar_arrive_expect_tx(&full[sl], bytes);
+              const int rb = few_raw_bar(Cfg::kRS, kv, sl);
+              full_ph ^= 1u << rb;
+              mbar_arrive_expect_tx(&full[rb], bytes);
               if (in_bounds(at >= 0 && bytes > 0 && bytes <= (uint32_t)Cfg::kRaw &&
                                 at + bytes <= (long long)p.B_all * p.Hkv * p.C * Cfg::kRow,
                             p.status, kSiteTreeKV))
-                bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + at, bytes, &full[sl]);
+                bulk_load(ring + sl * Cfg::kRaw, (kv ? p.v : p.k) + at, bytes, &full[rb]);
             } else {
               // V of a masked tile goes by way of the clearing warps
               const bool raw = warp == 3 && j >= jm;
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
           }
       }
       if (!ok)   // copies in flight land before the CTA can leave: the last armed phase of each barrier
-        for (int i = 0; i < ns; ++i) {
+        for (int i = 0; i < (Q8 ? 2 * ns : ns); ++i) {
           mbar_wait_drain(&full[i], ((full_ph >> i) & 1) ^ 1, 100000000ull);
           if (!Q8 && warp == 3) mbar_wait_drain(&v_raw[i], ((raw_ph >> i) & 1) ^ 1, 100000000ull);
         }
@@ -589,7 +593,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
     const DecK K = make_deck();
     bool ok = true;
     int g = 0;
-    uint32_t raw_ph = 0;                        // phase bits of v_raw of each stage
+    uint32_t raw_ph = 0;                        // phase bits of v_raw of each stage, or of r_full of each slot
     Ring<KS> kr;
     Ring<VS> vr;
     Ring<RS> rr;
@@ -633,17 +637,19 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
         const int ks = kr.at, vs = vr.at;
         if constexpr (Q8) {
           const int rs = rr.at;
-          const uint32_t rph = rr.ph;
+          const uint32_t rph = (raw_ph >> rs) & 1u;   // of the slot's barrier for this kind of tile
+          raw_ph ^= 1u << rs;
           rr.step();   // K and V tiles alternate in the raw ring
           rr.step();
           if (PG > 1 && (g & 1) != turn) continue;
           const int sh = (int)(((head * p.C + (long long)j * kTile) * Cfg::kRow) & 15);
-          // The stage first: its last tile's MMAs are done, so the raw slot's last
-          // tile (the other group's, perhaps, and no later one: static_assert) has
-          // landed, and the slot's parity can only mean this tile.
+          // The stage first: with two groups of a kind the slot's last tile is the other
+          // group's, and was decoded before the stage's last tile was read (few_groups_ok),
+          // so that the parity can only mean this tile.  One group waits for every tile
+          // that lands on its kind's barrier of the slot.
           bool go = true;
           if (kv == 0 ? g >= KS : g >= VS) go = mbar_wait(kv ? &v_empty[vs] : &k_empty[ks], (kv ? vr.ph : kr.ph) ^ 1u, ctl);
-          go = go && mbar_wait(&r_full[rs], rph, ctl);
+          go = go && mbar_wait(&r_full[few_raw_bar(Cfg::kRS, kv, rs)], rph, ctl);
           ok = __all_sync(0xffffffffu, go);
           if (!ok) break;
           const uint8_t* src = raws + rs * Cfg::kRaw + sh;

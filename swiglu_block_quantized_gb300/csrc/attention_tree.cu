@@ -71,6 +71,7 @@
 #include <algorithm>
 
 #include "tree_common.cuh"
+#include "tree_rings.h"
 
 namespace m4q {
 
@@ -82,14 +83,15 @@ template <int D, bool Q8>
 struct TreeCfg {
   static constexpr int kRow = Q8 ? D / 32 * 34 : 2 * D;
   static constexpr int kTileBytes = kTile * D * 2;     // an fp16 tile: D / 64 panels of [128][128 B]
-  static constexpr int kKS = Q8 ? 2 : D == 128 ? 3 : 6;
-  static constexpr int kVS = Q8 ? 2 : D == 128 ? 2 : 5;
-  static constexpr int kRS = Q8 ? (D == 128 ? 3 : 8) : 0;       // raw ring (K, V, K, ...)
+  static constexpr RowsRings kRings = rows_rings(D, Q8);
+  static constexpr int kKS = kRings.ks;
+  static constexpr int kVS = kRings.vs;
+  static constexpr int kRS = kRings.rs;                // raw ring (K, V, K, ...)
   static constexpr int kRaw = kTile * kRow + 32;       // a tile, its 16-byte shift, and the decode's overread
   static constexpr int kPrep = Q8 ? 8 : 4;             // preparing warps
   static constexpr int kThreads = 32 * (4 + kSoft + kPrep);
-  static constexpr int kSB = D == 64 ? 3 : 2;          // score buffers
-  static constexpr int kBars = 2 * kKS + 4 * kVS + 3 * kRS + 17;
+  static constexpr int kSB = kRings.sb;                // score buffers
+  static constexpr int kBars = 3 * kKS + 4 * kVS + 3 * kRS + 17;
   static constexpr int kFixed = 8 * kTile * 4          // ancestor bits [8][128]
                                 + 6 * kTile * 4        // maxima [team][half][128], sums [team][128]
                                 + 2 * 2 * kTile * 8    // (m, l) [parity][team][128]
@@ -144,8 +146,8 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
   int16_t* up = reinterpret_cast<int16_t*>(noted + 64);                           // [256]
   TreeSched* sched = reinterpret_cast<TreeSched*>(up + 256);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sched) +
-                                                  (sizeof(TreeSched) + 7) / 8 * 8);   // [KS] K of a tile in its stage
-  uint64_t* k_empty = k_full + KS;     // [KS] S done with it
+                                                  (sizeof(TreeSched) + 7) / 8 * 8);   // [team][KS] K of a tile in its stage
+  uint64_t* k_empty = k_full + 2 * KS; // [KS] S done with it
   uint64_t* v_full = k_empty + KS;     // [VS] V of a tile in its stage
   uint64_t* v_raw = v_full + VS;       // [VS] (fp16) V of a masked tile, not yet cleared (v_full: the others')
   uint64_t* v_clean = v_raw + VS;      // [VS] (fp16) V of a masked tile, cleared
@@ -167,7 +169,8 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) {
-      mbar_init(&k_full[i], Q8 ? 4 : 1);
+      mbar_init(&k_full[rows_k_bar(KS, 0, i)], Q8 ? 4 : 1);
+      mbar_init(&k_full[rows_k_bar(KS, 1, i)], Q8 ? 4 : 1);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < VS; ++i) {
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
       const uint64_t kd = sdesc_sw128_kmajor(smem_u32(kst));
       const uint64_t vd = sdesc_sw128_nmajor(smem_u32(vst), kTile * 128);
       const uint32_t ocol = tmem + Cfg::kOCol + D * team;
-      uint32_t full_ph = 0, clean_ph = 0;   // phase bits of v_full and v_clean of each stage
+      uint32_t k_ph = 0, full_ph = 0, clean_ph = 0;   // phase bits of the team's k_full, of v_full and v_clean
       bool ok = true;
       int g = 0;                  // tiles of the CTA
       Ring<KS> kr;
@@ -245,7 +248,8 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
             const bool wants_clean = !Q8 && j >= jm, mine = (g & 1) == team;
             at.x = g;
             at.ks = kr.at;
-            at.k_ph = kr.ph;
+            at.k_ph = (k_ph >> kr.at) & 1u;
+            if (mine) k_ph ^= 1u << kr.at;
             at.vs = vr.at;
             at.v_ready = wants_clean ? &v_clean[vr.at] : &v_full[vr.at];
             at.v_ph = ((wants_clean ? clean_ph : full_ph) >> vr.at) & 1u;
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
         auto pv_wait = [&](int x) { return x < 0 || mbar_wait(&pv_done[x % SB], (x / SB) & 1, ctl); };
         // S of the tile looked up, into its buffer, which is free
         auto scores = [&]() {
-          if (!mbar_wait(&k_full[at.ks], at.k_ph, ctl)) return false;
+          if (!mbar_wait(&k_full[rows_k_bar(KS, team, at.ks)], at.k_ph, ctl)) return false;
           tc_fence_after();
           const uint64_t kds = kd + (uint64_t)(at.ks * (Cfg::kTileBytes >> 4));
           const uint32_t scol = tmem + 128 * (at.x % SB);
@@ -348,8 +352,9 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
             } else {
               // V of a masked tile goes by way of the clearing warps
               const bool raw = warp == 3 && j >= jm;
-              uint64_t* bar = raw ? &v_raw[sl] : &full[sl];
-              (raw ? raw_ph : full_ph) ^= 1u << sl;
+              const int fb = warp == 2 ? rows_k_bar(KS, n & 1, sl) : sl;
+              uint64_t* bar = raw ? &v_raw[sl] : &full[fb];
+              (raw ? raw_ph : full_ph) ^= 1u << (raw ? sl : fb);
               mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
 #pragma unroll
               for (int pn = 0; pn < D / 64; ++pn)
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
           }
       }
       if (!ok)   // copies in flight land before the CTA can leave: the last armed phase of each barrier
-        for (int i = 0; i < (Q8 ? 2 * ns : ns); ++i) {
+        for (int i = 0; i < (Q8 || warp == 2 ? 2 * ns : ns); ++i) {
           mbar_wait_drain(&full[i], ((full_ph >> i) & 1) ^ 1, 100000000ull);
           if (!Q8 && warp == 3) mbar_wait_drain(&v_raw[i], ((raw_ph >> i) & 1) ^ 1, 100000000ull);
         }
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
             if (lane == 0) nt[j - jm] = bits & rows_in_use(p, sg, j * kTile + 32 * (pw & 3));
           }
           fence_proxy_async_smem();
-          mbar_arrive_warp(kv ? &v_full[st] : &k_full[st]);
+          mbar_arrive_warp(kv ? &v_full[st] : &k_full[rows_k_bar(KS, g & 1, st)]);
           mbar_arrive_warp(&r_empty[rs]);
         } else if (j >= jm) {
           ok = __all_sync(0xffffffffu, mbar_wait_idle(&v_raw[vs], (raw_ph >> vs) & 1, run_ctl, 64));

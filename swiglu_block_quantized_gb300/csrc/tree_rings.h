@@ -36,4 +36,22 @@ constexpr bool few_groups_ok(const FewRings& r) {
   return r.groups == 1 || (r.rs % 2 == 0 && r.rs / 2 >= r.ks && r.rs / 2 >= r.vs);
 }
 
+
+// attention_tree.cu: two tile teams, each with an MMA issuer of its own, take the
+// tiles in turn.
+struct RowsRings {
+  int ks, vs;   // K and V stages
+  int rs;       // Q8_0: slots of raw tiles, K, V, K, ...
+  int sb;       // score buffers
+};
+constexpr RowsRings rows_rings(int d, bool q8) {
+  return q8 ? RowsRings{2, 2, d == 128 ? 3 : 8, d == 64 ? 3 : 2} : RowsRings{d == 128 ? 3 : 6, d == 128 ? 2 : 5, 0, d == 64 ? 3 : 2};
+}
+// Landing barrier of a team's K tile in a stage.  With an odd ring a stage holds the
+// teams' tiles in turn, and with two score buffers nothing keeps an issuer from its
+// next tile until the other team's last one has landed.  (V has one barrier a stage:
+// there a stage is always the same team's, or the third score buffer keeps P V of all
+// tiles in order.)
+M4Q_HD constexpr int rows_k_bar(int ks, int team, int stage) { return team * ks + stage; }
+
 }  // namespace m4q

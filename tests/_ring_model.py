@@ -309,7 +309,220 @@ FEW_ROLES = ["S issuer", "PV issuer", "copies", "K copies", "V copies", "softmax
              "prepare 1", "prepare %d" % W, "prepare %d" % (2 * W), "prepare %d" % (3 * W)]
 
 
+def rows(geo, q8, runs, seed, held):
+    """tree_kernel: geo = ks, vs, rs, sb (score buffers) and k_bar[team][stage], the
+    landing barrier of a K stage (csrc/tree_rings.h)."""
+    ks_n, vs_n, rs_n, sb_n = geo["ks"], geo["vs"], geo["rs"], geo["sb"]
+    sim = Sim(seed, held)
+    tiles = tiles_of(runs)
+    quads = (0, 1)                      # two stand for four; the second has no row
+    soft = 2 * 2 * len(quads)           # teams, halves
+    prep_w = 2 * W if q8 else W
+    k_full, k_empty = Ring(2 * ks_n, "k_full", W if q8 else 1), Ring(ks_n, "k_empty")
+    v_full, v_empty = Ring(vs_n, "v_full", W if q8 else 1), Ring(vs_n, "v_empty")
+    v_raw, v_clean = Ring(vs_n, "v_raw"), Ring(vs_n, "v_clean", prep_w)
+    r_full, r_empty = Ring(2 * rs_n, "r_full"), Ring(rs_n, "r_empty", W)
+    s_full, p_full = Ring(4, "s_full"), Ring(4, "p_full", 2 * len(quads))
+    pv_done = Ring(sb_n, "pv_done")
+    q_full, q_empty = Bar("q_full", prep_w), Bar("q_empty", 2)
+    ml_rdy, nf_rdy, o_free = Bar("ml_rdy", 2 * len(quads)), Bar("nf_rdy", prep_w), Bar("o_free", soft)
+    kst, vst, raw, buf = {}, {}, {}, {}
+
+    def holds(store, key, tile, what):
+        if store.get(key) != tile:
+            raise Fault("%s of tile %s read from %s, which holds %s" % (what, tile, key, store.get(key)))
+
+    k_land, r_land, v_land, team_use = Uses(), Uses(), Uses(), Uses()
+    for g, (_, _, masked) in enumerate(tiles):
+        k_land.add(geo["k_bar"][g & 1][g % ks_n], g)
+        v_land.add(("clean" if not q8 and masked else "full", g % vs_n), g)
+        team_use.add(2 * (g & 1) + ((g >> 1) & 1), g)
+        for kv in range(2):
+            if q8:
+                r_land.add((kv, (2 * g + kv) % rs_n), g)
+
+    def sp_of(g):
+        return 2 * (g & 1) + ((g >> 1) & 1)
+
+    def issue(team):
+        yield STEP
+        g = 0
+        who = "S%d" % team
+
+        def pv_wait(x):
+            if x >= 0:
+                yield wait(pv_done[x % sb_n], x // sb_n)
+
+        def scores(x):
+            st = x % ks_n
+            yield wait(k_full[geo["k_bar"][team][st]], k_land(geo["k_bar"][team][st], x))
+            holds(kst, st, x, "K")
+
+            def done():
+                holds(kst, st, x, "K")
+                buf[x % sb_n] = ("s", x)
+                s_full[sp_of(x)].arrive()
+                k_empty[st].arrive()
+            sim.later(who, "%s %d" % (who, x), done)
+
+        for w, (n, mk) in enumerate(runs):
+            mine = [(x, x - g >= n - mk) for x in range(g, g + n) if (x & 1) == team]
+            g += n
+            yield wait(q_full, w)
+            if not mine:
+                sim.later(who, "%s q %d" % (who, w), q_empty.arrive)
+                continue
+            if sb_n == 3:
+                yield from pv_wait(mine[0][0] - 3)
+                yield from scores(mine[0][0])
+            for i, (x, masked) in enumerate(mine):
+                more = i + 1 < len(mine)
+                if sb_n == 2:
+                    yield from pv_wait(x - 2)
+                    yield from scores(x)
+                else:
+                    yield from pv_wait(x - 1)
+                    if more:
+                        yield from scores(mine[i + 1][0])
+                if not more:
+                    sim.later(who, "%s q %d" % (who, w), q_empty.arrive)
+                vs = x % vs_n
+                clean = not q8 and masked
+                yield wait((v_clean if clean else v_full)[vs], v_land(("clean" if clean else "full", vs), x))
+                if i == 0 and w > 0:
+                    yield wait(o_free, w - 1)
+                yield wait(p_full[sp_of(x)], team_use(sp_of(x), x))
+                holds(vst, vs, x, "V")
+                holds(buf, x % sb_n, ("p", x), "P")
+
+                def done(x=x, vs=vs):
+                    holds(vst, vs, x, "V")
+                    holds(buf, x % sb_n, ("p", x), "P")
+                    pv_done[x % sb_n].arrive()
+                    v_empty[vs].arrive()
+                sim.later(who, "%s PV %d" % (who, x), done)
+
+    def copies(kinds):
+        yield STEP
+        n = 0
+        for g, (_, _, masked) in enumerate(tiles):
+            for kv in kinds:
+                if q8:
+                    sl = n % rs_n
+                    if n >= rs_n:
+                        yield wait(r_empty[sl], n // rs_n - 1)
+
+                    def lands(sl=sl, kv=kv, g=g):
+                        raw[sl] = (kv, g)
+                        r_full[kv * rs_n + sl].arrive()
+                else:
+                    size = vs_n if kv else ks_n
+                    sl = n % size
+                    if n >= size:
+                        yield wait((v_empty if kv else k_empty)[sl], n // size - 1)
+
+                    def lands(sl=sl, kv=kv, g=g, masked=masked):
+                        (vst if kv else kst)[sl] = g
+                        if kv:
+                            (v_raw if masked else v_full)[sl].arrive()
+                        else:
+                            k_full[geo["k_bar"][g & 1][sl]].arrive()
+                sim.later(("copy", kv, g), "copy %d %d" % (kv, g), lands)
+                n += 1
+
+    def softmax(team, half, quad):
+        busy = quad == 0
+        pair, whole = "pair %d %d" % (team, quad), "quad %d" % quad
+        yield STEP
+        g = 0
+        for w, (n, mk) in enumerate(runs):
+            if busy and mk:
+                yield ("sync", whole, 4)
+                yield ("sync", whole, 4)
+            for i in range(n):
+                x, g = g, g + 1
+                if (x & 1) != team:
+                    continue
+                sp = sp_of(x)
+                yield wait(s_full[sp], team_use(sp, x))
+                if not busy:
+                    p_full[sp].arrive()
+                    continue
+                holds(buf, x % sb_n, ("s", x) if not half else buf.get(x % sb_n), "S")
+                yield ("sync", pair, 2)
+                yield STEP
+                if sb_n == 3 and i >= 2 and sim.rng.random() < 0.5:   # references rise
+                    yield wait(pv_done[(x - 2) % sb_n], (x - 2) // sb_n)
+                yield STEP
+                buf[x % sb_n] = ("p", x)
+                p_full[sp].arrive()
+            yield ("sync", pair, 2)
+            yield STEP
+            if not half:
+                ml_rdy.arrive()
+            yield wait(ml_rdy, w)
+            yield wait(nf_rdy, w)
+            yield wait(pv_done[(g - 1) % sb_n], (g - 1) // sb_n)
+            if sb_n == 2 and g > 1:
+                yield wait(pv_done[(g - 2) % sb_n], (g - 2) // sb_n)
+            yield ("sync", whole, 4)
+            o_free.arrive()
+
+    def prepare(pw):
+        kv = pw // W
+        raw_waits = {}
+        yield STEP
+        g = 0
+        for w, (n, mk) in enumerate(runs):
+            if w > 0:
+                yield wait(q_empty, w - 1)
+            q_full.arrive()
+            for i in range(n):
+                ks, vs = g % ks_n, g % vs_n
+                if q8:
+                    rs = (2 * g + kv) % rs_n
+                    yield wait(r_full[kv * rs_n + rs], r_land((kv, rs), g))
+                    st, size = (vs, vs_n) if kv else (ks, ks_n)
+                    if g >= size:
+                        yield wait((v_empty if kv else k_empty)[st], g // size - 1)
+                    holds(raw, rs, (kv, g), "raw")
+                    yield STEP
+                    holds(raw, rs, (kv, g), "raw")
+                    (vst if kv else kst)[st] = g
+                    (v_full[st] if kv else k_full[geo["k_bar"][g & 1][st]]).arrive()
+                    yield STEP
+                    r_empty[rs].arrive()
+                elif i >= n - mk:
+                    raw_waits[vs] = raw_waits.get(vs, -1) + 1
+                    yield wait(v_raw[vs], raw_waits[vs])
+                    holds(vst, vs, g, "V to clear")
+                    v_clean[vs].arrive()
+                g += 1
+            if w >= 1:
+                yield wait(o_free, w - 1)
+            nf_rdy.arrive()
+
+    for team in range(2):
+        sim.role("issuer %d" % team, issue(team))
+        for half in range(2):
+            for quad in quads:
+                sim.role("softmax %d.%d.%d" % (team, half, quad), softmax(team, half, quad))
+    if q8:
+        sim.role("copies", copies((0, 1)))
+    else:
+        sim.role("K copies", copies((0,)))
+        sim.role("V copies", copies((1,)))
+    for pw in range(prep_w):
+        sim.role("prepare %d" % pw, prepare(pw))
+    sim.run()
+
+
+ROWS_ROLES = ["issuer 0", "issuer 1", "copies", "K copies", "V copies", "softmax 0.0.0", "softmax 0.1.0", "softmax 1.0.0",
+              "softmax 1.1.0", "softmax 0.0.1", "softmax 1.1.1", "prepare 0", "prepare 1", "prepare %d" % W]
+
+
 def held_things(tiles, roles):
     """What is held back, one at a time: each role, each of a few copies and MMAs."""
     copies = ["copy %d %d" % (kv, g) for g in range(min(tiles, 9)) for kv in range(2)]
-    return [None] + roles + copies + ["%s %d" % (q, g) for q in ("S", "PV", "S0", "S1") for g in range(min(tiles, 6))]
+    return [None] + roles + copies + \
+        ["%s %d" % (q, g) for q in ("S", "PV", "S0", "S1", "S0 PV", "S1 PV") for g in range(min(tiles, 6))]

@@ -40,6 +40,29 @@ int main() {
 }
 """
 
+PRINT_ROWS = """
+#include <cstdio>
+#include "tree_rings.h"
+using namespace m4q;
+int main() {
+  const char* sep = "[";
+  for (int d = 64; d <= 128; d += 64)
+    for (int q8 = 0; q8 < 2; ++q8) {
+      const RowsRings r = rows_rings(d, q8 != 0);
+      std::printf("%s{\\"d\\": %d, \\"q8\\": %d, \\"ks\\": %d, \\"vs\\": %d, \\"rs\\": %d, \\"sb\\": %d, \\"k_bar\\": [",
+                  sep, d, q8, r.ks, r.vs, r.rs, r.sb);
+      for (int t = 0; t < 2; ++t) {
+        std::printf("%s[", t ? ", " : "");
+        for (int s = 0; s < r.ks; ++s) std::printf("%s%d", s ? ", " : "", rows_k_bar(r.ks, t, s));
+        std::printf("]");
+      }
+      std::printf("]}");
+      sep = ", ";
+    }
+  std::printf("]");
+}
+"""
+
 
 def rings(tmp_path, source):
     src, exe = tmp_path / "rings.cpp", tmp_path / "rings"
@@ -77,3 +100,22 @@ def test_the_walk_finds_a_shared_landing_barrier(tmp_path):
                 walk(model.few, geo, model.FEW_ROLES, 2)
         else:
             walk(model.few, geo, model.FEW_ROLES, 1)
+
+
+def test_many_rows(tmp_path):
+    all_rings = rings(tmp_path, PRINT_ROWS)
+    assert len(all_rings) == 4
+    for geo in all_rings:
+        walk(model.rows, geo, model.ROWS_ROLES, 3)
+
+
+def test_the_walk_finds_k_stages_shared_by_two_issuers(tmp_path):
+    # one barrier a K stage: wrong with three stages and two score buffers
+    for geo in rings(tmp_path, PRINT_ROWS):
+        geo["k_bar"] = [list(range(geo["ks"]))] * 2
+        if geo["ks"] % 2:
+            assert geo["sb"] == 2
+            with pytest.raises(model.Fault):
+                walk(model.rows, geo, model.ROWS_ROLES, 3)
+        else:
+            walk(model.rows, geo, model.ROWS_ROLES, 1)

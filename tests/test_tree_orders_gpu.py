@@ -53,3 +53,11 @@ def repeated(codec, h, hkv, d, c, pasts, n, seed):
     (12, 4, 7, 640, [600] * 60), (8, 8, 31, 128, [90] * 40)])
 def test_few_rows_in_two_blocks(d, h, hkv, n, c, pasts):
     repeated(Q8, h, hkv, d, c, pasts, n, 7)
+
+
+# more than 32 rows over fp16 caches at D = 128: three K stages for two issuers
+@pytest.mark.parametrize("h,hkv,n,c,pasts", [
+    (32, 8, 24, 9000, [8900, 4000]), (8, 1, 64, 20000, [19900]), (16, 4, 16, 768, [700, 3, 350, 128] * 15),
+    (4, 1, 256, 520, [200])])
+def test_many_rows_fp16(h, hkv, n, c, pasts):
+    repeated(F16, h, hkv, 128, c, pasts, n, 11)

@@ -93,7 +93,7 @@ struct TreeCfg {
   static constexpr int kSB = kRings.sb;                // score buffers
   static constexpr int kBars = 3 * kKS + 4 * kVS + 3 * kRS + 17;
   static constexpr int kFixed = 8 * kTile * 4          // ancestor bits [8][128]
-                                + 6 * kTile * 4        // maxima [team][half][128], sums [team][128]
+                                + (4 * rows_max_slots(kSB) + 2) * kTile * 4   // maxima [slot][team][half][128], sums [team][128]
                                 + 2 * 2 * kTile * 8    // (m, l) [parity][team][128]
                                 + 256 * 2              // parents
                                 + 2 * 8 * 4 * 4        // noted V rows [parity][warp][masked tile]
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
   uint8_t* vst = kst + KS * Cfg::kTileBytes;
   uint8_t* raws = vst + VS * Cfg::kTileBytes;
   uint32_t* anc_all = reinterpret_cast<uint32_t*>(raws + Cfg::kRS * Cfg::kRaw);   // [8][128]
-  float* xmax = reinterpret_cast<float*>(anc_all + 8 * kTile);                    // [team][half][128]
-  float* xsum = xmax + 4 * kTile;                                                 // [team][128]
+  float* xmax = reinterpret_cast<float*>(anc_all + 8 * kTile);                    // [slot][team][half][128]
+  float* xsum = xmax + 4 * rows_max_slots(SB) * kTile;                            // [team][128]
   float2* ml = reinterpret_cast<float2*>(xsum + 2 * kTile);                       // [parity][team][128]
   uint32_t* noted = reinterpret_cast<uint32_t*>(ml + 4 * kTile);                  // [parity][8 warps][4]
   // parents of the run's tree: its writers, one warp for 32 rows, write the same,
@@ -445,14 +445,14 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
             for (int e = 0; e < 32; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
             t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
           }
-          *mine = t;
+          mine[4 * kTile * rows_max_slot(SB, g)] = t;
         }
         // the two halves go on, or leave, together (a named barrier has no time limit)
         if (vote_or(pair_bar, 64, !ok)) {
           ok = false;
           break;
         }
-        t = fmaxf(t, *others);
+        t = fmaxf(t, others[4 * kTile * rows_max_slot(SB, g)]);
         // the tile's maximum; -inf when the row sees no key of it
         const float mu = t == INFINITY ? -INFINITY : t * sc;   // (an infinite score gives NaN in the end)
         const float mj = mu > m + kRaise || m == -INFINITY ? fmaxf(mu, m) : m;

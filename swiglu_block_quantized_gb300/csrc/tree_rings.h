@@ -53,5 +53,11 @@ constexpr RowsRings rows_rings(int d, bool q8) {
 // there a stage is always the same team's, or the third score buffer keeps P V of all
 // tiles in order.)
 M4Q_HD constexpr int rows_k_bar(int ks, int team, int stage) { return team * ks + stage; }
+// Where the halves of a row exchange the maxima of tile g, of rows_max_slots: with a
+// third score buffer a half may have its next tile's scores, and write its next
+// maximum, before the other has read this one.  It cannot be two tiles ahead: both
+// meet once a tile between writing and reading.
+M4Q_HD constexpr int rows_max_slots(int sb) { return sb == 3 ? 2 : 1; }
+M4Q_HD constexpr int rows_max_slot(int sb, int g) { return sb == 3 ? (g >> 1) & 1 : 0; }
 
 }  // namespace m4q

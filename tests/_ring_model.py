@@ -310,8 +310,9 @@ FEW_ROLES = ["S issuer", "PV issuer", "copies", "K copies", "V copies", "softmax
 
 
 def rows(geo, q8, runs, seed, held):
-    """tree_kernel: geo = ks, vs, rs, sb (score buffers) and k_bar[team][stage], the
-    landing barrier of a K stage (csrc/tree_rings.h)."""
+    """tree_kernel: geo = ks, vs, rs, sb (score buffers), k_bar[team][stage], the
+    landing barrier of a K stage, and max_slot[g % 4], where the halves of a row
+    exchange the maxima of tile g (csrc/tree_rings.h)."""
     ks_n, vs_n, rs_n, sb_n = geo["ks"], geo["vs"], geo["rs"], geo["sb"]
     sim = Sim(seed, held)
     tiles = tiles_of(runs)
@@ -326,7 +327,7 @@ def rows(geo, q8, runs, seed, held):
     pv_done = Ring(sb_n, "pv_done")
     q_full, q_empty = Bar("q_full", prep_w), Bar("q_empty", 2)
     ml_rdy, nf_rdy, o_free = Bar("ml_rdy", 2 * len(quads)), Bar("nf_rdy", prep_w), Bar("o_free", soft)
-    kst, vst, raw, buf = {}, {}, {}, {}
+    kst, vst, raw, buf, maxima = {}, {}, {}, {}, {}
 
     def holds(store, key, tile, what):
         if store.get(key) != tile:
@@ -449,8 +450,11 @@ def rows(geo, q8, runs, seed, held):
                     p_full[sp].arrive()
                     continue
                 holds(buf, x % sb_n, ("s", x) if not half else buf.get(x % sb_n), "S")
+                slot = geo["max_slot"][x % 4]
+                maxima[slot, team, half] = x
                 yield ("sync", pair, 2)
                 yield STEP
+                holds(maxima, (slot, team, 1 - half), x, "maximum")
                 if sb_n == 3 and i >= 2 and sim.rng.random() < 0.5:   # references rise
                     yield wait(pv_done[(x - 2) % sb_n], (x - 2) // sb_n)
                 yield STEP

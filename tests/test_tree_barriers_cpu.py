@@ -56,6 +56,8 @@ int main() {
         for (int s = 0; s < r.ks; ++s) std::printf("%s%d", s ? ", " : "", rows_k_bar(r.ks, t, s));
         std::printf("]");
       }
+      std::printf("], \\"max_slots\\": %d, \\"max_slot\\": [", rows_max_slots(r.sb));
+      for (int g = 0; g < 4; ++g) std::printf("%s%d", g ? ", " : "", rows_max_slot(r.sb, g));
       std::printf("]}");
       sep = ", ";
     }
@@ -106,6 +108,7 @@ def test_many_rows(tmp_path):
     all_rings = rings(tmp_path, PRINT_ROWS)
     assert len(all_rings) == 4
     for geo in all_rings:
+        assert max(geo["max_slot"]) < geo["max_slots"]
         walk(model.rows, geo, model.ROWS_ROLES, 3)
 
 
@@ -116,6 +119,18 @@ def test_the_walk_finds_k_stages_shared_by_two_issuers(tmp_path):
         if geo["ks"] % 2:
             assert geo["sb"] == 2
             with pytest.raises(model.Fault):
+                walk(model.rows, geo, model.ROWS_ROLES, 3)
+        else:
+            walk(model.rows, geo, model.ROWS_ROLES, 1)
+
+
+def test_the_walk_finds_one_place_for_the_maxima(tmp_path):
+    # one place for the maxima of all tiles: wrong with a third score buffer, whose
+    # scores do not wait for P of the last tile
+    for geo in rings(tmp_path, PRINT_ROWS):
+        geo["max_slot"] = [0] * 4
+        if geo["sb"] == 3:
+            with pytest.raises(model.Fault, match="maximum"):
                 walk(model.rows, geo, model.ROWS_ROLES, 3)
         else:
             walk(model.rows, geo, model.ROWS_ROLES, 1)

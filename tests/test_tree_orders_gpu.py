@@ -61,3 +61,11 @@ def test_few_rows_in_two_blocks(d, h, hkv, n, c, pasts):
     (4, 1, 256, 520, [200])])
 def test_many_rows_fp16(h, hkv, n, c, pasts):
     repeated(F16, h, hkv, 128, c, pasts, n, 11)
+
+
+# D = 64: three score buffers, the halves of a row a tile apart
+@pytest.mark.parametrize("codec", [F16, Q8])
+@pytest.mark.parametrize("h,hkv,n,c,pasts", [
+    (32, 8, 24, 9000, [8900, 4000, 1]), (8, 1, 64, 20000, [19900]), (16, 4, 16, 768, [700, 3, 350, 128] * 15)])
+def test_many_rows_of_64(codec, h, hkv, n, c, pasts):
+    repeated(codec, h, hkv, 64, c, pasts, n, 13)

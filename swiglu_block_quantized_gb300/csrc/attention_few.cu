@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(FewCfg<D, Q8, NC>::kThreads, 1)
             const uint4* src =
                 reinterpret_cast<const uint4*>(p.q + ((long long)h * p.q_rows + (long long)sg.b * p.N + node) * D) + 4 * blk;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = __ldg(src + i);
+            for (int i = 0; i < 4; ++i) q[i] = __ldcg(src + i);   // (by way of L1: 97.0 us against 95.5 for the 32 tokens)
           }
         }
         if constexpr (Q8) order_block(q, blk & 1, o);

@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(TreeCfg<D, Q8>::kThreads, 1)
             const uint4* src =
                 reinterpret_cast<const uint4*>(p.q + ((long long)h * p.q_rows + (long long)sg.b * p.N + node) * D) + 4 * blk;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) q[c] = __ldg(src + c);
+            for (int c = 0; c < 4; ++c) q[c] = src[c];   // (not by way of L1: 33.5 us against 32.9 for the first case above)
           }
         }
         if constexpr (Q8) order_block(q, blk & 1, o);

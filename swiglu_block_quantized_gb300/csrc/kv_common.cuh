@@ -17,6 +17,11 @@ enum : uint32_t {
   kSiteTreeWs = 37,      // tree attention: partial result
 };
 
+// The serving kernels start while the kernel before them may still run (pdl_wait), so
+// what an earlier kernel of the stream may have written is read by ordinary loads:
+// __ldg is for memory that nobody writes from a kernel's start to its end, and is used
+// for the frequency table alone.
+
 // Larger of two, NaN if one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
@@ -59,12 +64,12 @@ __device__ __forceinline__ uint16_t q8_encode8(const float* x, float top, uint32
 // always followed by the odd block of the same row.
 __device__ __forceinline__ void q8_decode16(const uint8_t* row, int u, const DecK& K, uint32_t (&out)[8]) {
   const int blk = u >> 1, off = 34 * blk + 2 + 16 * (u & 1);
-  const uint32_t d2 = dup_scale(__ldg(reinterpret_cast<const unsigned short*>(row + 34 * blk)));
+  const uint32_t d2 = dup_scale(*reinterpret_cast<const unsigned short*>(row + 34 * blk));
   const uint32_t* w = reinterpret_cast<const uint32_t*>(row + (off & ~3));
   uint32_t a[5];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = __ldg(w + i);
-  a[4] = (blk & 1) ? 0u : __ldg(w + 4);
+  for (int i = 0; i < 4; ++i) a[i] = w[i];
+  a[4] = (blk & 1) ? 0u : w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t c = (blk & 1) ? a[i] : __funnelshift_r(a[i], a[i + 1], 16);

@@ -134,13 +134,13 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
   const UnitAt at = unit_at(u, p.rot, p.interleaved);
   Turn8 t;
   if (ok && at.turns && h0 < p.H + p.Hkv) {
-    const int pos = __ldg(p.pos + m);
+    const int pos = p.pos[m];
 #pragma unroll
     for (int i = 0; i < 8; ++i) turn(pos, __ldg(reinterpret_cast<const long long*>(p.freqs) + 8 * u + i), p.mscale, t.c[i], t.s[i]);
   }
   long long row = -1;                        // this token's cache row of head 0, or -1
   if (ok && h1 > p.H) {
-    const int slot = __ldg(p.slots + m);
+    const int slot = p.slots[m];
     if (slot >= 0 && (long long)slot < (long long)p.B * p.C)
       row = (long long)(slot / p.C) * p.Hkv * p.C + slot % p.C;
   }
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kBlock) kv_read_kernel(const KvReadParams p) {
   const long long j = (long long)blockIdx.x * (kBlock / U) + threadIdx.x / U;
   if (!dst || j >= p.n) return;
   const int u = threadIdx.x % U, h = blockIdx.y;
-  const int slot = __ldg(p.slots + j);
+  const int slot = p.slots[j];
   uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (slot >= 0 && (long long)slot < (long long)p.B * p.C) {
     const long long row = ((long long)(slot / p.C) * p.Hkv + h) * p.C + slot % p.C;
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kBlock) kv_read_kernel(const KvReadParams p) {
       q8_decode16(cache + row * RB, u, make_deck(), out);
     } else {
       const uint4* s = reinterpret_cast<const uint4*>(cache + row * RB) + 2 * u;
-      const uint4 a = __ldg(s), b = __ldg(s + 1);
+      const uint4 a = s[0], b = s[1];
       out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
       out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
     }

@@ -76,7 +76,7 @@ __device__ __forceinline__ void tree_schedule(const TreeParams& p, TreeSched* s,
     const int b = b0 + lane;
     int n = 0;
     if (b < p.B) {
-      const int past = min(max(__ldg(p.past + b), 0), p.C);
+      const int past = min(max(__ldcg(p.past + b), 0), p.C);
       s->past[b] = past;
       n = tiles_of(p, past);
     }
@@ -161,7 +161,7 @@ __device__ __forceinline__ int first_masked(const Seg& g) { return min(g.past / 
 // that waits for the last one.
 __device__ __forceinline__ bool ancestors32(const int* parents, int n, int node, uint32_t& bits) {
   const int lane = threadIdx.x & 31;
-  const int up = lane < n ? __ldg(parents + lane) : -2;
+  const int up = lane < n ? __ldcg(parents + lane) : -2;
   bits = 0u;
   bool used = true;
   int a = node;
@@ -183,7 +183,7 @@ __device__ __forceinline__ void ancestors256(const int* parents, int n, int16_t*
                                              int stride) {
 #pragma unroll 1
   for (int i = threadIdx.x & 31; i < n; i += 32) {
-    const int v = __ldg(parents + i);
+    const int v = __ldcg(parents + i);
     up[i] = (int16_t)(v >= -1 && v < i ? v : -2);
   }
 #pragma unroll

@@ -578,12 +578,12 @@ def rope(x, pos, freqs, layout: int = ROPE_HALF, mscale: float = 1.0, out=None, 
         oh, om, od, ohs, ors = _head_rows(out, "out")
         if (oh, om, od) != (h, m_, d):
             raise ValueError("out must be [%d, %d, %d]" % (h, m_, d))
-        reach = d   # rows in order of their step: each starts past the ones before
+        reach = d   # rows in order of their step: each starts past the end of the ones before
         for step, count in sorted(((ohs, oh), (ors, om))):
             if count > 1:
                 if step < reach:
                     raise ValueError("out's rows overlap")
-                reach = step * count
+                reach += step * (count - 1)
         if out.data_ptr() == x.data_ptr() and (hs, rs) != (ohs, ors):
             raise ValueError("out starts where x does, with other strides")
     dev = _one_device(x, pos, freqs, out)

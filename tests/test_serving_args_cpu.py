@@ -1,0 +1,24 @@
+"""More arguments of the serving operators that the binding or the C ABI accepts or
+refuses before touching the GPU (no GPU needed)."""
+import pytest
+
+import swiglu_block_quantized_gb300 as m
+
+torch = pytest.importorskip("torch")
+from test_serving_cpu import FR, cpu_binding, f16, i32   # noqa: E402,F401
+
+
+def rows(strides, h=2, n=4, d=64):
+    size = 1 + (h - 1) * strides[0] + (n - 1) * strides[1] + d - 1
+    return f16(size).as_strided((h, n, d), (*strides, 1))
+
+
+def test_rope_takes_rows_with_gaps(cpu_binding):
+    # rows that do not overlap, however they lie: the next head's first row may start
+    # in the gap behind this one's last
+    for strides in ((280, 72), (64, 136), (256, 64), (72, 200), (400, 96), (64, 128)):
+        with pytest.raises(AssertionError, match="m4q_rope was called"):
+            m.rope(f16(2, 4, 64), i32(4), FR, out=rows(strides))
+    for strides in ((272, 72), (64, 120), (248, 64), (0, 64), (64, 0), (56, 512)):
+        with pytest.raises(ValueError, match="overlap"):
+            m.rope(f16(2, 4, 64), i32(4), FR, out=rows(strides))

@@ -757,6 +757,8 @@ def norm_residual(h, r, w_pre, w_post=None, gate=None, res_scale: float = 1.0, b
     if gate is not None:
         gate_rows = int(gate.numel() != d)
         p_gate = _halfs(gate, total if gate_rows else d, "gate").data_ptr()
+        if gate.shape[-1] != d and not (gate_rows and gate.dim() == 1):   # a value for each row, say
+            raise ValueError("gate must be [%d] or hold one value for each of h" % d)
     if w_pre is not None:
         p_wpre = _halfs(w_pre, d, "w_pre").data_ptr()
         y = _allocate(shape, f16, r, stream) if out is None else _halfs(out, total, "out")

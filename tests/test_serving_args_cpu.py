@@ -22,3 +22,15 @@ def test_rope_takes_rows_with_gaps(cpu_binding):
     for strides in ((272, 72), (64, 120), (248, 64), (0, 64), (64, 0), (56, 512)):
         with pytest.raises(ValueError, match="overlap"):
             m.rope(f16(2, 4, 64), i32(4), FR, out=rows(strides))
+
+
+def test_norm_gate_of_another_shape(cpu_binding):
+    # as many rows as columns: one value a row holds as many values as one a column,
+    # and would be taken for it
+    h, r, w = f16(64, 64), f16(64, 64), f16(64)
+    for gate in (f16(64, 1), f16(1, 64, 1), f16(32, 128), f16(64, 32, 2)):
+        with pytest.raises(ValueError, match="gate"):
+            m.norm_residual(h, r, w, gate=gate)
+    for gate in (f16(64), f16(1, 64), f16(64, 64), f16(8, 8, 64), f16(64 * 64)):
+        with pytest.raises(AssertionError, match="m4q_norm_residual was called"):
+            m.norm_residual(h, r, w, gate=gate)

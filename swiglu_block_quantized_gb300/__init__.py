@@ -680,9 +680,9 @@ def attention_tree(q, kc, vc, kv_codec: int, past, parents, scale: float | None 
     """O fp16 [B * N, H * D]: attention of the drafted nodes q fp16 [H, B * N,
     D] (node i of sequence b is row b * N + i) over the caches kc, vc [B, Hkv,
     C, row].  A node sees the rows below past int32 [B], its ancestors by
-    parents int32 [B, N] (-1: the context; anything else that is not an earlier
-    used node: unused, a zero row) and itself, at rows past + node.  N = 1 is
-    one new token a sequence.  The workspace is allocated here when not given;
+    parents int32 [B, N] or [B * N] (-1: the context; anything else that is not
+    an earlier used node: unused, a zero row) and itself, at rows past + node.
+    N = 1 is one new token a sequence.  The workspace is allocated here when not given;
     workspace=False runs without one (no key split)."""
     _need(q, _t().float16, "q")
     if kc is None or vc is None:
@@ -696,6 +696,8 @@ def attention_tree(q, kc, vc, kv_codec: int, past, parents, scale: float | None 
     n = rows // b
     _ints(past, _torch.int32, b, "past")
     _ints(parents, _torch.int32, rows, "parents")
+    if parents.dim() > 1 and tuple(parents.shape) != (b, n):   # [N, B] holds as many
+        raise ValueError("parents must be [%d, %d]" % (b, n))
     if scale is None:
         scale = d ** -0.5
     if out is None:

@@ -34,3 +34,15 @@ def test_norm_gate_of_another_shape(cpu_binding):
     for gate in (f16(64), f16(1, 64), f16(64, 64), f16(8, 8, 64), f16(64 * 64)):
         with pytest.raises(AssertionError, match="m4q_norm_residual was called"):
             m.norm_residual(h, r, w, gate=gate)
+
+
+def test_parents_of_another_shape(cpu_binding):
+    # node by node instead of tree by tree: as many values, other trees
+    kc = f16(2, 2, 8, 64)
+    call = lambda p: m.attention_tree(f16(4, 6, 64), kc, kc, m.KV_F16, i32(2), p)   # noqa: E731
+    for shape in ((3, 2), (6, 1), (1, 6), (2, 3, 1)):
+        with pytest.raises(ValueError, match="parents"):
+            call(i32(6).view(shape))
+    for shape in ((2, 3), (6,)):
+        with pytest.raises(AssertionError, match="m4q_attention_tree was called"):
+            call(i32(6).view(shape))

@@ -385,7 +385,7 @@ int m4q_kv_read(const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t
  *    hold (infinities and NaN included).
  *  - D is 64 or 128, H % Hkv == 0, Hkv ceil(N G / 128) ceil(C / 128) <=
  *    INT32_MAX (else M4Q_ERR_BAD_SHAPE); 1 <= N <= 256, B, C >= 1,
- *    B * N * H <= INT32_MAX, scale finite (else
+ *    B * N * H <= INT32_MAX, scale log2(e) finite in 32 bits (else
  *    M4Q_ERR_INVALID_ARG).
  *  - Arithmetic as m4q_attention.
  *  - workspace: m4q_attention_tree_workspace() bytes (not cleared before or

@@ -943,7 +943,8 @@ size_t m4q_attention_tree_workspace(int kv_codec, int64_t B, int64_t H, int64_t 
 int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t H, int64_t Hkv,
                        int64_t N, int64_t C, int64_t D, const int32_t* past, const int32_t* parents, float scale,
                        void* O, void* workspace, size_t workspace_bytes, m4q_stream_t stream) {
-  if (!Q || !Kc || !Vc || !past || !parents || !O || !(scale - scale == 0.f)) return M4Q_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;   // the kernels work in powers of 2
+  if (!Q || !Kc || !Vc || !past || !parents || !O || !(scale_log2 - scale_log2 == 0.f)) return M4Q_ERR_INVALID_ARG;
   int rc = check_tree(kv_codec, B, H, Hkv, N, C, D);
   if (rc != M4Q_OK) return rc;
   if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) || !aligned_to(past, 4) ||
@@ -963,7 +964,7 @@ int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_cod
   p.N = (int)N;
   p.C = (int)C;
   p.D = (int)D;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.rtiles = t.rtiles;
   p.split = t.split ? 1 : 0;
   p.whole = t.whole;

@@ -1,5 +1,7 @@
 """More arguments of the serving operators that the binding or the C ABI accepts or
 refuses before touching the GPU (no GPU needed)."""
+import ctypes
+
 import pytest
 
 import swiglu_block_quantized_gb300 as m
@@ -46,3 +48,12 @@ def test_parents_of_another_shape(cpu_binding):
     for shape in ((2, 3), (6,)):
         with pytest.raises(AssertionError, match="m4q_attention_tree was called"):
             call(i32(6).view(shape))
+
+
+def test_tree_scale_in_powers_of_two():
+    # a finite scale whose product with log2(e) is not: every score would be NaN
+    m.build()
+    a = ctypes.c_void_p(0x100000)   # never dereferenced
+    for scale in (3e38, -3e38, 2.4e38):
+        assert m.load().m4q_attention_tree(a, a, a, m.KV_F16, 1, 4, 2, 3, 8, 64, a, a, scale, a, None, 0,
+                                           None) == m.ERR_INVALID_ARG

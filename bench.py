@@ -6,7 +6,8 @@ One step = one fused gate/up SwiGLU projection of the 8B-shaped layer
 (X fp16 [2048, 4096], Wg and Wu Q4_0 [14336, 4096], Y fp16 [2048, 14336]),
 the workload the headline metric is quoted on.  Inputs are resident in HBM
 and rotate through 4 distinct copies (332 MB > L2) so each step reads cold
-weights.  Prints one JSON line (rank 0).
+weights.  Prints one JSON line (rank 0) on stdout; the per-workload table
+("configs") is a JSON line on stderr.
 
 Extra keys: "roofline" of the SwiGLU kernel (tensor bound, against the
 measured dense bf16/fp16 peak), "m1" (the same weights at M = 1 through the
@@ -389,6 +390,21 @@ def run_ours(args, ws, rank, local):
         "cpu_baseline": cpu, "clocks": clocks,
         "gpu_launches": args.steps,
     }
+    emit(line)
+
+
+LINE_LIMIT = 4096   # bytes: a longer line does not reach whoever keeps only the output's end
+TABLES = ("configs", "attention", "mlx4", "m1")
+
+
+def emit(line):
+    """The benchmark's one line on stdout.  Tables beside the headline that would make
+    it too long go to stderr, the largest first, as a JSON line each."""
+    tables = sorted((k for k in TABLES if k in line), key=lambda k: len(json.dumps(line[k])), reverse=True)
+    while tables and len(json.dumps(line)) > LINE_LIMIT:
+        k = tables.pop(0)
+        print(json.dumps({k: line[k]}), file=sys.stderr, flush=True)
+        line = {key: v for key, v in line.items() if key != k}
     print(json.dumps(line), flush=True)
 
 

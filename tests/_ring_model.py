@@ -5,9 +5,9 @@ Every warp (two stand for four of a group) and every issuing or copying lane is
 a generator that waits on mbarriers, copies land and MMAs complete when the
 scheduler says so, and one of them at a time is held back until nothing else can
 move.  A wait passes by the parity rule of an mbarrier; it is an error if the
-phase that it was meant for is not complete (an alias), if an operand stage does
-not hold the tile that is read from it, if one half of a row reads the other's
-maximum of another tile, or if nothing can move."""
+phase that it was meant for is not complete (an alias), if an operand stage or
+what the warps hand each other (Q, O, P, maxima, sums, ancestor bits, noted rows)
+is not that of the tile or run it is read for, or if nothing can move."""
 import random
 
 W = 2   # warps that stand for a group of four
@@ -133,6 +133,7 @@ def few(geo, q8, runs, seed, held):
     sim = Sim(seed, held)
     tiles = tiles_of(runs)
     prep_w = 2 * pg * W if q8 else W
+    noters = range(pg * W, prep_w) if q8 else range(prep_w)
     k_full, k_empty = Ring(ks_n, "k_full", W if q8 else 1), Ring(ks_n, "k_empty")
     v_full, v_empty = Ring(vs_n, "v_full", W if q8 else 1), Ring(vs_n, "v_empty")
     v_raw, v_clean = Ring(vs_n, "v_raw"), Ring(vs_n, "v_clean", prep_w)
@@ -143,6 +144,7 @@ def few(geo, q8, runs, seed, held):
     o_done, o_free, ml_rdy, nf_rdy = Bar("o_done"), Bar("o_free", 2 * W), Bar("ml_rdy", 2), Bar("nf_rdy", prep_w)
     kst, vst, raw = {}, {}, {}
     held_by = {}
+    q_of, o_of, o_busy, ml, noted, unused = {}, {}, {}, {}, {}, {}
 
     def holds(store, key, tile, what):
         if store.get(key) != tile:
@@ -174,8 +176,10 @@ def few(geo, q8, runs, seed, held):
                     yield wait(s_free[sb], (g >> 2) - 1)
                 holds(kst, st, g, "K")
 
-                def done(g=g, st=st, sb=sb):
+                def done(g=g, st=st, sb=sb, w=w):
                     holds(kst, st, g, "K")
+                    for pw in range(prep_w):
+                        holds(q_of, pw, w, "Q")
                     held_by["s", sb] = g
                     s_full[sb].arrive()
                     k_empty[st].arrive()
@@ -196,9 +200,14 @@ def few(geo, q8, runs, seed, held):
                     yield wait(o_free, w - 1)
                 holds(vst, vs, g, "V")
                 holds(held_by, ("p", pb), g, "P")
+                o_of[pb] = w
+                o_busy[pb] = g
 
                 def done(g=g, vs=vs, pb=pb):
                     holds(vst, vs, g, "V")
+                    holds(held_by, ("p", pb), g, "P")
+                    if o_busy[pb] == g:
+                        o_busy[pb] = None
                     v_empty[vs].arrive()
                     p_free[pb].arrive()
                 commit("PV", g, done)
@@ -232,8 +241,10 @@ def few(geo, q8, runs, seed, held):
     def softmax(team, sw):
         yield STEP
         g = 0
-        for w, (n, _) in enumerate(runs):
-            for _ in range(n):
+        for w, (n, mk) in enumerate(runs):
+            if mk and team == 0 and sw == 0:
+                unused[w & 1] = w
+            for i in range(n):
                 if (g & 1) == team:
                     sb = g & 3
                     yield wait(s_full[sb], g >> 2)
@@ -242,6 +253,9 @@ def few(geo, q8, runs, seed, held):
                     holds(held_by, ("s", sb), g, "S")
                     s_free[sb].arrive()
                     yield ("sync", "team %d" % team, W)
+                    if i >= 2:   # O rescaled
+                        holds(o_busy, team, None, "O")
+                        holds(o_of, team, w, "O")
                     yield STEP
                     held_by["p", team] = g
                     p_full[team].arrive()
@@ -249,11 +263,22 @@ def few(geo, q8, runs, seed, held):
             yield ("sync", "team %d" % team, W)
             yield STEP
             if sw == 0:
+                ml[w & 1, team] = w
                 ml_rdy.arrive()
             yield wait(ml_rdy, w)
             yield wait(o_done, w)
             yield wait(nf_rdy, w)
             yield ("sync", "team %d" % team, W)
+            yield STEP
+            for t in range(2):
+                holds(ml, (w & 1, t), w, "(m, l)")
+                if any((x & 1) == t for x in range(g - n, g)):
+                    holds(o_busy, t, None, "O")
+                    holds(o_of, t, w, "O")
+            if mk:
+                holds(unused, w & 1, w, "unused rows")
+                for pw in noters:
+                    holds(noted, (w & 1, pw), w, "noted rows")
             o_free.arrive()
 
     def prepare(pw):
@@ -264,6 +289,9 @@ def few(geo, q8, runs, seed, held):
         for w, (n, mk) in enumerate(runs):
             if w > 0:
                 yield wait(q_empty, w - 1)
+            noted[w & 1, pw] = w
+            q_of[pw] = w
+            yield STEP
             q_full.arrive()
             for i in range(n):
                 ks, vs = g % ks_n, g % vs_n
@@ -316,9 +344,11 @@ def rows(geo, q8, runs, seed, held):
     ks_n, vs_n, rs_n, sb_n = geo["ks"], geo["vs"], geo["rs"], geo["sb"]
     sim = Sim(seed, held)
     tiles = tiles_of(runs)
-    quads = (0, 1)                      # two stand for four; the second has no row
+    quads = (0, 1)                      # two stand for four; the second has rows in odd seeds
+    parts = [(quad, half) for quad in quads[:1 + seed % 2] for half in range(2)]   # of a score buffer
     soft = 2 * 2 * len(quads)           # teams, halves
     prep_w = 2 * W if q8 else W
+    noters = range(W, prep_w) if q8 else range(prep_w)
     k_full, k_empty = Ring(2 * ks_n, "k_full", W if q8 else 1), Ring(ks_n, "k_empty")
     v_full, v_empty = Ring(vs_n, "v_full", W if q8 else 1), Ring(vs_n, "v_empty")
     v_raw, v_clean = Ring(vs_n, "v_raw"), Ring(vs_n, "v_clean", prep_w)
@@ -328,6 +358,7 @@ def rows(geo, q8, runs, seed, held):
     q_full, q_empty = Bar("q_full", prep_w), Bar("q_empty", 2)
     ml_rdy, nf_rdy, o_free = Bar("ml_rdy", 2 * len(quads)), Bar("nf_rdy", prep_w), Bar("o_free", soft)
     kst, vst, raw, buf, maxima = {}, {}, {}, {}, {}
+    q_of, o_of, o_busy, ml, sums, noted, bits, up = {}, {}, {}, {}, {}, {}, {}, {}
 
     def holds(store, key, tile, what):
         if store.get(key) != tile:
@@ -354,14 +385,17 @@ def rows(geo, q8, runs, seed, held):
             if x >= 0:
                 yield wait(pv_done[x % sb_n], x // sb_n)
 
-        def scores(x):
+        def scores(x, w):
             st = x % ks_n
             yield wait(k_full[geo["k_bar"][team][st]], k_land(geo["k_bar"][team][st], x))
             holds(kst, st, x, "K")
 
             def done():
                 holds(kst, st, x, "K")
-                buf[x % sb_n] = ("s", x)
+                for pw in range(prep_w):
+                    holds(q_of, pw, w, "Q")
+                for part in parts:
+                    buf[x % sb_n, part] = ("s", x)
                 s_full[sp_of(x)].arrive()
                 k_empty[st].arrive()
             sim.later(who, "%s %d" % (who, x), done)
@@ -375,16 +409,16 @@ def rows(geo, q8, runs, seed, held):
                 continue
             if sb_n == 3:
                 yield from pv_wait(mine[0][0] - 3)
-                yield from scores(mine[0][0])
+                yield from scores(mine[0][0], w)
             for i, (x, masked) in enumerate(mine):
                 more = i + 1 < len(mine)
                 if sb_n == 2:
                     yield from pv_wait(x - 2)
-                    yield from scores(x)
+                    yield from scores(x, w)
                 else:
                     yield from pv_wait(x - 1)
                     if more:
-                        yield from scores(mine[i + 1][0])
+                        yield from scores(mine[i + 1][0], w)
                 if not more:
                     sim.later(who, "%s q %d" % (who, w), q_empty.arrive)
                 vs = x % vs_n
@@ -394,11 +428,16 @@ def rows(geo, q8, runs, seed, held):
                     yield wait(o_free, w - 1)
                 yield wait(p_full[sp_of(x)], team_use(sp_of(x), x))
                 holds(vst, vs, x, "V")
-                holds(buf, x % sb_n, ("p", x), "P")
+                for part in parts:
+                    holds(buf, (x % sb_n, part), ("p", x), "P")
+                o_of[team] = w
+                o_busy[team] = x
 
                 def done(x=x, vs=vs):
+                    o_busy[team] = None
                     holds(vst, vs, x, "V")
-                    holds(buf, x % sb_n, ("p", x), "P")
+                    for part in parts:
+                        holds(buf, (x % sb_n, part), ("p", x), "P")
                     pv_done[x % sb_n].arrive()
                     v_empty[vs].arrive()
                 sim.later(who, "%s PV %d" % (who, x), done)
@@ -432,14 +471,22 @@ def rows(geo, q8, runs, seed, held):
                 n += 1
 
     def softmax(team, half, quad):
-        busy = quad == 0
+        busy = quad <= seed % 2
         pair, whole = "pair %d %d" % (team, quad), "quad %d" % quad
         yield STEP
         g = 0
         for w, (n, mk) in enumerate(runs):
             if busy and mk:
                 yield ("sync", whole, 4)
+                yield STEP
+                if team == 0 and not half:
+                    up["tree"] = w
+                    yield STEP
+                    holds(up, "tree", w, "parents")
+                    bits[quad] = w
                 yield ("sync", whole, 4)
+                yield STEP
+                holds(bits, quad, w, "ancestor bits")
             for i in range(n):
                 x, g = g, g + 1
                 if (x & 1) != team:
@@ -449,7 +496,7 @@ def rows(geo, q8, runs, seed, held):
                 if not busy:
                     p_full[sp].arrive()
                     continue
-                holds(buf, x % sb_n, ("s", x) if not half else buf.get(x % sb_n), "S")
+                holds(buf, (x % sb_n, (quad, half)), ("s", x), "S")
                 slot = geo["max_slot"][x % 4]
                 maxima[slot, team, half] = x
                 yield ("sync", pair, 2)
@@ -457,12 +504,24 @@ def rows(geo, q8, runs, seed, held):
                 holds(maxima, (slot, team, 1 - half), x, "maximum")
                 if sb_n == 3 and i >= 2 and sim.rng.random() < 0.5:   # references rise
                     yield wait(pv_done[(x - 2) % sb_n], (x - 2) // sb_n)
+                    holds(o_busy, team, None, "O")
+                    holds(o_of, team, w, "O")
+                elif sb_n == 2 and i >= 2:
+                    holds(o_busy, team, None, "O")
+                    holds(o_of, team, w, "O")
                 yield STEP
-                buf[x % sb_n] = ("p", x)
+                if mk:
+                    holds(bits, quad, w, "ancestor bits")
+                holds(buf, (x % sb_n, (quad, half)), ("s", x), "S")
+                buf[x % sb_n, (quad, half)] = ("p", x)
                 p_full[sp].arrive()
+            if half:
+                sums[team, quad] = w
             yield ("sync", pair, 2)
             yield STEP
             if not half:
+                holds(sums, (team, quad), w, "sums")
+                ml[w & 1, team, quad] = w
                 ml_rdy.arrive()
             yield wait(ml_rdy, w)
             yield wait(nf_rdy, w)
@@ -470,6 +529,16 @@ def rows(geo, q8, runs, seed, held):
             if sb_n == 2 and g > 1:
                 yield wait(pv_done[(g - 2) % sb_n], (g - 2) // sb_n)
             yield ("sync", whole, 4)
+            yield STEP
+            for t in range(2):
+                holds(ml, (w & 1, t, quad), w, "(m, l)")
+                if any((x & 1) == t for x in range(g - n, g)):
+                    holds(o_busy, t, None, "O")
+                    holds(o_of, t, w, "O")
+            if busy and mk:
+                holds(bits, quad, w, "ancestor bits")
+                for pw in noters:
+                    holds(noted, (w & 1, pw), w, "noted rows")
             o_free.arrive()
 
     def prepare(pw):
@@ -480,6 +549,9 @@ def rows(geo, q8, runs, seed, held):
         for w, (n, mk) in enumerate(runs):
             if w > 0:
                 yield wait(q_empty, w - 1)
+            noted[w & 1, pw] = w
+            q_of[pw] = w
+            yield STEP
             q_full.arrive()
             for i in range(n):
                 ks, vs = g % ks_n, g % vs_n

@@ -305,7 +305,11 @@ size_t m4q_attention_workspace(int kv_codec, int64_t H, int64_t Hkv, int64_t M, 
  *  BANDS   by r_i = original f_i / (2 pi), the turns of pair i over the
  *          original length: f_i / factor where r_i <= low, f_i where r_i >=
  *          high, the linear mix in between;
- *  YARN    the same, with the magnitude factor 0.1 ln(factor) + 1. */
+ *  YARN    the same, with the magnitude factor 0.1 ln(factor) + 1.
+ * BANDS and YARN mix by turns.  Models that were trained with a ramp over the pair
+ * index i between two rounded indices (the turns beta_slow and beta_fast turned into
+ * indices first) have other frequencies between the bands: give a table of one's
+ * own for those. */
 #define M4Q_ROPE_PLAIN 0
 #define M4Q_ROPE_LINEAR 1
 #define M4Q_ROPE_NTK 2
@@ -333,8 +337,9 @@ int m4q_rope_freqs(int64_t rot, double base, int scaling, double factor, double 
  *  - pos: int32 [M], any value (a negative position turns backwards).
  *  - freqs: the table of m4q_rope_freqs on the device; rot a multiple of 16,
  *    16 <= rot <= D; layout M4Q_ROPE_HALF or _INTERLEAVED.
- *  - The angle is exact to 2^-32 of a turn at every position, sines, cosines
- *    and products are fp32, and each value is rounded once. */
+ *  - The fraction of a turn pos f_i of the table's f_i is exact at every position and
+ *    rounded by at most 2^-28 of a turn; sines, cosines and products are fp32, and each
+ *    value is rounded once. */
 int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t H, int64_t M, int64_t D,
              const int32_t* pos, const int64_t* freqs, int64_t rot, int layout, float mscale, void* Y,
              int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream);
@@ -363,7 +368,8 @@ int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, con
 
 /* Reads cache rows back: Kout, Vout fp16 [Hkv][n][D], row j the cache row
  * slots[j] (Q8_0: each value RNE(q d)); a slot outside [0, B * C) gives zeros,
- * and slots may repeat.  Kc with Kout, or Vc with Vout, may be NULL, not both. */
+ * and slots may repeat.  Kc with Kout, or Vc with Vout, may be NULL, not both.  Kout
+ * and Vout overlap neither each other nor the caches (not checked). */
 int m4q_kv_read(const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t Hkv, int64_t C, int64_t D,
                 const int32_t* slots, int64_t n, void* Kout, void* Vout, m4q_stream_t stream);
 
@@ -373,7 +379,8 @@ int m4q_kv_read(const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t
  *   O[b N + i, h D + d] = sum_j softmax_j(scale Q[h, b N + i] . K[b, h / G, j]) V[b, h / G, j, d]
  * with G = H / Hkv.  The nodes' own keys and values are in the cache already
  * (m4q_kv_write with slots b C + past[b] + i).
- *  - Q: fp16 [H][B N][D]; O: fp16 [B N][H D].
+ *  - Q: fp16 [H][B N][D]; O: fp16 [B N][H D], which overlaps no other argument (not
+ *    checked).
  *  - past: int32 [B] on the device (read by the kernel: a captured call
  *    follows its changes), clamped to [0, C]; a node whose row past[b] + i is
  *    not below C has no key of its own.

@@ -549,7 +549,9 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, facto
                original: float = 0.0, low: float = 1.0, high: float = 32.0, device="cuda"):
     """(freqs, mscale): the table of rotary frequencies for rope and kv_write,
     int64 [rot / 2] on `device` (turns per position in units of 2^-64), and the
-    magnitude factor of the scaling (m4q_rope_freqs)."""
+    magnitude factor of the scaling (m4q_rope_freqs).  ROPE_BANDS and ROPE_YARN
+    mix by the turns of a pair over the original length; a model trained with a
+    ramp over pair indices needs a table of its own."""
     import torch
     host = (ctypes.c_int64 * max(1, rot // 2))()
     mscale = ctypes.c_float()

@@ -30,10 +30,18 @@
 // two of them overlap.
 //
 // Measured: 32 sequences of one token, 4 heads a group, D = 128, over 500 to 8,100
-// Q8_0 keys in 96 us (300 MB: 3.1 TB/s), 8 nodes over 300 fp16 keys in 9.6 us.
-// fp16 calls are at HBM when long; Q8_0 is bound by the decode warps' instructions,
-// whose fetch is the second stall after TMEM and shared memory loads (72 KB of
-// code); short calls by the start and end of a run.
+// Q8_0 keys in 95 us (300 MB: 3.1 TB/s) and as many fp16 keys in 95 (564 MB: 5.9
+// TB/s), over 32,000 to 32,700 in 411 (5.5 TB/s) and 602 (4.24 GB: 7.0 TB/s, HBM's
+// rate for reads); at D = 64, 70, 63, 333 and 329 us (2.1, 4.4, 3.4, 6.4 TB/s).  8
+// nodes over 300 fp16 keys take 9.7.  Q8_0 is bound by the decode warps: their
+// instructions, the fetch of these (72 KB of code; the second stall after TMEM and
+// shared memory loads) and the latency of a group (half of the issue slots are
+// empty, 64 bytes a thread are spilled at 72 registers); short calls by the start and
+// end of a run.
+//
+// P is rounded to fp16, the type of the MMA with V (V is fp16, or decoded to it): 2^-11
+// of each weight, 2.9e-4 of the result against 2.1e-4 when only that is rounded.  The
+// sums are of the unrounded P.
 //
 // Warps: 0 issues the S MMAs (four TMEM buffers ahead), 1 the P V MMAs, 2 and 3
 // the copies, 4-11 are the softmax teams (lane = key), the others prepare (Q, the

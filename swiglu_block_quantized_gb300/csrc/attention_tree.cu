@@ -25,13 +25,14 @@
 // for 256 rows over 32K Q8_0 keys: both teams then wait for the same tile.)
 //
 // Measured: 8 sequences of 24 nodes, 4 heads a group, D = 64, over 1,000 to 8,100
-// fp16 keys in 32.8 us (75.6 MB: 2.3 TB/s), one of 64 nodes, D = 128, over 32,500
-// Q8_0 keys in 55.7 us (34 GFLOP: 612 TFLOP/s).  Long calls are at HBM for fp16 at
-// D = 128 (1.38 us a tile and SM, 7.2 TB/s) and at 5.5 TB/s for D = 64 (0.91 us a
-// tile), and Q8_0 at D = 128 takes 1.3 us a tile: there a team's chain of a tile bounds
-// them (scores 650 to 950 clocks, maxima 500, exponentials 1300, hand-over 350, P V
-// 700); short calls the start (schedule, Q: 3 us), the end of a run (2 us) and the
-// join (3 us).
+// fp16 keys in 32.9 us (75.6 MB: 2.3 TB/s), one of 64 nodes, D = 128, over 32,500
+// Q8_0 keys in 56.2 us (34 GFLOP: 607 TFLOP/s).  Long calls, the 8 sequences over
+// 32,000 to 32,700 keys: fp16 in 171 us at D = 128 (1.06 GB: 6.2 TB/s) and 115 at D =
+// 64 (4.6 TB/s), Q8_0 in 168 and 129 (3.3 and 2.2 TB/s).  All but the first of these
+// are bound by a team's chain of a tile (scores 650 to 950 clocks, maxima 500,
+// exponentials 1300, hand-over 350, P V 700); short calls by the start (schedule, Q: 3
+// us), the end of a run (2 us) and the join (3 us).  (Q8_0 at D = 128 spills 44 bytes a
+// thread at 72 registers.)
 //
 // TMEM holds two O and, at D = 64, three score buffers: a team's next scores are
 // formed in the third while it works on the last ones, off its chain (1.10 to 0.91
@@ -48,8 +49,10 @@
 //           keys 0-63 and 64-127: the row's maximum (exchanged through shared
 //           memory), P = 2^(s - m) against a reference m that is raised only
 //           when the maximum passes it by 2^8 (O is then rescaled in TMEM),
-//           fp32 row sums, P rounded to fp16 (one thread a row: 37.7 us against
-//           35.9 for the first case above as it then was);
+//           fp32 row sums, P rounded to fp16, the type of the MMA with V (2^-11 of
+//           each weight: 2.9e-4 of the result against 2.1e-4 when only that is
+//           rounded) (one thread a row: 37.7 us against 35.9 for the first case above
+//           as it then was);
 //   20-     per run: Q into swizzled shared memory; Q8_0: four warps decode each
 //           raw K tile and four each V tile to fp16 (RNE(q d), the weights'
 //           exact decode) in the swizzled stages; in tiles that hold keys which

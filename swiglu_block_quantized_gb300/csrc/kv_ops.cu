@@ -9,7 +9,10 @@
 // a turn, exactly: no position, however far, costs the angle any accuracy
 // (an fp32 product is off by 0.03 rad at position 10^6), and no 64-bit float
 // is needed.  The fraction is cut to the nearest quarter turn in integers,
-// and the remainder (at most 1/8 turn, 30 bits) goes to fp32 and sincospif.
+// and the remainder (at most 1/8 turn, 30 bits) goes to fp32 and sincospif: at most
+// 2^-28 of a turn off, where an fp16 result is rounded by 2^-11.  (Of Q8_0 codes one
+// beside a tie may go the other way, as it may with sines rounded from 64 bits: a
+// prompt's rows are off by 2.6e-5 and 2.9e-5 of their size.)
 //
 // Quantisation of a block of 32 values x (Q8_0): d = max|x| / 127 rounded up
 // to fp16, so that no code is cut off at 127 even where d is subnormal; codes
@@ -30,8 +33,8 @@
 //
 // Bound by memory from a few thousand tokens on, by the launch below that.
 // Measured: 32 heads of 8,192 tokens, 128 values, rotated in 24.9 us (5.4 TB/s
-// of input and output), of 128 tokens in 3.0 us; 8,000 tokens of 8 + 8 heads
-// written to Q8_0 rows and read back in 25.5 us (3.9 TB/s); 32,000 Q8_0 rows of
+// of input and output), of 128 tokens in 3.1 us; 8,000 tokens of 8 + 8 heads
+// written to Q8_0 rows and read back in 25.6 us (3.9 TB/s); 32,000 Q8_0 rows of
 // 8 heads read back in 17.9 us (5.6 TB/s).
 #include <type_traits>
 
@@ -288,7 +291,9 @@ cudaError_t launch_rope_kv(const KvOpsParams& p, bool q8, cudaStream_t s) {
   const int tokens = kBlock / (p.D / 16);   // a CTA's
   const long long tiles = ((long long)p.M + tokens - 1) / tokens;
   // Heads a thread walks with its sines and cosines: as many as still leave
-  // eight CTAs an SM, at most 8 (their cost is then well under the copy's).
+  // eight CTAs an SM, at most 8 (their cost is then well under the copy's).  (Of the
+  // Q8_0 kernels seven fit an SM: the 8,000 tokens above are 1,500 CTAs of 6, 6 and 4
+  // heads, 1.4 waves; the 8,192 rotated ones are 1.7.)
   long long per = tiles * heads / (8ll * (p.nsm > 0 ? p.nsm : 1));
   per = per < 1 ? 1 : per > 8 ? 8 : per;
   const dim3 grid((unsigned)tiles, (unsigned)((heads + per - 1) / per), 1);

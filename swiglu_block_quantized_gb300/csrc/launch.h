@@ -195,10 +195,29 @@ constexpr int kTreeSeqs = 256;
 constexpr int kTreeFewRows = 32;
 // Items are cut when the longest, as often as an SM takes one, has `join` tiles
 // more than the SM's share u of all tiles, and u / 2, at most `run`, more on top:
-// otherwise the join, and the second run of a CTA, cost more than they save.  Measured, whole against cut, in us (G = 4, D = 64, fp16): 8
-// sequences of 24 nodes 14.7 / 15.0 with 8 tiles each and 16.9 / 15.9 with 10, one of
-// 64 nodes 10.7 / 10.1 with 4 and 12.9 / 10.4 with 6; few rows: 8 sequences of 4 nodes
-// 16.0 / 17.0 with 16 tiles and 18.3 / 17.8 with 20, one of one 8.6 / 8.3 with 6.
+// otherwise the join, and the second run of a CTA, cost more than they save.  One bound
+// for both head sizes and cache types, set at D = 64, fp16.  Measured, whole / cut, in
+// us, 8 KV heads of 4 heads each, by tiles of a sequence:
+//   8 sequences of 24 nodes (cut from 7 on)   4 tiles      6           8          10
+//     D = 64, fp16                         9.7/11.9   11.7/12.8   13.6/15.0   15.4/15.7
+//     D = 64, Q8_0                        12.8/12.5   14.9/13.9   17.1/16.5   19.2/16.8
+//     D = 128, fp16                       13.0/13.5   16.5/18.4   20.0/21.1   22.7/22.2
+//     D = 128, Q8_0                       17.1/15.7   19.8/17.6   22.4/20.7   25.4/21.7
+//   one of 64 nodes (from 5 on)               3 tiles      4           6
+//     D = 64, fp16                        11.3/13.2   12.1/12.1   14.1/12.5
+//     D = 64, Q8_0                        14.2/14.1   15.1/13.0   17.3/13.4
+//     D = 128, fp16                       14.2/14.9   14.8/13.2   17.6/13.5
+//     D = 128, Q8_0                       19.2/17.4   20.9/14.8   23.6/15.1
+//   few rows, 8 sequences of 4 (from 17 on)  16 tiles     20          24
+//     D = 64, fp16                        16.4/18.2   19.4/20.1   21.9/21.8
+//     D = 64, Q8_0                        19.9/20.0   23.0/20.9   26.2/22.9
+//     D = 128, fp16                       18.9/22.7   21.8/25.8   24.5/28.4
+//     D = 128, Q8_0                       23.0/24.7   26.8/27.2   30.5/29.4
+//   few rows, one of one (from 7 on)          4 tiles      6           8
+//     D = 64, fp16                          7.2/7.7     8.4/8.2     9.6/9.0
+//     D = 64, Q8_0                          8.8/9.1    10.3/9.5    11.8/10.3
+//     D = 128, fp16                         8.0/8.0     9.2/8.3    10.5/8.5
+//     D = 128, Q8_0                        10.3/9.7   11.8/10.1    13.5/10.2
 struct TreeWhole {
   float join, run;
 };

@@ -3,14 +3,18 @@
 //   u  = h / rms(h) * w_post                 (or h, without w_post)
 //   r' = res_scale r + branch_scale gate u   (gate: none, [D] or [M][D])
 //   y  = r' / rms(r') * w_pre                (rms(x)^2 = mean x^2 + eps)
-// Every input is read once and every output written once: a row stays in the
-// registers of its group of warps (V 16-byte vectors of 8 values a thread)
-// between the two reductions.  Sums and r' are fp32; r' is rounded once where
+// Every input is read once and every output written once: a row of up to 8,192
+// values stays in the registers of its group of warps (V 16-byte vectors of 8 values a
+// thread) between the two reductions.  Sums and r' are fp32; r' is rounded once where
 // it is stored, and y is formed from the unrounded r'.
 //
-// Bound by HBM: 8,192 rows of 4,096 with an fp32 residual, both norms and a gate in
-// 67.7 us (6.0 TB/s of the 403 MB it has to move); 64 rows of 2,048 in 1.7 us, a
-// launch's own time.
+// Bound by HBM up to there: 8,192 rows of 4,096 with an fp32 residual, both norms and a
+// gate in 67.6 us (6.0 TB/s of the 403 MB it has to move), with an fp16 one in 54 (5.0
+// TB/s), 4,096 rows of 8,192 in 75 and 60; 64 rows of 2,048 in 1.8 us, a launch's own
+// time.  Wider rows do not fit: 1,024 threads have at most 64 registers each, for 96
+// values of r', h and the gate, so that they spill (stacks of 288 bytes a thread with
+// an fp32 residual, of 376 with an fp16 one) and local memory bounds them: as many values in rows of 8,200 take 254 and
+// 434 us, of 16,384 167 and 264, of 32,768 140 and 187.
 #include "kv_common.cuh"
 #include "launch.h"
 

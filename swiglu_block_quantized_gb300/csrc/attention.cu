@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(128, KS ? 3 : 2) attn_kernel(const AttnParams 
     lim[h2] = (int)l;
   }
 
-  // Q fragments (A operand), zero for rows past R.
+  // Q fragments (A operand), zero for rows past R.  (Ordinary loads: the kernel that
+  // writes Q may still run when this one starts.)
   uint32_t qa[DK][4];
 #pragma unroll
   for (int kk = 0; kk < DK; ++kk)
@@ -276,8 +277,8 @@ __global__ void __launch_bounds__(128, KS ? 3 : 2) attn_kernel(const AttnParams 
       const uint32_t* qrow =
           reinterpret_cast<const uint32_t*>(p.q + ((long long)qh[h2] * p.M + qi[h2]) * D + 16 * kk + 2 * t);
       const bool qok = rok[h2] && in_bounds(qh[h2] < p.H && qi[h2] < p.M, p.status, kSiteAttnQ);
-      qa[kk][h2] = qok ? __ldg(qrow) : 0u;
-      qa[kk][2 + h2] = qok ? __ldg(qrow + 4) : 0u;
+      qa[kk][h2] = qok ? *qrow : 0u;
+      qa[kk][2 + h2] = qok ? qrow[4] : 0u;
     }
 
   float o[DN][4];

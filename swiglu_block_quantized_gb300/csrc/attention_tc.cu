@@ -562,10 +562,11 @@ __global__ void __launch_bounds__(640, 1)
 // 16 values of a row (half of a 32-value block), K for blockIdx.y == 0 and V
 // for 1.  Each value is RNE(q d): q is exact in fp16, so one fp16 multiply
 // rounds the exact product once.  Blocks start on 2-byte boundaries (34-byte
-// blocks), so the codes are read in 2-byte words.
+// blocks), so the codes are read in 2-byte words.  By ordinary loads (no
+// __restrict__ either): the kernel that writes the rows may still run when this one
+// starts.
 __global__ void __launch_bounds__(256)
-    kv_q8_stage_kernel(const uint8_t* __restrict__ k, const uint8_t* __restrict__ v, long long rows, int D,
-                       __half* __restrict__ kf, __half* __restrict__ vf) {
+    kv_q8_stage_kernel(const uint8_t* k, const uint8_t* v, long long rows, int D, __half* kf, __half* vf) {
   pdl_wait();   // the caches may come from the previous kernel
   pdl_launch_dependents();
   const uint8_t* src = blockIdx.y ? v : k;
@@ -576,12 +577,12 @@ __global__ void __launch_bounds__(256)
   const long long n = idx / per_row;
   const int c = (int)(idx % per_row);
   const uint8_t* blk = src + n * (D / 32) * 34 + (long long)(c >> 1) * 34;
-  const __half2 d2 = __half2half2(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(blk))));
+  const __half2 d2 = __half2half2(__ushort_as_half(*reinterpret_cast<const unsigned short*>(blk)));
   const unsigned short* q = reinterpret_cast<const unsigned short*>(blk + 2 + 16 * (c & 1));
   uint32_t out[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int two = __ldg(q + e);
+    const int two = q[e];
     int q0 = two & 0xff, q1 = (two >> 8) & 0xff;
     q0 -= (q0 & 0x80) << 1;   // the codes are signed bytes
     q1 -= (q1 & 0x80) << 1;

@@ -110,16 +110,17 @@ __device__ __forceinline__ uint32_t lds_u16(const uint8_t* p) {
 
 __device__ __forceinline__ uint32_t spread16(uint32_t v) { return __byte_perm(v, 0u, 0x4140u); }
 
-// X fragment loads for activation row m (zero when m >= M).
+// X fragment loads for activation row m (zero when m >= M).  Ordinary loads: the
+// kernel that writes X may still run when this one starts.
 template <int BYTES>
 __device__ __forceinline__ void ldx(uint32_t* dst, const __half* xrow, bool ok) {
   if constexpr (BYTES == 8) {
-    uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(xrow)) : make_uint2(0, 0);
+    uint2 v = ok ? *reinterpret_cast<const uint2*>(xrow) : make_uint2(0, 0);
     dst[0] = v.x; dst[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < BYTES / 16; ++i) {
-      uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(xrow) + i) : make_uint4(0, 0, 0, 0);
+      uint4 v = ok ? reinterpret_cast<const uint4*>(xrow)[i] : make_uint4(0, 0, 0, 0);
       dst[4 * i] = v.x; dst[4 * i + 1] = v.y; dst[4 * i + 2] = v.z; dst[4 * i + 3] = v.w;
     }
   }
@@ -477,8 +478,8 @@ __global__ void __launch_bounds__(GemvCfg<C, MT>::kThreads, 1) gemv_kernel(const
         const int blk = kPairs ? 2 * (cw + NC * (j >> 1)) + (j & 1) : cw + NC * j;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint32_t lo = ok_m ? __ldg(xrow + blk * S::B + xh_k<C>(j & 1, t, r, 0)) : 0u;
-          const uint32_t hi = ok_m ? __ldg(xrow + blk * S::B + xh_k<C>(j & 1, t, r, 1)) : 0u;
+          const uint32_t lo = ok_m ? xrow[blk * S::B + xh_k<C>(j & 1, t, r, 0)] : 0u;
+          const uint32_t hi = ok_m ? xrow[blk * S::B + xh_k<C>(j & 1, t, r, 1)] : 0u;
           xh[j][r] = lo | (hi << 16);
         }
       }

@@ -17,3 +17,16 @@ def test_only_the_frequency_table_is_read_only(name):
     assert "ld.global.nc" not in code and "__restrict__" not in code
     for call in re.finditer(r"__ldg\(", code):
         assert "p.freqs" in code[call.start():call.start() + 60].split(";")[0], code[call.start():call.start() + 80]
+
+
+# The kernels of before that read what the serving kernels write: activations (the
+# norms), queries (the rotation) and cache rows.  Packed weights are nobody's output.
+@pytest.mark.parametrize("name", ["gemv.cuh", "attention.cu", "attention_tc.cu", "tc_proj.cuh", "tc_small.cuh"])
+def test_activations_queries_and_cache_rows_are_not_read_only(name):
+    with open(os.path.join(CSRC, name)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    for call in re.finditer(r"__ldg\(", code):
+        arg = code[call.start():call.start() + 90].split(";")[0]
+        assert "p.row_bytes" in arg or "(row + o" in arg, arg   # packed weight rows
+    for kernel in re.finditer(r"__global__[^{;]*\{", code):
+        assert "__restrict__" not in kernel.group(0), kernel.group(0)

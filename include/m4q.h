@@ -344,6 +344,17 @@ int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t
              const int32_t* pos, const int64_t* freqs, int64_t rot, int layout, float mscale, void* Y,
              int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream);
 
+/* The same with positions of several axes (time, height and width of an image's or a
+ * video's patches): pair i turns by pos[axes[i]][m] f_i.
+ *  - pos: int32 [A][M], 1 <= A <= M4Q_ROPE_MAX_AXES (else M4Q_ERR_INVALID_ARG).
+ *  - axes: int32 [rot / 2] on the device, the axis of each pair; a pair whose axis is
+ *    outside [0, A) is not turned (position 0).  With every axis 0 the result is
+ *    m4q_rope's, bit for bit. */
+#define M4Q_ROPE_MAX_AXES 8
+int m4q_rope_axes(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t H, int64_t M, int64_t D,
+                  const int32_t* pos, int64_t A, const int64_t* freqs, const int32_t* axes, int64_t rot, int layout,
+                  float mscale, void* Y, int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream);
+
 /* Writes the K and V rows of M tokens to the caches, K turned as by m4q_rope
  * on the way (freqs NULL: as it is; pos, rot, layout and mscale are then not
  * read), and in the same launch turns the tokens' queries (Q NULL: none).
@@ -365,6 +376,15 @@ int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, con
                  const int32_t* pos, const int64_t* freqs, int64_t rot, int layout, float mscale,
                  const int32_t* slots, void* Kc, void* Vc, int kv_codec, int64_t B, int64_t C, const void* Q,
                  int64_t q_head_stride, int64_t q_row_stride, int64_t H, void* Qout, m4q_stream_t stream);
+
+/* The same with positions of several axes, as m4q_rope_axes (freqs and axes are
+ * needed, else M4Q_ERR_INVALID_ARG). */
+int m4q_kv_write_axes(const void* K, int64_t k_head_stride, int64_t k_row_stride, const void* V,
+                      int64_t v_head_stride, int64_t v_row_stride, int64_t Hkv, int64_t M, int64_t D,
+                      const int32_t* pos, int64_t A, const int64_t* freqs, const int32_t* axes, int64_t rot, int layout,
+                      float mscale, const int32_t* slots, void* Kc, void* Vc, int kv_codec, int64_t B, int64_t C,
+                      const void* Q, int64_t q_head_stride, int64_t q_row_stride, int64_t H, void* Qout,
+                      m4q_stream_t stream);
 
 /* Reads cache rows back: Kout, Vout fp16 [Hkv][n][D], row j the cache row
  * slots[j] (Q8_0: each value RNE(q d)); a slot outside [0, B * C) gives zeros,
@@ -408,6 +428,107 @@ int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_cod
  * device (0 when it uses none, or for an invalid shape). */
 size_t m4q_attention_tree_workspace(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t C,
                                     int64_t D);
+
+/* ---------------------------------------------------------------------------
+ * A paged cache: pools Kc, Vc of P pages [P][Hkv][page] rows, shared by all sequences.
+ * For m4q_kv_write and m4q_kv_read it is a batch of caches with B = P and C = page: row
+ * r of page i has the slot i * page + r.  Each sequence has a row of the block table,
+ * int32 [B][W]: its rows j lie at place j % page of page table[b][j / page].  A decode
+ * step is m4q_page_plan -> (a layer: m4q_kv_write -> m4q_attention_paged) ->
+ * m4q_verify_tree.
+ */
+
+/* Pages and slots of a step, from lengths on the device (a captured call follows
+ * them).  Sequence b has past[b] rows in the cache and gets fresh[b] tokens; fresh[b] <
+ * 0 says that it has ended.
+ *  - table int32 [B][W], held int32 [B], free_pages int32 [P], n_free int32 [1]: the
+ *    state, on the device, updated.  held[b] entries of table[b] are pages of b (more
+ *    than its rows need where drafted tokens were turned down); the first n_free
+ *    entries of free_pages are free, the last of them handed out first.
+ *  - b needs ceil((past[b] + fresh[b]) / page) pages, at most W, and is handed what it
+ *    lacks, sequence by sequence; when the free ones run out the rest of the entries are
+ *    -1.  An ended sequence's pages go on top of the free ones that are left (and are
+ *    handed out from the next call on), its entries become -1 and held[b] 0.  Other
+ *    entries of table and free_pages stay as they are.
+ *  - The tokens of all sequences lie one after the other in T places: starts int32
+ *    [B + 1] is where each sequence's begin (starts[B]: their number; tokens behind the
+ *    T-th are left out, as if fresh were smaller).  slots int32 [T], pos int32 [T]: the
+ *    slot and the position past[b] + i of token i of b; the slot is -1 where b has no
+ *    page for it.  Places behind the last token get slot -1 and position 0, so a padded
+ *    m4q_kv_write of all T writes nothing for them.
+ *  - lengths int32 [B]: the rows of b after the step, min(past[b] + fresh[b], held[b] *
+ *    page), 0 for an ended one: what m4q_attention_paged reads.
+ *  - Called again on its results with the same past and fresh it changes nothing, unless
+ *    pages were missing or went back.
+ *  - Values below 0 or above their range (past, held, n_free) count as the nearest in
+ *    it; a table entry of b that is not a page gives slots of -1.
+ *  - 1 <= B <= 4096, page, W, P, T >= 1, T <= INT32_MAX - 8192 (else
+ *    M4Q_ERR_INVALID_ARG), P * page and W * page <= INT32_MAX (else
+ *    M4Q_ERR_BAD_SHAPE).  The arrays do not overlap (not checked). */
+int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t page, int32_t* table, int64_t W,
+                  int32_t* held, int32_t* free_pages, int64_t P, int32_t* n_free, int64_t T, int32_t* slots,
+                  int32_t* pos, int32_t* lengths, int32_t* starts, m4q_stream_t stream);
+
+/* Attention of one new token of each of B sequences over a paged cache:
+ *   O[b, h D + d] = sum_{j < lengths[b]} softmax_j(scale Q[h, b] . K[b, h / G, j]) V[b, h / G, j, d]
+ * with G = H / Hkv; the token's own row is one of them (lengths counts it).
+ *  - Q: fp16 [H][B][D] (m4q_kv_write's Qout); O: fp16 [B][H D], which overlaps no other
+ *    argument (not checked).
+ *  - table int32 [B][W], lengths int32 [B] on the device, read by the kernel; lengths are
+ *    clamped to [0, W * page].  Sequences may share pages.  Rows of an entry outside [0,
+ *    P) are not seen; a sequence that sees no row gets zeros.
+ *  - Rows behind the last do not enter the result, whatever they hold (infinities and
+ *    NaN included).
+ *  - D is 64 or 128, H % Hkv == 0, page % 8 == 0, W * page <= INT32_MAX, the pools as
+ *    for m4q_kv_write (else M4Q_ERR_BAD_SHAPE); B, H <= 65535, scale log2(e) finite in 32
+ *    bits (else M4Q_ERR_INVALID_ARG).
+ *  - Arithmetic as m4q_attention.
+ *  - workspace: m4q_attention_paged_workspace() bytes (not cleared before or after,
+ *    16-byte aligned) for the partial results of keys split across CTAs; NULL or a
+ *    smaller size runs without a split, slower.  Calls whose work overlaps need a
+ *    workspace each. */
+int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t H,
+                        int64_t Hkv, int64_t P, int64_t page, int64_t D, const int32_t* table, int64_t W,
+                        const int32_t* lengths, float scale, void* O, void* workspace, size_t workspace_bytes,
+                        m4q_stream_t stream);
+
+/* Workspace bytes m4q_attention_paged uses for this shape on the current device (0 when
+ * it uses none, or for an invalid shape). */
+size_t m4q_attention_paged_workspace(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t P, int64_t page,
+                                     int64_t W, int64_t D);
+
+/* Types of the probabilities of m4q_verify_tree. */
+#define M4Q_PROB_F32 0
+#define M4Q_PROB_F16 1
+
+/* Drafted trees of tokens verified against the target's probabilities (speculative
+ * sampling; siblings tried in turn), so that the tokens kept and the next one are
+ * distributed as the target's own samples when each child was drawn from its parent's
+ * draft distribution.
+ *  - Node 0 of a sequence is its last known token (parents -1; any other value: an unused
+ *    sequence, whose count is 0, token and path -1); node i > 0 is the drafted token
+ *    tokens[b][i] behind node parents[b][i] in [0, i).  Nodes with other parents, or
+ *    tokens outside [0, V), are unused.  (As m4q_attention_tree's nodes, with one root.)
+ *  - target, draft: rows of V probabilities behind node i of sequence b, at
+ *    b * seq_stride + i * row_stride elements, prob_type M4Q_PROB_F32 or _F16; p and q
+ *    below.  Values that are not finite positive numbers count as 0.  draft may be NULL
+ *    with N = 1: the next token is then a plain sample.
+ *  - u: fp32 [B][N] in [0, 1): u[b][i] decides on node i, u[b][0] draws the next token.
+ *  - From c = 0 on, with M = 0 and m = 1: the children of c in order of their index; x is
+ *    taken, and becomes c, if u m q(x) < p(x) - M q(x); else M grows by m, and m becomes
+ *    the sum of the rest r = max(p - M q, 0).  When no child is left the next token is
+ *    the smallest x for which the sum of r up to x exceeds u[b][0] times the whole sum
+ *    (M = 0: r = p).  Where r is 0 throughout (the draft covers the target, but for
+ *    roundings) p stands for it; where p is 0 throughout the token is -1.
+ *  - path int32 [B][N]: the nodes kept, 0 first, -1 behind them; count int32 [B]: their
+ *    number; token int32 [B]: the next token.
+ *  - Differences and sums are formed to 2^-44 of their size, in a fixed order.
+ *  - 1 <= N <= 256, 1 <= V <= 2^24 (else M4Q_ERR_INVALID_ARG).  The outputs overlap
+ *    nothing (not checked). */
+int m4q_verify_tree(const void* target, int64_t t_seq_stride, int64_t t_row_stride, const void* draft,
+                    int64_t d_seq_stride, int64_t d_row_stride, int prob_type, int64_t B, int64_t N, int64_t V,
+                    const int32_t* tokens, const int32_t* parents, const float* u, int32_t* path, int32_t* count,
+                    int32_t* token, m4q_stream_t stream);
 
 /* Types of the residual stream of m4q_norm_residual. */
 #define M4Q_RES_F16 0

@@ -17,10 +17,13 @@ Functions mirror the C ABI (same names without the ``m4q_`` prefix):
     dequant(w, codec, n, k, out=None)
     mlx4_pack(words, scales, biases, n, k, out=None)
     attention(q, k, v, kv_codec, hkv, t, q_offset=None, causal=True, scale=None, out=None)
-    rope_freqs(rot, base=10000.0, ...), rope(x, pos, freqs, ...)
-    kv_write(k, v, kc, vc, kv_codec, slots, pos=None, freqs=None, ..., q=None)
+    rope_freqs(rot, base=10000.0, ...), rope_axes(sections, ...), rope(x, pos, freqs, ..., axes=None)
+    kv_write(k, v, kc, vc, kv_codec, slots, pos=None, freqs=None, ..., q=None, axes=None)
     kv_read(kc, vc, kv_codec, slots, ...)
     attention_tree(q, kc, vc, kv_codec, past, parents, ...)
+    page_plan(past, new, table, held, free, n_free, page, tokens)
+    attention_paged(q, kc, vc, kv_codec, table, lengths, ...)
+    verify_tree(target, draft, tokens, parents, u)
     norm_residual(h, r, w_pre, w_post=None, gate=None, ...)
     weight_bytes(codec, n, k), check_finite(t), check_device_status(),
     selftest_wait_timeout(limit_ns), status_string(code), version()
@@ -52,6 +55,7 @@ ACT_SILU, ACT_GELU = 0, 1
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = 0, 1, 2, 3, 4
 RES_F16, RES_F32 = 0, 1
+PROB_F32, PROB_F16 = 0, 1
 
 OK = 0
 ERR_INVALID_ARG = -1
@@ -101,6 +105,16 @@ SIGNATURES = {
     "m4q_attention_tree": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp,
                                   ctypes.c_float, _vp, _vp, _sz, _vp]),
     "m4q_attention_tree_workspace": (_sz, [_i32, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "m4q_rope_axes": (_i32, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i32, ctypes.c_float, _vp,
+                             _i64, _i64, _vp]),
+    "m4q_kv_write_axes": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i32,
+                                 ctypes.c_float, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "m4q_page_plan": (_i32, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "m4q_attention_paged": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp,
+                                   ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "m4q_attention_paged_workspace": (_sz, [_i32, _i64, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "m4q_verify_tree": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _vp]),
     "m4q_norm_residual": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _i64, _i64, ctypes.c_float, ctypes.c_float,
                                  ctypes.c_float, _vp, _vp, _vp]),
     "m4q_weight_bytes": (_sz, [_i32, _i64, _i64]),
@@ -560,19 +574,47 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, facto
     return torch.tensor(list(host), dtype=torch.int64).to(device), float(mscale.value)
 
 
-def _turn_args(pos, freqs, m_):
-    _ints(pos, _t().int32, m_, "pos")
+def rope_axes(sections, dealt: bool = False, device="cuda"):
+    """The table of axes for rope and kv_write, int32 [sum(sections)] on
+    `device`: sections[a] pairs turn by the positions of axis a, one section
+    after the other; dealt: pair i belongs to axis i % len(sections) while that
+    axis has pairs left, and to axis 0 otherwise (sections[0] is the rest)."""
+    import torch
+    n = [int(v) for v in sections]
+    if not n or len(n) > 8 or min(n) < 0 or sum(n) < 1:
+        raise ValueError("sections must be up to 8 counts of pairs")
+    if not dealt:
+        table = [a for a, c in enumerate(n) for _ in range(c)]
+    else:
+        table = [i % len(n) if i < len(n) * n[i % len(n)] else 0 for i in range(sum(n))]
+        if [table.count(a) for a in range(len(n))] != n:
+            raise ValueError("%s pairs cannot be dealt out in turn" % (n,))
+    return torch.tensor(table, dtype=torch.int32).to(device)
+
+
+def _turn_args(pos, freqs, m_, axes):
+    """(rot, axes, their pointer): one axis (0, None) without a table."""
+    pairs = freqs.numel()
+    if axes is None:
+        _ints(pos, _t().int32, m_, "pos")
+        _need(freqs, _torch.int64, "freqs")
+        return 2 * pairs, 0, None
+    _need(pos, _t().int32, "pos")
+    if pos.dim() != 2 or pos.shape[1] != m_:
+        raise ValueError("pos must be [axes, %d]" % m_)
     _need(freqs, _torch.int64, "freqs")
-    return 2 * freqs.numel()
+    _ints(axes, _torch.int32, pairs, "axes")
+    return 2 * pairs, pos.shape[0], axes.data_ptr()
 
 
-def rope(x, pos, freqs, layout: int = ROPE_HALF, mscale: float = 1.0, out=None, stream=None):
+def rope(x, pos, freqs, layout: int = ROPE_HALF, mscale: float = 1.0, out=None, stream=None, axes=None):
     """Rotary positions: the first 2 * len(freqs) values of each row of x fp16
     [H, M, D] turned by pos int32 [M].  x may have any head and row strides
     that are multiples of 8.  out (fp16 [H, M, D], rows that do not overlap)
-    may be x itself."""
+    may be x itself.  With axes int32 [len(freqs)] (rope_axes) pos is [A, M],
+    and pair i turns by pos[axes[i]]."""
     h, m_, d, hs, rs = _head_rows(x, "x")
-    rot = _turn_args(pos, freqs, m_)
+    rot, n_axes, p_axes = _turn_args(pos, freqs, m_, axes)
     if out is None:
         out = _allocate((h, m_, d), _torch.float16, x, stream)
         ohs, ors = m_ * d, d
@@ -588,8 +630,14 @@ def rope(x, pos, freqs, layout: int = ROPE_HALF, mscale: float = 1.0, out=None, 
                 reach += step * (count - 1)
         if out.data_ptr() == x.data_ptr() and (hs, rs) != (ohs, ors):
             raise ValueError("out starts where x does, with other strides")
-    dev = _one_device(x, pos, freqs, out)
+    dev = _one_device(x, pos, freqs, out, axes)
     if h == 0 or m_ == 0:
+        return out
+    if p_axes is not None:
+        rc = load().m4q_rope_axes(x.data_ptr(), hs, rs, h, m_, d, pos.data_ptr(), n_axes, freqs.data_ptr(), p_axes,
+                                  rot, layout, mscale, out.data_ptr(), ohs, ors, _raw_stream(stream, dev))
+        if rc:
+            raise M4QError(rc, "m4q_rope_axes")
         return out
     rc = load().m4q_rope(x.data_ptr(), hs, rs, h, m_, d, pos.data_ptr(), freqs.data_ptr(), rot, layout, mscale,
                          out.data_ptr(), ohs, ors, _raw_stream(stream, dev))
@@ -599,11 +647,13 @@ def rope(x, pos, freqs, layout: int = ROPE_HALF, mscale: float = 1.0, out=None, 
 
 
 def kv_write(k, v, kc, vc, kv_codec: int, slots, pos=None, freqs=None, layout: int = ROPE_HALF,
-             mscale: float = 1.0, q=None, q_out=None, stream=None):
+             mscale: float = 1.0, q=None, q_out=None, stream=None, axes=None):
     """Write the rows k, v fp16 [Hkv, M, D] of M tokens to the caches kc, vc
     [B, Hkv, C, row] at slots int32 [M] (b * C + j; outside the cache: not
     written), k turned by pos and freqs when given.  With q fp16 [H, M, D] the
-    queries are turned in the same launch and returned as q_out [H, M, D]."""
+    queries are turned in the same launch and returned as q_out [H, M, D].  With
+    axes (rope) pos is [A, M].  Pages [P, Hkv, page, row] are written by the slots
+    of page_plan."""
     hkv, m_, d, khs, krs = _head_rows(k, "k")
     vh, vm, vd, vhs, vrs = _head_rows(v, "v")
     b, ch, c, cd = _cache_shape(kc, vc, kv_codec)
@@ -612,11 +662,11 @@ def kv_write(k, v, kc, vc, kv_codec: int, slots, pos=None, freqs=None, layout: i
     if vh != hkv or vm != m_ or vd != d or ch != hkv or cd != d:
         raise ValueError("k, v and the caches must agree on heads, rows and D")
     _ints(slots, _torch.int32, m_, "slots")
-    rot, h, qhs, qrs, p_pos, p_freqs, p_q, p_qo = 0, 0, 0, 0, None, None, None, None
+    rot, h, qhs, qrs, p_pos, p_freqs, p_q, p_qo, p_axes = 0, 0, 0, 0, None, None, None, None, None
     if freqs is not None:
         if pos is None:
             raise ValueError("freqs needs pos")
-        rot = _turn_args(pos, freqs, m_)
+        rot, n_axes, p_axes = _turn_args(pos, freqs, m_, axes)
         p_pos, p_freqs = pos.data_ptr(), freqs.data_ptr()
     if q is not None:
         if freqs is None:
@@ -633,11 +683,18 @@ def kv_write(k, v, kc, vc, kv_codec: int, slots, pos=None, freqs=None, layout: i
             p_qo = q_out.data_ptr()
             if p_qo == p_q and not q.is_contiguous():
                 raise ValueError("q_out starts where q does, with other strides")
-        dev = _one_device(k, v, kc, vc, slots, pos, freqs, q, q_out)
+        dev = _one_device(k, v, kc, vc, slots, pos, freqs, q, q_out, axes)
     else:
         q_out = None
-        dev = _one_device(k, v, kc, vc, slots, pos if rot else None, freqs)
+        dev = _one_device(k, v, kc, vc, slots, pos if rot else None, freqs, axes if rot else None)
     if m_ == 0:
+        return q_out
+    if p_axes is not None:
+        rc = load().m4q_kv_write_axes(k.data_ptr(), khs, krs, v.data_ptr(), vhs, vrs, hkv, m_, d, p_pos, n_axes,
+                                      p_freqs, p_axes, rot, layout, mscale, slots.data_ptr(), kc.data_ptr(),
+                                      vc.data_ptr(), kv_codec, b, c, p_q, qhs, qrs, h, p_qo, _raw_stream(stream, dev))
+        if rc:
+            raise M4QError(rc, "m4q_kv_write_axes")
         return q_out
     rc = load().m4q_kv_write(k.data_ptr(), khs, krs, v.data_ptr(), vhs, vrs, hkv, m_, d, p_pos, p_freqs, rot, layout,
                              mscale, slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, c, p_q, qhs, qrs, h,
@@ -728,6 +785,158 @@ def attention_tree(q, kc, vc, kv_codec: int, past, parents, scale: float | None 
     if rc:
         raise M4QError(rc, "m4q_attention_tree")
     return out
+
+
+def page_plan(past, new, table, held, free, n_free, page: int, tokens: int, out=None, stream=None):
+    """(slots, pos, lengths, starts): the cache rows of a step's tokens, planned on
+    the GPU.  Sequence b has past int32 [B] rows and gets new int32 [B] tokens
+    (below 0: it has ended).  table int32 [B, W], held int32 [B], free int32 [P]
+    and n_free int32 [1] are the pages' state and are updated: pages of `page`
+    rows that b lacks come from the end of free[:n_free], those of an ended
+    sequence go back on top.  slots and pos int32 [tokens] are those of all
+    sequences' tokens one after the other, from starts int32 [B + 1] on (behind
+    them -1 and 0; -1 too where the pages ran out); lengths int32 [B] counts the
+    rows after the step.  out: int32 [2 * tokens + 2 * B + 1] for the results, one
+    after the other."""
+    i32 = _t().int32
+    if not isinstance(table, _torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be [B, W]")
+    b, w = table.shape
+    _need(table, i32, "table")
+    for t, n, what in ((past, b, "past"), (new, b, "new"), (held, b, "held"), (n_free, 1, "n_free")):
+        _need(t, i32, what)
+        if t.numel() != n:
+            raise ValueError("%s holds %d values, expected %d" % (what, t.numel(), n))
+    _need(free, i32, "free")
+    tokens = int(tokens)
+    total = 2 * tokens + 2 * b + 1
+    if tokens < 1:
+        raise ValueError("tokens must be at least 1")
+    if out is None:
+        out = _allocate((total,), i32, table, stream)
+    else:
+        _ints(out, i32, total, "out")
+        out = out.view(-1)
+    dev = _one_device(table, past, new, held, free, n_free, out)
+    p = out.data_ptr()
+    rc = load().m4q_page_plan(past.data_ptr(), new.data_ptr(), b, page, table.data_ptr(), w, held.data_ptr(),
+                              free.data_ptr(), free.numel(), n_free.data_ptr(), tokens, p, p + 4 * tokens,
+                              p + 8 * tokens, p + 8 * tokens + 4 * b, _raw_stream(stream, dev))
+    if rc:
+        raise M4QError(rc, "m4q_page_plan")
+    return out.split((tokens, tokens, b, b + 1))
+
+
+def attention_paged(q, kc, vc, kv_codec: int, table, lengths, scale: float | None = None, out=None, workspace=None,
+                    stream=None):
+    """O fp16 [B, H * D]: attention of one new token of each of B sequences, q
+    fp16 [H, B, D], over the pages kc, vc [P, Hkv, page, row].  Sequence b sees
+    its rows j < lengths int32 [B], row j at place j % page of page
+    table[b, j // page] (table int32 [B, W]); none: a zero row.  The workspace is
+    allocated here when not given; workspace=False runs without one (no key
+    split)."""
+    _need(q, _t().float16, "q")
+    if kc is None or vc is None:
+        raise ValueError("both pools are read")
+    pages, hkv, page, d = _cache_shape(kc, vc, kv_codec)
+    if kc.dim() != 4:
+        raise ValueError("a page pool must be [P, Hkv, page, row]")
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [H, B, %d]" % d)
+    h, b, _ = q.shape
+    _need(table, _torch.int32, "table")
+    if table.dim() != 2 or table.shape[0] != b:
+        raise ValueError("table must be [%d, W]" % b)
+    w = table.shape[1]
+    _ints(lengths, _torch.int32, b, "lengths")
+    if scale is None:
+        scale = d ** -0.5
+    if out is None:
+        out = _allocate((b, h * d), _torch.float16, q, stream)
+    else:
+        _halfs(out, b * h * d, "out")
+    if b == 0 or h == 0:
+        return out
+    lib = load()
+    p_ws, n_ws = None, 0
+    if workspace is None:
+        n_ws = lib.m4q_attention_paged_workspace(kv_codec, b, h, hkv, pages, page, w, d)
+        if n_ws:
+            workspace = _allocate((n_ws,), _torch.uint8, q, stream)
+            p_ws = workspace.data_ptr()
+    elif workspace is False:
+        workspace = None
+    else:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        p_ws, n_ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    dev = _one_device(q, kc, vc, table, lengths, out, workspace)
+    rc = lib.m4q_attention_paged(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), kv_codec, b, h, hkv, pages, page, d,
+                                 table.data_ptr(), w, lengths.data_ptr(), scale, out.data_ptr(), p_ws, n_ws,
+                                 _raw_stream(stream, dev))
+    if rc:
+        raise M4QError(rc, "m4q_attention_paged")
+    return out
+
+
+def _prob_rows(x, what):
+    """fp32 or fp16 probabilities [B, N, V] with unit-stride rows; returns the
+    sequence and row strides."""
+    if not isinstance(x, _t().Tensor) or not (x.dtype is _torch.float32 or x.dtype is _torch.float16):
+        raise TypeError("%s must be an fp32 or fp16 tensor" % what)
+    if x.dim() != 3:
+        raise ValueError("%s must be [B, N, V]" % what)
+    if not x.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % what)
+    (b, n, v), (bs, rs, one) = x.shape, x.stride()
+    if one != 1 and v > 1:
+        raise ValueError("%s must be [B, N, V] with unit-stride rows" % what)
+    return bs if b > 1 else 0, rs if n > 1 else 0
+
+
+def verify_tree(target, draft, tokens, parents, u, out=None, stream=None):
+    """(path, count, token): drafted trees verified against the target's
+    probabilities.  target and draft [B, N, V] (both fp32 or both fp16, any
+    sequence and row strides) are the distributions behind node i of sequence b;
+    node 0 is its last known token (parents -1), node i > 0 the drafted token
+    tokens int32 [B, N] behind node parents int32 [B, N] in [0, i).  u fp32 [B, N]
+    in [0, 1): u[b, i] decides on node i, u[b, 0] draws the next token.  path
+    int32 [B, N] holds the nodes kept (0 first, -1 behind them), count int32 [B]
+    their number, token int32 [B] the next token.  draft may be None with N = 1.
+    out: int32 [B * (N + 2)] for the results, one after the other."""
+    tbs, trs = _prob_rows(target, "target")
+    b, n, v = target.shape
+    p_draft, dbs, drs = None, 0, 0
+    if draft is not None:
+        if draft.dtype is not target.dtype:
+            raise TypeError("draft must be of target's type")
+        dbs, drs = _prob_rows(draft, "draft")
+        if draft.shape != target.shape:
+            raise ValueError("draft must be [%d, %d, %d]" % (b, n, v))
+        p_draft = draft.data_ptr()
+    elif n > 1:
+        raise ValueError("draft is needed with drafted nodes")
+    for t, dtype, what in ((tokens, _torch.int32, "tokens"), (parents, _torch.int32, "parents"),
+                           (u, _torch.float32, "u")):
+        _ints(t, dtype, b * n, what)
+        if t.dim() > 1 and tuple(t.shape) != (b, n):
+            raise ValueError("%s must be [%d, %d]" % (what, b, n))
+    if out is None:
+        out = _allocate((b * (n + 2),), _torch.int32, target, stream)
+    else:
+        _ints(out, _torch.int32, b * (n + 2), "out")
+        out = out.view(-1)
+    dev = _one_device(target, draft, tokens, parents, u, out)
+    if b:
+        p = out.data_ptr()
+        rc = load().m4q_verify_tree(target.data_ptr(), tbs, trs, p_draft, dbs, drs,
+                                    PROB_F16 if target.dtype is _torch.float16 else PROB_F32, b, n, v,
+                                    tokens.data_ptr(), parents.data_ptr(), u.data_ptr(), p, p + 4 * b * n,
+                                    p + 4 * b * (n + 1), _raw_stream(stream, dev))
+        if rc:
+            raise M4QError(rc, "m4q_verify_tree")
+    path, count, token = out.split((b * n, b, b))
+    return path.view(b, n), count, token
 
 
 def norm_residual(h, r, w_pre, w_post=None, gate=None, res_scale: float = 1.0, branch_scale: float = 1.0,

@@ -777,13 +777,19 @@ int m4q_rope_freqs(int64_t rot, double base, int scaling, double factor, double 
   return M4Q_OK;
 }
 
-int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t H, int64_t M, int64_t D,
-             const int32_t* pos, const int64_t* freqs, int64_t rot, int layout, float mscale, void* Y,
-             int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream) {
-  if (!X || !Y || !freqs) return M4Q_ERR_INVALID_ARG;
+}  // extern "C"
+
+namespace {
+
+// One axis: A = 1 and axes NULL.
+int rope_call(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t H, int64_t M, int64_t D,
+              const int32_t* pos, int64_t A, const int64_t* freqs, const int32_t* axes, int64_t rot, int layout,
+              float mscale, void* Y, int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream) {
+  if (!X || !Y || !freqs || A < 1 || A > M4Q_ROPE_MAX_AXES) return M4Q_ERR_INVALID_ARG;
   if (H < 1 || M < 1 || H > 65535 || M > INT32_MAX) return M4Q_ERR_INVALID_ARG;
   int rc = check_turn(pos, D, rot, layout, mscale);
   if (rc != M4Q_OK) return rc;
+  if (!aligned_to(axes, 4)) return M4Q_ERR_MISALIGNED;
   if (!aligned16(X) || !aligned16(Y) || !aligned_to(pos, 4) || !aligned_to(freqs, 8) || !stride_ok(x_head_stride) ||
       !stride_ok(x_row_stride) || !stride_ok(y_head_stride) || !stride_ok(y_row_stride))
     return M4Q_ERR_MISALIGNED;
@@ -800,6 +806,8 @@ int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t
   p.D = (int)D;
   p.pos = pos;
   p.freqs = freqs;
+  p.axes = axes;
+  p.A = (int)A;
   p.rot = (int)rot;
   p.interleaved = layout == M4Q_ROPE_INTERLEAVED;
   p.mscale = mscale;
@@ -807,12 +815,13 @@ int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t
   return done(m4q::launch_rope_kv(p, false, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, const void* V, int64_t v_head_stride,
-                 int64_t v_row_stride, int64_t Hkv, int64_t M, int64_t D, const int32_t* pos, const int64_t* freqs,
-                 int64_t rot, int layout, float mscale, const int32_t* slots, void* Kc, void* Vc, int kv_codec,
-                 int64_t B, int64_t C, const void* Q, int64_t q_head_stride, int64_t q_row_stride, int64_t H,
-                 void* Qout, m4q_stream_t stream) {
+int kv_write_call(const void* K, int64_t k_head_stride, int64_t k_row_stride, const void* V, int64_t v_head_stride,
+                  int64_t v_row_stride, int64_t Hkv, int64_t M, int64_t D, const int32_t* pos, int64_t A,
+                  const int64_t* freqs, const int32_t* axes, int64_t rot, int layout, float mscale,
+                  const int32_t* slots, void* Kc, void* Vc, int kv_codec, int64_t B, int64_t C, const void* Q,
+                  int64_t q_head_stride, int64_t q_row_stride, int64_t H, void* Qout, m4q_stream_t stream) {
   if (!K || !V || !slots || !Kc || !Vc || (Q && (!Qout || !freqs))) return M4Q_ERR_INVALID_ARG;
+  if (freqs && (A < 1 || A > M4Q_ROPE_MAX_AXES)) return M4Q_ERR_INVALID_ARG;
   int rc = check_cache(kv_codec, B, Hkv, C, D);
   if (rc != M4Q_OK) return rc;
   if (M < 1 || M > INT32_MAX || (Q && H < 1) || (Q ? H : 0) + 2 * Hkv > 65535) return M4Q_ERR_INVALID_ARG;
@@ -822,7 +831,7 @@ int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, con
   }
   if (!aligned16(K) || !aligned16(V) || !aligned16(Kc) || !aligned16(Vc) || !aligned_to(slots, 4) ||
       !stride_ok(k_head_stride) || !stride_ok(k_row_stride) || !stride_ok(v_head_stride) || !stride_ok(v_row_stride) ||
-      (freqs && (!aligned_to(pos, 4) || !aligned_to(freqs, 8))) ||
+      (freqs && (!aligned_to(pos, 4) || !aligned_to(freqs, 8) || !aligned_to(axes, 4))) ||
       (Q && (!aligned16(Q) || !aligned16(Qout) || !stride_ok(q_head_stride) || !stride_ok(q_row_stride))))
     return M4Q_ERR_MISALIGNED;
   DevInfo dev;
@@ -844,6 +853,8 @@ int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, con
   if (freqs) {
     p.pos = pos;
     p.freqs = freqs;
+    p.axes = axes;
+    p.A = (int)A;
     p.rot = (int)rot;
     p.interleaved = layout == M4Q_ROPE_INTERLEAVED;
     p.mscale = mscale;
@@ -855,6 +866,47 @@ int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, con
   p.C = (int)C;
   p.nsm = dev.sms;
   return done(m4q::launch_rope_kv(p, kv_codec == M4Q_Q8_0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int m4q_rope(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t H, int64_t M, int64_t D,
+             const int32_t* pos, const int64_t* freqs, int64_t rot, int layout, float mscale, void* Y,
+             int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream) {
+  return rope_call(X, x_head_stride, x_row_stride, H, M, D, pos, 1, freqs, nullptr, rot, layout, mscale, Y,
+                   y_head_stride, y_row_stride, stream);
+}
+
+int m4q_rope_axes(const void* X, int64_t x_head_stride, int64_t x_row_stride, int64_t H, int64_t M, int64_t D,
+                  const int32_t* pos, int64_t A, const int64_t* freqs, const int32_t* axes, int64_t rot, int layout,
+                  float mscale, void* Y, int64_t y_head_stride, int64_t y_row_stride, m4q_stream_t stream) {
+  if (!axes) return M4Q_ERR_INVALID_ARG;
+  return rope_call(X, x_head_stride, x_row_stride, H, M, D, pos, A, freqs, axes, rot, layout, mscale, Y,
+                   y_head_stride, y_row_stride, stream);
+}
+
+int m4q_kv_write(const void* K, int64_t k_head_stride, int64_t k_row_stride, const void* V, int64_t v_head_stride,
+                 int64_t v_row_stride, int64_t Hkv, int64_t M, int64_t D, const int32_t* pos, const int64_t* freqs,
+                 int64_t rot, int layout, float mscale, const int32_t* slots, void* Kc, void* Vc, int kv_codec,
+                 int64_t B, int64_t C, const void* Q, int64_t q_head_stride, int64_t q_row_stride, int64_t H,
+                 void* Qout, m4q_stream_t stream) {
+  return kv_write_call(K, k_head_stride, k_row_stride, V, v_head_stride, v_row_stride, Hkv, M, D, pos, 1, freqs,
+                       nullptr, rot, layout, mscale, slots, Kc, Vc, kv_codec, B, C, Q, q_head_stride, q_row_stride, H,
+                       Qout, stream);
+}
+
+int m4q_kv_write_axes(const void* K, int64_t k_head_stride, int64_t k_row_stride, const void* V,
+                      int64_t v_head_stride, int64_t v_row_stride, int64_t Hkv, int64_t M, int64_t D,
+                      const int32_t* pos, int64_t A, const int64_t* freqs, const int32_t* axes, int64_t rot, int layout,
+                      float mscale, const int32_t* slots, void* Kc, void* Vc, int kv_codec, int64_t B, int64_t C,
+                      const void* Q, int64_t q_head_stride, int64_t q_row_stride, int64_t H, void* Qout,
+                      m4q_stream_t stream) {
+  if (!freqs || !axes) return M4Q_ERR_INVALID_ARG;
+  return kv_write_call(K, k_head_stride, k_row_stride, V, v_head_stride, v_row_stride, Hkv, M, D, pos, A, freqs, axes,
+                       rot, layout, mscale, slots, Kc, Vc, kv_codec, B, C, Q, q_head_stride, q_row_stride, H, Qout,
+                       stream);
 }
 
 int m4q_kv_read(const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t Hkv, int64_t C, int64_t D,
@@ -992,6 +1044,129 @@ int m4q_attention_tree(const void* Q, const void* Kc, const void* Vc, int kv_cod
     if (rc != M4Q_OK) return rc;
   }
   return M4Q_OK;
+}
+
+int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t page, int32_t* table, int64_t W,
+                  int32_t* held, int32_t* free_pages, int64_t P, int32_t* n_free, int64_t T, int32_t* slots,
+                  int32_t* pos, int32_t* lengths, int32_t* starts, m4q_stream_t stream) {
+  if (!past || !fresh || !table || !held || !free_pages || !n_free || !slots || !pos || !lengths || !starts)
+    return M4Q_ERR_INVALID_ARG;
+  if (B < 1 || B > m4q::kPlanSeqs || page < 1 || W < 1 || P < 1 || T < 1 || T > INT32_MAX - 8192)
+    return M4Q_ERR_INVALID_ARG;
+  if (page > INT32_MAX || P > INT32_MAX / page || W > INT32_MAX / page) return M4Q_ERR_BAD_SHAPE;
+  const void* all[] = {past, fresh, table, held, free_pages, n_free, slots, pos, lengths, starts};
+  for (const void* a : all)
+    if (!aligned_to(a, 4)) return M4Q_ERR_MISALIGNED;
+  DevInfo dev;
+  m4q::PlanParams p{};
+  const int rc = ready(&dev, &p.status);
+  if (rc != M4Q_OK) return rc;
+  p.past = past;
+  p.fresh = fresh;
+  p.table = table;
+  p.held = held;
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.slots = slots;
+  p.pos = pos;
+  p.lengths = lengths;
+  p.starts = starts;
+  p.B = (int)B;
+  p.W = (int)W;
+  p.P = (int)P;
+  p.page = (int)page;
+  p.T = (int)T;
+  return done(m4q::launch_page_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_paged(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t P, int64_t page, int64_t W, int64_t D) {
+  const int rc = check_cache(kv_codec, P, Hkv, page, D);
+  if (rc != M4Q_OK) return rc;
+  if (B < 1 || H < 1 || W < 1 || H > 65535 || B > 65535) return M4Q_ERR_INVALID_ARG;
+  return H % Hkv == 0 && page % 8 == 0 && W <= INT32_MAX / page ? M4Q_OK : M4Q_ERR_BAD_SHAPE;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t m4q_attention_paged_workspace(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t P, int64_t page,
+                                     int64_t W, int64_t D) {
+  if (check_paged(kv_codec, B, H, Hkv, P, page, W, D) != M4Q_OK) return 0;
+  return 0;
+}
+
+int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t H, int64_t Hkv,
+                        int64_t P, int64_t page, int64_t D, const int32_t* table, int64_t W, const int32_t* lengths,
+                        float scale, void* O, void* workspace, size_t workspace_bytes, m4q_stream_t stream) {
+  const float scale_log2 = scale * 1.4426950408889634f;   // the kernels work in powers of 2
+  if (!Q || !Kc || !Vc || !table || !lengths || !O || !(scale_log2 - scale_log2 == 0.f)) return M4Q_ERR_INVALID_ARG;
+  int rc = check_paged(kv_codec, B, H, Hkv, P, page, W, D);
+  if (rc != M4Q_OK) return rc;
+  if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) || !aligned_to(table, 4) ||
+      !aligned_to(lengths, 4) || (workspace && !aligned16(workspace)))
+    return M4Q_ERR_MISALIGNED;
+  DevInfo dev;
+  m4q::PagedParams p{};
+  rc = ready(&dev, &p.status);
+  if (rc != M4Q_OK) return rc;
+  (void)workspace_bytes;
+  p.q = static_cast<const __half*>(Q);
+  p.k = static_cast<const uint8_t*>(Kc);
+  p.v = static_cast<const uint8_t*>(Vc);
+  p.o = static_cast<__half*>(O);
+  p.table = table;
+  p.lengths = lengths;
+  p.B = (int)B;
+  p.H = (int)H;
+  p.Hkv = (int)Hkv;
+  p.G = (int)(H / Hkv);
+  p.P = (int)P;
+  p.page = (int)page;
+  p.W = (int)W;
+  p.D = (int)D;
+  p.scale_log2 = scale_log2;
+  return done(m4q::launch_attention_paged(p, kv_codec == M4Q_Q8_0, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int m4q_verify_tree(const void* target, int64_t t_seq_stride, int64_t t_row_stride, const void* draft,
+                    int64_t d_seq_stride, int64_t d_row_stride, int prob_type, int64_t B, int64_t N, int64_t V,
+                    const int32_t* tokens, const int32_t* parents, const float* u, int32_t* path, int32_t* count,
+                    int32_t* token, m4q_stream_t stream) {
+  if (!target || (!draft && N > 1) || !tokens || !parents || !u || !path || !count || !token)
+    return M4Q_ERR_INVALID_ARG;
+  if (prob_type != M4Q_PROB_F32 && prob_type != M4Q_PROB_F16) return M4Q_ERR_INVALID_ARG;
+  if (B < 1 || B > INT32_MAX / m4q::kVerifyNodes || N < 1 || N > m4q::kVerifyNodes || V < 1 || V > 1 << 24)
+    return M4Q_ERR_INVALID_ARG;
+  const int size = prob_type == M4Q_PROB_F32 ? 4 : 2;
+  if (!aligned_to(target, size) || !aligned_to(draft, size)) return M4Q_ERR_MISALIGNED;
+  const void* all[] = {tokens, parents, u, path, count, token};
+  for (const void* a : all)
+    if (!aligned_to(a, 4)) return M4Q_ERR_MISALIGNED;
+  DevInfo dev;
+  m4q::VerifyParams p{};
+  const int rc = ready(&dev, &p.status);
+  if (rc != M4Q_OK) return rc;
+  p.target = target;
+  p.draft = draft;
+  p.t_bs = t_seq_stride;
+  p.t_rs = t_row_stride;
+  p.d_bs = d_seq_stride;
+  p.d_rs = d_row_stride;
+  p.tokens = tokens;
+  p.parents = parents;
+  p.u = u;
+  p.path = path;
+  p.count = count;
+  p.token = token;
+  p.B = (int)B;
+  p.N = (int)N;
+  p.V = (int)V;
+  return done(m4q::launch_verify(p, prob_type == M4Q_PROB_F16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int m4q_norm_residual(const void* h, const void* R, int res_type, const void* w_post, const void* gate, int gate_rows,

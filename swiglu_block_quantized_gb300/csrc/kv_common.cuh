@@ -15,6 +15,11 @@ enum : uint32_t {
   kSiteTreeKV = 35,      // tree attention: cache rows
   kSiteTreeO = 36,       // tree attention: output row
   kSiteTreeWs = 37,      // tree attention: partial result
+  kSitePagedKV = 38,     // paged attention: cache rows
+  kSitePagedO = 39,      // paged attention: output row
+  kSitePagedWs = 40,     // paged attention: partial result
+  kSitePlan = 41,        // page plan: table entry, free page or token
+  kSiteVerify = 42,      // verification: probability row
 };
 
 // The serving kernels start while the kernel before them may still run (pdl_wait), so

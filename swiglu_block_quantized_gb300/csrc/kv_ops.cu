@@ -14,6 +14,10 @@
 // beside a tie may go the other way, as it may with sines rounded from 64 bits: a
 // prompt's rows are off by 2.6e-5 and 2.9e-5 of their size.)
 //
+// With several axes (images, video) pair i turns by the position that its token has on
+// axis axes[i]: up to eight positions a thread instead of one, looked up once for all
+// its heads.
+//
 // Quantisation of a block of 32 values x (Q8_0): d = max|x| / 127 rounded up
 // to fp16, so that no code is cut off at 127 even where d is subnormal; codes
 // q = x / d to the nearest integer, ties to even.  Rotated keys are quantised
@@ -117,7 +121,7 @@ __device__ __forceinline__ void rotate16(float (&x)[16], const Turn8& t, bool in
 
 // Grid: x over token tiles, y over chunks of `per` of the H + 2 Hkv heads
 // (Q heads, then K, then V).  D / 16 threads a token.
-template <int D, bool Q8>
+template <int D, bool Q8, bool AX>
 __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, int per) {
   constexpr int U = D / 16;                  // units (threads) a row
   constexpr int RB = Q8 ? D / 32 * 34 : 2 * D;
@@ -137,9 +141,15 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
   const UnitAt at = unit_at(u, p.rot, p.interleaved);
   Turn8 t;
   if (ok && at.turns && h0 < p.H + p.Hkv) {
-    const int pos = p.pos[m];
+    int pos = AX ? 0 : p.pos[m];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn(pos, __ldg(reinterpret_cast<const long long*>(p.freqs) + 8 * u + i), p.mscale, t.c[i], t.s[i]);
+    for (int i = 0; i < 8; ++i) {
+      if (AX) {
+        const int a = p.axes[8 * u + i];
+        pos = (unsigned)a < (unsigned)p.A ? p.pos[(long long)a * p.M + m] : 0;
+      }
+      turn(pos, __ldg(reinterpret_cast<const long long*>(p.freqs) + 8 * u + i), p.mscale, t.c[i], t.s[i]);
+    }
   }
   long long row = -1;                        // this token's cache row of head 0, or -1
   if (ok && h1 > p.H) {
@@ -297,8 +307,15 @@ cudaError_t launch_rope_kv(const KvOpsParams& p, bool q8, cudaStream_t s) {
   long long per = tiles * heads / (8ll * (p.nsm > 0 ? p.nsm : 1));
   per = per < 1 ? 1 : per > 8 ? 8 : per;
   const dim3 grid((unsigned)tiles, (unsigned)((heads + per - 1) / per), 1);
-  if (p.D == 64) return launch_grid(q8 ? rope_kv_kernel<64, true> : rope_kv_kernel<64, false>, grid, s, p, (int)per);
-  return launch_grid(q8 ? rope_kv_kernel<128, true> : rope_kv_kernel<128, false>, grid, s, p, (int)per);
+  auto go = [&](auto d, auto ax) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool AX = decltype(ax)::value;
+    return launch_grid(q8 ? rope_kv_kernel<D, true, AX> : rope_kv_kernel<D, false, AX>, grid, s, p, (int)per);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (p.axes) return p.D == 64 ? go(D64(), std::true_type()) : go(D128(), std::true_type());
+  return p.D == 64 ? go(D64(), std::false_type()) : go(D128(), std::false_type());
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, bool q8, cudaStream_t s) {

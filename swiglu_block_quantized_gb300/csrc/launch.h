@@ -143,8 +143,10 @@ struct KvOpsParams {
   __half* qo;             // rotated Q, strides qo_hs, qo_rs
   long long qo_hs, qo_rs;
   int H, Hkv, M, D;
-  const int32_t* pos;     // [M]
+  const int32_t* pos;     // [M], or [A][M] with axes
   const int64_t* freqs;   // [rot / 2] turns per position in units of 2^-64, or null: no rotation
+  const int32_t* axes;    // [rot / 2] the axis of each pair (outside [0, A): not turned), or null: one axis
+  int A;
   int rot, interleaved;
   float mscale;
   const int32_t* slots;   // [M] cache row b C + j of each token; outside [0, B C): not written
@@ -251,6 +253,57 @@ cudaError_t launch_attention_tree(const TreeParams& p, bool q8, const CUtensorMa
 // attention_few.cu: the same for N G <= 32 rows an item
 cudaError_t launch_attention_few(const TreeParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                  int grid, cudaStream_t s);
+
+// attention_paged.cu: attention of one new token of each of B sequences over the rows
+// of a page pool [P][Hkv][page] that its table names.
+struct PagedParams {
+  const __half* q;        // [H][B][D]
+  const uint8_t* k;       // [P][Hkv][page] rows
+  const uint8_t* v;
+  __half* o;              // [B][H D]
+  const int32_t* table;   // [B][W]
+  const int32_t* lengths; // [B]
+  int B, H, Hkv, G, P, page, W, D;
+  float scale_log2;       // softmax scale * log2(e)
+  uint32_t* status;
+};
+cudaError_t launch_attention_paged(const PagedParams& p, bool q8, cudaStream_t s);
+
+// page_plan.cu: pages handed to sequences and taken back, and the slots of a step's
+// tokens.
+constexpr int kPlanSeqs = 4096;
+struct PlanParams {
+  const int32_t* past;    // [B]
+  const int32_t* fresh;   // [B] new tokens; below 0: ended
+  int32_t* table;         // [B][W]
+  int32_t* held;          // [B]
+  int32_t* free_pages;    // [P]
+  int32_t* n_free;        // [1]
+  int32_t* slots;         // [T]
+  int32_t* pos;           // [T]
+  int32_t* lengths;       // [B]
+  int32_t* starts;        // [B + 1]
+  int B, W, P, page, T;
+  uint32_t* status;
+};
+cudaError_t launch_page_plan(const PlanParams& p, cudaStream_t s);
+
+// verify.cu: drafted trees verified against the target's probabilities.
+constexpr int kVerifyNodes = 256;
+struct VerifyParams {
+  const void* target;     // [B][N] rows of V probabilities, strides in elements
+  const void* draft;
+  long long t_bs, t_rs, d_bs, d_rs;
+  const int32_t* tokens;  // [B][N]
+  const int32_t* parents; // [B][N]
+  const float* u;         // [B][N]
+  int32_t* path;          // [B][N]
+  int32_t* count;         // [B]
+  int32_t* token;         // [B]
+  int B, N, V;
+  uint32_t* status;
+};
+cudaError_t launch_verify(const VerifyParams& p, bool f16, cudaStream_t s);
 
 // misc.cu
 // Status bit of a failed bounds check (the kernels' kErrBounds), and the

@@ -1083,6 +1083,31 @@ int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t 
 
 namespace {
 
+// How a paged attention call is laid out: persistent CTAs, and the workspace of the
+// pieces that an even split of the chunks leaves.
+struct PagedPlan {
+  int rtiles, seqs, grid, whole;   // whole: CTAs without a split
+  bool split;
+  size_t ws_ml, ws_o, ws_bytes;
+};
+
+PagedPlan paged_plan(int64_t B, int64_t H, int64_t Hkv, int64_t page, int64_t W, int64_t D, int sms) {
+  PagedPlan t;
+  const int G = (int)(H / Hkv), R = m4q::paged_rows(G);
+  t.rtiles = (G + R - 1) / R;
+  t.seqs = (int)(B < m4q::kPagedSeqs ? B : m4q::kPagedSeqs);
+  const int64_t items = (int64_t)t.seqs * Hkv * t.rtiles;
+  const int64_t chunks = (W * page + m4q::paged_chunk((int)D) - 1) / m4q::paged_chunk((int)D);
+  const int64_t most = (int64_t)sms * m4q::paged_ctas(G);
+  t.split = chunks > 1;
+  t.whole = (int)(items < most ? items : most);
+  t.grid = !t.split ? t.whole : (int)(chunks > most / items ? most : items * chunks);
+  t.ws_ml = ((size_t)t.grid * sizeof(int4) + 255) / 256 * 256;
+  t.ws_o = t.ws_ml + ((size_t)2 * t.grid * R * sizeof(float2) + 255) / 256 * 256;
+  t.ws_bytes = t.split ? t.ws_o + (size_t)2 * t.grid * R * D * sizeof(float) : 0;
+  return t;
+}
+
 int check_paged(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t P, int64_t page, int64_t W, int64_t D) {
   const int rc = check_cache(kv_codec, P, Hkv, page, D);
   if (rc != M4Q_OK) return rc;
@@ -1097,7 +1122,9 @@ extern "C" {
 size_t m4q_attention_paged_workspace(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t P, int64_t page,
                                      int64_t W, int64_t D) {
   if (check_paged(kv_codec, B, H, Hkv, P, page, W, D) != M4Q_OK) return 0;
-  return 0;
+  DevInfo dev;
+  if (current_device_info(&dev) != M4Q_OK) return 0;
+  return paged_plan(B, H, Hkv, page, W, D, dev.sms).ws_bytes;
 }
 
 int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t H, int64_t Hkv,
@@ -1114,14 +1141,14 @@ int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_co
   m4q::PagedParams p{};
   rc = ready(&dev, &p.status);
   if (rc != M4Q_OK) return rc;
-  (void)workspace_bytes;
-  p.q = static_cast<const __half*>(Q);
+  PagedPlan t = paged_plan(B, H, Hkv, page, W, D, dev.sms);
+  if (t.split && (!workspace || workspace_bytes < t.ws_bytes)) {
+    t.split = false;
+    t.grid = t.whole;
+  }
   p.k = static_cast<const uint8_t*>(Kc);
   p.v = static_cast<const uint8_t*>(Vc);
-  p.o = static_cast<__half*>(O);
-  p.table = table;
-  p.lengths = lengths;
-  p.B = (int)B;
+  p.q_rows = B;
   p.H = (int)H;
   p.Hkv = (int)Hkv;
   p.G = (int)(H / Hkv);
@@ -1130,7 +1157,24 @@ int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_co
   p.W = (int)W;
   p.D = (int)D;
   p.scale_log2 = scale_log2;
-  return done(m4q::launch_attention_paged(p, kv_codec == M4Q_Q8_0, reinterpret_cast<cudaStream_t>(stream)));
+  p.rtiles = t.rtiles;
+  p.split = t.split ? 1 : 0;
+  if (t.split) {
+    char* ws = static_cast<char*>(workspace);
+    p.ws_cut = reinterpret_cast<int4*>(ws);
+    p.ws_ml = reinterpret_cast<float2*>(ws + t.ws_ml);
+    p.ws_o = reinterpret_cast<float*>(ws + t.ws_o);
+  }
+  for (int64_t b0 = 0; b0 < B; b0 += t.seqs) {
+    p.B = (int)(B - b0 < t.seqs ? B - b0 : t.seqs);
+    p.q = static_cast<const __half*>(Q) + b0 * D;
+    p.o = static_cast<__half*>(O) + b0 * H * D;
+    p.table = table + b0 * W;
+    p.lengths = lengths + b0;
+    rc = done(m4q::launch_attention_paged(p, kv_codec == M4Q_Q8_0, t.grid, reinterpret_cast<cudaStream_t>(stream)));
+    if (rc != M4Q_OK) return rc;
+  }
+  return M4Q_OK;
 }
 
 int m4q_verify_tree(const void* target, int64_t t_seq_stride, int64_t t_row_stride, const void* draft,

@@ -255,19 +255,32 @@ cudaError_t launch_attention_few(const TreeParams& p, bool q8, const CUtensorMap
                                  int grid, cudaStream_t s);
 
 // attention_paged.cu: attention of one new token of each of B sequences over the rows
-// of a page pool [P][Hkv][page] that its table names.
+// of a page pool [P][Hkv][page] that its table names.  One launch takes up to kPagedSeqs
+// sequences (where their chunks of keys begin stays in shared memory); the pointers are
+// those of the launch's first one.
+constexpr int kPagedSeqs = 512;
 struct PagedParams {
-  const __half* q;        // [H][B][D]
+  const __half* q;        // [H][q_rows][D]
   const uint8_t* k;       // [P][Hkv][page] rows
   const uint8_t* v;
   __half* o;              // [B][H D]
   const int32_t* table;   // [B][W]
   const int32_t* lengths; // [B]
+  long long q_rows;       // sequences of the call
   int B, H, Hkv, G, P, page, W, D;
   float scale_log2;       // softmax scale * log2(e)
+  int rtiles;             // items of a sequence and KV head: ceil(G / rows of an item)
+  int split;              // chunks are dealt out evenly over the CTAs, pieces of items joined
+  int4* ws_cut;           // [grid] of the item cut whose first chunk is the CTA's: sequence, item, last CTA, 1
+  float2* ws_ml;          // [2 grid][rows] (max, sum) of a piece
+  float* ws_o;            // [2 grid][rows][D] its unnormalised O
   uint32_t* status;
 };
-cudaError_t launch_attention_paged(const PagedParams& p, bool q8, cudaStream_t s);
+// Query heads of an item, keys of a chunk, and CTAs an SM.
+constexpr int paged_rows(int G) { return G <= 8 ? 8 : 16; }
+constexpr int paged_chunk(int D) { return D == 64 ? 128 : 64; }
+constexpr int paged_ctas(int G) { return G <= 8 ? 3 : 2; }
+cudaError_t launch_attention_paged(const PagedParams& p, bool q8, int grid, cudaStream_t s);
 
 // page_plan.cu: pages handed to sequences and taken back, and the slots of a step's
 // tokens.

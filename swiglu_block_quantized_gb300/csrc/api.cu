@@ -1091,14 +1091,16 @@ struct PagedPlan {
   size_t ws_ml, ws_o, ws_bytes;
 };
 
-PagedPlan paged_plan(int64_t B, int64_t H, int64_t Hkv, int64_t page, int64_t W, int64_t D, int sms) {
+PagedPlan paged_plan(bool q8, int64_t B, int64_t H, int64_t Hkv, int64_t page, int64_t W, int64_t D, int sms) {
   PagedPlan t;
   const int G = (int)(H / Hkv), R = m4q::paged_rows(G);
   t.rtiles = (G + R - 1) / R;
+  const int64_t chunk = m4q::paged_chunk((int)D, q8), chunks = (W * page + chunk - 1) / chunk;
+  const int64_t fit = INT32_MAX / chunks;   // a launch's chunks fit 31 bits
   t.seqs = (int)(B < m4q::kPagedSeqs ? B : m4q::kPagedSeqs);
+  if (t.seqs > fit) t.seqs = (int)fit;
   const int64_t items = (int64_t)t.seqs * Hkv * t.rtiles;
-  const int64_t chunks = (W * page + m4q::paged_chunk((int)D) - 1) / m4q::paged_chunk((int)D);
-  const int64_t most = (int64_t)sms * m4q::paged_ctas(G);
+  const int64_t most = (int64_t)sms * m4q::paged_ctas(G, q8);
   t.split = chunks > 1;
   t.whole = (int)(items < most ? items : most);
   t.grid = !t.split ? t.whole : (int)(chunks > most / items ? most : items * chunks);
@@ -1124,7 +1126,7 @@ size_t m4q_attention_paged_workspace(int kv_codec, int64_t B, int64_t H, int64_t
   if (check_paged(kv_codec, B, H, Hkv, P, page, W, D) != M4Q_OK) return 0;
   DevInfo dev;
   if (current_device_info(&dev) != M4Q_OK) return 0;
-  return paged_plan(B, H, Hkv, page, W, D, dev.sms).ws_bytes;
+  return paged_plan(kv_codec == M4Q_Q8_0, B, H, Hkv, page, W, D, dev.sms).ws_bytes;
 }
 
 int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_codec, int64_t B, int64_t H, int64_t Hkv,
@@ -1141,7 +1143,11 @@ int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_co
   m4q::PagedParams p{};
   rc = ready(&dev, &p.status);
   if (rc != M4Q_OK) return rc;
-  PagedPlan t = paged_plan(B, H, Hkv, page, W, D, dev.sms);
+  const bool q8 = kv_codec == M4Q_Q8_0;
+  PagedPlan t = paged_plan(q8, B, H, Hkv, page, W, D, dev.sms);
+  CUtensorMap tm_k{}, tm_v{};
+  if (!q8 && (!encode_kv(&tm_k, Kc, P * Hkv, page, D, 8) || !encode_kv(&tm_v, Vc, P * Hkv, page, D, 8)))
+    return M4Q_ERR_CUDA;
   if (t.split && (!workspace || workspace_bytes < t.ws_bytes)) {
     t.split = false;
     t.grid = t.whole;
@@ -1171,7 +1177,7 @@ int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_co
     p.o = static_cast<__half*>(O) + b0 * H * D;
     p.table = table + b0 * W;
     p.lengths = lengths + b0;
-    rc = done(m4q::launch_attention_paged(p, kv_codec == M4Q_Q8_0, t.grid, reinterpret_cast<cudaStream_t>(stream)));
+    rc = done(m4q::launch_attention_paged(p, q8, tm_k, tm_v, t.grid, reinterpret_cast<cudaStream_t>(stream)));
     if (rc != M4Q_OK) return rc;
   }
   return M4Q_OK;

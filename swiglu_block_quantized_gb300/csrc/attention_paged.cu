@@ -17,12 +17,11 @@
 // read in one piece: 16 bytes of a K row (fp16), a block of codes (Q8_0), 16 bytes of two
 // V rows whose values are paired by byte permutes.  P^T comes from S^T by an 8 x 8
 // transposition in registers.
-//  - fp16: K and V rows go from global memory to registers, the next step's K while this
-//    step's V is used and the other way round.
-//  - Q8_0: rows are copied as they are to a ring in shared memory (bulk copies of 8 rows,
-//    each warp its own), and a thread decodes the codes it needs: 34-byte blocks are read
-//    as aligned words, whose first and last codes of a block (where it starts between
-//    words) are put together in one word, so that no word is shifted.
+// Rows come through a ring in shared memory, each warp's its own, in groups of 8 (a group
+// lies within a page): fp16 by TMA boxes with the 128-byte swizzle, Q8_0 as they are by
+// bulk copies.  Of Q8_0 a thread decodes the codes it needs: 34-byte blocks are read as
+// aligned words, and where a block starts between words its first and last codes are put
+// together in one, so that no word is shifted.
 // The reference of a row's softmax is raised when a score exceeds it by 2^8 (one vote a
 // step); P is fp16, sums are fp32.
 #include "codec.cuh"
@@ -34,7 +33,6 @@ namespace m4q {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStages = 3;        // Q8_0: steps of a warp in its ring
 constexpr int kPiece = 2;         // pieces of cut items a CTA may have: its first and its last
 constexpr float kLowest = -3.402823466e38f;
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -68,28 +66,39 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 template <int D, bool Q8, int NT>
 struct Cfg {
   static constexpr int RB = Q8 ? D / 32 * 34 : 2 * D;   // bytes of a row
-  static constexpr int KS = 128 / D;                    // 16-key MMA rows a step
-  static constexpr int KT = 16 * KS;                    // keys of a warp's step
-  static constexpr int GR = KT / 8;                     // groups of 8 keys of a step: within a page
+  static constexpr int KT = paged_chunk(D, Q8) / 4;     // keys of a warp's step
+  static constexpr int KS = KT / 16;                    // its 16-key MMA rows
+  static constexpr int GR = KT / 8;                     // its groups of 8 keys: within a page
   static constexpr int CH = 4 * KT;                     // keys of a chunk
   static constexpr int QS = D / 16;                     // k16 steps of S, and m16 tiles of O
   static constexpr int R = 8 * NT;                      // query rows of an item
-  static constexpr int kStage = 2 * KT * RB;            // Q8_0: K rows, then V rows
-  static constexpr int kRing = Q8 ? 4 * kStages * kStage : 0;
+  static constexpr int NS = Q8 ? 2 : 3;                 // steps of a warp in its ring
+  static constexpr int kHalf = KT * RB;                 // K rows of a step, then V rows
+  static constexpr int kRing = 4 * NS * 2 * kHalf;
+  static constexpr int kCopies = 2 * GR * (Q8 ? 1 : D / 64);   // copies of a step, a lane each
   static constexpr int kPitch = D + 4;                  // floats of a row of O in shared memory
-  static constexpr int kJoin = 4 * R * kPitch * 4 + 4 * R * 8;
-  static constexpr int kSmem = kRing + kJoin + (kPagedSeqs + 1) * 8;
+  static constexpr int kJoin = 4 * R * kPitch * 4 + 4 * R * 8;   // in the ring, when it is idle
+  static_assert(kJoin <= kRing && kCopies <= 32 && GR <= 8 && (GR & (GR - 1)) == 0, "layout");
+  static constexpr int kSmem = 1024 + kRing + (2 * kPagedSeqs + 1) * 4;
 };
 
-// Which key of a step's 16 stands on row r of the MMA.  Q8_0: an order in which the reads
-// of K (rows r, 4 threads a row) and of V (keys 2t, 2t + 1, 2t + 8, 2t + 9 of a thread)
-// meet no bank twice at D = 128; fp16: rows as they are.
+// Which key of a step's 16 stands on row r of the MMA: orders in which the reads of K (rows
+// r, 4 threads a row) and of V (keys 2t, 2t + 1, 2t + 8, 2t + 9 of a thread) meet no bank
+// twice (Q8_0: at D = 128).
 template <bool Q8>
 __device__ __forceinline__ int key_of(int r) {
-  return Q8 ? 8 * ((r >> 2) & 1) + 4 * (r >> 3) + 2 * (r & 1) + ((r >> 1) & 1) : r;
+  return Q8 ? 8 * ((r >> 2) & 1) + 4 * (r >> 3) + 2 * (r & 1) + ((r >> 1) & 1) : r ^ ((r & 1) << 2);
 }
 
 // What a warp keeps of its keys so far.
@@ -165,88 +174,94 @@ __device__ __forceinline__ void softmax_step(float (&s)[KS][NT][4], Acc<D, NT>& 
     }
 }
 
-// Where the chunks of sequences b0 .. b0 + B - 1 begin, in shared memory: at[0 .. B].
+// Where the chunks of the sequences begin, at[0 .. B], and their keys, in shared memory.
 template <int CH>
-__device__ __forceinline__ void count_chunks(const PagedParams& p, long long* at, long long (&part)[4]) {
+__device__ __forceinline__ void count_chunks(const PagedParams& p, int* at, int* lens, int (&part)[4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int each = (p.B + kThreads - 1) / kThreads, first = threadIdx.x * each;
-  const long long most = (long long)p.W * p.page;
-  long long sum = 0;
-  for (int i = first; i < min(first + each, p.B); ++i)
-    sum += (min((long long)max(p.lengths[i], 0), most) + CH - 1) / CH;
-  long long in = sum;
+  int sum = 0;
+  for (int i = first; i < min(first + each, p.B); ++i) {
+    const int n = min(max(p.lengths[i], 0), p.W * p.page);
+    lens[i] = n;
+    at[i] = sum;
+    sum += (n + CH - 1) / CH;
+  }
+  int in = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, in, o);
+    const int y = __shfl_up_sync(0xffffffffu, in, o);
     if (lane >= o) in += y;
   }
   if (lane == 31) part[warp] = in;
   __syncthreads();
   for (int w = 0; w < warp; ++w) in += part[w];
-  long long before = in - sum;
-  for (int i = first; i < min(first + each, p.B); ++i) {
-    at[i] = before;
-    before += (min((long long)max(p.lengths[i], 0), most) + CH - 1) / CH;
-  }
+  for (int i = first; i < min(first + each, p.B); ++i) at[i] += in - sum;
   if (threadIdx.x == kThreads - 1) at[p.B] = in;
   __syncthreads();
 }
 
-// Rows of a warp's groups of 8 keys, 32 groups at a time: lane l holds the pool row of
-// group l of the window (-1: not seen), the next window's table entries are on their way.
+// Rows of a warp's groups of 8 keys, 32 groups at a time: lane l holds page and place of
+// group l of the window (page -1: not seen); the next window's table entries are on their
+// way.
 template <typename C>
 struct Rows {
-  const int32_t* table;   // the sequence's entries
-  int hk, first, last;    // keys [first, last) of the warp's piece; steps CH apart
-  int cur;                // rows of this window
-  int entry, key;         // next window: the lane's entry and key (last: none)
+  const int32_t* table;    // the sequence's entries
+  int first, last;         // keys [first, last) of the warp's piece, steps CH apart
+  int page_id, place;      // this window
+  int entry, next_place;   // the next one
   static constexpr int kSteps = 32 / C::GR;
   __device__ __forceinline__ void fetch(const PagedParams& p, int step) {
     const int lane = threadIdx.x & 31;
     const long long k = (long long)first + (long long)(step + lane / C::GR) * C::CH + 8 * (lane % C::GR);
-    key = (int)min(k, (long long)last);
-    entry = key < last ? table[key / p.page] : -1;
+    entry = -1;
+    next_place = 0;
+    if (k < last) {
+      const int j = (int)k / p.page;
+      next_place = (int)k - j * p.page;
+      entry = table[j];
+    }
   }
   __device__ __forceinline__ void advance(const PagedParams& p, int step) {   // to the window of `step`
-    cur = -1;
-    if ((unsigned)entry < (unsigned)p.P) {
-      cur = (entry * p.Hkv + hk) * p.page + key % p.page;
-      if (!in_bounds(cur >= 0 && (long long)cur + 8 <= (long long)p.P * p.Hkv * p.page, p.status, kSitePagedKV)) cur = -1;
-    }
+    page_id = (unsigned)entry < (unsigned)p.P ? entry : -1;
+    place = next_place;
+    if (!in_bounds(page_id < p.P && place >= 0 && place + 8 <= p.page, p.status, kSitePagedKV)) page_id = -1;
     fetch(p, step + kSteps);
-  }
-  __device__ __forceinline__ int group(int step, int i) const {
-    return __shfl_sync(0xffffffffu, cur, step % kSteps * C::GR + i);
   }
 };
 
 template <int D, bool Q8, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const PagedParams p, const __grid_constant__ CUtensorMap tm_k,
+             const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D, Q8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long part[4];
-  __shared__ __align__(8) uint64_t full[4][kStages];
+  __shared__ int part[4];
+  __shared__ __align__(8) uint64_t full[4][C::NS];
   __shared__ int abort_flag;
-  uint8_t* ring = smem;
-  float* so = reinterpret_cast<float*>(smem + C::kRing);              // [4][R][kPitch]
+  uint8_t* ring = smem_align<1024>(smem);
+  float* so = reinterpret_cast<float*>(ring);                         // [4][R][kPitch]
   float2* sml = reinterpret_cast<float2*>(so + 4 * C::R * C::kPitch); // [4][R]
-  long long* at = reinterpret_cast<long long*>(smem + C::kRing + C::kJoin);
+  int* at = reinterpret_cast<int*>(ring + C::kRing);                  // [B + 1]
+  int* lens = at + kPagedSeqs + 1;                                    // [B]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x, ctas = gridDim.x;
-  if (Q8 && threadIdx.x == 0) {
+  if (threadIdx.x == 0) {
     for (int w = 0; w < 4; ++w)
-      for (int i = 0; i < kStages; ++i) mbar_init(&full[w][i], 1);
+      for (int i = 0; i < C::NS; ++i) mbar_init(&full[w][i], 1);
     abort_flag = 0;
     fence_mbar_init();
+    if (!Q8) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
   }
   const WaitCtl ctl{&abort_flag, p.status, kWaitNs};
   const DecK dk = make_deck();
   pdl_launch_dependents();
   pdl_wait();
-  count_chunks<C::CH>(p, at, part);
+  count_chunks<C::CH>(p, at, lens, part);
 
   const int per = p.Hkv * p.rtiles;                  // items of a sequence
-  const long long total = at[p.B] * per;
+  const long long total = (long long)at[p.B] * per;
   // this CTA's chunks [u, u1) of all (none for those past the chunks' number: every CTA
   // between an item's first and its last has a piece of it), or, not split, its items u, u +
   // ctas, ...
@@ -260,7 +275,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
       for (int i = threadIdx.x; i < p.H * D / 8; i += kThreads)
         *reinterpret_cast<uint4*>(p.o + (long long)b * p.H * D + 8 * i) = make_uint4(0, 0, 0, 0);
 
-  uint32_t step_no = 0;   // Q8_0: steps this warp has issued to its ring so far, consumed ones below
+  uint8_t* mine = ring + warp * C::NS * 2 * C::kHalf;
+  int put = 0, get = 0;             // stages to fill and to read next
+  uint32_t phase = 0;               // of the stage to read next
   bool ok = true;
   while (u < u1) {
     // the item, and its chunks [c0, c1)
@@ -270,12 +287,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
       int lo = 0, hi = p.B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (at[mid] * per <= u) lo = mid;
+        if ((long long)at[mid] * per <= u) lo = mid;
         else hi = mid;
       }
       b = lo;
       chunks = at[b + 1] - at[b];
-      const long long rel = u - at[b] * per;
+      const long long rel = u - (long long)at[b] * per;
       item = (int)(rel / chunks);
       c0 = rel % chunks;
       c1 = min(chunks, c0 + (u1 - u));
@@ -290,11 +307,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
       if (chunks == 0) continue;
     }
     const int hk = item / p.rtiles, row0 = item % p.rtiles * C::R;   // query heads hk G + row0 ...
-    const int len = (int)min((long long)max(p.lengths[b], 0), (long long)p.W * p.page);
     Rows<C> rows;
     rows.table = p.table + (long long)b * p.W;
-    rows.hk = hk;
-    rows.last = (int)min((long long)len, c1 * C::CH);
+    rows.last = (int)min((long long)lens[b], c1 * C::CH);
     rows.first = (int)min(c0 * C::CH + warp * C::KT, (long long)rows.last);
     const int steps = (rows.last - rows.first + C::CH - 1) / C::CH;   // of this warp
     rows.fetch(p, 0);
@@ -344,172 +359,78 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
     Acc<D, NT> acc;
     acc.clear();
     rows.advance(p, 0);
-    // Rows g, g + 8 of MMA k that are seen in `step`; all: every key of the step is.
-    auto seen_of = [&](int step, bool& all) {
-      const int k0 = rows.first + step * C::CH;
-      uint32_t there = 0;
-#pragma unroll
-      for (int i = 0; i < C::GR; ++i) there |= (rows.group(step, i) >= 0 ? 1u : 0u) << i;
-      all = there == (1u << C::GR) - 1 && k0 + C::KT <= rows.last;
-      uint32_t seen = 0;
-#pragma unroll
-      for (int k = 0; k < C::KS; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = 16 * k + key_of<Q8>(g + 8 * h);
-          seen |= (((there >> (key >> 3)) & 1) && k0 + key < rows.last ? 1u : 0u) << (2 * k + h);
+    // A step's copies: its groups of K, then of V (fp16: of each half of the head dim).
+    // Groups that are there are kept for the step's turn, a byte a stage.
+    uint32_t kept = 0;
+    auto issue = [&](int step) {
+      const int in = step % Rows<C>::kSteps;
+      if (in == 0 && step > 0) rows.advance(p, step);
+      const int i = lane % C::GR;
+      const int id = __shfl_sync(0xffffffffu, rows.page_id, in * C::GR + i);
+      const int place = __shfl_sync(0xffffffffu, rows.place, in * C::GR + i);
+      const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & ((1u << C::GR) - 1);
+      kept = (kept & ~(0xFFu << (8 * put))) | (there << (8 * put));
+      uint64_t* bar = &full[warp][put];
+      uint8_t* dst = mine + put * 2 * C::kHalf;
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * 16 * C::RB);
+      __syncwarp();
+      if (lane < C::kCopies && id >= 0) {
+        const int part_no = lane / C::GR;
+        if constexpr (Q8) {
+          const long long row = ((long long)id * p.Hkv + hk) * p.page + place;
+          bulk_load(dst + part_no * C::kHalf + i * 8 * C::RB, (part_no ? p.v : p.k) + row * C::RB, 8 * C::RB, bar);
+        } else {
+          const int is_v = part_no / (D / 64), half = part_no % (D / 64);
+          tma_load_3d(dst + is_v * C::kHalf + half * C::KT * 128 + i * 1024, is_v ? &tm_v : &tm_k, bar, 64 * half,
+                      place, id * p.Hkv + hk);
         }
-      return seen;
-    };
-    // which of the thread's V keys (2t, 2t + 1, 2t + 8, 2t + 9 of MMA k) are seen
-    auto seen_v = [&](int step, int k, int j, uint32_t there) {
-      const int key = 16 * k + key_of<Q8>(2 * t + (j & 1) + 8 * (j >> 1));
-      return ((there >> (key >> 3)) & 1) && rows.first + step * C::CH + key < rows.last;
-    };
-    auto groups_of = [&](int step) {
-      uint32_t there = 0;
-#pragma unroll
-      for (int i = 0; i < C::GR; ++i) there |= (rows.group(step, i) >= 0 ? 1u : 0u) << i;
-      return there;
-    };
-
-    if constexpr (!Q8) {
-      constexpr int KL = C::QS / 2;    // 16-byte pieces of a K row a thread has
-      constexpr int VL = D / 64;       // and of a V row
-      uint4 kr[C::KS][2][KL], vr[C::KS][4][VL];
-      auto load_k = [&](int step) {
-#pragma unroll
-        for (int k = 0; k < C::KS; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = rows.group(step, 2 * k + h);
-            const uint4* src = reinterpret_cast<const uint4*>(p.k + (long long)(r + g) * C::RB) + t;
-            if (r >= 0) {
-#pragma unroll
-              for (int j = 0; j < KL; ++j) kr[k][h][j] = src[4 * j];
-            } else {
-#pragma unroll
-              for (int j = 0; j < KL; ++j) kr[k][h][j] = make_uint4(0, 0, 0, 0);
-            }
-          }
-      };
-      auto load_v = [&](int step) {
-        const int k0 = rows.first + step * C::CH;
-#pragma unroll
-        for (int k = 0; k < C::KS; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = rows.group(step, 2 * k + h);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint4* src = reinterpret_cast<const uint4*>(p.v + (long long)(r + 2 * t + e) * C::RB) + g;
-              const bool has = r >= 0 && k0 + 16 * k + 8 * h + 2 * t + e < rows.last;
-#pragma unroll
-              for (int j = 0; j < VL; ++j) vr[k][2 * h + e][j] = has ? src[8 * j] : make_uint4(0, 0, 0, 0);
-            }
-          }
-      };
-      if (steps > 0) {
-        load_k(0);
-        load_v(0);
       }
+      put = put + 1 == C::NS ? 0 : put + 1;
+    };
+    int issued = min(steps, C::NS);
+    for (int i = 0; i < issued; ++i) issue(i);
 #pragma unroll 1
-      for (int step = 0; step < steps; ++step) {
-        bool all;
-        const uint32_t seen = seen_of(step, all);
-        float s[C::KS][NT][4];
+    for (int step = 0; step < steps; ++step) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][get], phase, ctl));
+      if (!ok) break;
+      const uint8_t* kt = mine + get * 2 * C::kHalf;
+      const uint8_t* vt = kt + C::kHalf;
+      const uint32_t there = (kept >> (8 * get)) & 0xFFu;
+      const int left = rows.last - (rows.first + step * C::CH);   // keys from the step's first on
+      const bool all = there == (1u << C::GR) - 1 && left >= C::KT;
+      uint32_t seen = 0;   // bit 2 k + h: the key on row g + 8 h of MMA k
+      if (!all) {
 #pragma unroll
         for (int k = 0; k < C::KS; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) s[k][n][0] = s[k][n][1] = s[k][n][2] = s[k][n][3] = 0.f;
+          for (int h = 0; h < 2; ++h) {
+            const int key = 16 * k + key_of<Q8>(g + 8 * h);
+            seen |= (((there >> (key >> 3)) & 1) && key < left ? 1u : 0u) << (2 * k + h);
+          }
+      }
+      float s[C::KS][NT][4];
 #pragma unroll
-        for (int j = 0; j < KL; ++j)
+      for (int k = 0; k < C::KS; ++k) {
 #pragma unroll
-          for (int k = 0; k < C::KS; ++k)
+        for (int n = 0; n < NT; ++n) s[k][n][0] = s[k][n][1] = s[k][n][2] = s[k][n][3] = 0.f;
+        if constexpr (!Q8) {
+          // pieces t, t + 4, ... of 16 bytes of rows g and g + 8 (each half of the head dim has
+          // eight of a row, swizzled by the row)
+          const int row = 16 * k + key_of<false>(g);   // the other is 8 below: the same swizzle
+          const uint8_t* src = kt + row * 128 + 16 * (t ^ (row & 3));
+          const int flip = row & 4 ? 64 : 0;
+#pragma unroll
+          for (int j = 0; j < C::QS / 2; ++j) {
+            const uint8_t* at_j = src + (j >> 1) * C::KT * 128 + ((j & 1) ? 64 - flip : flip);
+            const uint4 x = *reinterpret_cast<const uint4*>(at_j);
+            const uint4 y = *reinterpret_cast<const uint4*>(at_j + 8 * 128);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const uint4 &x = kr[k][0][j], &y = kr[k][1][j];
               mma16816(s[k][n], x.x, y.x, x.y, y.y, qf[n][2 * j][0], qf[n][2 * j][1]);
               mma16816(s[k][n], x.z, y.z, x.w, y.w, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
             }
-        const bool more = step + 1 < steps;
-        if (more) {
-          if ((step + 1) % Rows<C>::kSteps == 0) rows.advance(p, step + 1);
-          load_k(step + 1);
-        }
-        uint32_t pf[C::KS][NT][2];
-        softmax_step<D, NT, C::KS>(s, acc, p.scale_log2, all, seen, pf);
-#pragma unroll
-        for (int k = 0; k < C::KS; ++k)
-#pragma unroll
-          for (int j = 0; j < VL; ++j) {
-            const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&vr[k][0][j]);
-            const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&vr[k][1][j]);
-            const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&vr[k][2][j]);
-            const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&vr[k][3][j]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
-              const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816(acc.o[n][4 * j + i], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
-            }
           }
-        if (more) load_v(step + 1);
-      }
-    } else {
-      uint8_t* mine = ring + warp * kStages * C::kStage;
-      // Copies of a step's rows: K's groups, then V's, a lane each.
-      auto issue = [&](int step, uint32_t no) {
-        const uint32_t there = groups_of(step);
-        uint64_t* bar = &full[warp][no % kStages];
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * 16 * C::RB);
-        const int i = lane % C::GR;
-        const int r = rows.group(step, i);
-        __syncwarp();
-        if (lane < 2 * C::GR && r >= 0) {
-          uint8_t* dst = mine + (no % kStages) * C::kStage + (lane < C::GR ? 0 : C::KT * C::RB) + 8 * i * C::RB;
-          bulk_load(dst, (lane < C::GR ? p.k : p.v) + (long long)r * C::RB, 8 * C::RB, bar);
-        }
-      };
-      // Rows of a step are looked up when it is issued; what is seen of it is kept for its
-      // turn: groups that are there, a byte a stage.
-      uint32_t kept = 0, issued = step_no;
-      auto issue_next = [&](int step, uint32_t no) {
-        if (step > 0 && step % Rows<C>::kSteps == 0) rows.advance(p, step);
-        const int sh = 8 * (no % kStages);
-        kept = (kept & ~(0xFFu << sh)) | (groups_of(step) << sh);
-        issue(step, no);
-        ++issued;
-      };
-      const int ahead = min(steps, kStages);
-      for (int i = 0; i < ahead; ++i) issue_next(i, step_no + i);
-#pragma unroll 1
-      for (int step = 0; step < steps && ok; ++step) {
-        const uint32_t no = step_no + step, slot = no % kStages;
-        ok = mbar_wait(&full[warp][slot], (no / kStages) & 1, ctl);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint8_t* kt = mine + slot * C::kStage;
-        const uint8_t* vt = kt + C::KT * C::RB;
-        const uint32_t there = (kept >> (8 * slot)) & 0xFFu;
-        const int k0 = rows.first + step * C::CH;
-        const bool all = there == (1u << C::GR) - 1 && k0 + C::KT <= rows.last;
-        uint32_t seen = 0;
-        if (!all) {
-#pragma unroll
-          for (int k = 0; k < C::KS; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int key = 16 * k + key_of<Q8>(g + 8 * h);
-              seen |= (((there >> (key >> 3)) & 1) && k0 + key < rows.last ? 1u : 0u) << (2 * k + h);
-            }
-        }
-        float s[C::KS][NT][4];
-#pragma unroll
-        for (int k = 0; k < C::KS; ++k) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) s[k][n][0] = s[k][n][1] = s[k][n][2] = s[k][n][3] = 0.f;
+        } else {
           // the codes of rows g, g + 8 that the thread has of each, and their scale
           uint32_t w[2][C::QS], d2[2];
 #pragma unroll
@@ -549,10 +470,53 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
             for (int n = 0; n < NT; ++n) mma16816(s[k][n], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
           }
         }
-        uint32_t pf[C::KS][NT][2];
-        softmax_step<D, NT, C::KS>(s, acc, p.scale_log2, all, seen, pf);
+      }
+      uint32_t pf[C::KS][NT][2];
+      softmax_step<D, NT, C::KS>(s, acc, p.scale_log2, all, seen, pf);
 #pragma unroll
-        for (int k = 0; k < C::KS; ++k) {
+      for (int k = 0; k < C::KS; ++k) {
+        // values of keys that are not seen become 0
+        uint32_t mask01 = 0xFFFFFFFFu, mask23 = 0xFFFFFFFFu;
+        if (!all) {
+          auto has = [&](int j) {
+            const int key = 16 * k + key_of<Q8>(2 * t + (j & 1) + 8 * (j >> 1));
+            return ((there >> (key >> 3)) & 1) && key < left;
+          };
+          mask01 = (has(0) ? 0xFFFFu : 0u) | (has(1) ? 0xFFFF0000u : 0u);
+          mask23 = (has(2) ? 0xFFFFu : 0u) | (has(3) ? 0xFFFF0000u : 0u);
+        }
+        auto product = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          if (!all) {
+            a0 &= mask01;
+            a1 &= mask01;
+            a2 &= mask23;
+            a3 &= mask23;
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(acc.o[n][i], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
+        };
+        if constexpr (!Q8) {
+          // piece g (and g + 8) of 16 bytes of the four rows
+          const int r0 = key_of<false>(2 * t), r1 = key_of<false>(2 * t + 1);   // the others 8 below
+          const uint8_t* src0 = vt + (16 * k + r0) * 128 + 16 * (g ^ r0);
+          const uint8_t* src1 = vt + (16 * k + r1) * 128 + 16 * (g ^ r1);
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            uint4 v[4];
+            v[0] = *reinterpret_cast<const uint4*>(src0 + j * C::KT * 128);
+            v[1] = *reinterpret_cast<const uint4*>(src1 + j * C::KT * 128);
+            v[2] = *reinterpret_cast<const uint4*>(src0 + j * C::KT * 128 + 8 * 128);
+            v[3] = *reinterpret_cast<const uint4*>(src1 + j * C::KT * 128 + 8 * 128);
+            const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&v[0]);
+            const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&v[1]);
+            const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&v[2]);
+            const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&v[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              product(4 * j + i, __byte_perm(w0[i], w1[i], 0x5410), __byte_perm(w0[i], w1[i], 0x7632),
+                      __byte_perm(w2[i], w3[i], 0x5410), __byte_perm(w2[i], w3[i], 0x7632));
+          }
+        } else {
           // codes of the four V rows, D / 8 neighbours a thread, and their scales
           uint32_t w[4][D / 32], ds[4];
 #pragma unroll
@@ -582,11 +546,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
             }
           }
           const uint32_t d01 = __byte_perm(ds[0], ds[1], 0x5410), d23 = __byte_perm(ds[2], ds[3], 0x5410);
-          uint32_t mask01 = 0xFFFFFFFFu, mask23 = 0xFFFFFFFFu;   // values of keys that are not seen become 0
-          if (!all) {
-            mask01 = (seen_v(step, k, 0, there) ? 0xFFFFu : 0u) | (seen_v(step, k, 1, there) ? 0xFFFF0000u : 0u);
-            mask23 = (seen_v(step, k, 2, there) ? 0xFFFFu : 0u) | (seen_v(step, k, 3, there) ? 0xFFFF0000u : 0u);
-          }
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
 #pragma unroll
@@ -595,27 +554,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
               uint32_t a0, a1, a2, a3;
               q8_word(__byte_perm(w[0][i], w[1][i], sel), d01, dk, a0, a1);
               q8_word(__byte_perm(w[2][i], w[3][i], sel), d23, dk, a2, a3);
-              if (!all) {
-                a0 &= mask01;
-                a1 &= mask01;
-                a2 &= mask23;
-                a3 &= mask23;
-              }
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816(acc.o[n][2 * i + half], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
+              product(2 * i + half, a0, a1, a2, a3);
             }
           }
         }
-        __syncwarp();   // the stage has been read
-        if (step + kStages < steps) issue_next(step + kStages, no + kStages);
       }
-      if (!ok)   // copies still under way land before the block leaves
-        for (uint32_t i = 0; i < (uint32_t)kStages && i < issued; ++i) {
-          const uint32_t no = issued - 1 - i;
-          mbar_wait_drain(&full[warp][no % kStages], (no / kStages) & 1, 100000000ull);
-        }
-      step_no = issued;
+      __syncwarp();   // the stage has been read
+      get = get + 1 == C::NS ? 0 : get + 1;
+      phase ^= get == 0;
+      if (issued < steps) issue(issued++);
     }
+    if (!ok) {
+      // copies still under way land before the block leaves
+      for (int i = 0; i < C::NS; ++i) {
+        mbar_wait_drain(&full[warp][get], phase, 100000000ull);
+        get = get + 1 == C::NS ? 0 : get + 1;
+        phase ^= get == 0;
+      }
+    }
+    __syncthreads();   // the ring is idle: O goes there
 
     // The four warps' maxima, sums and O.
 #pragma unroll
@@ -681,10 +638,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
     }
     if (!whole && c0 == 0 && threadIdx.x == 0) {
       // the CTA of the item's last chunk; this one has its first
-      const long long end = at[b] * per + (long long)(item + 1) * chunks - 1;
+      const long long end = (long long)at[b] * per + (long long)(item + 1) * chunks - 1;
       const int last = (int)(((end + 1) * used - 1) / total);
       p.ws_cut[cta] = make_int4(b, item, last, 1);
     }
+    fence_proxy_async_smem();   // the ring's next copies come after these reads and writes
     __syncthreads();
   }
 }
@@ -739,7 +697,7 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedParams p) {
 }
 
 template <int D, bool Q8, int NT>
-cudaError_t launch(const PagedParams& p, int grid, cudaStream_t s) {
+cudaError_t launch(const PagedParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid, cudaStream_t s) {
   using C = Cfg<D, Q8, NT>;
   auto kern = paged_kernel<D, Q8, NT>;
   std::atomic<unsigned long long>& configured = attr_flag<std::integer_sequence<int, 11, D, Q8, NT>>();
@@ -752,7 +710,7 @@ cudaError_t launch(const PagedParams& p, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  e = launch_proj(kern, (unsigned)grid, (unsigned)kThreads, C::kSmem, s, 1u, p);
+  e = launch_proj(kern, (unsigned)grid, (unsigned)kThreads, C::kSmem, s, 1u, p, tm_k, tm_v);
   if (e != cudaSuccess || !p.split) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -767,15 +725,17 @@ cudaError_t launch(const PagedParams& p, int grid, cudaStream_t s) {
 }
 
 template <int D, bool Q8>
-cudaError_t launch_nt(const PagedParams& p, int grid, cudaStream_t s) {
-  return p.G <= 8 ? launch<D, Q8, 1>(p, grid, s) : launch<D, Q8, 2>(p, grid, s);
+cudaError_t launch_nt(const PagedParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
+                      cudaStream_t s) {
+  return p.G <= 8 ? launch<D, Q8, 1>(p, tm_k, tm_v, grid, s) : launch<D, Q8, 2>(p, tm_k, tm_v, grid, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_paged(const PagedParams& p, bool q8, int grid, cudaStream_t s) {
-  if (p.D == 64) return q8 ? launch_nt<64, true>(p, grid, s) : launch_nt<64, false>(p, grid, s);
-  return q8 ? launch_nt<128, true>(p, grid, s) : launch_nt<128, false>(p, grid, s);
+cudaError_t launch_attention_paged(const PagedParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                   int grid, cudaStream_t s) {
+  if (p.D == 64) return q8 ? launch_nt<64, true>(p, tm_k, tm_v, grid, s) : launch_nt<64, false>(p, tm_k, tm_v, grid, s);
+  return q8 ? launch_nt<128, true>(p, tm_k, tm_v, grid, s) : launch_nt<128, false>(p, tm_k, tm_v, grid, s);
 }
 
 }  // namespace m4q

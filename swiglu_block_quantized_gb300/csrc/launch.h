@@ -276,11 +276,15 @@ struct PagedParams {
   float* ws_o;            // [2 grid][rows][D] its unnormalised O
   uint32_t* status;
 };
-// Query heads of an item, keys of a chunk, and CTAs an SM.
+// Query heads of an item, keys of a chunk (four warps' steps: 17 KB of rows of Q8_0 a
+// warp, 8 of fp16), and CTAs an SM.
 constexpr int paged_rows(int G) { return G <= 8 ? 8 : 16; }
-constexpr int paged_chunk(int D) { return D == 64 ? 128 : 64; }
-constexpr int paged_ctas(int G) { return G <= 8 ? 3 : 2; }
-cudaError_t launch_attention_paged(const PagedParams& p, bool q8, int grid, cudaStream_t s);
+constexpr int paged_chunk(int D, bool q8) { return (q8 ? 16384 : 8192) / D; }
+constexpr int paged_ctas(int G, bool q8) { return q8 && G <= 8 ? 3 : 2; }
+// tm_k, tm_v: [P Hkv][page][D] of fp16 pools, boxes of [1][8 rows][64 d], 128-byte swizzle
+// (not read for Q8_0).
+cudaError_t launch_attention_paged(const PagedParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                   int grid, cudaStream_t s);
 
 // page_plan.cu: pages handed to sequences and taken back, and the slots of a step's
 // tokens.

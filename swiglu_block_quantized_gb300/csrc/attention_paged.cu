@@ -118,10 +118,9 @@ struct Acc {
 };
 
 // Scores of 16 KS keys -> P^T fragments.  s[k][n]: rows g, g + 8 of MMA k, columns 2t,
-// 2t + 1 of n; seen: bit 2 k + h says that row g + 8 h of MMA k counts.
+// 2t + 1 of n, scaled; -inf for keys that do not count.
 template <int D, int NT, int KS>
-__device__ __forceinline__ void softmax_step(float (&s)[KS][NT][4], Acc<D, NT>& a, float scale, bool all,
-                                             uint32_t seen, uint32_t (&pf)[KS][NT][2]) {
+__device__ __forceinline__ void softmax_step(float (&s)[KS][NT][4], Acc<D, NT>& a, uint32_t (&pf)[KS][NT][2]) {
   bool raise = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -131,12 +130,7 @@ __device__ __forceinline__ void softmax_step(float (&s)[KS][NT][4], Acc<D, NT>& 
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& x = s[k][n][2 * h + c];
-          x *= scale;
-          if (!all && !((seen >> (2 * k + h)) & 1)) x = -INFINITY;
-          top = fmaxf(top, x);
-        }
+        for (int h = 0; h < 2; ++h) top = fmaxf(top, s[k][n][2 * h + c]);
       raise |= top > a.m[n][c] + 8.f;
     }
   if (__any_sync(0xffffffffu, raise)) {
@@ -398,16 +392,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
       const uint32_t there = (kept >> (8 * get)) & 0xFFu;
       const int left = rows.last - (rows.first + step * C::CH);   // keys from the step's first on
       const bool all = there == (1u << C::GR) - 1 && left >= C::KT;
-      uint32_t seen = 0;   // bit 2 k + h: the key on row g + 8 h of MMA k
-      if (!all) {
-#pragma unroll
-        for (int k = 0; k < C::KS; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = 16 * k + key_of<Q8>(g + 8 * h);
-            seen |= (((there >> (key >> 3)) & 1) && key < left ? 1u : 0u) << (2 * k + h);
-          }
-      }
       float s[C::KS][NT][4];
 #pragma unroll
       for (int k = 0; k < C::KS; ++k) {
@@ -471,27 +455,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
           }
         }
       }
+#pragma unroll
+      for (int k = 0; k < C::KS; ++k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[k][n][c] *= p.scale_log2;
+      if (!all) {
+        // keys that are not seen: no score, and V's rows become 0 (the product would make
+        // NaN of infinities with a weight of 0)
+#pragma unroll
+        for (int k = 0; k < C::KS; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = 16 * k + key_of<Q8>(g + 8 * h);
+            if (!((there >> (key >> 3)) & 1) || key >= left)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) s[k][n][2 * h] = s[k][n][2 * h + 1] = -INFINITY;
+          }
+        for (int key = 0; key < C::KT; ++key) {
+          if (((there >> (key >> 3)) & 1) && key < left) continue;
+          if constexpr (Q8) {
+            if (lane < D / 32) *reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(vt) + key * C::RB + 34 * lane) = 0;
+          } else if (lane < D / 8) {
+            uint8_t* row = const_cast<uint8_t*>(vt) + (lane >> 3) * C::KT * 128 + key * 128;
+            *reinterpret_cast<uint4*>(row + 16 * (lane & 7)) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();   // before the copies that fill the stage next
+        __syncwarp();
+      }
       uint32_t pf[C::KS][NT][2];
-      softmax_step<D, NT, C::KS>(s, acc, p.scale_log2, all, seen, pf);
+      softmax_step<D, NT, C::KS>(s, acc, pf);
 #pragma unroll
       for (int k = 0; k < C::KS; ++k) {
-        // values of keys that are not seen become 0
-        uint32_t mask01 = 0xFFFFFFFFu, mask23 = 0xFFFFFFFFu;
-        if (!all) {
-          auto has = [&](int j) {
-            const int key = 16 * k + key_of<Q8>(2 * t + (j & 1) + 8 * (j >> 1));
-            return ((there >> (key >> 3)) & 1) && key < left;
-          };
-          mask01 = (has(0) ? 0xFFFFu : 0u) | (has(1) ? 0xFFFF0000u : 0u);
-          mask23 = (has(2) ? 0xFFFFu : 0u) | (has(3) ? 0xFFFF0000u : 0u);
-        }
         auto product = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-          if (!all) {
-            a0 &= mask01;
-            a1 &= mask01;
-            a2 &= mask23;
-            a3 &= mask23;
-          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma16816(acc.o[n][i], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
         };

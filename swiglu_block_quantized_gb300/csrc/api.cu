@@ -1100,7 +1100,7 @@ PagedPlan paged_plan(bool q8, int64_t B, int64_t H, int64_t Hkv, int64_t page, i
   t.seqs = (int)(B < m4q::kPagedSeqs ? B : m4q::kPagedSeqs);
   if (t.seqs > fit) t.seqs = (int)fit;
   const int64_t items = (int64_t)t.seqs * Hkv * t.rtiles;
-  const int64_t most = (int64_t)sms * m4q::paged_ctas(G, q8);
+  const int64_t most = (int64_t)sms * m4q::paged_ctas(G, (int)D, q8);
   t.split = chunks > 1;
   t.whole = (int)(items < most ? items : most);
   t.grid = !t.split ? t.whole : (int)(chunks > most / items ? most : items * chunks);

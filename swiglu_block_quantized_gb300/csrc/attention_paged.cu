@@ -50,6 +50,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -83,22 +95,22 @@ struct Cfg {
   static constexpr int CH = 4 * KT;                     // keys of a chunk
   static constexpr int QS = D / 16;                     // k16 steps of S, and m16 tiles of O
   static constexpr int R = 8 * NT;                      // query rows of an item
-  static constexpr int NS = Q8 ? 2 : 3;                 // steps of a warp in its ring
+  static constexpr int NS = Q8 && D == 128 ? 2 : 3;                 // steps of a warp in its ring
   static constexpr int kHalf = KT * RB;                 // K rows of a step, then V rows
   static constexpr int kRing = 4 * NS * 2 * kHalf;
   static constexpr int kCopies = 2 * GR * (Q8 ? 1 : D / 64);   // copies of a step, a lane each
   static constexpr int kPitch = D + 4;                  // floats of a row of O in shared memory
   static constexpr int kJoin = 4 * R * kPitch * 4 + 4 * R * 8;   // in the ring, when it is idle
   static_assert(kJoin <= kRing && kCopies <= 32 && GR <= 8 && (GR & (GR - 1)) == 0, "layout");
-  static constexpr int kSmem = 1024 + kRing + (2 * kPagedSeqs + 1) * 4;
+  static constexpr int kSmem = (Q8 ? 0 : 1024) + kRing + (2 * kPagedSeqs + 1) * 4;
 };
 
-// Which key of a step's 16 stands on row r of the MMA: orders in which the reads of K (rows
-// r, 4 threads a row) and of V (keys 2t, 2t + 1, 2t + 8, 2t + 9 of a thread) meet no bank
-// twice (Q8_0: at D = 128).
+// Which key of a step's 16 stands on row r of the MMA.  Q8_0: an order in which the reads
+// of K (rows r, 4 threads a row) and of V (keys 2t, 2t + 1, 2t + 8, 2t + 9 of a thread)
+// meet no bank twice at D = 128; fp16: as they are (ldmatrix).
 template <bool Q8>
 __device__ __forceinline__ int key_of(int r) {
-  return Q8 ? 8 * ((r >> 2) & 1) + 4 * (r >> 3) + 2 * (r & 1) + ((r >> 1) & 1) : r ^ ((r & 1) << 2);
+  return Q8 ? 8 * ((r >> 2) & 1) + 4 * (r >> 3) + 2 * (r & 1) + ((r >> 1) & 1) : r;
 }
 
 // What a warp keeps of its keys so far.
@@ -224,14 +236,14 @@ struct Rows {
 };
 
 template <int D, bool Q8, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const PagedParams p, const __grid_constant__ CUtensorMap tm_k,
+__global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3) : 2) paged_kernel(const PagedParams p, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D, Q8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int part[4];
   __shared__ __align__(8) uint64_t full[4][C::NS];
   __shared__ int abort_flag;
-  uint8_t* ring = smem_align<1024>(smem);
+  uint8_t* ring = Q8 ? smem : smem_align<1024>(smem);
   float* so = reinterpret_cast<float*>(ring);                         // [4][R][kPitch]
   float2* sml = reinterpret_cast<float2*>(so + 4 * C::R * C::kPitch); // [4][R]
   int* at = reinterpret_cast<int*>(ring + C::kRing);                  // [B + 1]
@@ -317,13 +329,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
       const __half* q = p.q + ((long long)(hk * p.G + (has ? r : 0)) * p.q_rows + b) * D;
       if constexpr (!Q8) {
 #pragma unroll
-        for (int j = 0; j < C::QS / 2; ++j) {
-          const uint4 v = has ? *reinterpret_cast<const uint4*>(q + 8 * (t + 4 * j)) : make_uint4(0, 0, 0, 0);
-          qf[n][2 * j][0] = v.x;
-          qf[n][2 * j][1] = v.y;
-          qf[n][2 * j + 1][0] = v.z;
-          qf[n][2 * j + 1][1] = v.w;
-        }
+        for (int i = 0; i < C::QS; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            qf[n][i][h] = has ? *reinterpret_cast<const uint32_t*>(q + 16 * i + 8 * h + 2 * t) : 0u;
       } else {
         // word i of the thread's codes (see k_words): head dims of its codes 0, 2 and 1, 3
 #pragma unroll
@@ -398,21 +407,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[k][n][0] = s[k][n][1] = s[k][n][2] = s[k][n][3] = 0.f;
         if constexpr (!Q8) {
-          // pieces t, t + 4, ... of 16 bytes of rows g and g + 8 (each half of the head dim has
-          // eight of a row, swizzled by the row)
-          const int row = 16 * k + key_of<false>(g);   // the other is 8 below: the same swizzle
-          const uint8_t* src = kt + row * 128 + 16 * (t ^ (row & 3));
-          const int flip = row & 4 ? 64 : 0;
+          // lanes 0-7: pieces 2 i of the first 8 rows, 8-15 of the other 8, 16-31 the pieces next to
+          // them; pieces lie swizzled by their row, each half of the head dim apart
+          const uint32_t row = 16 * k + (lane & 15), src = smem_u32(kt) + row * 128;
 #pragma unroll
-          for (int j = 0; j < C::QS / 2; ++j) {
-            const uint8_t* at_j = src + (j >> 1) * C::KT * 128 + ((j & 1) ? 64 - flip : flip);
-            const uint4 x = *reinterpret_cast<const uint4*>(at_j);
-            const uint4 y = *reinterpret_cast<const uint4*>(at_j + 8 * 128);
+          for (int i = 0; i < C::QS; ++i) {
+            uint32_t a[4];
+            ldsm_x4(a, src + (i >> 2) * C::KT * 128 + 16 * ((2 * (i & 3) + (lane >> 4)) ^ (row & 7)));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816(s[k][n], x.x, y.x, x.y, y.y, qf[n][2 * j][0], qf[n][2 * j][1]);
-              mma16816(s[k][n], x.z, y.z, x.w, y.w, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
-            }
+            for (int n = 0; n < NT; ++n) mma16816(s[k][n], a[0], a[1], a[2], a[3], qf[n][i][0], qf[n][i][1]);
           }
         } else {
           // the codes of rows g, g + 8 that the thread has of each, and their scale
@@ -494,25 +497,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
           for (int n = 0; n < NT; ++n) mma16816(acc.o[n][i], a0, a1, a2, a3, pf[k][n][0], pf[k][n][1]);
         };
         if constexpr (!Q8) {
-          // piece g (and g + 8) of 16 bytes of the four rows
-          const int r0 = key_of<false>(2 * t), r1 = key_of<false>(2 * t + 1);   // the others 8 below
-          const uint8_t* src0 = vt + (16 * k + r0) * 128 + 16 * (g ^ r0);
-          const uint8_t* src1 = vt + (16 * k + r1) * 128 + 16 * (g ^ r1);
+          // lanes 0-7: piece 2 i of the first 8 rows, 8-15 the piece next to it, 16-31 of the other
+          // 8 rows; transposed, so that head dims are the MMA's rows
+          const uint32_t row = 16 * k + (lane & 7) + 8 * (lane >> 4), src = smem_u32(vt) + row * 128;
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            uint4 v[4];
-            v[0] = *reinterpret_cast<const uint4*>(src0 + j * C::KT * 128);
-            v[1] = *reinterpret_cast<const uint4*>(src1 + j * C::KT * 128);
-            v[2] = *reinterpret_cast<const uint4*>(src0 + j * C::KT * 128 + 8 * 128);
-            v[3] = *reinterpret_cast<const uint4*>(src1 + j * C::KT * 128 + 8 * 128);
-            const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&v[0]);
-            const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&v[1]);
-            const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&v[2]);
-            const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&v[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              product(4 * j + i, __byte_perm(w0[i], w1[i], 0x5410), __byte_perm(w0[i], w1[i], 0x7632),
-                      __byte_perm(w2[i], w3[i], 0x5410), __byte_perm(w2[i], w3[i], 0x7632));
+          for (int i = 0; i < C::QS; ++i) {
+            uint32_t a[4];
+            ldsm_x4_t(a, src + (i >> 2) * C::KT * 128 + 16 * ((2 * (i & 3) + ((lane >> 3) & 1)) ^ (row & 7)));
+            product(i, a[0], a[1], a[2], a[3]);
           }
         } else {
           // codes of the four V rows, D / 8 neighbours a thread, and their scales
@@ -584,9 +576,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
         if (g == 0) sml[r] = make_float2(acc.m[n][c], l);
 #pragma unroll
         for (int i = 0; i < C::QS; ++i) {
-          int d;   // of the fragment's row g; row g + 8 is d + 1
+          int d;   // of the fragment's row g; row g + 8 is d + 1 (fp16: d + 8)
           if constexpr (!Q8) {
-            d = 8 * (g + 8 * (i >> 2)) + 2 * (i & 3);
+            d = 16 * i + g;
           } else if constexpr (D == 128) {
             const int sh = 2 + 2 * (g >> 1), w = i >> 1, half = i & 1;
             if (w < 2) d = 4 * (w + 2) - sh + 2 * half;
@@ -599,7 +591,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) paged_kernel(const 
             else d = g < 4 ? 6 * half : 4 + 2 * half;
             d += 8 * g;
           }
-          *reinterpret_cast<float2*>(so + r * C::kPitch + d) = make_float2(acc.o[n][i][c], acc.o[n][i][2 + c]);
+          if constexpr (Q8) {
+            *reinterpret_cast<float2*>(so + r * C::kPitch + d) = make_float2(acc.o[n][i][c], acc.o[n][i][2 + c]);
+          } else {
+            so[r * C::kPitch + d] = acc.o[n][i][c];
+            so[r * C::kPitch + d + 8] = acc.o[n][i][2 + c];
+          }
         }
       }
     ok = __syncthreads_and(ok);

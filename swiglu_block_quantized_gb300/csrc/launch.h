@@ -279,8 +279,8 @@ struct PagedParams {
 // Query heads of an item, keys of a chunk (four warps' steps: 17 KB of rows of Q8_0 a
 // warp, 8 of fp16), and CTAs an SM.
 constexpr int paged_rows(int G) { return G <= 8 ? 8 : 16; }
-constexpr int paged_chunk(int D, bool q8) { return (q8 ? 16384 : 8192) / D; }
-constexpr int paged_ctas(int G, bool q8) { return q8 && G <= 8 ? 3 : 2; }
+constexpr int paged_chunk(int D, bool q8) { return q8 ? 128 : 8192 / D; }
+constexpr int paged_ctas(int G, int D, bool q8) { return G > 8 || !q8 ? 2 : D == 64 ? 4 : 3; }
 // tm_k, tm_v: [P Hkv][page][D] of fp16 pools, boxes of [1][8 rows][64 d], 128-byte swizzle
 // (not read for Q8_0).
 cudaError_t launch_attention_paged(const PagedParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,

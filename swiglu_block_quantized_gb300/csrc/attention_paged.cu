@@ -99,9 +99,8 @@ struct Cfg {
   static constexpr int kHalf = KT * RB;                 // K rows of a step, then V rows
   static constexpr int kRing = 4 * NS * 2 * kHalf;
   static constexpr int kCopies = 2 * GR * (Q8 ? 1 : D / 64);   // copies of a step, a lane each
-  static constexpr int kPitch = D + 4;                  // floats of a row of O in shared memory
-  static constexpr int kJoin = 4 * R * kPitch * 4 + 4 * R * 8;   // in the ring, when it is idle
-  static_assert(kJoin <= kRing && kCopies <= 32 && GR <= 8 && (GR & (GR - 1)) == 0, "layout");
+  // (a warp's O is handed to the others in the stage that it read last)
+  static_assert(R * D * 4 <= 2 * kHalf && kCopies <= 32 && GR <= 8 && (GR & (GR - 1)) == 0, "layout");
   static constexpr int kSmem = (Q8 ? 0 : 1024) + kRing + (2 * kPagedSeqs + 1) * 4;
 };
 
@@ -235,6 +234,61 @@ struct Rows {
   }
 };
 
+// A part of an item that a CTA takes: chunks [c0, c1) of `chunks`.  u: where the CTA goes
+// on, as a chunk of all (split) or an item.
+struct Part {
+  int b, item, c0, c1, chunks;
+  long long u;
+  // The next part before u1 (the first one, from u on, with `at_start`); false: none.
+  __device__ __forceinline__ bool next(const PagedParams& p, const int* at, int per, long long u1, bool at_start) {
+    if (u >= u1) return false;
+    if (!p.split) {
+      for (; u < u1; u += gridDim.x) {
+        b = (int)(u / per);
+        item = (int)(u - (long long)b * per);
+        chunks = at[b + 1] - at[b];
+        if (chunks > 0) break;
+      }
+      if (u >= u1) return false;
+      c0 = 0;
+      c1 = chunks;
+      u += gridDim.x;
+      return true;
+    }
+    if (at_start) {
+      int lo = 0, hi = p.B;   // the last sequence that starts at or before u has chunks
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)at[mid] * per <= u) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      chunks = at[b + 1] - at[b];
+      const long long rel = u - (long long)at[b] * per;
+      item = (int)(rel / chunks);
+      c0 = (int)(rel - (long long)item * chunks);
+    } else {   // the part before ended its item
+      c0 = 0;
+      if (++item == per) {
+        item = 0;
+        do ++b;
+        while (at[b + 1] == at[b]);
+        chunks = at[b + 1] - at[b];
+      }
+    }
+    c1 = (int)min((long long)chunks, c0 + (u1 - u));
+    u += c1 - c0;
+    return true;
+  }
+  // Keys [first, last) from the warp's first one on; its steps, CH keys apart.
+  template <typename C>
+  __device__ __forceinline__ int keys(const int* lens, int& first, int& last) const {
+    last = (int)min((long long)lens[b], (long long)c1 * C::CH);
+    first = (int)min((long long)c0 * C::CH + (threadIdx.x >> 5) * C::KT, (long long)last);
+    return (last - first + C::CH - 1) / C::CH;
+  }
+};
+
 template <int D, bool Q8, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3) : 2) paged_kernel(const PagedParams p, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v) {
@@ -243,11 +297,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
   __shared__ int part[4];
   __shared__ __align__(8) uint64_t full[4][C::NS];
   __shared__ int abort_flag;
+  __shared__ float2 sml[4][C::R];   // (max, sum) of the warps' rows
+  __shared__ int so_at[4];          // where their O lies in the ring (-1: no keys)
   uint8_t* ring = Q8 ? smem : smem_align<1024>(smem);
-  float* so = reinterpret_cast<float*>(ring);                         // [4][R][kPitch]
-  float2* sml = reinterpret_cast<float2*>(so + 4 * C::R * C::kPitch); // [4][R]
-  int* at = reinterpret_cast<int*>(ring + C::kRing);                  // [B + 1]
-  int* lens = at + kPagedSeqs + 1;                                    // [B]
+  int* at = reinterpret_cast<int*>(ring + C::kRing);   // [B + 1]
+  int* lens = at + kPagedSeqs + 1;                     // [B]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x, ctas = gridDim.x;
   if (threadIdx.x == 0) {
@@ -272,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
   // between an item's first and its last has a piece of it), or, not split, its items u, u +
   // ctas, ...
   const int used = (int)min(total, (long long)ctas);
-  long long u = p.split ? (cta < used ? total * cta / used : 0) : cta;
+  Part now;
+  now.u = p.split ? (cta < used ? total * cta / used : 0) : cta;
   const long long u1 = p.split ? (cta < used ? total * (cta + 1) / used : 0) : (long long)p.B * per;
   if (p.split && threadIdx.x == 0) p.ws_cut[cta] = make_int4(0, 0, 0, 0);
   // rows of sequences without keys
@@ -281,47 +336,68 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
       for (int i = threadIdx.x; i < p.H * D / 8; i += kThreads)
         *reinterpret_cast<uint4*>(p.o + (long long)b * p.H * D + 8 * i) = make_uint4(0, 0, 0, 0);
 
+  // Copies of a warp's steps run ahead of their use by the stages of its ring, into the
+  // parts that come next as well.
   uint8_t* mine = ring + warp * C::NS * 2 * C::kHalf;
   int put = 0, get = 0;             // stages to fill and to read next
   uint32_t phase = 0;               // of the stage to read next
-  bool ok = true;
-  while (u < u1) {
-    // the item, and its chunks [c0, c1)
-    int b, item;
-    long long c0, c1, chunks;
-    if (p.split) {
-      int lo = 0, hi = p.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)at[mid] * per <= u) lo = mid;
-        else hi = mid;
+  uint32_t kept = 0;                // groups that are there, a byte a stage
+  Part ahead = now;
+  Rows<C> rows;
+  int in_hk = 0, in_step = 0, in_steps = 0;
+  bool in_more = ahead.next(p, at, per, u1, true);
+  now = ahead;
+  auto open = [&]() {   // the next part with keys for this warp
+    while (in_more) {
+      in_steps = ahead.template keys<C>(lens, rows.first, rows.last);
+      in_step = 0;
+      if (in_steps > 0) {
+        in_hk = ahead.item / p.rtiles;
+        rows.table = p.table + (long long)ahead.b * p.W;
+        rows.fetch(p, 0);
+        return;
       }
-      b = lo;
-      chunks = at[b + 1] - at[b];
-      const long long rel = u - (long long)at[b] * per;
-      item = (int)(rel / chunks);
-      c0 = rel % chunks;
-      c1 = min(chunks, c0 + (u1 - u));
-      u += c1 - c0;
-    } else {
-      b = (int)(u / per);
-      item = (int)(u % per);
-      chunks = at[b + 1] - at[b];
-      c0 = 0;
-      c1 = chunks;
-      u += ctas;
-      if (chunks == 0) continue;
+      in_more = ahead.next(p, at, per, u1, false);
     }
-    const int hk = item / p.rtiles, row0 = item % p.rtiles * C::R;   // query heads hk G + row0 ...
-    Rows<C> rows;
-    rows.table = p.table + (long long)b * p.W;
-    rows.last = (int)min((long long)lens[b], c1 * C::CH);
-    rows.first = (int)min(c0 * C::CH + warp * C::KT, (long long)rows.last);
-    const int steps = (rows.last - rows.first + C::CH - 1) / C::CH;   // of this warp
-    rows.fetch(p, 0);
+  };
+  // A step's copies: its groups of K, then of V (fp16: of each half of the head dim).
+  auto issue = [&]() {
+    if (!in_more) return;
+    const int in = in_step % Rows<C>::kSteps;
+    if (in == 0) rows.advance(p, in_step);
+    const int i = lane % C::GR;
+    const int id = __shfl_sync(0xffffffffu, rows.page_id, in * C::GR + i);
+    const int place = __shfl_sync(0xffffffffu, rows.place, in * C::GR + i);
+    const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & ((1u << C::GR) - 1);
+    kept = (kept & ~(0xFFu << (8 * put))) | (there << (8 * put));
+    uint64_t* bar = &full[warp][put];
+    uint8_t* dst = mine + put * 2 * C::kHalf;
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * 16 * C::RB);
+    __syncwarp();
+    if (lane < C::kCopies && id >= 0) {
+      const int part_no = lane / C::GR;
+      if constexpr (Q8) {
+        const long long row = ((long long)id * p.Hkv + in_hk) * p.page + place;
+        bulk_load(dst + part_no * C::kHalf + i * 8 * C::RB, (part_no ? p.v : p.k) + row * C::RB, 8 * C::RB, bar);
+      } else {
+        const int is_v = part_no / (D / 64), half = part_no % (D / 64);
+        tma_load_3d(dst + is_v * C::kHalf + half * C::KT * 128 + i * 1024, is_v ? &tm_v : &tm_k, bar, 64 * half, place,
+                    id * p.Hkv + in_hk);
+      }
+    }
+    put = put + 1 == C::NS ? 0 : put + 1;
+    if (++in_step == in_steps) {
+      in_more = ahead.next(p, at, per, u1, false);
+      open();
+    }
+  };
+  bool more = in_more, ok = true;
+  open();
+  for (int i = 0; i < C::NS; ++i) issue();
 
+  uint32_t qf[NT][C::QS][2];
+  auto load_q = [&](int b, int hk, int row0) {
     // Q fragments: column g is query head row0 + 8 n + g
-    uint32_t qf[NT][C::QS][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = row0 + 8 * n + g;
@@ -359,39 +435,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
       }
     }
 
-    Acc<D, NT> acc;
+  };
+  if (more) load_q(now.b, now.item / p.rtiles, now.item % p.rtiles * C::R);
+
+  Acc<D, NT> acc;
+  while (more) {
+    const int hk = now.item / p.rtiles, row0 = now.item % p.rtiles * C::R;   // query heads hk G + row0 ...
+    int first, last;
+    const int steps = now.template keys<C>(lens, first, last);
     acc.clear();
-    rows.advance(p, 0);
-    // A step's copies: its groups of K, then of V (fp16: of each half of the head dim).
-    // Groups that are there are kept for the step's turn, a byte a stage.
-    uint32_t kept = 0;
-    auto issue = [&](int step) {
-      const int in = step % Rows<C>::kSteps;
-      if (in == 0 && step > 0) rows.advance(p, step);
-      const int i = lane % C::GR;
-      const int id = __shfl_sync(0xffffffffu, rows.page_id, in * C::GR + i);
-      const int place = __shfl_sync(0xffffffffu, rows.place, in * C::GR + i);
-      const uint32_t there = __ballot_sync(0xffffffffu, id >= 0) & ((1u << C::GR) - 1);
-      kept = (kept & ~(0xFFu << (8 * put))) | (there << (8 * put));
-      uint64_t* bar = &full[warp][put];
-      uint8_t* dst = mine + put * 2 * C::kHalf;
-      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * 16 * C::RB);
-      __syncwarp();
-      if (lane < C::kCopies && id >= 0) {
-        const int part_no = lane / C::GR;
-        if constexpr (Q8) {
-          const long long row = ((long long)id * p.Hkv + hk) * p.page + place;
-          bulk_load(dst + part_no * C::kHalf + i * 8 * C::RB, (part_no ? p.v : p.k) + row * C::RB, 8 * C::RB, bar);
-        } else {
-          const int is_v = part_no / (D / 64), half = part_no % (D / 64);
-          tma_load_3d(dst + is_v * C::kHalf + half * C::KT * 128 + i * 1024, is_v ? &tm_v : &tm_k, bar, 64 * half,
-                      place, id * p.Hkv + hk);
-        }
-      }
-      put = put + 1 == C::NS ? 0 : put + 1;
-    };
-    int issued = min(steps, C::NS);
-    for (int i = 0; i < issued; ++i) issue(i);
+    int slot = 0;
 #pragma unroll 1
     for (int step = 0; step < steps; ++step) {
       ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][get], phase, ctl));
@@ -399,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
       const uint8_t* kt = mine + get * 2 * C::kHalf;
       const uint8_t* vt = kt + C::kHalf;
       const uint32_t there = (kept >> (8 * get)) & 0xFFu;
-      const int left = rows.last - (rows.first + step * C::CH);   // keys from the step's first on
+      const int left = last - (first + step * C::CH);   // keys from the step's first on
       const bool all = there == (1u << C::GR) - 1 && left >= C::KT;
       float s[C::KS][NT][4];
 #pragma unroll
@@ -550,71 +603,73 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
         }
       }
       __syncwarp();   // the stage has been read
+      slot = get;
       get = get + 1 == C::NS ? 0 : get + 1;
       phase ^= get == 0;
-      if (issued < steps) issue(issued++);
+      if (step + 1 < steps) issue();   // (the last stage first takes O)
     }
-    if (!ok) {
-      // copies still under way land before the block leaves
-      for (int i = 0; i < C::NS; ++i) {
-        mbar_wait_drain(&full[warp][get], phase, 100000000ull);
-        get = get + 1 == C::NS ? 0 : get + 1;
-        phase ^= get == 0;
-      }
-    }
-    __syncthreads();   // the ring is idle: O goes there
-
-    // The four warps' maxima, sums and O.
+    // The four warps' maxima, sums and O (each row's head dims in an order of its own, by
+    // bits 1 and 2 of the row, so that the threads of a quad write to different banks).
+    if (lane == 0) so_at[warp] = steps > 0 ? (int)(mine - ring) + slot * 2 * C::kHalf : -1;
+    if (steps > 0) {
+      float* so = reinterpret_cast<float*>(mine + slot * 2 * C::kHalf);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float l = acc.l[n][c];
+        for (int c = 0; c < 2; ++c) {
+          float l = acc.l[n][c];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        const int r = warp * C::R + 8 * n + 2 * t + c;
-        if (g == 0) sml[r] = make_float2(acc.m[n][c], l);
+          for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          const int r = 8 * n + 2 * t + c;
+          if (g == 0) sml[warp][r] = make_float2(acc.m[n][c], l);
 #pragma unroll
-        for (int i = 0; i < C::QS; ++i) {
-          int d;   // of the fragment's row g; row g + 8 is d + 1 (fp16: d + 8)
-          if constexpr (!Q8) {
-            d = 16 * i + g;
-          } else if constexpr (D == 128) {
-            const int sh = 2 + 2 * (g >> 1), w = i >> 1, half = i & 1;
-            if (w < 2) d = 4 * (w + 2) - sh + 2 * half;
-            else if (w == 2) d = (g < 4 ? 4 : 16) - sh + 2 * half;
-            else d = (g & 2) ? 12 + 2 * half : 14 * half;
-            d += 16 * g;
-          } else {
-            const int w = i >> 1, half = i & 1;
-            if (w == 0) d = (g < 4 ? 2 : 0) + 2 * half;
-            else d = g < 4 ? 6 * half : 4 + 2 * half;
-            d += 8 * g;
-          }
-          if constexpr (Q8) {
-            *reinterpret_cast<float2*>(so + r * C::kPitch + d) = make_float2(acc.o[n][i][c], acc.o[n][i][2 + c]);
-          } else {
-            so[r * C::kPitch + d] = acc.o[n][i][c];
-            so[r * C::kPitch + d + 8] = acc.o[n][i][2 + c];
+          for (int i = 0; i < C::QS; ++i) {
+            int d;   // of the fragment's row g; row g + 8 is d + 1 (fp16: d + 8)
+            if constexpr (!Q8) {
+              d = 16 * i + g;
+            } else if constexpr (D == 128) {
+              const int sh = 2 + 2 * (g >> 1), w = i >> 1, half = i & 1;
+              if (w < 2) d = 4 * (w + 2) - sh + 2 * half;
+              else if (w == 2) d = (g < 4 ? 4 : 16) - sh + 2 * half;
+              else d = (g & 2) ? 12 + 2 * half : 14 * half;
+              d += 16 * g;
+            } else {
+              const int w = i >> 1, half = i & 1;
+              if (w == 0) d = (g < 4 ? 2 : 0) + 2 * half;
+              else d = g < 4 ? 6 * half : 4 + 2 * half;
+              d += 8 * g;
+            }
+            if constexpr (Q8) {
+              *reinterpret_cast<float2*>(so + r * D + (d ^ (8 * t))) = make_float2(acc.o[n][i][c], acc.o[n][i][2 + c]);
+            } else {
+              so[r * D + (d ^ (8 * t))] = acc.o[n][i][c];
+              so[r * D + ((d + 8) ^ (8 * t))] = acc.o[n][i][2 + c];
+            }
           }
         }
-      }
+    }
+    // the next part, its queries on their way
+    const Part was = now;
+    more = now.next(p, at, per, u1, false);
+    if (more) load_q(now.b, now.item / p.rtiles, now.item % p.rtiles * C::R);
     ok = __syncthreads_and(ok);
     if (!ok) break;
-    const bool whole = c0 == 0 && c1 == chunks;
-    const int piece = kPiece * cta + (c0 == 0 ? 1 : 0);
+    const bool whole = was.c0 == 0 && was.c1 == was.chunks;
+    const int piece = kPiece * cta + (was.c0 == 0 ? 1 : 0);
     for (int i = threadIdx.x; i < C::R * D / 4; i += kThreads) {
       const int r = i / (D / 4), d = i % (D / 4) * 4, q = row0 + r;
       if (q >= p.G) break;
       float m = kLowest, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w * C::R + r].x);
+      for (int w = 0; w < 4; ++w)
+        if (so_at[w] >= 0) m = fmaxf(m, sml[w][r].x);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float2 ml = sml[w * C::R + r];
+        if (so_at[w] < 0) continue;
+        const float2 ml = sml[w][r];
         const float f = fast_exp2(ml.x - m);
-        const float4 x = *reinterpret_cast<const float4*>(so + (w * C::R + r) * C::kPitch + d);
+        const float4 x = *reinterpret_cast<const float4*>(ring + so_at[w] + 4 * (r * D + (d ^ (8 * ((r >> 1) & 3)))));
         l += f * ml.y;
         o.x += f * x.x;
         o.y += f * x.y;
@@ -623,22 +678,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
       }
       if (whole) {
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // NaN stays
-        if (in_bounds(hk * p.G + q < p.H && b < p.B, p.status, kSitePagedO))
-          *reinterpret_cast<uint2*>(p.o + ((long long)b * p.H + hk * p.G + q) * D + d) =
+        if (in_bounds(hk * p.G + q < p.H && was.b < p.B, p.status, kSitePagedO))
+          *reinterpret_cast<uint2*>(p.o + ((long long)was.b * p.H + hk * p.G + q) * D + d) =
               make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
       } else if (in_bounds(piece < kPiece * ctas, p.status, kSitePagedWs)) {
         *reinterpret_cast<float4*>(p.ws_o + ((long long)piece * C::R + r) * D + d) = o;
         if (d == 0) p.ws_ml[piece * C::R + r] = make_float2(m, l);
       }
     }
-    if (!whole && c0 == 0 && threadIdx.x == 0) {
+    if (!whole && was.c0 == 0 && threadIdx.x == 0) {
       // the CTA of the item's last chunk; this one has its first
-      const long long end = (long long)at[b] * per + (long long)(item + 1) * chunks - 1;
-      const int last = (int)(((end + 1) * used - 1) / total);
-      p.ws_cut[cta] = make_int4(b, item, last, 1);
+      const long long end = (long long)at[was.b] * per + (long long)(was.item + 1) * was.chunks - 1;
+      const int last_cta = (int)(((end + 1) * used - 1) / total);
+      p.ws_cut[cta] = make_int4(was.b, was.item, last_cta, 1);
     }
-    fence_proxy_async_smem();   // the ring's next copies come after these reads and writes
+    fence_proxy_async_smem();   // the stage's next copies come after these reads and writes
     __syncthreads();
+    if (steps > 0) issue();
+  }
+  // given up: copies still under way land before the block leaves
+  for (int i = 0; !ok && i < C::NS; ++i) {
+    mbar_wait_drain(&full[warp][get], phase, 100000000ull);
+    get = get + 1 == C::NS ? 0 : get + 1;
+    phase ^= get == 0;
   }
 }
 

@@ -1101,7 +1101,7 @@ PagedPlan paged_plan(bool q8, int64_t B, int64_t H, int64_t Hkv, int64_t page, i
   if (t.seqs > fit) t.seqs = (int)fit;
   const int64_t items = (int64_t)t.seqs * Hkv * t.rtiles;
   const int64_t most = (int64_t)sms * m4q::paged_ctas(G, (int)D, q8);
-  t.split = chunks > 1;
+  t.split = (float)chunks > m4q::paged_join((int)D, q8);   // short sequences stay whole
   t.whole = (int)(items < most ? items : most);
   t.grid = !t.split ? t.whole : (int)(chunks > most / items ? most : items * chunks);
   t.ws_ml = ((size_t)t.grid * sizeof(int4) + 255) / 256 * 256;
@@ -1165,6 +1165,7 @@ int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_co
   p.scale_log2 = scale_log2;
   p.rtiles = t.rtiles;
   p.split = t.split ? 1 : 0;
+  p.join = m4q::paged_join((int)D, q8);
   if (t.split) {
     char* ws = static_cast<char*>(workspace);
     p.ws_cut = reinterpret_cast<int4*>(ws);

@@ -95,7 +95,7 @@ struct Cfg {
   static constexpr int CH = 4 * KT;                     // keys of a chunk
   static constexpr int QS = D / 16;                     // k16 steps of S, and m16 tiles of O
   static constexpr int R = 8 * NT;                      // query rows of an item
-  static constexpr int NS = Q8 && D == 128 ? 2 : 3;                 // steps of a warp in its ring
+  static constexpr int NS = (Q8 && D == 128) || (!Q8 && NT == 1) ? 2 : 3;                 // steps of a warp in its ring
   static constexpr int kHalf = KT * RB;                 // K rows of a step, then V rows
   static constexpr int kRing = 4 * NS * 2 * kHalf;
   static constexpr int kCopies = 2 * GR * (Q8 ? 1 : D / 64);   // copies of a step, a lane each
@@ -180,16 +180,18 @@ __device__ __forceinline__ void softmax_step(float (&s)[KS][NT][4], Acc<D, NT>& 
 }
 
 // Where the chunks of the sequences begin, at[0 .. B], and their keys, in shared memory.
+// Returns the chunks of the longest.
 template <int CH>
-__device__ __forceinline__ void count_chunks(const PagedParams& p, int* at, int* lens, int (&part)[4]) {
+__device__ __forceinline__ int count_chunks(const PagedParams& p, int* at, int* lens, int2 (&part)[4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int each = (p.B + kThreads - 1) / kThreads, first = threadIdx.x * each;
-  int sum = 0;
+  int sum = 0, longest = 0;
   for (int i = first; i < min(first + each, p.B); ++i) {
     const int n = min(max(p.lengths[i], 0), p.W * p.page);
     lens[i] = n;
     at[i] = sum;
     sum += (n + CH - 1) / CH;
+    longest = max(longest, (n + CH - 1) / CH);
   }
   int in = sum;
 #pragma unroll
@@ -197,12 +199,17 @@ __device__ __forceinline__ void count_chunks(const PagedParams& p, int* at, int*
     const int y = __shfl_up_sync(0xffffffffu, in, o);
     if (lane >= o) in += y;
   }
-  if (lane == 31) part[warp] = in;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) part[warp] = make_int2(in, longest);
   __syncthreads();
-  for (int w = 0; w < warp; ++w) in += part[w];
+  for (int w = 0; w < 4; ++w) {
+    if (w < warp) in += part[w].x;
+    longest = max(longest, part[w].y);
+  }
   for (int i = first; i < min(first + each, p.B); ++i) at[i] += in - sum;
   if (threadIdx.x == kThreads - 1) at[p.B] = in;
   __syncthreads();
+  return longest;
 }
 
 // Rows of a warp's groups of 8 keys, 32 groups at a time: lane l holds page and place of
@@ -235,14 +242,14 @@ struct Rows {
 };
 
 // A part of an item that a CTA takes: chunks [c0, c1) of `chunks`.  u: where the CTA goes
-// on, as a chunk of all (split) or an item.
+// on, as a chunk of all (cut) or an item.
 struct Part {
   int b, item, c0, c1, chunks;
   long long u;
   // The next part before u1 (the first one, from u on, with `at_start`); false: none.
-  __device__ __forceinline__ bool next(const PagedParams& p, const int* at, int per, long long u1, bool at_start) {
+  __device__ __forceinline__ bool next(const PagedParams& p, const int* at, int per, long long u1, bool cut, bool at_start) {
     if (u >= u1) return false;
-    if (!p.split) {
+    if (!cut) {
       for (; u < u1; u += gridDim.x) {
         b = (int)(u / per);
         item = (int)(u - (long long)b * per);
@@ -290,11 +297,11 @@ struct Part {
 };
 
 template <int D, bool Q8, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3) : 2) paged_kernel(const PagedParams p, const __grid_constant__ CUtensorMap tm_k,
+__global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 2) paged_kernel(const PagedParams p, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D, Q8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int part[4];
+  __shared__ int2 part[4];
   __shared__ __align__(8) uint64_t full[4][C::NS];
   __shared__ int abort_flag;
   __shared__ float2 sml[4][C::R];   // (max, sum) of the warps' rows
@@ -318,17 +325,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
   const DecK dk = make_deck();
   pdl_launch_dependents();
   pdl_wait();
-  count_chunks<C::CH>(p, at, lens, part);
+  const int longest = count_chunks<C::CH>(p, at, lens, part);
 
   const int per = p.Hkv * p.rtiles;                  // items of a sequence
   const long long total = (long long)at[p.B] * per;
+  // Dealt out evenly, or item by item where that loses less than the join costs.
+  const int waves = (int)(((long long)p.B * per + ctas - 1) / ctas);
+  const bool cut = p.split && (float)waves * longest > 1.5f * (float)total / ctas + p.join;
   // this CTA's chunks [u, u1) of all (none for those past the chunks' number: every CTA
-  // between an item's first and its last has a piece of it), or, not split, its items u, u +
+  // between an item's first and its last has a piece of it), or, not cut, its items u, u +
   // ctas, ...
   const int used = (int)min(total, (long long)ctas);
   Part now;
-  now.u = p.split ? (cta < used ? total * cta / used : 0) : cta;
-  const long long u1 = p.split ? (cta < used ? total * (cta + 1) / used : 0) : (long long)p.B * per;
+  now.u = cut ? (cta < used ? total * cta / used : 0) : cta;
+  const long long u1 = cut ? (cta < used ? total * (cta + 1) / used : 0) : (long long)p.B * per;
   if (p.split && threadIdx.x == 0) p.ws_cut[cta] = make_int4(0, 0, 0, 0);
   // rows of sequences without keys
   for (int b = cta; b < p.B; b += ctas)
@@ -345,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
   Part ahead = now;
   Rows<C> rows;
   int in_hk = 0, in_step = 0, in_steps = 0;
-  bool in_more = ahead.next(p, at, per, u1, true);
+  bool in_more = ahead.next(p, at, per, u1, cut, true);
   now = ahead;
   auto open = [&]() {   // the next part with keys for this warp
     while (in_more) {
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
         rows.fetch(p, 0);
         return;
       }
-      in_more = ahead.next(p, at, per, u1, false);
+      in_more = ahead.next(p, at, per, u1, cut, false);
     }
   };
   // A step's copies: its groups of K, then of V (fp16: of each half of the head dim).
@@ -387,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
     }
     put = put + 1 == C::NS ? 0 : put + 1;
     if (++in_step == in_steps) {
-      in_more = ahead.next(p, at, per, u1, false);
+      in_more = ahead.next(p, at, per, u1, cut, false);
       open();
     }
   };
@@ -650,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
     }
     // the next part, its queries on their way
     const Part was = now;
-    more = now.next(p, at, per, u1, false);
+    more = now.next(p, at, per, u1, cut, false);
     if (more) load_q(now.b, now.item / p.rtiles, now.item % p.rtiles * C::R);
     ok = __syncthreads_and(ok);
     if (!ok) break;
@@ -704,22 +714,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (!Q8 ? 2 : D == 64 ? 4 : 3
   }
 }
 
-// The pieces of an item that was cut: x the CTA that has its first chunk, y the query
-// row.  Eight warps take every eighth piece each.
+// The pieces of an item that was cut: x the CTA that has its first chunk, y the query rows,
+// `slices` warps a row, which take every slices-th piece each.
 template <int D, int R>
-__global__ void __launch_bounds__(256) join_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(256) join_kernel(const PagedParams p, int slices) {
   __shared__ float so[8][D];
-  __shared__ float sl[8], sm[8];
+  __shared__ float2 sml[8];
   constexpr int E = D / 32;
+  // No early launch_dependents: a kernel of persistent CTAs that started beside these would
+  // find its places on the SMs taken unevenly (86.6 us against 61 for 32 sequences over
+  // Q8_0 pages).
   pdl_wait();
   const int4 cut = p.ws_cut[blockIdx.x];
   if (!cut.w) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * (8 / slices) + warp / slices;
   const int hk = cut.y / p.rtiles, q = cut.y % p.rtiles * R + r;
-  if (q >= p.G) return;
-  const int first = blockIdx.x, n = cut.z - first + 1;
+  const int first = blockIdx.x, n = r < R && q < p.G ? cut.z - first + 1 : 0;
   float m = kLowest, l = 0.f, o[E] = {};
-  for (int i = warp; i < n; i += 8) {
+#pragma unroll 4
+  for (int i = warp % slices; i < n; i += slices) {
     const long long at = (long long)(kPiece * (first + i) + (i == 0 ? 1 : 0)) * R + r;
     const float2 ml = p.ws_ml[at];
     float x[E];
@@ -731,26 +745,27 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedParams p) {
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = o[e] * f + x[e] * h;
   }
+  if (slices > 1) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp % slices) return;
+    for (int w = warp + 1; w < warp + slices; ++w) {
+      const float2 ml = sml[w];
+      const float top = fmaxf(m, ml.x), f = fast_exp2(m - top), h = fast_exp2(ml.x - top);
+      m = top;
+      l = l * f + ml.y * h;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * f + so[w][lane + 32 * e] * h;
+    }
   }
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float top = kLowest, sum = 0.f, x = 0.f;
+  if (n == 0) return;
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+  if (!in_bounds(hk * p.G + q < p.H && cut.x < p.B, p.status, kSitePagedO)) return;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, sm[w]);
-#pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const float f = fast_exp2(sm[w] - top);
-    sum += f * sl[w];
-    x += f * so[w][threadIdx.x];
-  }
-  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-  if (in_bounds(hk * p.G + q < p.H && cut.x < p.B, p.status, kSitePagedO))
-    p.o[((long long)cut.x * p.H + hk * p.G + q) * D + threadIdx.x] = __float2half_rn(x * inv);
+  for (int e = 0; e < E; ++e)
+    p.o[((long long)cut.x * p.H + hk * p.G + q) * D + lane + 32 * e] = __float2half_rn(o[e] * inv);
 }
 
 template <int D, bool Q8, int NT>
@@ -769,16 +784,20 @@ cudaError_t launch(const PagedParams& p, const CUtensorMap& tm_k, const CUtensor
   }
   e = launch_proj(kern, (unsigned)grid, (unsigned)kThreads, C::kSmem, s, 1u, p, tm_k, tm_v);
   if (e != cudaSuccess || !p.split) return e;
+  // Pieces of an item: few in a batch (a warp a row takes them all), many of a long sequence.
+  const int items = p.B * p.Hkv * p.rtiles, pieces = grid / items + 2;
+  const int slices = pieces <= 4 ? 1 : pieces <= 12 ? 4 : 8;
+  const int rows = p.G < C::R ? p.G : C::R, each = 8 / slices;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.G < C::R ? p.G : C::R), 1);
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((rows + each - 1) / each), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, C::R>, p);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, C::R>, p, slices);
 }
 
 template <int D, bool Q8>

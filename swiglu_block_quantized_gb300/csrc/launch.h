@@ -270,7 +270,9 @@ struct PagedParams {
   int B, H, Hkv, G, P, page, W, D;
   float scale_log2;       // softmax scale * log2(e)
   int rtiles;             // items of a sequence and KV head: ceil(G / rows of an item)
-  int split;              // chunks are dealt out evenly over the CTAs, pieces of items joined
+  int split;              // chunks may be dealt out evenly over the CTAs, pieces of items joined
+  float join;             // (on the device: where an item's chunks, as often as a CTA takes one, are
+                          // this many more than 1.5 times a CTA's share of all)
   int4* ws_cut;           // [grid] of the item cut whose first chunk is the CTA's: sequence, item, last CTA, 1
   float2* ws_ml;          // [2 grid][rows] (max, sum) of a piece
   float* ws_o;            // [2 grid][rows][D] its unnormalised O
@@ -280,7 +282,8 @@ struct PagedParams {
 // warp, 8 of fp16), and CTAs an SM.
 constexpr int paged_rows(int G) { return G <= 8 ? 8 : 16; }
 constexpr int paged_chunk(int D, bool q8) { return q8 ? 128 : 8192 / D; }
-constexpr int paged_ctas(int G, int D, bool q8) { return G > 8 || !q8 ? 2 : D == 64 ? 4 : 3; }
+constexpr int paged_ctas(int G, int D, bool q8) { return G > 8 ? 2 : q8 && D == 64 ? 4 : 3; }
+constexpr float paged_join(int D, bool q8) { return q8 ? 4.f : D == 64 ? 6.f : 7.f; }
 // tm_k, tm_v: [P Hkv][page][D] of fp16 pools, boxes of [1][8 rows][64 d], 128-byte swizzle
 // (not read for Q8_0).
 cudaError_t launch_attention_paged(const PagedParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,

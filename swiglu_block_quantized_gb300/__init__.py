@@ -824,7 +824,7 @@ def page_plan(past, new, table, held, free, n_free, page: int, tokens: int, out=
                               p + 8 * tokens, p + 8 * tokens + 4 * b, _raw_stream(stream, dev))
     if rc:
         raise M4QError(rc, "m4q_page_plan")
-    return out.split((tokens, tokens, b, b + 1))
+    return _torch.split_with_sizes(out, (tokens, tokens, b, b + 1))
 
 
 def attention_paged(q, kc, vc, kv_codec: int, table, lengths, scale: float | None = None, out=None, workspace=None,
@@ -935,7 +935,7 @@ def verify_tree(target, draft, tokens, parents, u, out=None, stream=None):
                                     p + 4 * b * (n + 1), _raw_stream(stream, dev))
         if rc:
             raise M4QError(rc, "m4q_verify_tree")
-    path, count, token = out.split((b * n, b, b))
+    path, count, token = _torch.split_with_sizes(out, (b * n, b, b))
     return path.view(b, n), count, token
 
 

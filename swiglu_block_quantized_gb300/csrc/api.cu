@@ -1076,7 +1076,12 @@ int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t 
   p.P = (int)P;
   p.page = (int)page;
   p.T = (int)T;
-  return done(m4q::launch_page_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+  // A token a thread up to eight CTAs of 1024 (and no more threads than there is work for).
+  p.ctas = 1;
+  while (p.ctas < 8 && T > 1024 * p.ctas) p.ctas *= 2;
+  const int64_t work = T > B ? T : B;
+  const int threads = work >= 1024 ? 1024 : (int)((work + 127) / 128 * 128);
+  return done(m4q::launch_page_plan(p, threads, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -1217,6 +1222,12 @@ int m4q_verify_tree(const void* target, int64_t t_seq_stride, int64_t t_row_stri
   p.B = (int)B;
   p.N = (int)N;
   p.V = (int)V;
+  // CTAs of a sequence: as many as fit the device at once, two an SM, each with at least
+  // 4,096 values (12.1 us with 16, 14.7 with 8 and 52.6 with 1 for one sequence over 128,000
+  // values; 28.5 with 8, 38.5 with 4 and 37.1 with 16 for 32; 8.3 with 1, 9.0 with 2 for 16
+  // over 4,000).
+  p.ctas = 1;
+  while (p.ctas < 16 && p.ctas * B <= dev.sms && V > 4096 * p.ctas) p.ctas *= 2;
   return done(m4q::launch_verify(p, prob_type == M4Q_PROB_F16, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -139,18 +139,6 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
   pdl_launch_dependents();
   pdl_wait();
   const UnitAt at = unit_at(u, p.rot, p.interleaved);
-  Turn8 t;
-  if (ok && at.turns && h0 < p.H + p.Hkv) {
-    int pos = AX ? 0 : p.pos[m];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (AX) {
-        const int a = p.axes[8 * u + i];
-        pos = (unsigned)a < (unsigned)p.A ? p.pos[(long long)a * p.M + m] : 0;
-      }
-      turn(pos, __ldg(reinterpret_cast<const long long*>(p.freqs) + 8 * u + i), p.mscale, t.c[i], t.s[i]);
-    }
-  }
   long long row = -1;                        // this token's cache row of head 0, or -1
   if (ok && h1 > p.H) {
     const int slot = p.slots[m];
@@ -169,7 +157,19 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
     }
   };
   uint4 n0, n1;
-  fetch(h0, n0, n1);
+  fetch(h0, n0, n1);   // (on their way while the angles are formed)
+  Turn8 t;
+  if (ok && at.turns && h0 < p.H + p.Hkv) {
+    int pos = AX ? 0 : p.pos[m];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (AX) {
+        const int a = p.axes[8 * u + i];
+        pos = (unsigned)a < (unsigned)p.A ? p.pos[(long long)a * p.M + m] : 0;
+      }
+      turn(pos, __ldg(reinterpret_cast<const long long*>(p.freqs) + 8 * u + i), p.mscale, t.c[i], t.s[i]);
+    }
+  }
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
     const bool isq = h < p.H, isv = h >= p.H + p.Hkv;

@@ -304,9 +304,10 @@ struct PlanParams {
   int32_t* lengths;       // [B]
   int32_t* starts;        // [B + 1]
   int B, W, P, page, T;
+  int ctas;               // of the cluster: 1, 2, 4 or 8
   uint32_t* status;
 };
-cudaError_t launch_page_plan(const PlanParams& p, cudaStream_t s);
+cudaError_t launch_page_plan(const PlanParams& p, int threads, cudaStream_t s);
 
 // verify.cu: drafted trees verified against the target's probabilities.
 constexpr int kVerifyNodes = 256;
@@ -321,6 +322,7 @@ struct VerifyParams {
   int32_t* count;         // [B]
   int32_t* token;         // [B]
   int B, N, V;
+  int ctas;               // of a sequence's cluster: 1, 2, 4, 8 or 16
   uint32_t* status;
 };
 cudaError_t launch_verify(const VerifyParams& p, bool f16, cudaStream_t s);

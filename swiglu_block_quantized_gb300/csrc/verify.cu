@@ -11,8 +11,13 @@
 //
 // Decisions stand beside borders, so every difference p - M q and every sum over a row
 // is a pair of fp32 values (their exact sum and what its rounding lost: TwoSum, and a
-// product's error by fma), good to 2^-45; 64-bit floats would cost more than the
-// reading: 16 of them an SM and clock at most.
+// product's error by fma), good to 2^-45; the 64-bit units would need ten times as long.
+//
+// A sequence is one cluster of CTAs.  All of them walk its nodes (one thread, from
+// shared memory; the drafted tokens' p and q are gathered ahead); a row's sum is formed
+// by strips, a CTA's and then a warp's, and the CTAs' sums are exchanged through
+// distributed shared memory in a fixed order.  The CTA in whose strip the next token lies
+// sums its warp's strip again by finer strips, then scans the one that holds it.
 #include "kv_common.cuh"
 #include "launch.h"
 
@@ -20,7 +25,8 @@ namespace m4q {
 
 namespace {
 
-constexpr int kThreads = 1024, kVWarps = kThreads / 32;
+constexpr int kThreads = 512, kVWarps = kThreads / 32;
+constexpr int kBatch = 2;   // 16-byte vectors of p and of q that a thread has on their way
 
 struct Two {   // hi + lo, |lo| within an ulp of hi
   float hi, lo;
@@ -65,20 +71,27 @@ __device__ __forceinline__ float load(const float* p) { return prob(*p); }
 __device__ __forceinline__ float load(const __half* p) { return prob(__half2float(*p)); }
 
 // A row's rest r(x) = max(p(x) - M q(x), 0).
+__device__ __forceinline__ Two rest_of(float a, float b, float mh, float ml) {
+  const float ph = __fmul_rn(mh, b);
+  const float pl = __fmaf_rn(ml, b, __fmaf_rn(mh, b, -ph));   // mh b + ml b - ph
+  const Two d = two_sum(a, -ph);
+  const Two r = quick(d.hi, __fadd_rn(d.lo, -pl));
+  return r.hi > 0.f ? r : Two{0.f, 0.f};
+}
 template <typename T>
 struct Rest {
   const T* p;
   const T* q;
   float mh, ml;   // M; 0: q is not read
+  // Elements from the 16-byte boundary at or before the row to its start: vectors are cut
+  // by p's, q's are read as such where it lies alike (rows of one layout do).
+  __device__ __forceinline__ int skew() const { return (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T)); }
+  __device__ __forceinline__ bool alike() const {
+    return ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+  }
   __device__ __forceinline__ Two operator()(int x) const {
     const float a = load(p + x);
-    if (mh == 0.f) return {a, 0.f};
-    const float b = load(q + x);
-    const float ph = __fmul_rn(mh, b);
-    const float pl = __fmaf_rn(ml, b, __fmaf_rn(mh, b, -ph));   // mh b + ml b - ph
-    const Two d = two_sum(a, -ph);
-    const Two r = quick(d.hi, __fadd_rn(d.lo, -pl));
-    return r.hi > 0.f ? r : Two{0.f, 0.f};
+    return mh == 0.f ? Two{a, 0.f} : rest_of(a, load(q + x), mh, ml);
   }
 };
 
@@ -86,30 +99,86 @@ struct Shared {
   int par[kVerifyNodes], path[kVerifyNodes];
   float p[kVerifyNodes], q[kVerifyNodes], u[kVerifyNodes];
   Two sum[kVWarps];
-  Two total;
+  Two mine[2];       // the CTA's sum of a pass, for the others (two passes' in turn)
+  Two total, aim;    // of the row; what the next token's running sum has to exceed, in its CTA
+  int rank;          // that CTA
   int node, count, next, pass;
   double off, mass;
   int strip;
-  Two aim;
 };
+
+// The 16 bytes of a row from value x on, those outside [a, e) 0: one load where all of
+// them are inside and aligned.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T* row, int x, int a, int e, bool vec) {
+  constexpr int W = 16 / sizeof(T);
+  if (vec && x >= a && x + W <= e) return *reinterpret_cast<const uint4*>(row + x);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (x + i >= a && x + i < e) {
+      if constexpr (sizeof(T) == 4) w[i] = reinterpret_cast<const uint32_t*>(row)[x + i];
+      else w[i / 2] |= (uint32_t) reinterpret_cast<const unsigned short*>(row)[x + i] << (16 * (i & 1));
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Probability i of a vector.
+template <typename T>
+__device__ __forceinline__ float value(const uint4& v, int i) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(T) == 4) return prob(__uint_as_float(w[i]));
+  else return prob(__half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i & 1))))));
+}
 
 // Sums of r over the strips [lo + w step, lo + (w + 1) step) of [lo, hi), one a warp.
 template <typename T>
 __device__ void strips(const Rest<T>& r, int lo, int hi, int step, Shared& s) {
+  constexpr int W = 16 / sizeof(T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long a = lo + (long long)warp * step;
-  const int e = (int)min((long long)hi, a + step);
+  const int a = min(lo + warp * step, hi), e = min(hi, a + step), skew = r.skew();
+  const bool alike = r.alike();
   Two acc = {0.f, 0.f};
   float low = 0.f;
-  for (long long x = a + lane; x < e; x += 32) {
-    const Two v = r((int)x);
-    const Two t = two_sum(acc.hi, v.hi);
-    acc.hi = t.hi;
-    low = __fadd_rn(low, __fadd_rn(t.lo, v.lo));
+  for (int x0 = (a + skew) / W * W - skew + lane * W; x0 < e; x0 += 32 * W * kBatch) {
+    uint4 p[kBatch], q[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) p[i] = load_vec(r.p, x0 + 32 * W * i, a, e, true);
+    if (r.mh != 0.f) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) q[i] = load_vec(r.q, x0 + 32 * W * i, a, e, alike);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const Two v = rest_of(value<T>(p[i], j), value<T>(q[i], j), r.mh, r.ml);
+          const Two t = two_sum(acc.hi, v.hi);
+          acc.hi = t.hi;
+          low = __fadd_rn(low, __fadd_rn(t.lo, v.lo));
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const Two t = two_sum(acc.hi, value<T>(p[i], j));
+          acc.hi = t.hi;
+          low = __fadd_rn(low, t.lo);
+        }
+    }
   }
   acc = warp_sum(quick(acc.hi, low));
   if (lane == 0) s.sum[warp] = acc;
   __syncthreads();
+}
+
+__device__ __forceinline__ Two peer(const Two* mine, uint32_t rank) {
+  Two v;
+  const uint32_t at = mapa_shared(smem_u32(mine), rank);
+  asm volatile("ld.shared::cluster.f32 %0, [%2];\n\tld.shared::cluster.f32 %1, [%2 + 4];"
+               : "=f"(v.hi), "=f"(v.lo)
+               : "r"(at)
+               : "memory");
+  return v;
 }
 
 // The first lane whose running sum of v exceeds `aim`, else the last with a value
@@ -127,9 +196,10 @@ __device__ __forceinline__ int pick(Two v, Two& aim, int lane) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams p) {
   __shared__ Shared s;
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ctas = p.ctas, rank = ctas > 1 ? (int)cluster_ctarank() : 0, b = blockIdx.x / ctas;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   pdl_wait();
   const T* target = static_cast<const T*>(p.target) + b * p.t_bs;
@@ -143,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
     if (tid > 0) {
       if (par < 0 || par >= tid || x < 0 || x >= p.V) {
         par = -2;
-      } else {
+      } else if (in_bounds(b < p.B && par < p.N, p.status, kSiteVerify)) {
         s.p[tid] = load(target + par * p.t_rs + x);
         s.q[tid] = load(draft + par * p.d_rs + x);
       }
@@ -152,16 +222,38 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
   }
   __syncthreads();
   if (s.par[0] != -1) {   // an unused sequence
-    if (tid < p.N) p.path[(long long)b * p.N + tid] = -1;
-    if (tid == 0) p.count[b] = 0, p.token[b] = -1;
+    if (rank == 0 && tid < p.N) p.path[(long long)b * p.N + tid] = -1;
+    if (rank == 0 && tid == 0) p.count[b] = 0, p.token[b] = -1;
     return;
   }
   if (tid == 0) {
     s.node = 0, s.count = 1, s.path[0] = 0, s.next = 1;
     s.off = 0., s.mass = 1.;
   }
-  const int step = ((p.V + kVWarps - 1) / kVWarps + 31) / 32 * 32;
+  // this CTA's strip of a row, and its warps'
+  const int step = ((p.V + ctas * kVWarps - 1) / (ctas * kVWarps) + 31) / 32 * 32;
+  const int first = min(rank * kVWarps * step, p.V), last = min(first + kVWarps * step, p.V);
   Rest<T> r;
+  int pass = 0;
+  // Sum of r over the row, in s.total; the CTAs' sums stay in their s.mine[pass & 1].
+  auto row_sum = [&]() {
+    strips(r, first, last, step, s);
+    if (warp == 0) {
+      const Two all = warp_sum(lane < kVWarps ? s.sum[lane] : Two{0.f, 0.f});
+      if (lane == 0) s.mine[pass & 1] = all;
+    }
+    if (ctas > 1) cluster_sync_all();
+    if (warp == 0) {
+      __syncwarp();
+      const Two all = ctas > 1 ? warp_sum(lane < ctas ? peer(&s.mine[pass & 1], lane) : Two{0.f, 0.f}) : s.mine[pass & 1];
+      if (lane == 0) {
+        s.total = all;
+        s.mass = (double)all.hi + (double)all.lo;
+      }
+    }
+    ++pass;
+    __syncthreads();
+  };
   for (;;) {
     // Children in turn, until one is turned down or there are none.
     if (tid == 0) {
@@ -191,81 +283,90 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
     r.ml = (float)(s.off - (double)r.mh);
     // a node whose rest has been summed (its last child was turned down) is done
     const bool known = !more && s.off > 0.;
-    if (!known) {
-      strips(r, 0, p.V, step, s);
-      if (warp == 0) {
-        const Two all = warp_sum(lane < kVWarps ? s.sum[lane] : Two{0.f, 0.f});
-        if (lane == 0) {
-          s.total = all;
-          s.mass = (double)all.hi + (double)all.lo;
-        }
-      }
-      __syncthreads();
-    }
+    if (!known) row_sum();
     if (!more) break;
   }
   // The target is covered by the draft (only roundings led here): its own samples.
   if (!(s.total.hi > 0.f) && r.mh != 0.f) {
     r.mh = r.ml = 0.f;
     __syncthreads();
-    strips(r, 0, p.V, step, s);
-    if (warp == 0) {
-      const Two all = warp_sum(lane < kVWarps ? s.sum[lane] : Two{0.f, 0.f});
-      if (lane == 0) s.total = all;
-    }
-    __syncthreads();
+    row_sum();
   }
-  // The strip, the strip of the strip, and the token in it.
-  int lo = 0, hi = p.V, width = step;
-  Two aim = {0.f, 0.f};
+  // The CTA in whose strip the token lies (none of them where p is 0 throughout).
   if (warp == 0) {
     const float u = s.u[0];
     const float h = __fmul_rn(u, s.total.hi);
-    aim = quick(h, __fmaf_rn(u, s.total.lo, __fmaf_rn(u, s.total.hi, -h)));
+    Two aim = quick(h, __fmaf_rn(u, s.total.lo, __fmaf_rn(u, s.total.hi, -h)));
+    int l = s.total.hi > 0.f ? 0 : -1;
+    if (ctas > 1) l = pick(lane < ctas ? peer(&s.mine[(pass - 1) & 1], lane) : Two{0.f, 0.f}, aim, lane);
+    if (lane == 0) {
+      s.rank = l;
+      s.aim = aim;
+    }
   }
-  for (int level = 0; level < 2; ++level) {
-    if (level) {
-      width = ((hi - lo + kVWarps - 1) / kVWarps + 31) / 32 * 32;
-      strips(r, lo, hi, width, s);
+  __syncthreads();
+  if (rank == max(s.rank, 0)) {
+    // The warp's strip, the strip of the strip, and the token in it.
+    int lo = first, hi = last, width = step;
+    Two aim = s.aim;   // (kept by warp 0)
+    bool some = s.rank >= 0;
+    for (int level = 0; level < 2 && some && (!level || hi - lo > 64); ++level) {
+      if (level) {
+        width = ((hi - lo + kVWarps - 1) / kVWarps + 31) / 32 * 32;
+        strips(r, lo, hi, width, s);
+      }
+      if (warp == 0) {
+        const int l = pick(lane < kVWarps ? s.sum[lane] : Two{0.f, 0.f}, aim, lane);
+        if (lane == 0) s.strip = l;
+      }
+      __syncthreads();
+      some = s.strip >= 0;
+      lo += max(s.strip, 0) * width;
+      hi = min(hi, lo + width);
     }
     if (warp == 0) {
-      const int l = pick(lane < kVWarps ? s.sum[lane] : Two{0.f, 0.f}, aim, lane);
-      if (lane == 0) s.strip = l;
-    }
-    __syncthreads();
-    if (s.strip < 0) break;
-    lo += s.strip * width;
-    hi = min(hi, lo + width);
-  }
-  if (warp == 0) {
-    int token = -1;
-    if (s.strip >= 0)
-      for (int x0 = lo; x0 < hi; x0 += 32) {
-        const Two v = x0 + lane < hi ? r(x0 + lane) : Two{0.f, 0.f};
-        const Two upto = warp_scan(v, lane);
-        const uint32_t over = __ballot_sync(0xffffffffu, above(upto, aim) && v.hi > 0.f);
-        const uint32_t some = __ballot_sync(0xffffffffu, v.hi > 0.f);
-        if (over) {
-          token = x0 + __ffs(over) - 1;
-          break;
+      int token = -1;
+      if (some)
+        for (int x0 = lo; x0 < hi; x0 += 32) {
+          const Two v = x0 + lane < hi ? r(x0 + lane) : Two{0.f, 0.f};
+          const Two upto = warp_scan(v, lane);
+          const uint32_t over = __ballot_sync(0xffffffffu, above(upto, aim) && v.hi > 0.f);
+          const uint32_t any = __ballot_sync(0xffffffffu, v.hi > 0.f);
+          if (over) {
+            token = x0 + __ffs(over) - 1;
+            break;
+          }
+          if (any) token = x0 + 31 - __clz(any);
+          const Two all = shfl(upto, 31);
+          aim = add(aim, Two{-all.hi, -all.lo});
         }
-        if (some) token = x0 + 31 - __clz(some);
-        const Two all = shfl(upto, 31);
-        aim = add(aim, Two{-all.hi, -all.lo});
+      if (lane == 0) {
+        p.token[b] = token;
+        p.count[b] = s.count;
       }
-    if (lane == 0) {
-      p.token[b] = token;
-      p.count[b] = s.count;
     }
+    if (tid < p.N) p.path[(long long)b * p.N + tid] = s.path[tid];
   }
-  if (tid < p.N) p.path[(long long)b * p.N + tid] = s.path[tid];
+  if (ctas > 1) cluster_sync_all();   // the others have read this CTA's sums
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const VerifyParams& p, bool f16, cudaStream_t s) {
-  return launch_proj(f16 ? verify_kernel<__half> : verify_kernel<float>, (unsigned)p.B, (unsigned)kThreads, 0, s, 1u,
-                     p);
+  auto kern = f16 ? verify_kernel<__half> : verify_kernel<float>;
+  if (p.ctas > 8) {   // more than every device takes
+    std::atomic<unsigned long long>& configured = attr_flag<VerifyParams>();
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+      for (auto k : {verify_kernel<__half>, verify_kernel<float>})
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+      configured.fetch_or(bit);
+    }
+  }
+  return launch_proj(kern, (unsigned)(p.B * p.ctas), (unsigned)kThreads, 0, s, (unsigned)p.ctas, p);
 }
 
 }  // namespace m4q

@@ -796,8 +796,7 @@ def page_plan(past, new, table, held, free, n_free, page: int, tokens: int, out=
     sequence go back on top.  slots and pos int32 [tokens] are those of all
     sequences' tokens one after the other, from starts int32 [B + 1] on (behind
     them -1 and 0; -1 too where the pages ran out); lengths int32 [B] counts the
-    rows after the step.  out: int32 [2 * tokens + 2 * B + 1] for the results, one
-    after the other."""
+    rows after the step.  out: the four tensors of the results."""
     i32 = _t().int32
     if not isinstance(table, _torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be [B, W]")
@@ -809,22 +808,23 @@ def page_plan(past, new, table, held, free, n_free, page: int, tokens: int, out=
             raise ValueError("%s holds %d values, expected %d" % (what, t.numel(), n))
     _need(free, i32, "free")
     tokens = int(tokens)
-    total = 2 * tokens + 2 * b + 1
     if tokens < 1:
         raise ValueError("tokens must be at least 1")
-    if out is None:
-        out = _allocate((total,), i32, table, stream)
+    if out is None:   # (four small tensors cost less of the host's time than views of one)
+        slots, pos = _allocate((tokens,), i32, table, stream), _allocate((tokens,), i32, table, stream)
+        lengths, starts = _allocate((b,), i32, table, stream), _allocate((b + 1,), i32, table, stream)
     else:
-        _ints(out, i32, total, "out")
-        out = out.view(-1)
-    dev = _one_device(table, past, new, held, free, n_free, out)
-    p = out.data_ptr()
+        slots, pos, lengths, starts = out
+        for t, n, what in ((slots, tokens, "slots"), (pos, tokens, "pos"), (lengths, b, "lengths"),
+                           (starts, b + 1, "starts")):
+            _ints(t, i32, n, what)
+    dev = _one_device(table, past, new, held, free, n_free, slots, pos, lengths, starts)
     rc = load().m4q_page_plan(past.data_ptr(), new.data_ptr(), b, page, table.data_ptr(), w, held.data_ptr(),
-                              free.data_ptr(), free.numel(), n_free.data_ptr(), tokens, p, p + 4 * tokens,
-                              p + 8 * tokens, p + 8 * tokens + 4 * b, _raw_stream(stream, dev))
+                              free.data_ptr(), free.numel(), n_free.data_ptr(), tokens, slots.data_ptr(),
+                              pos.data_ptr(), lengths.data_ptr(), starts.data_ptr(), _raw_stream(stream, dev))
     if rc:
         raise M4QError(rc, "m4q_page_plan")
-    return _torch.split_with_sizes(out, (tokens, tokens, b, b + 1))
+    return slots, pos, lengths, starts
 
 
 def attention_paged(q, kc, vc, kv_codec: int, table, lengths, scale: float | None = None, out=None, workspace=None,
@@ -903,7 +903,7 @@ def verify_tree(target, draft, tokens, parents, u, out=None, stream=None):
     in [0, 1): u[b, i] decides on node i, u[b, 0] draws the next token.  path
     int32 [B, N] holds the nodes kept (0 first, -1 behind them), count int32 [B]
     their number, token int32 [B] the next token.  draft may be None with N = 1.
-    out: int32 [B * (N + 2)] for the results, one after the other."""
+    out: the three tensors of the results."""
     tbs, trs = _prob_rows(target, "target")
     b, n, v = target.shape
     p_draft, dbs, drs = None, 0, 0
@@ -922,21 +922,21 @@ def verify_tree(target, draft, tokens, parents, u, out=None, stream=None):
         if t.dim() > 1 and tuple(t.shape) != (b, n):
             raise ValueError("%s must be [%d, %d]" % (what, b, n))
     if out is None:
-        out = _allocate((b * (n + 2),), _torch.int32, target, stream)
+        path, count = _allocate((b, n), _torch.int32, target, stream), _allocate((b,), _torch.int32, target, stream)
+        token = _allocate((b,), _torch.int32, target, stream)
     else:
-        _ints(out, _torch.int32, b * (n + 2), "out")
-        out = out.view(-1)
-    dev = _one_device(target, draft, tokens, parents, u, out)
+        path, count, token = out
+        for t, size, what in ((path, b * n, "path"), (count, b, "count"), (token, b, "token")):
+            _ints(t, _torch.int32, size, what)
+    dev = _one_device(target, draft, tokens, parents, u, path, count, token)
     if b:
-        p = out.data_ptr()
         rc = load().m4q_verify_tree(target.data_ptr(), tbs, trs, p_draft, dbs, drs,
                                     PROB_F16 if target.dtype is _torch.float16 else PROB_F32, b, n, v,
-                                    tokens.data_ptr(), parents.data_ptr(), u.data_ptr(), p, p + 4 * b * n,
-                                    p + 4 * b * (n + 1), _raw_stream(stream, dev))
+                                    tokens.data_ptr(), parents.data_ptr(), u.data_ptr(), path.data_ptr(),
+                                    count.data_ptr(), token.data_ptr(), _raw_stream(stream, dev))
         if rc:
             raise M4QError(rc, "m4q_verify_tree")
-    path, count, token = _torch.split_with_sizes(out, (b * n, b, b))
-    return path.view(b, n), count, token
+    return path, count, token
 
 
 def norm_residual(h, r, w_pre, w_post=None, gate=None, res_scale: float = 1.0, branch_scale: float = 1.0,

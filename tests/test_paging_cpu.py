@@ -135,9 +135,9 @@ def test_page_plan_binding(cpu_binding):
     with pytest.raises(AssertionError, match="m4q_page_plan was called"):
         call()
     with pytest.raises(AssertionError, match="m4q_page_plan was called"):
-        call(out=i32(21))
+        call(out=(i32(7), i32(7), i32(3), i32(4)))
     for kw in (dict(past=i32(2)), dict(new=i32(4)), dict(held=i32(0)), dict(n_free=i32(2)), dict(table=i32(12)),
-               dict(tokens=0), dict(tokens=-3), dict(out=i32(20)), dict(table=i32(24).view(3, 8)[:, :4])):
+               dict(tokens=0), dict(tokens=-3), dict(out=(i32(7), i32(7), i32(3), i32(3))), dict(out=(i32(7), i32(7), i32(3))), dict(table=i32(24).view(3, 8)[:, :4])):
         with pytest.raises(ValueError):
             call(**kw)
     for kw in (dict(past=torch.zeros(3)), dict(free=torch.zeros(20, dtype=torch.int64))):
@@ -171,7 +171,7 @@ def test_verify_tree_binding(cpu_binding, monkeypatch):
     with pytest.raises(AssertionError, match="m4q_verify_tree was called"):
         call()
     for kw in (dict(draft=None), dict(draft=torch.zeros(2, 3, 49)), dict(tokens=i32(5)), dict(parents=i32(6).view(3, 2)),
-               dict(u=torch.zeros(3, 2)), dict(out=i32(9))):
+               dict(u=torch.zeros(3, 2)), dict(out=(n, i32(2), i32(3))), dict(out=(n, i32(2)))):
         with pytest.raises(ValueError):
             call(**kw)
     for kw in (dict(draft=p.half()), dict(u=torch.zeros(2, 3).double())):

@@ -199,7 +199,7 @@ def test_plan_captured():
     table, held = ints([[-1] * width for _ in range(b)]), ints([0] * b)
     free, n_free = ints(list(map(int, r.permutation(pages)))), ints([pages])
     state = ([[-1] * width for _ in range(b)], [0] * b, free.tolist(), pages)
-    out = torch.empty(2 * tokens + 2 * b + 1, dtype=torch.int32, device="cuda")
+    out = [torch.empty(k, dtype=torch.int32, device="cuda") for k in (tokens, tokens, b, b + 1)]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         res = m.page_plan(past, new, table, held, free, n_free, page, tokens, out=out)

@@ -211,7 +211,7 @@ def test_captured_and_on_streams():
     p, q = distributions(g, b, n, v, torch.float32)
     parents = ints(trees(r, b, n, "random"))
     tokens, u = drawn(g, q, parents), torch.rand(b, n, generator=g, device="cuda")
-    out = torch.empty(b * (n + 2), dtype=torch.int32, device="cuda")
+    out = [torch.empty(k, dtype=torch.int32, device="cuda") for k in ((b, n), b, b)]
     m.verify_tree(p, q, tokens, parents, u, out=out)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

@@ -1101,7 +1101,7 @@ PagedPlan paged_plan(bool q8, int64_t B, int64_t H, int64_t Hkv, int64_t page, i
   const int G = (int)(H / Hkv), R = m4q::paged_rows(G);
   t.rtiles = (G + R - 1) / R;
   const int64_t chunk = m4q::paged_chunk((int)D, q8), chunks = (W * page + chunk - 1) / chunk;
-  const int64_t fit = INT32_MAX / chunks;   // a launch's chunks fit 31 bits
+  const int64_t fit = INT32_MAX / (chunks * Hkv * t.rtiles);   // a launch's chunks fit 31 bits (check_paged: one sequence's do)
   t.seqs = (int)(B < m4q::kPagedSeqs ? B : m4q::kPagedSeqs);
   if (t.seqs > fit) t.seqs = (int)fit;
   const int64_t items = (int64_t)t.seqs * Hkv * t.rtiles;
@@ -1119,7 +1119,9 @@ int check_paged(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t P, int6
   const int rc = check_cache(kv_codec, P, Hkv, page, D);
   if (rc != M4Q_OK) return rc;
   if (B < 1 || H < 1 || W < 1 || H > 65535 || B > 65535) return M4Q_ERR_INVALID_ARG;
-  return H % Hkv == 0 && page % 8 == 0 && W <= INT32_MAX / page ? M4Q_OK : M4Q_ERR_BAD_SHAPE;
+  if (H % Hkv != 0 || page % 8 != 0 || W > INT32_MAX / page) return M4Q_ERR_BAD_SHAPE;
+  // a sequence's chunks times its items fit 31 bits (a chunk is 64 keys or more)
+  return (W * page + 63) / 64 <= INT32_MAX / H ? M4Q_OK : M4Q_ERR_BAD_SHAPE;
 }
 
 }  // namespace
@@ -1171,6 +1173,7 @@ int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_co
   p.rtiles = t.rtiles;
   p.split = t.split ? 1 : 0;
   p.join = m4q::paged_join((int)D, q8);
+  p.share = 1.5f / (float)t.grid;
   if (t.split) {
     char* ws = static_cast<char*>(workspace);
     p.ws_cut = reinterpret_cast<int4*>(ws);
@@ -1183,6 +1186,7 @@ int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_co
     p.o = static_cast<__half*>(O) + b0 * H * D;
     p.table = table + b0 * W;
     p.lengths = lengths + b0;
+    p.waves = (float)((p.B * (int)Hkv * t.rtiles + t.grid - 1) / t.grid);
     rc = done(m4q::launch_attention_paged(p, q8, tm_k, tm_v, t.grid, reinterpret_cast<cudaStream_t>(stream)));
     if (rc != M4Q_OK) return rc;
   }

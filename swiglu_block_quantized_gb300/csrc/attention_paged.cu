@@ -242,17 +242,18 @@ struct Rows {
 };
 
 // A part of an item that a CTA takes: chunks [c0, c1) of `chunks`.  u: where the CTA goes
-// on, as a chunk of all (cut) or an item.
+// on, as a chunk of all (cut) or an item (both fit 31 bits: 64-bit divisions took most of
+// the 6 us that a call's first copies once waited).
 struct Part {
   int b, item, c0, c1, chunks;
-  long long u;
+  int u;
   // The next part before u1 (the first one, from u on, with `at_start`); false: none.
-  __device__ __forceinline__ bool next(const PagedParams& p, const int* at, int per, long long u1, bool cut, bool at_start) {
+  __device__ __forceinline__ bool next(const PagedParams& p, const int* at, int per, int u1, bool cut, bool at_start) {
     if (u >= u1) return false;
     if (!cut) {
       for (; u < u1; u += gridDim.x) {
-        b = (int)(u / per);
-        item = (int)(u - (long long)b * per);
+        b = u / per;
+        item = u - b * per;
         chunks = at[b + 1] - at[b];
         if (chunks > 0) break;
       }
@@ -266,14 +267,14 @@ struct Part {
       int lo = 0, hi = p.B;   // the last sequence that starts at or before u has chunks
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((long long)at[mid] * per <= u) lo = mid;
+        if (at[mid] * per <= u) lo = mid;
         else hi = mid;
       }
       b = lo;
       chunks = at[b + 1] - at[b];
-      const long long rel = u - (long long)at[b] * per;
-      item = (int)(rel / chunks);
-      c0 = (int)(rel - (long long)item * chunks);
+      const int rel = u - at[b] * per;
+      item = rel / chunks;
+      c0 = rel - item * chunks;
     } else {   // the part before ended its item
       c0 = 0;
       if (++item == per) {
@@ -283,7 +284,7 @@ struct Part {
         chunks = at[b + 1] - at[b];
       }
     }
-    c1 = (int)min((long long)chunks, c0 + (u1 - u));
+    c1 = min(chunks, c0 + (u1 - u));
     u += c1 - c0;
     return true;
   }
@@ -328,17 +329,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
   const int longest = count_chunks<C::CH>(p, at, lens, part);
 
   const int per = p.Hkv * p.rtiles;                  // items of a sequence
-  const long long total = (long long)at[p.B] * per;
+  const int total = at[p.B] * per;
   // Dealt out evenly, or item by item where that loses less than the join costs.
-  const int waves = (int)(((long long)p.B * per + ctas - 1) / ctas);
-  const bool cut = p.split && (float)waves * longest > 1.5f * (float)total / ctas + p.join;
+  const bool cut = p.split && p.waves * (float)longest > p.share * (float)total + p.join;
   // this CTA's chunks [u, u1) of all (none for those past the chunks' number: every CTA
   // between an item's first and its last has a piece of it), or, not cut, its items u, u +
   // ctas, ...
-  const int used = (int)min(total, (long long)ctas);
+  const int used = min(total, ctas);
+  const int each = cut ? total / used : 0, over = total - each * used;   // the first `over` CTAs have one more
   Part now;
-  now.u = cut ? (cta < used ? total * cta / used : 0) : cta;
-  const long long u1 = cut ? (cta < used ? total * (cta + 1) / used : 0) : (long long)p.B * per;
+  now.u = cut ? (cta < used ? each * cta + min(cta, over) : 0) : cta;
+  const int u1 = cut ? (cta < used ? each * (cta + 1) + min(cta + 1, over) : 0) : p.B * per;
   if (p.split && threadIdx.x == 0) p.ws_cut[cta] = make_int4(0, 0, 0, 0);
   // rows of sequences without keys
   for (int b = cta; b < p.B; b += ctas)
@@ -698,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
     }
     if (!whole && was.c0 == 0 && threadIdx.x == 0) {
       // the CTA of the item's last chunk; this one has its first
-      const long long end = (long long)at[was.b] * per + (long long)(was.item + 1) * was.chunks - 1;
-      const int last_cta = (int)(((end + 1) * used - 1) / total);
+      const int end = at[was.b] * per + (was.item + 1) * was.chunks - 1;
+      const int last_cta = end < over * (each + 1) ? end / (each + 1) : over + (end - over * (each + 1)) / each;
       p.ws_cut[cta] = make_int4(was.b, was.item, last_cta, 1);
     }
     fence_proxy_async_smem();   // the stage's next copies come after these reads and writes
@@ -732,18 +733,29 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedParams p, int slic
   const int hk = cut.y / p.rtiles, q = cut.y % p.rtiles * R + r;
   const int first = blockIdx.x, n = r < R && q < p.G ? cut.z - first + 1 : 0;
   float m = kLowest, l = 0.f, o[E] = {};
-#pragma unroll 4
-  for (int i = warp % slices; i < n; i += slices) {
-    const long long at = (long long)(kPiece * (first + i) + (i == 0 ? 1 : 0)) * R + r;
-    const float2 ml = p.ws_ml[at];
-    float x[E];
+  for (int i0 = warp % slices; i0 < n; i0 += 4 * slices) {   // four pieces on their way at once
+    float2 ml[4];
+    float x[4][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = p.ws_o[at * D + lane + 32 * e];
-    const float top = fmaxf(m, ml.x), f = fast_exp2(m - top), h = fast_exp2(ml.x - top);
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * slices;
+      const long long at = (long long)(kPiece * (first + i) + (i == 0 ? 1 : 0)) * R + r;
+      ml[j] = i < n ? p.ws_ml[at] : make_float2(kLowest, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[j][e] = i < n ? p.ws_o[at * D + lane + 32 * e] : 0.f;
+    }
+    const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m), f = fast_exp2(m - top);
     m = top;
-    l = l * f + ml.y * h;
+    l *= f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + x[e] * h;
+    for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float h = fast_exp2(ml[j].x - top);
+      l += ml[j].y * h;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += x[j][e] * h;
+    }
   }
   if (slices > 1) {
 #pragma unroll

@@ -271,8 +271,8 @@ struct PagedParams {
   float scale_log2;       // softmax scale * log2(e)
   int rtiles;             // items of a sequence and KV head: ceil(G / rows of an item)
   int split;              // chunks may be dealt out evenly over the CTAs, pieces of items joined
-  float join;             // (on the device: where an item's chunks, as often as a CTA takes one, are
-                          // this many more than 1.5 times a CTA's share of all)
+  float waves, share, join;   // (on the device: where the longest item's chunks times `waves`, the items a
+                          // CTA takes, are more than `share`, 1.5 / CTAs, of all and `join` on top)
   int4* ws_cut;           // [grid] of the item cut whose first chunk is the CTA's: sequence, item, last CTA, 1
   float2* ws_ml;          // [2 grid][rows] (max, sum) of a piece
   float* ws_o;            // [2 grid][rows][D] its unnormalised O

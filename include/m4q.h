@@ -479,8 +479,8 @@ int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t 
  *    P) are not seen; a sequence that sees no row gets zeros.
  *  - Rows behind the last do not enter the result, whatever they hold (infinities and
  *    NaN included).
- *  - D is 64 or 128, H % Hkv == 0, page % 8 == 0, W * page <= INT32_MAX, H ceil(W page /
- *    64) <= INT32_MAX, the pools as for m4q_kv_write (else M4Q_ERR_BAD_SHAPE); B, H <= 65535, scale log2(e) finite in 32
+ *  - D is 64 or 128, H % Hkv == 0, page % 8 == 0, W * page <= INT32_MAX, H (ceil(W page /
+ *    64) + 1) <= INT32_MAX, the pools as for m4q_kv_write (else M4Q_ERR_BAD_SHAPE); B, H <= 65535, scale log2(e) finite in 32
  *    bits (else M4Q_ERR_INVALID_ARG).
  *  - Arithmetic as m4q_attention.
  *  - workspace: m4q_attention_paged_workspace() bytes (not cleared before or after,

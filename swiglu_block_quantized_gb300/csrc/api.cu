@@ -1101,7 +1101,7 @@ PagedPlan paged_plan(bool q8, int64_t B, int64_t H, int64_t Hkv, int64_t page, i
   const int G = (int)(H / Hkv), R = m4q::paged_rows(G);
   t.rtiles = (G + R - 1) / R;
   const int64_t chunk = m4q::paged_chunk((int)D, q8), chunks = (W * page + chunk - 1) / chunk;
-  const int64_t fit = INT32_MAX / (chunks * Hkv * t.rtiles);   // a launch's chunks fit 31 bits (check_paged: one sequence's do)
+  const int64_t fit = INT32_MAX / ((chunks + 1) * Hkv * t.rtiles);   // a launch's units fit 31 bits (check_paged: one sequence's do)
   t.seqs = (int)(B < m4q::kPagedSeqs ? B : m4q::kPagedSeqs);
   if (t.seqs > fit) t.seqs = (int)fit;
   const int64_t items = (int64_t)t.seqs * Hkv * t.rtiles;
@@ -1120,8 +1120,8 @@ int check_paged(int kv_codec, int64_t B, int64_t H, int64_t Hkv, int64_t P, int6
   if (rc != M4Q_OK) return rc;
   if (B < 1 || H < 1 || W < 1 || H > 65535 || B > 65535) return M4Q_ERR_INVALID_ARG;
   if (H % Hkv != 0 || page % 8 != 0 || W > INT32_MAX / page) return M4Q_ERR_BAD_SHAPE;
-  // a sequence's chunks times its items fit 31 bits (a chunk is 64 keys or more)
-  return (W * page + 63) / 64 <= INT32_MAX / H ? M4Q_OK : M4Q_ERR_BAD_SHAPE;
+  // a sequence's chunks (of 64 keys or more) and one, times its items, fit 31 bits
+  return (W * page + 127) / 64 <= INT32_MAX / H ? M4Q_OK : M4Q_ERR_BAD_SHAPE;
 }
 
 }  // namespace

@@ -179,8 +179,9 @@ __device__ __forceinline__ void softmax_step(float (&s)[KS][NT][4], Acc<D, NT>& 
     }
 }
 
-// Where the chunks of the sequences begin, at[0 .. B], and their keys, in shared memory.
-// Returns the chunks of the longest.
+// What the sequences' items cost and where they begin, at[0 .. B], and their keys, in
+// shared memory.  An item costs its chunks and one more: its O is put together by all warps
+// at the end, about the time of a chunk.  Returns the longest's cost.
 template <int CH>
 __device__ __forceinline__ int count_chunks(const PagedParams& p, int* at, int* lens, int2 (&part)[4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -190,8 +191,9 @@ __device__ __forceinline__ int count_chunks(const PagedParams& p, int* at, int* 
     const int n = min(max(p.lengths[i], 0), p.W * p.page);
     lens[i] = n;
     at[i] = sum;
-    sum += (n + CH - 1) / CH;
-    longest = max(longest, (n + CH - 1) / CH);
+    const int cost = n > 0 ? (n + CH - 1) / CH + 1 : 0;
+    sum += cost;
+    longest = max(longest, cost);
   }
   int in = sum;
 #pragma unroll
@@ -242,7 +244,7 @@ struct Rows {
 };
 
 // A part of an item that a CTA takes: chunks [c0, c1) of `chunks`.  u: where the CTA goes
-// on, as a chunk of all (cut) or an item (both fit 31 bits: 64-bit divisions took most of
+// on, in the cost of all (cut; an item's first unit is the extra one) or as an item (both fit 31 bits: 64-bit divisions took most of
 // the 6 us that a call's first copies once waited).
 struct Part {
   int b, item, c0, c1, chunks;
@@ -254,7 +256,7 @@ struct Part {
       for (; u < u1; u += gridDim.x) {
         b = u / per;
         item = u - b * per;
-        chunks = at[b + 1] - at[b];
+        chunks = at[b + 1] - at[b] - 1;
         if (chunks > 0) break;
       }
       if (u >= u1) return false;
@@ -271,22 +273,26 @@ struct Part {
         else hi = mid;
       }
       b = lo;
-      chunks = at[b + 1] - at[b];
+      chunks = at[b + 1] - at[b] - 1;
       const int rel = u - at[b] * per;
-      item = rel / chunks;
-      c0 = rel - item * chunks;
-    } else {   // the part before ended its item
-      c0 = 0;
-      if (++item == per) {
-        item = 0;
-        do ++b;
-        while (at[b + 1] == at[b]);
-        chunks = at[b + 1] - at[b];
-      }
+      item = rel / (chunks + 1);
+      const int r = rel - item * (chunks + 1);
+      c0 = max(r - 1, 0);
+      c1 = min(chunks, r - 1 + (u1 - u));
+      u += c1 + 1 - r;
+      return c1 > c0;   // (a run that ends with an item's extra unit)
     }
-    c1 = min(chunks, c0 + (u1 - u));
-    u += c1 - c0;
-    return true;
+    // the part before ended its item
+    if (++item == per) {
+      item = 0;
+      do ++b;
+      while (at[b + 1] == at[b]);
+      chunks = at[b + 1] - at[b] - 1;
+    }
+    c0 = 0;
+    c1 = min(chunks, u1 - u - 1);
+    u += c1 + 1;
+    return c1 > 0;
   }
   // Keys [first, last) from the warp's first one on; its steps, CH keys apart.
   template <typename C>
@@ -699,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
     }
     if (!whole && was.c0 == 0 && threadIdx.x == 0) {
       // the CTA of the item's last chunk; this one has its first
-      const int end = at[was.b] * per + (was.item + 1) * was.chunks - 1;
+      const int end = at[was.b] * per + (was.item + 1) * (was.chunks + 1) - 1;
       const int last_cta = end < over * (each + 1) ? end / (each + 1) : over + (end - over * (each + 1)) / each;
       p.ws_cut[cta] = make_int4(was.b, was.item, last_cta, 1);
     }

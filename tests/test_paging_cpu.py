@@ -196,3 +196,15 @@ def test_nothing_is_read_only(name):
     with open(os.path.join(os.path.dirname(m.__file__), "csrc", name)) as f:
         code = re.sub(r"//[^\n]*", "", f.read())
     assert "ld.global.nc" not in code and "__restrict__" not in code and "__ldg" not in code
+
+
+def test_cpu_tensors_are_refused(lib):
+    x, pos, n = f16(2, 4, 64), i32(12).view(3, 4), i32(6).view(2, 3)
+    p, kc = torch.zeros(2, 3, 50), f16(9, 2, 16, 64)
+    for call in (lambda: m.rope(x, pos, FR, axes=i32(32)),
+                 lambda: m.kv_write(x, x, kc, kc, m.KV_F16, i32(4), pos=pos, freqs=FR, axes=i32(32)),
+                 lambda: m.page_plan(i32(2), i32(2), n, i32(2), i32(9), i32(1), 16, 4),
+                 lambda: m.attention_paged(x, kc, kc, m.KV_F16, i32(8).view(4, 2), i32(4)),
+                 lambda: m.verify_tree(p, p, n, n, torch.zeros(2, 3))):
+        with pytest.raises(TypeError):
+            call()

@@ -1227,11 +1227,12 @@ int m4q_verify_tree(const void* target, int64_t t_seq_stride, int64_t t_row_stri
   p.N = (int)N;
   p.V = (int)V;
   // CTAs of a sequence: as many as fit the device at once, two an SM, each with at least
-  // 4,096 values (12.1 us with 16, 14.7 with 8 and 52.6 with 1 for one sequence over 128,000
-  // values; 28.5 with 8, 38.5 with 4 and 37.1 with 16 for 32; 8.3 with 1, 9.0 with 2 for 16
-  // over 4,000).
-  p.ctas = 1;
-  while (p.ctas < 16 && p.ctas * B <= dev.sms && V > 4096 * p.ctas) p.ctas *= 2;
+  // 4,096 values; up to 8, or 16 where that many fit (12.1 us with 16, 14.7 with 8 and 52.6
+  // with 1 for one sequence over 128,000 values; 28.5 with 8, 38.5 with 4 and 37.1 with 16
+  // for 32; 8.3 with 1, 9.0 with 2 for 16 over 4,000).
+  int64_t ctas = 2 * dev.sms / B;
+  if (ctas > V / 4096) ctas = V / 4096;
+  p.ctas = ctas >= 16 ? 16 : ctas > 8 ? 8 : ctas < 1 ? 1 : (int)ctas;
   return done(m4q::launch_verify(p, prob_type == M4Q_PROB_F16, reinterpret_cast<cudaStream_t>(stream)));
 }
 

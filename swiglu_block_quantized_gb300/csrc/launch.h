@@ -322,7 +322,7 @@ struct VerifyParams {
   int32_t* count;         // [B]
   int32_t* token;         // [B]
   int B, N, V;
-  int ctas;               // of a sequence's cluster: 1, 2, 4, 8 or 16
+  int ctas;               // of a sequence's cluster: 1 to 8, or 16
   uint32_t* status;
 };
 cudaError_t launch_verify(const VerifyParams& p, bool f16, cudaStream_t s);

@@ -18,6 +18,8 @@
 // by strips, a CTA's and then a warp's, and the CTAs' sums are exchanged through
 // distributed shared memory in a fixed order.  The CTA in whose strip the next token lies
 // sums its warp's strip again by finer strips, then scans the one that holds it.
+#include <type_traits>
+
 #include "kv_common.cuh"
 #include "launch.h"
 
@@ -65,8 +67,9 @@ __device__ __forceinline__ Two warp_sum(Two x) {
   return x;
 }
 
-// A probability: what is not a finite positive number counts as zero.
-__device__ __forceinline__ float prob(float x) { return x > 0.f && x <= 3.402823466e38f ? x : 0.f; }
+// A probability: what is not a finite positive number counts as zero (as bits: below those
+// of infinity, which the sign's, too, lie above).
+__device__ __forceinline__ float prob(float x) { return __float_as_uint(x) < 0x7F800000u ? x : 0.f; }
 __device__ __forceinline__ float load(const float* p) { return prob(*p); }
 __device__ __forceinline__ float load(const __half* p) { return prob(__half2float(*p)); }
 
@@ -122,12 +125,19 @@ __device__ __forceinline__ uint4 load_vec(const T* row, int x, int a, int e, boo
     }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// Probability i of a vector.
-template <typename T>
-__device__ __forceinline__ float value(const uint4& v, int i) {
+// The probabilities of a vector.
+__device__ __forceinline__ void values(const uint4& v, float (&x)[4]) {
+  x[0] = prob(__uint_as_float(v.x)), x[1] = prob(__uint_as_float(v.y));
+  x[2] = prob(__uint_as_float(v.z)), x[3] = prob(__uint_as_float(v.w));
+}
+__device__ __forceinline__ void values(const uint4& v, float (&x)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if constexpr (sizeof(T) == 4) return prob(__uint_as_float(w[i]));
-  else return prob(__half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i & 1))))));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = prob(h.x);
+    x[2 * i + 1] = prob(h.y);
+  }
 }
 
 // Sums of r over the strips [lo + w step, lo + (w + 1) step) of [lo, hi), one a warp.
@@ -137,37 +147,54 @@ __device__ void strips(const Rest<T>& r, int lo, int hi, int step, Shared& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int a = min(lo + warp * step, hi), e = min(hi, a + step), skew = r.skew();
   const bool alike = r.alike();
-  Two acc = {0.f, 0.f};
-  float low = 0.f;
+  float acc = 0.f, low = 0.f;   // the sum and what its roundings lost
+  auto take = [&](float hi, float lo) {
+    const Two t = two_sum(acc, hi);
+    acc = t.hi;
+    low = __fadd_rn(low, __fadd_rn(t.lo, lo));
+  };
   for (int x0 = (a + skew) / W * W - skew + lane * W; x0 < e; x0 += 32 * W * kBatch) {
-    uint4 p[kBatch], q[kBatch];
+    uint4 pv[kBatch], qv[kBatch];
+    float p[W], q[W];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) p[i] = load_vec(r.p, x0 + 32 * W * i, a, e, true);
+    for (int i = 0; i < kBatch; ++i) pv[i] = load_vec(r.p, x0 + 32 * W * i, a, e, true);
     if (r.mh != 0.f) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) q[i] = load_vec(r.q, x0 + 32 * W * i, a, e, alike);
+      for (int i = 0; i < kBatch; ++i) qv[i] = load_vec(r.q, x0 + 32 * W * i, a, e, alike);
+      // as rest_of, but for the last step: hi and lo are taken as they are (and after one
+      // child, M = 1, the product is q itself)
+      auto each = [&](auto one) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
+        for (int i = 0; i < kBatch; ++i) {
+          values(pv[i], p);
+          values(qv[i], q);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const Two v = rest_of(value<T>(p[i], j), value<T>(q[i], j), r.mh, r.ml);
-          const Two t = two_sum(acc.hi, v.hi);
-          acc.hi = t.hi;
-          low = __fadd_rn(low, __fadd_rn(t.lo, v.lo));
+          for (int j = 0; j < W; ++j) {
+            const float ph = one.value ? q[j] : __fmul_rn(r.mh, q[j]);
+            const Two d = two_sum(p[j], -ph);
+            const float lo = one.value ? d.lo : __fadd_rn(d.lo, -__fmaf_rn(r.ml, q[j], __fmaf_rn(r.mh, q[j], -ph)));
+            const bool some = __fadd_rn(d.hi, lo) > 0.f;
+            take(some ? d.hi : 0.f, some ? lo : 0.f);
+          }
         }
+      };
+      if (r.mh == 1.f && r.ml == 0.f) each(std::true_type());
+      else each(std::false_type());
     } else {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
+      for (int i = 0; i < kBatch; ++i) {
+        values(pv[i], p);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-          const Two t = two_sum(acc.hi, value<T>(p[i], j));
-          acc.hi = t.hi;
+          const Two t = two_sum(acc, p[j]);
+          acc = t.hi;
           low = __fadd_rn(low, t.lo);
         }
+      }
     }
   }
-  acc = warp_sum(quick(acc.hi, low));
-  if (lane == 0) s.sum[warp] = acc;
+  const Two all = warp_sum(quick(acc, low));
+  if (lane == 0) s.sum[warp] = all;
   __syncthreads();
 }
 

@@ -668,6 +668,8 @@ def kv_write(k, v, kc, vc, kv_codec: int, slots, pos=None, freqs=None, layout: i
             raise ValueError("freqs needs pos")
         rot, n_axes, p_axes = _turn_args(pos, freqs, m_, axes)
         p_pos, p_freqs = pos.data_ptr(), freqs.data_ptr()
+    elif axes is not None:
+        raise ValueError("axes needs freqs")
     if q is not None:
         if freqs is None:
             raise ValueError("q needs freqs")

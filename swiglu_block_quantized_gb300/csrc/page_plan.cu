@@ -49,6 +49,12 @@ __device__ __forceinline__ Sums scan(long long x, long long y, longlong2* part) 
   return s;
 }
 
+// Pages of `rows` rows, at most W (rows + page may be past 32 bits).
+__device__ __forceinline__ int pages_of(const PlanParams& p, uint32_t rows) {
+  const uint32_t n = rows / p.page;
+  return (int)min(n + (n * p.page < rows ? 1u : 0u), (uint32_t)p.W);
+}
+
 __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p) {
   extern __shared__ int mem[];
   int* starts = mem;               // [B + 1]
@@ -74,8 +80,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p) {
     const int s1 = (int)min(tokens + t.x + max(fresh, 0), (long long)p.T);
     tokens += t.all_x;
     long long take = 0;
-    if (b < p.B && fresh >= 0)
-      take = max((long long)min(((uint32_t)n + (uint32_t)(s1 - s0) + p.page - 1u) / p.page, (uint32_t)p.W) - h, 0ll);
+    if (b < p.B && fresh >= 0) take = max(pages_of(p, (uint32_t)n + (uint32_t)(s1 - s0)) - h, 0);
     const Sums g = scan(take, fresh < 0 ? h : 0, part);
     if (b < p.B) {
       starts[b] = s0;
@@ -95,9 +100,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p) {
   const int left = avail - (int)min(takes, (long long)avail);   // free pages that stay
   // The k-th page of the call.
   auto page_of = [&](long long k) { return k < avail ? p.free_pages[avail - 1 - k] : -1; };
-  auto want_of = [&](int b) {
-    return (int)min(((uint32_t)past[b] + (uint32_t)(starts[b + 1] - starts[b]) + p.page - 1u) / p.page, (uint32_t)p.W);
-  };
+  auto want_of = [&](int b) { return pages_of(p, (uint32_t)past[b] + (uint32_t)(starts[b + 1] - starts[b])); };
   // Slots: a thread a token, its sequence the last that starts at or before it.
   const int used = starts[p.B];
   for (int t = rank * threads + threadIdx.x; t < p.T; t += p.ctas * threads) {

@@ -123,7 +123,7 @@ def test_rope_axes_binding(cpu_binding):
                                           axes=ax), **kw})
     with pytest.raises(AssertionError, match="m4q_kv_write_axes was called"):
         w()
-    for kw in (dict(pos=i32(4)), dict(axes=i32(16)), dict(pos=None)):
+    for kw in (dict(pos=i32(4)), dict(axes=i32(16)), dict(pos=None), dict(freqs=None, pos=None)):
         with pytest.raises(ValueError):
             w(**kw)
 

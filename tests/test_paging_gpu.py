@@ -190,6 +190,14 @@ def test_plan_values_out_of_range():
                     check_plan(past, new, table, held, [5, 0, 1, 2, 3, 4], n_free, page, 40)
 
 
+def test_plan_largest_pages():
+    # past + new + page are past 32 bits
+    big = 2 ** 31 - 1
+    for page in (big, 2 ** 30):
+        for past in (big, page, page - 1, 5, 0):
+            check_plan([past], [40], [[-1]], [0], [0], 1, page, 40)
+
+
 def test_plan_captured():
     # a captured plan follows the lengths; pages come and go over many steps, and no page
     # is ever held twice

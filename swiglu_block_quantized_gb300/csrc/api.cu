@@ -734,13 +734,30 @@ int check_turn(const int32_t* pos, int64_t D, int64_t rot, int layout, float msc
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// The device's facts and status word, for the launches below.
+// The device's facts and status word, for the launches below (asked for once a device).
 int ready(DevInfo* dev, uint32_t** status) {
-  const int rc = current_device_info(dev);
-  if (rc != M4Q_OK) return rc;
-  if (!dev->sm103) return M4Q_ERR_UNSUPPORTED_DEVICE;
-  *status = m4q::status_words();
-  return *status ? M4Q_OK : M4Q_ERR_CUDA;
+  struct Known {
+    std::atomic<bool> known{false};
+    DevInfo dev;
+    uint32_t* status = nullptr;
+  };
+  static Known all[128];
+  static std::mutex mu;
+  int id = 0;
+  if (cudaGetDevice(&id) != cudaSuccess || id < 0 || id >= 128) return M4Q_ERR_CUDA;
+  Known& k = all[id];
+  if (!k.known.load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(mu);
+    const int rc = current_device_info(&k.dev);
+    if (rc != M4Q_OK) return rc;
+    if (!k.dev.sm103) return M4Q_ERR_UNSUPPORTED_DEVICE;
+    k.status = m4q::status_words();
+    if (!k.status) return M4Q_ERR_CUDA;
+    k.known.store(true, std::memory_order_release);
+  }
+  *dev = k.dev;
+  *status = k.status;
+  return M4Q_OK;
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? M4Q_OK : M4Q_ERR_CUDA; }
@@ -1110,7 +1127,10 @@ PagedPlan paged_plan(bool q8, int64_t B, int64_t H, int64_t Hkv, int64_t page, i
   const m4q::PagedCut cut = m4q::paged_cut(q8);
   t.join = cut.join;
   t.share = cut.share / (float)most;
-  t.split = (float)(chunks + 1) > cut.join;   // short sequences stay whole
+  // Short tables stay whole by their width alone, two chunks past where a cut begins to pay
+  // on the device: what the second launch and the workspace cost the host (4.5 us a call)
+  // is more than it saves there (at most 2 us).
+  t.split = (float)(chunks + 1) > cut.join + 2.f;
   t.whole = (int)(items < most ? items : most);
   t.grid = !t.split ? t.whole : (int)(chunks > most / items ? most : items * chunks);
   t.ws_ml = ((size_t)t.grid * sizeof(int4) + 255) / 256 * 256;

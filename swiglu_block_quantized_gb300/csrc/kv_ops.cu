@@ -16,7 +16,7 @@
 //
 // With several axes (images, video) pair i turns by the position that its token has on
 // axis axes[i]: up to eight positions a thread instead of one, looked up once for all
-// its heads (26.5 us against 25.4 for the 32 heads of 8,192 tokens below, 27.7 against 26.7
+// its heads (25.4 us against 24.2 for the 32 heads of 8,192 tokens below, 26.6 against 25.3
 // where a token's heads lie together).
 //
 // Quantisation of a block of 32 values x (Q8_0): d = max|x| / 127 rounded up
@@ -34,10 +34,11 @@
 // vectors there (a block's vectors may come from units rot / 2 apart), not its
 // values (25.5 us against 26.6 for the write and read back below).  The next
 // head's vectors are under way while a head is turned and packed (31.5 to 26.6 us,
-// and 25.4 to 24.9 for the rotation).
+// and 25.4 to 24.9 for the rotation), fp16's of the head after it too (25.4 to 24.2; Q8_0
+// would need 88 registers for that, 26.7 against 25.7).
 //
 // Bound by memory from a few thousand tokens on, by the launch below that.
-// Measured: 32 heads of 8,192 tokens, 128 values, rotated in 24.9 us (5.4 TB/s
+// Measured: 32 heads of 8,192 tokens, 128 values, rotated in 24.2 us (5.5 TB/s
 // of input and output), of 128 tokens in 3.1 us; 8,000 tokens of 8 + 8 heads
 // written to Q8_0 rows and read back in 25.6 us (3.9 TB/s); 32,000 Q8_0 rows of
 // 8 heads read back in 17.9 us (5.6 TB/s).
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
     if (slot >= 0 && (long long)slot < (long long)p.B * p.C)
       row = (long long)(slot / p.C) * p.Hkv * p.C + slot % p.C;
   }
-  // A head's two vectors are loaded one head ahead of their use.
+  // A head's two vectors are loaded one head ahead of their use, two where nothing is packed.
   auto fetch = [&](int h, uint4& v0, uint4& v1) {
     const bool q = h < p.H, v = h >= p.H + p.Hkv;
     v0 = v1 = make_uint4(0, 0, 0, 0);
@@ -157,8 +158,9 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
       v1 = __ldcs(reinterpret_cast<const uint4*>(s + (v ? 16 * u + 8 : at.hi)));
     }
   };
-  uint4 n0, n1;
+  uint4 n0, n1, f0, f1;
   fetch(h0, n0, n1);   // (on their way while the angles are formed)
+  if constexpr (!Q8) fetch(h0 + 1, f0, f1);
   Turn8 t;
   if (ok && at.turns && h0 < p.H + p.Hkv) {
     int pos = AX ? 0 : p.pos[m];
@@ -178,7 +180,13 @@ __global__ void __launch_bounds__(kBlock) rope_kv_kernel(const KvOpsParams p, in
     const bool work = ok && (isq || row >= 0);
     const int lo = isv ? 16 * u : at.lo, hi = isv ? 16 * u + 8 : at.hi;
     uint4 v0 = n0, v1 = n1;
-    fetch(h + 1, n0, n1);
+    if constexpr (!Q8) {
+      n0 = f0;
+      n1 = f1;
+      fetch(h + 2, f0, f1);
+    } else {
+      fetch(h + 1, n0, n1);
+    }
     const bool turns = at.turns && !isv;
     if (isq || !Q8) {
       if (!work) continue;

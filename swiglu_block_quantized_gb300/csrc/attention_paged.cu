@@ -3,25 +3,24 @@
 // j % page of page table[b][j / page].
 //
 // An item is a sequence, a KV head and up to 8 NT of the query heads that share it.  Its
-// keys are cut into chunks of 64 (D = 128) or 128 (D = 64); the chunks of all items form
-// one sequence, dealt out evenly over persistent CTAs (lengths are read on the device).
-// A CTA's four warps take a quarter of each chunk each, with a running maximum, sum and O
-// of their own, joined when the CTA's part of the item ends.  Parts of items that are cut
-// go to the workspace, and a second kernel joins them in a fixed order.
+// keys are cut into chunks of 128 (fp16 at D = 128: 64); the chunks of all items form one
+// sequence, dealt out evenly over persistent CTAs (lengths are read on the device).  A CTA's
+// four warps take a quarter of each chunk each, with a running maximum, sum and O of their
+// own, joined when the CTA's part of the item ends.  Parts of items that are cut go to the
+// workspace, and a second kernel joins them in a fixed order.
 //
-// A warp's step of 16 keys (two at D = 64): S^T = K Q^T with the keys on the MMA's 16
-// rows and the query heads on its 8 columns, then O^T += V^T P^T with the head dim on the
-// rows (mma.sync m16n8k16: a group of up to 8 heads fills it, and the operands need no
-// shared memory).  The MMA's k index may stand for any head dim that Q's fragment agrees
-// with, and its rows for any head dim of V, so fragments are made from what a thread can
-// read in one piece: 16 bytes of a K row (fp16), a block of codes (Q8_0), 16 bytes of two
-// V rows whose values are paired by byte permutes.  P^T comes from S^T by an 8 x 8
-// transposition in registers.
-// Rows come through a ring in shared memory, each warp's its own, in groups of 8 (a group
-// lies within a page): fp16 by TMA boxes with the 128-byte swizzle, Q8_0 as they are by
-// bulk copies.  Of Q8_0 a thread decodes the codes it needs: 34-byte blocks are read as
-// aligned words, and where a block starts between words its first and last codes are put
-// together in one, so that no word is shifted.
+// A warp's step, 16 keys at a time: S^T = K Q^T with the keys on the MMA's 16 rows and the
+// query heads on its 8 columns, then O^T += V^T P^T with the head dim on the rows (mma.sync
+// m16n8k16: a group of up to 8 heads fills it).  P^T comes from S^T by an 8 x 8
+// transposition in registers.  Rows come through a ring in shared memory, each warp's its
+// own, in groups of 8 (a group lies within a page):
+//  - fp16 by TMA boxes with the 128-byte swizzle, read by ldmatrix;
+//  - Q8_0 as they are, by bulk copies.  The MMA's k index may stand for any head dim that
+//    Q's fragment agrees with, and its rows for any head dim of V, so a thread decodes what
+//    it can read in one piece: a block of a K row, half a block of four V rows, their codes
+//    paired by byte permutes.  34-byte blocks are read as aligned words, and where a block
+//    starts between words its first and last codes are put together in one, so that no word
+//    is shifted.
 // The reference of a row's softmax is raised when a score exceeds it by 2^8 (one vote a
 // step); P is fp16, sums are fp32.
 //
@@ -107,7 +106,10 @@ struct Cfg {
   static constexpr int CH = 4 * KT;                     // keys of a chunk
   static constexpr int QS = D / 16;                     // k16 steps of S, and m16 tiles of O
   static constexpr int R = 8 * NT;                      // query rows of an item
-  static constexpr int NS = (Q8 && D == 128) || (!Q8 && NT == 1) ? 2 : 3;                 // steps of a warp in its ring
+  // Steps of a warp in its ring: what lets three CTAs share an SM (four of Q8_0 at D = 64; two
+  // where an item has 16 rows, by their registers).  fp16, two steps and three CTAs against
+  // three and two: 104 us against 122 for 256 short sequences, 92 against 95 for 32.
+  static constexpr int NS = (Q8 && D == 128) || (!Q8 && NT == 1) ? 2 : 3;
   static constexpr int kHalf = KT * RB;                 // K rows of a step, then V rows
   static constexpr int kRing = 4 * NS * 2 * kHalf;
   static constexpr int kCopies = 2 * GR * (Q8 ? 1 : D / 64);   // copies of a step, a lane each
@@ -256,8 +258,9 @@ struct Rows {
 };
 
 // A part of an item that a CTA takes: chunks [c0, c1) of `chunks`.  u: where the CTA goes
-// on, in the cost of all (cut; an item's first unit is the extra one) or as an item (both fit 31 bits: 64-bit divisions took most of
-// the 6 us that a call's first copies once waited).
+// on, in the cost of all (cut; an item's first unit is the extra one) or as an item (both
+// fit 31 bits: 64-bit divisions took most of the 6 us that a call's first copies once
+// waited).
 struct Part {
   int b, item, c0, c1, chunks;
   int u;
@@ -316,8 +319,9 @@ struct Part {
 };
 
 template <int D, bool Q8, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 2) paged_kernel(const PagedParams p, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 2)
+    paged_kernel(const PagedParams p, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D, Q8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int2 part[4];
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
           for (int h = 0; h < 2; ++h)
             qf[n][i][h] = has ? *reinterpret_cast<const uint32_t*>(q + 16 * i + 8 * h + 2 * t) : 0u;
       } else {
-        // word i of the thread's codes (see k_words): head dims of its codes 0, 2 and 1, 3
+        // word i of the thread's codes (as they are read below): head dims of codes 0, 2 and 1, 3
 #pragma unroll
         for (int i = 0; i < C::QS; ++i) {
           int d0, d2;   // of code 0 (code 1 next to it), of code 2
@@ -463,7 +467,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
         }
       }
     }
-
   };
   if (more) load_q(now.b, now.item / p.rtiles, now.item % p.rtiles * C::R);
 

@@ -278,8 +278,9 @@ struct PagedParams {
   float* ws_o;            // [2 grid][rows][D] its unnormalised O
   uint32_t* status;
 };
-// Query heads of an item, keys of a chunk (four warps' steps: 17 KB of rows of Q8_0 a
-// warp, 8 of fp16), and CTAs an SM.
+// Query heads of an item, keys of a chunk (four warps' steps of 16 or 32 keys, 4 to 9 KB of
+// rows each), and CTAs an SM.  Q8_0, 32 sequences: 16 keys a step and four CTAs took 62.5 us
+// against 61.0 at D = 128, 64 keys and three CTAs 40.1 against 38.0 at D = 64.
 constexpr int paged_rows(int G) { return G <= 8 ? 8 : 16; }
 constexpr int paged_chunk(int D, bool q8) { return q8 ? 128 : 8192 / D; }
 constexpr int paged_ctas(int G, int D, bool q8) { return G > 8 ? 2 : q8 && D == 64 ? 4 : 3; }

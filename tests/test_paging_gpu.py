@@ -225,6 +225,14 @@ def test_plan_captured():
         at = [0 if n < 0 else int(r.randint(max(0, x - 3), x + 1)) for x, n in zip(want[2], want_new)]
 
 
+def test_plan_largest_batch():
+    # 4096 sequences, more tokens than a cluster takes in one go
+    r = np.random.RandomState(6)
+    past, held, table, free, n_free = plan_state(r, 4096, 16, 12, 4096 * 10, 100)
+    new = [int(r.randint(-1, 120)) for _ in range(4096)]
+    check_plan(past, new, table, held, free, n_free, 16, 200000)
+
+
 # ---------------------------------------------------------------- attention over pages
 
 def tables(r, lengths, page, width, pages):
@@ -467,6 +475,20 @@ def test_paged_graph_follows_lengths_and_streams(codec):
         torch.cuda.synchronize()
         for o in got:
             assert torch.equal(o, out)
+
+
+@pytest.mark.parametrize("codec", [F16, Q8])
+def test_paged_two_million_keys(codec):
+    # a few pages named again and again, beside short sequences under the same wide table
+    g = gen(67)
+    h, hkv, d, page, width = 2, 1, 64, 8, 260000
+    kc, vc = pools(g, codec, 5, hkv, page, d)
+    q = randn(g, h, 3, d)
+    table = torch.randint(0, 5, (3, width), generator=g, device="cuda").to(torch.int32)
+    lengths = [2000003, 0, 77]
+    o = m.attention_paged(q, kc, vc, codec, table, ints(lengths))
+    want, tol = pref.paged_attention(q, kc, vc, codec, table, lengths, d ** -0.5)
+    check(o, want, tol, "two million keys")
 
 
 @pytest.mark.parametrize("codec", [F16, Q8])

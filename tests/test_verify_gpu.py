@@ -88,6 +88,19 @@ def test_long_rows(dtype, v):
         compare(p, q, drawn(g, q, parents), parents, torch.rand(b, n, generator=g, device="cuda"))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_longest_rows(dtype):
+    v = 2 ** 24
+    g = gen(3)
+    for n in (1, 3):
+        p, q = distributions(g, 1, n, v, torch.float32, spread=1.0)
+        if dtype is torch.float16:   # (probabilities of fp16's range, not summing to 1)
+            p, q = (p * 4096).half(), (q * 4096).half()
+        parents = ints([[-1] + [0] * (n - 1)])
+        compare(p, q, torch.randint(0, v, (1, n), generator=g, device="cuda").to(torch.int32), parents,
+                torch.rand(1, n, generator=g, device="cuda"))
+
+
 @pytest.mark.parametrize("b,n", [(1, 256), (300, 3), (2000, 1)])
 def test_many(b, n):
     g, r = gen(b), np.random.RandomState(b)

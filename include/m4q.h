@@ -482,6 +482,9 @@ int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t 
  *  - D is 64 or 128, H % Hkv == 0, page % 8 == 0, W * page <= INT32_MAX, H (ceil(W page /
  *    64) + 1) <= INT32_MAX, the pools as for m4q_kv_write (else M4Q_ERR_BAD_SHAPE); B, H <= 65535, scale log2(e) finite in 32
  *    bits (else M4Q_ERR_INVALID_ARG).
+ *  - A batch of caches [B][Hkv][C] (C % 8 == 0) is a pool of B pages of C rows, its table
+ *    {{0}, {1}, ...}: for one new token a sequence m4q_attention_tree's result, up to
+ *    roundings, in less time.
  *  - Arithmetic as m4q_attention.
  *  - workspace: m4q_attention_paged_workspace() bytes (not cleared before or after,
  *    16-byte aligned) for the partial results of keys split across CTAs; NULL or a

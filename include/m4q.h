@@ -525,8 +525,10 @@ size_t m4q_attention_paged_workspace(int kv_codec, int64_t B, int64_t H, int64_t
  *    roundings) p stands for it; where p is 0 throughout the token is -1.
  *  - path int32 [B][N]: the nodes kept, 0 first, -1 behind them; count int32 [B]: their
  *    number; token int32 [B]: the next token.
- *  - Differences and sums are formed to 2^-44 of their size (but no finer than 2^-146),
- *    in a fixed order.
+ *  - A difference p - M q is formed to 2^-46 of p + M q.  A row's sum is formed to 2^-44 of
+ *    it for rows of any one kind (softmaxes, equal or sorted values, up to 2^24 of them), and
+ *    to 2^-34 whatever they hold (a thread's additions, up to 4,096 of 2^-47, all off to one
+ *    side); neither is finer than 2^-146.  The order is fixed.
  *  - 1 <= N <= 256, 1 <= V <= 2^24 (else M4Q_ERR_INVALID_ARG).  The outputs overlap
  *    nothing (not checked). */
 int m4q_verify_tree(const void* target, int64_t t_seq_stride, int64_t t_row_stride, const void* draft,

@@ -11,8 +11,12 @@
 //
 // Decisions stand beside borders, so every difference p - M q and every sum over a row
 // is a pair of fp32 values (their exact sum and what its rounding lost: TwoSum, and a
-// product's error by fma), good to 2^-45; the 64-bit units, 2 operations an SM and clock,
-// would need several times as long (the walk alone took 5 us of 24 with them).
+// product's error by fma); the 64-bit units, 2 operations an SM and clock, would need
+// several times as long (the walk alone took 5 us of 24 with them).  What is lost in a sum
+// is itself summed in fp32, so only the 8 or 16 values of a thread's step share such a sum,
+// good to 2^-41; steps and strips are added as pairs, each addition good to 2^-47.  (One sum
+// of all of a thread's values, up to 32,768, was off by 2^-26 for equal values and 2^-34 for
+// a softmax's; it took 20.9, 17.0 and 16.1 us below, not 21.2, 17.4 and 16.6.)
 //
 // A sequence is one cluster of CTAs.  All of them walk its nodes (a warp, from shared
 // memory; the drafted tokens' p and q are gathered ahead); a row's sum is formed
@@ -21,10 +25,10 @@
 // sums its warp's strip again by finer strips, then goes through the one that holds it.
 //
 // Bound by latency: a row's sum takes about 4 us (its loads, two sums over warps, a cluster
-// barrier), one for each child turned down; with many sequences by the 22 to 25 additions a
-// value.  16 trees of 8 nodes over 128,000 values in 20.9 us (one CTA a sequence and 4-byte
-// loads: 88.6), one chain of 5 over 32,000 in 7.6, 96 chains of 4 over 50,001 fp16 values in
-// 17.1, 128 samples (N = 1) from 128,000 fp16 values in 16.1 (2.0 TB/s).
+// barrier), one for each child turned down; with many sequences by the 23 to 27 additions a
+// value.  16 trees of 8 nodes over 128,000 values in 21.2 us (one CTA a sequence and 4-byte
+// loads: 88.6), one chain of 5 over 32,000 in 7.7, 96 chains of 4 over 50,001 fp16 values in
+// 17.4, 128 samples (N = 1) from 128,000 fp16 values in 16.6 (2.0 TB/s).
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -163,13 +167,15 @@ __device__ void strips(const Rest<T>& r, int lo, int hi, int step, Shared& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int a = min(lo + warp * step, hi), e = min(hi, a + step), skew = r.skew();
   const bool alike = r.alike();
-  float acc = 0.f, low = 0.f;   // the sum and what its roundings lost
+  Two sum = {0.f, 0.f};
+  float acc, low;   // a step's values: their sum and what its roundings lost
   auto take = [&](float hi, float lo) {
     const Two t = two_sum(acc, hi);
     acc = t.hi;
     low = __fadd_rn(low, __fadd_rn(t.lo, lo));
   };
   for (int x0 = (a + skew) / W * W - skew + lane * W; x0 < e; x0 += 32 * W * kBatch) {
+    acc = low = 0.f;
     uint4 pv[kBatch], qv[kBatch];
     float p[W], q[W];
 #pragma unroll
@@ -208,8 +214,9 @@ __device__ void strips(const Rest<T>& r, int lo, int hi, int step, Shared& s) {
         }
       }
     }
+    sum = add(sum, two_sum(acc, low));   // (of rests beside 0 `low` may be the larger one)
   }
-  const Two all = warp_sum(quick(acc, low));
+  const Two all = warp_sum(sum);
   if (lane == 0) s.sum[warp] = all;
   __syncthreads();
 }

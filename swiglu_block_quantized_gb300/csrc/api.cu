@@ -11,6 +11,7 @@
 
 #include "../../include/m4q.h"
 #include "launch.h"
+#include "per_device.h"
 
 namespace {
 
@@ -736,27 +737,24 @@ bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t
 
 // The device's facts and status word, for the launches below (asked for once a device).
 int ready(DevInfo* dev, uint32_t** status) {
-  struct Known {
-    std::atomic<bool> known{false};
+  struct Facts {
     DevInfo dev;
     uint32_t* status = nullptr;
   };
-  static Known all[128];
-  static std::mutex mu;
+  static m4q::PerDevice<Facts, 128> all;
   int id = 0;
   if (cudaGetDevice(&id) != cudaSuccess || id < 0 || id >= 128) return M4Q_ERR_CUDA;
-  Known& k = all[id];
-  if (!k.known.load(std::memory_order_acquire)) {
-    std::lock_guard<std::mutex> lock(mu);
-    const int rc = current_device_info(&k.dev);
-    if (rc != M4Q_OK) return rc;
-    if (!k.dev.sm103) return M4Q_ERR_UNSUPPORTED_DEVICE;
-    k.status = m4q::status_words();
-    if (!k.status) return M4Q_ERR_CUDA;
-    k.known.store(true, std::memory_order_release);
-  }
-  *dev = k.dev;
-  *status = k.status;
+  Facts f;
+  const int rc = all.get(id, &f, [](Facts* k) -> int {
+    const int e = current_device_info(&k->dev);
+    if (e != M4Q_OK) return e;
+    if (!k->dev.sm103) return M4Q_ERR_UNSUPPORTED_DEVICE;
+    k->status = m4q::status_words();
+    return k->status ? M4Q_OK : M4Q_ERR_CUDA;
+  });
+  if (rc != M4Q_OK) return rc;
+  *dev = f.dev;
+  *status = f.status;
   return M4Q_OK;
 }
 

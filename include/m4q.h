@@ -485,7 +485,10 @@ int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t 
  *  - A batch of caches [B][Hkv][C] (C % 8 == 0) is a pool of B pages of C rows, its table
  *    {{0}, {1}, ...}: for one new token a sequence m4q_attention_tree's result, up to
  *    roundings, in less time.
- *  - Arithmetic as m4q_attention.
+ *  - Arithmetic as m4q_attention (probabilities are rounded to fp16 before the product with
+ *    V, 2^-11 of each, scores and sums are fp32), in runs of at most 2,048 keys a warp that are
+ *    joined in fp32.  Within a run weights down to 2^-21 of its largest keep all of fp16's
+ *    bits, those down to 2^-32 still count.
  *  - workspace: m4q_attention_paged_workspace() bytes (not cleared before or after,
  *    16-byte aligned) for the partial results of keys split across CTAs; NULL or a
  *    smaller size runs without a split, slower.  Calls whose work overlaps need a

@@ -21,8 +21,19 @@
 //    paired by byte permutes.  34-byte blocks are read as aligned words, and where a block
 //    starts between words its first and last codes are put together in one, so that no word
 //    is shifted.
-// The reference of a row's softmax is raised when a score exceeds it by 2^8 (one vote a
-// step); P is fp16, sums are fp32.
+// P is fp16, as V is (the second product of what that rounding loses would cost Q8_0 pages,
+// which are bound by issue slots, another half of their MMAs and packing; without it O is off
+// by 2.8e-4 of its size, 2.1e-4 of which is O's own rounding).  So that weights far below the
+// largest do not leave fp16's range, the reference of a row's softmax lies 2^7 to 2^15 below
+// its largest score (one vote a step says whether it has to be raised): weights down to 2^-21
+// of the largest keep all bits, those down to 2^-32 still count.  Sums are fp32, and no more
+// than kFoldMmas products go into one: the tensor cores cut off what falls below an fp32
+// sum's last bit, always to the same side, which took 0.3% off the mean of two million
+// values.  A part that is longer is taken in runs, with a reference and sums of their own,
+// joined in fp32 as the warps' sums are.  (Runs cost items of any length the test for their
+// end: 65.5 to 66.7 us for 256 short sequences over Q8_0 pages, 36.2 to 36.6 at D = 64, 28.3
+// to 29.1 for groups of 16 heads, below 1% elsewhere.  Adding to sums of the warp's own in
+// its registers' place took 68.7, 37.5 and 30.2.)
 //
 // A warp has its ring for itself, and its copies run ahead into the parts of items that
 // come next: warps meet only where an item's part ends, to put their O together.  (fp16
@@ -46,6 +57,11 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kPiece = 2;         // pieces of cut items a CTA may have: its first and its last
 constexpr float kLowest = -3.402823466e38f;
+// The reference of a row's softmax, in powers of 2: set kBelow below the largest score, raised
+// when a score exceeds it by more than kAbove, so that P (fp16) is at most 2^15.
+constexpr float kBelow = 7.f, kAbove = 15.f;
+// MMAs of 16 keys that go into one sum before it is added to the sum of those before.
+constexpr int kFoldMmas = 128;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -156,18 +172,19 @@ __device__ __forceinline__ void softmax_step(float (&s)[KS][NT][4], Acc<D, NT>& 
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int h = 0; h < 2; ++h) top = fmaxf(top, s[k][n][2 * h + c]);
-      raise |= top > a.m[n][c] + 8.f;
+      raise |= top > a.m[n][c] + kAbove;
     }
   if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float top = a.m[n][c];
+        float top = s[0][n][c];
 #pragma unroll
         for (int k = 0; k < KS; ++k) top = fmaxf(top, fmaxf(s[k][n][c], s[k][n][2 + c]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top - kBelow, a.m[n][c]);
         const float f = fast_exp2(a.m[n][c] - top);
         a.m[n][c] = top;
         a.l[n][c] *= f;
@@ -471,14 +488,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
   if (more) load_q(now.b, now.item / p.rtiles, now.item % p.rtiles * C::R);
 
   Acc<D, NT> acc;
+  // A part is taken kFold steps at a time: where a run of them ends the warps' sums are put
+  // together, and with what this thread has of the runs before (volatile: in local memory, for
+  // long parts only).
+  constexpr int kFold = kFoldMmas / C::KS;
+  volatile float before[C::R * D / 4 / kThreads][6];   // o[4], m, l
+  int from = 0;
   while (more) {
     const int hk = now.item / p.rtiles, row0 = now.item % p.rtiles * C::R;   // query heads hk G + row0 ...
     int first, last;
-    const int steps = now.template keys<C>(lens, first, last);
+    const int steps = now.template keys<C>(lens, first, last), stop = min(steps, from + kFold);
     acc.clear();
     int slot = 0;
 #pragma unroll 1
-    for (int step = 0; step < steps; ++step) {
+    for (int step = from; step < stop; ++step) {
       ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][get], phase, ctl));
       if (!ok) break;
       const uint8_t* kt = mine + get * 2 * C::kHalf;
@@ -638,12 +661,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
       slot = get;
       get = get + 1 == C::NS ? 0 : get + 1;
       phase ^= get == 0;
-      if (step + 1 < steps) issue();   // (the last stage first takes O)
+      if (step + 1 < stop) issue();   // (the last stage first takes O)
     }
     // The four warps' maxima, sums and O (each row's head dims in an order of its own, by
     // bits 1 and 2 of the row, so that the threads of a quad write to different banks).
-    if (lane == 0) so_at[warp] = steps > 0 ? (int)(mine - ring) + slot * 2 * C::kHalf : -1;
-    if (steps > 0) {
+    const bool some = stop > from;
+    if (lane == 0) so_at[warp] = some ? (int)(mine - ring) + slot * 2 * C::kHalf : -1;
+    if (some) {
       float* so = reinterpret_cast<float*>(mine + slot * 2 * C::kHalf);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -682,8 +706,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
     }
     // the next part, its queries on their way
     const Part was = now;
-    more = now.next(p, at, per, u1, cut, false);
-    if (more) load_q(now.b, now.item / p.rtiles, now.item % p.rtiles * C::R);
+    const bool again = from > 0, end = was.c1 - was.c0 <= from + kFold;   // (a chunk is a step of each warp)
+    from = end ? 0 : from + kFold;
+    if (end) {
+      more = now.next(p, at, per, u1, cut, false);
+      if (more) load_q(now.b, now.item / p.rtiles, now.item % p.rtiles * C::R);
+    }
     ok = __syncthreads_and(ok);
     if (!ok) break;
     const bool whole = was.c0 == 0 && was.c1 == was.chunks;
@@ -708,6 +736,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
         o.z += f * x.z;
         o.w += f * x.w;
       }
+      if (again || !end) {
+        volatile float* b = before[i / kThreads];
+        if (again) {
+          const float top = fmaxf(m, b[4]), f = fast_exp2(b[4] - top), h = fast_exp2(m - top);
+          o = make_float4(o.x * h + b[0] * f, o.y * h + b[1] * f, o.z * h + b[2] * f, o.w * h + b[3] * f);
+          l = l * h + b[5] * f;
+          m = top;
+        }
+        b[0] = o.x, b[1] = o.y, b[2] = o.z, b[3] = o.w, b[4] = m, b[5] = l;
+        if (!end) continue;
+      }
       if (whole) {
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // NaN stays
         if (in_bounds(hk * p.G + q < p.H && was.b < p.B, p.status, kSitePagedO))
@@ -718,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
         if (d == 0) p.ws_ml[piece * C::R + r] = make_float2(m, l);
       }
     }
-    if (!whole && was.c0 == 0 && threadIdx.x == 0) {
+    if (end && !whole && was.c0 == 0 && threadIdx.x == 0) {
       // the CTA of the item's last chunk; this one has its first
       const int end = at[was.b] * per + (was.item + 1) * (was.chunks + 1) - 1;
       const int last_cta = end < over * (each + 1) ? end / (each + 1) : over + (end - over * (each + 1)) / each;
@@ -726,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? (Q8 && D == 64 ? 4 : 3) : 
     }
     fence_proxy_async_smem();   // the stage's next copies come after these reads and writes
     __syncthreads();
-    if (steps > 0) issue();
+    if (some) issue();
   }
   // given up: copies still under way land before the block leaves
   for (int i = 0; !ok && i < C::NS; ++i) {

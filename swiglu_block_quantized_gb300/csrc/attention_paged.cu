@@ -222,7 +222,7 @@ __device__ __forceinline__ int count_chunks(const PagedParams& p, int* at, int* 
     const int n = min(max(p.lengths[i], 0), p.W * p.page);
     lens[i] = n;
     at[i] = sum;
-    const int cost = n > 0 ? (n + CH - 1) / CH + 1 : 0;
+    const int cost = n > 0 ? (n - 1) / CH + 2 : 0;   // (n may be INT32_MAX)
     sum += cost;
     longest = max(longest, cost);
   }
@@ -331,7 +331,7 @@ struct Part {
   __device__ __forceinline__ int keys(const int* lens, int& first, int& last) const {
     last = (int)min((long long)lens[b], (long long)c1 * C::CH);
     first = (int)min((long long)c0 * C::CH + (threadIdx.x >> 5) * C::KT, (long long)last);
-    return (last - first + C::CH - 1) / C::CH;
+    return last > first ? (last - first - 1) / C::CH + 1 : 0;
   }
 };
 

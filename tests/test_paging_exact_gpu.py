@@ -153,3 +153,34 @@ def test_two_million_keys_that_count(codec, whole):
     o = m.attention_paged(q, kc, vc, codec, table, ints([n]), workspace=False if whole else None).view(h, d)
     want, tol = exact.sequence(q[:, 0], kc, vc, codec, table[0], n, d ** -0.5, rounded=False)
     check(o, want, tol, "two million")
+
+
+# Tables of nearly 2^31 rows: lengths near INT32_MAX, whose last chunk ends past 32 bits.
+@pytest.mark.parametrize("codec,d,page", [(Q8, 64, 64), (F16, 128, 120), (F16, 64, 8), (Q8, 128, 24)])
+@pytest.mark.parametrize("first", [True, False])
+def test_widest_tables(codec, d, page, first):
+    g = gen(page)
+    width = (2 ** 31 - 1) // page
+    rows = width * page
+    v = torch.rand(5, page, d, generator=g, device="cuda") + 0.5
+    vc = pool(v[:, None], codec)
+    kc = torch.zeros_like(vc)
+    table = torch.randint(0, 5, (3, width), generator=g, device="cuda").to(torch.int32)
+    lengths = [rows, 5, 0] if first else [0, 5, 2 ** 31 - 1]
+    q = randn(g, 1, 3, d)
+    o = m.attention_paged(q, kc, vc, codec, table, ints(lengths))
+    values = ref.values(vc[:, 0], codec)
+    for s, n in enumerate(lengths):
+        n = min(n, rows)
+        if n == 0:
+            assert (o[s] == 0).all()
+            continue
+        full, rest = divmod(n, page)
+        times = torch.bincount(table[s, :full], minlength=5).double()
+        want = torch.einsum("p,pd->d", times, values.sum(1))
+        if rest:
+            want += values[int(table[s, full]), :rest].sum(0)
+        want /= n
+        # equal weights and values of one sign (_paging_exact, without roundings of weights)
+        tol = (2.0 ** -12 + 2.0 ** -11) * want + 2.0 ** -25
+        check(o[s], want, tol, "%d rows" % n)

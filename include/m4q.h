@@ -450,6 +450,13 @@ size_t m4q_attention_tree_workspace(int kv_codec, int64_t B, int64_t H, int64_t 
  *    -1.  An ended sequence's pages go on top of the free ones that are left (and are
  *    handed out from the next call on), its entries become -1 and held[b] 0.  Other
  *    entries of table and free_pages stay as they are.
+ *  - A page is free or belongs to one sequence: among the free entries and those held no
+ *    page is named twice (not checked), for one named twice goes back twice and is then
+ *    handed to two sequences.  Sequences may share a prefix of whole pages all the same:
+ *    one is given the prefix's entries as its first, held and past counting them, and
+ *    before it ends its own entries move to the front of its row, held their number
+ *    (the shared ones leave the row), so that the prefix goes back once, with the sequence
+ *    that it came from, which ends after all that share it.
  *  - The tokens of all sequences lie one after the other in T places: starts int32
  *    [B + 1] is where each sequence's begin (starts[B]: their number; tokens behind the
  *    T-th are left out, as if fresh were smaller).  slots int32 [T], pos int32 [T]: the
@@ -475,7 +482,8 @@ int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t 
  *  - Q: fp16 [H][B][D] (m4q_kv_write's Qout); O: fp16 [B][H D], which overlaps no other
  *    argument (not checked).
  *  - table int32 [B][W], lengths int32 [B] on the device, read by the kernel; lengths are
- *    clamped to [0, W * page].  Sequences may share pages.  Rows of an entry outside [0,
+ *    clamped to [0, W * page].  Sequences may share pages (m4q_page_plan says how such
+ *    pages are given back).  Rows of an entry outside [0,
  *    P) are not seen; a sequence that sees no row gets zeros.
  *  - Rows behind the last do not enter the result, whatever they hold (infinities and
  *    NaN included).

@@ -802,7 +802,8 @@ def page_plan(past, new, table, held, free, n_free, page: int, tokens: int, out=
     (below 0: it has ended).  table int32 [B, W], held int32 [B], free int32 [P]
     and n_free int32 [1] are the pages' state and are updated: pages of `page`
     rows that b lacks come from the end of free[:n_free], those of an ended
-    sequence go back on top.  slots and pos int32 [tokens] are those of all
+    sequence go back on top (a page is held by one sequence only: m4q_page_plan says
+    how a shared prefix is given back).  slots and pos int32 [tokens] are those of all
     sequences' tokens one after the other, from starts int32 [B + 1] on (behind
     them -1 and 0; -1 too where the pages ran out); lengths int32 [B] counts the
     rows after the step.  out: the four tensors of the results."""

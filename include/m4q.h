@@ -433,9 +433,16 @@ size_t m4q_attention_tree_workspace(int kv_codec, int64_t B, int64_t H, int64_t 
  * A paged cache: pools Kc, Vc of P pages [P][Hkv][page] rows, shared by all sequences.
  * For m4q_kv_write and m4q_kv_read it is a batch of caches with B = P and C = page: row
  * r of page i has the slot i * page + r.  Each sequence has a row of the block table,
- * int32 [B][W]: its rows j lie at place j % page of page table[b][j / page].  A decode
- * step is m4q_page_plan -> (a layer: m4q_kv_write -> m4q_attention_paged) ->
- * m4q_verify_tree.
+ * int32 [B][W]: its rows j lie at place j % page of page table[b][j / page].
+ *
+ * A step of one new token a sequence is m4q_page_plan -> (a layer: m4q_kv_write ->
+ * m4q_attention_paged).  Where several tokens of a sequence attend (a prompt's, in every
+ * layer but the last; a chain of drafted ones, before m4q_verify_tree) each of them is a
+ * row of m4q_attention_paged of its own: its sequence's row of the table again, and a
+ * length up to itself.  Each row reads its keys again, so the time grows with their
+ * number.  The nodes of a drafted tree see keys that do not lie one behind the other:
+ * m4q_kv_read brings the pages' rows into caches [B][Hkv][C] of fp16 rows, which
+ * m4q_attention_tree takes.
  */
 
 /* Pages and slots of a step, from lengths on the device (a captured call follows
@@ -482,14 +489,14 @@ int m4q_page_plan(const int32_t* past, const int32_t* fresh, int64_t B, int64_t 
  *  - Q: fp16 [H][B][D] (m4q_kv_write's Qout); O: fp16 [B][H D], which overlaps no other
  *    argument (not checked).
  *  - table int32 [B][W], lengths int32 [B] on the device, read by the kernel; lengths are
- *    clamped to [0, W * page].  Sequences may share pages (m4q_page_plan says how such
- *    pages are given back).  Rows of an entry outside [0,
- *    P) are not seen; a sequence that sees no row gets zeros.
+ *    clamped to [0, W * page].  Sequences may share pages, and several rows of a call may be
+ *    tokens of one sequence (m4q_page_plan says how shared pages are given back).  Rows of
+ *    an entry outside [0, P) are not seen; a sequence that sees no row gets zeros.
  *  - Rows behind the last do not enter the result, whatever they hold (infinities and
  *    NaN included).
  *  - D is 64 or 128, H % Hkv == 0, page % 8 == 0, W * page <= INT32_MAX, H (ceil(W page /
- *    64) + 1) <= INT32_MAX, the pools as for m4q_kv_write (else M4Q_ERR_BAD_SHAPE); B, H <= 65535, scale log2(e) finite in 32
- *    bits (else M4Q_ERR_INVALID_ARG).
+ *    64) + 1) <= INT32_MAX, the pools as for m4q_kv_write (else M4Q_ERR_BAD_SHAPE); B, H <=
+ *    65535, scale log2(e) finite in 32 bits (else M4Q_ERR_INVALID_ARG).
  *  - A batch of caches [B][Hkv][C] (C % 8 == 0) is a pool of B pages of C rows, its table
  *    {{0}, {1}, ...}: for one new token a sequence m4q_attention_tree's result, up to
  *    roundings, in less time.

@@ -842,9 +842,11 @@ def attention_paged(q, kc, vc, kv_codec: int, table, lengths, scale: float | Non
     """O fp16 [B, H * D]: attention of one new token of each of B sequences, q
     fp16 [H, B, D], over the pages kc, vc [P, Hkv, page, row].  Sequence b sees
     its rows j < lengths int32 [B], row j at place j % page of page
-    table[b, j // page] (table int32 [B, W]); none: a zero row.  The workspace is
-    allocated here when not given; workspace=False runs without one (no key
-    split)."""
+    table[b, j // page] (table int32 [B, W]); none: a zero row.  Several tokens of a
+    sequence (a prompt's, a drafted chain's) are rows of their own: q [H, T, D], the
+    table's row for each and lengths up to itself; each reads its keys again.  The
+    workspace is allocated here when not given; workspace=False runs without one (no
+    key split)."""
     _need(q, _t().float16, "q")
     if kc is None or vc is None:
         raise ValueError("both pools are read")

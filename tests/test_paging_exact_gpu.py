@@ -184,3 +184,36 @@ def test_widest_tables(codec, d, page, first):
         # equal weights and values of one sign (_paging_exact, without roundings of weights)
         tol = (2.0 ** -12 + 2.0 ** -11) * want + 2.0 ** -25
         check(o[s], want, tol, "%d rows" % n)
+
+
+@pytest.mark.parametrize("codec", [F16, Q8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h,hkv", [(8, 8), (48, 4)])
+@pytest.mark.parametrize("whole", [False, True])
+def test_long_parts_of_many_items(codec, d, h, hkv, whole):
+    # so many long sequences that a CTA's parts of them take several runs, between short and empty
+    # ones; the pages of a 64th of a sequence are one page, which has its own dim
+    g = gen(h)
+    page, b = 16, 90
+    at = torch.arange(64, device="cuda")
+    v = torch.nn.functional.one_hot(at, d).float()[:, None, None].expand(64, hkv, page, d)
+    vc = pool(v, codec)
+    kc = torch.zeros_like(vc)
+    lengths = [[40000, 5, 33333, 0, 8192, 8193, 16400, 1, 24577, 300][s % 10] + 7 * (s // 10) * (s % 10 != 3)
+               for s in range(b)]
+    width = -(-max(lengths) // page)
+    table = torch.full((b, width), -1, dtype=torch.int32, device="cuda")
+    for s, n in enumerate(lengths):
+        w = -(-n // page)
+        table[s, :w] = torch.arange(w, device="cuda") * 64 // max(w, 1)
+    q = randn(g, h, b, d)
+    o = m.attention_paged(q, kc, vc, codec, table, ints(lengths), workspace=False if whole else None).view(b, h, d)
+    one = ref.values(vc[0, 0, 0], codec)[0]
+    for s, n in enumerate(lengths):
+        if n == 0:
+            assert (o[s] == 0).all()
+            continue
+        rows = table[s].long().repeat_interleave(page)[:n]
+        want = torch.zeros(d, dtype=torch.float64, device="cuda")
+        want[:64] = torch.bincount(rows, minlength=64).double() * one / n
+        check(o[s], want.expand(h, d), (2.0 ** -12 + 2.0 ** -11) * want.expand(h, d) + 2.0 ** -25, "sequence %d" % s)

@@ -532,7 +532,8 @@ size_t m4q_attention_paged_workspace(int kv_codec, int64_t B, int64_t H, int64_t
  *    tokens outside [0, V), are unused.  (As m4q_attention_tree's nodes, with one root.)
  *  - target, draft: rows of V probabilities behind node i of sequence b, at
  *    b * seq_stride + i * row_stride elements, prob_type M4Q_PROB_F32 or _F16; p and q
- *    below.  Values that are not finite positive numbers count as 0.  draft may be NULL
+ *    below.  Values that are not finite positive numbers count as 0; a row's sum is below
+ *    2^120 (not checked).  draft may be NULL
  *    with N = 1: the next token is then a plain sample.
  *  - u: fp32 [B][N] in [0, 1): u[b][i] decides on node i, u[b][0] draws the next token.
  *  - From c = 0 on, with M = 0 and m = 1: the children of c in order of their index; x is

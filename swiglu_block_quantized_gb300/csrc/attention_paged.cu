@@ -42,10 +42,14 @@
 // sequences of 50 to 1,000 keys took 150.7 against 121.7.)
 //
 // Bound by HBM while it streams.  Measured, 8 KV heads of 4 heads: one sequence of 131,001
-// keys, D = 128, in 84.3 us over fp16 pages (6.37 TB/s) and 53.1 over Q8_0 (5.37, issue slots
-// 56% taken); 32 sequences of 500 to 8,100 in 89.9 and 54.8, at D = 64 in 49.2 and 36.2; 256 of
-// 50 to 1,000 in 91.6 and 65.4; one of 300 fp16 keys in 6.5.  CTAs of equal shares end 11%
-// apart, as SMs get unequal bandwidth.
+// keys, D = 128, in 85.2 us over fp16 pages (6.30 TB/s) and 53.5 over Q8_0 (5.33, issue slots
+// 55% taken); 32 sequences of 500 to 8,100 in 90.3 and 55.0, at D = 64 in 49.4 and 36.6; 256 of
+// 50 to 1,000 in 92.5 and 66.7; 128 of 20,000 to 22,000, groups of 2, in 780 (7.06 TB/s) and
+// 440; one of 300 fp16 keys in 6.9.  CTAs of equal shares end 11% apart, as SMs get unequal
+// bandwidth.  Groups of more than 8 heads take 16 rows an item and two CTAs an SM: 16 sequences
+// of 500 to 8,100 keys, 4 KV heads, groups of 16, in 34.5 us over fp16 and 29.2 over Q8_0 pages
+// (D = 64: 21.4 and 21.3), and read their rows again for each 16 heads of a group: groups of 32
+// in 43.4 and 44.0.
 #include "codec.cuh"
 #include "kv_common.cuh"
 #include "launch.h"
@@ -857,6 +861,12 @@ cudaError_t launch(const PagedParams& p, const CUtensorMap& tm_k, const CUtensor
   e = launch_proj(kern, (unsigned)grid, (unsigned)kThreads, C::kSmem, s, 1u, p, tm_k, tm_v);
   if (e != cudaSuccess || !p.split) return e;
   // Pieces of an item: few in a batch (a warp a row takes them all), many of a long sequence.
+  // Measured, us of the whole call with 1, 4 and 8 warps a row, by `pieces`, 8 KV heads of 4,
+  // 8,000 keys a sequence, D = 128, fp16 (Q8_0: the same differences within 0.3),
+  //   59: 16.5, 12.2, 11.7   30: 19.6, 17.6, 17.6   21: 24.4, 22.9, 22.8   16: 28.9, 27.8, 28.0
+  //   11: 38.0, 37.5, 38.1    9: 46.6, 46.3, 46.9    6: 65.5, 65.8, 66.2    4: 122.0, 122.8, 123.9
+  // so the sides are within 0.4 of each other near the bounds.  For items of 16 rows 4 warps
+  // would be the better choice at 40 and 14 pieces, too (by 0.6 and 1.4); the rule is one.
   const int items = p.B * p.Hkv * p.rtiles, pieces = grid / items + 2;
   const int slices = pieces <= 4 ? 1 : pieces <= 12 ? 4 : 8;
   const int rows = p.G < C::R ? p.G : C::R, each = 8 / slices;

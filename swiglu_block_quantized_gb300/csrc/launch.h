@@ -307,7 +307,14 @@ constexpr int paged_ctas(int G, int D, bool q8) { return G > 8 ? 2 : q8 && D == 
 //     D = 128, fp16                          27.2/28.1  37.4/38.7  47.2/48.4  85.2/87.6
 //     D = 64, Q8_0                           13.5/16.0  16.9/20.0  20.5/22.3  36.8/37.0
 //     D = 128, Q8_0                          20.1/21.3  28.3/29.0  35.0/34.3  59.4/53.9
-// Of unequal lengths the longest decides, and cutting gains more.
+// Of unequal lengths the longest decides, and cutting gains more.  The rule is one for both head
+// dims, so it is not the faster side at every point: it cuts 8 sequences of 768 fp16 keys at D =
+// 64, 32 of 1,024 and 1,536 at D = 128 and 128 of 384 Q8_0 keys at D = 128, for 1 to 3% more
+// time.
+// Short sequences under a wide table (a call's launches follow the table, whose lengths only the
+// device knows): 300 keys of one sequence take 6.9 us of device time and 14 called under a table
+// of 304 rows, 7.2 and 19 to 20 under one of 4,096 or 131,072 (Q8_0: 7.5 and 14, 9.3 and 19); 20
+// keys 3.8 and 5.9.
 struct PagedCut {
   float share, join;
 };
